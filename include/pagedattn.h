@@ -369,6 +369,108 @@ int pa_prefill_chunk_small_m(void* out, const void* q, const void* k_cache, cons
                              int head_dim, int block_size, int64_t num_blocks, float scale, int dtype, void* stream);
 
 /*
+ * pa_norm_rope_reshape_and_cache -- pa_rope_reshape_and_cache with the per-head RMS norm of the
+ * queries and keys that models with normalised heads apply first: one pass over the rows of the
+ * qkv projection.
+ * Source: mini_engine, "Features" (the Qwen3 decoder) and "Roadmap" (folding the rotary embedding
+ * and small per-step kernels into the KV-cache write).
+ *
+ * Every query and key head row x becomes y = x * w / sqrt(mean(x^2) + eps) (w: q_weight or
+ * k_weight, shared by the heads), then turns by its token's position as in
+ * pa_rope_reshape_and_cache; fp32 throughout, one rounding to dtype at the end.  Values are copied
+ * unchanged.
+ *
+ *  q        [num_tokens, n_q_heads, head_dim], tokens q_stride elements apart (heads and columns
+ *           contiguous), as in a slice of a fused projection; key, value likewise with n_kv_heads
+ *  q_out    the same shape, tokens q_out_stride apart; q itself with q_stride (in place) is
+ *           allowed, any other overlap is not
+ *  q_weight, k_weight [head_dim], dtype
+ *  slot_mapping, positions, cos_sin, caches: as pa_rope_reshape_and_cache (a row with slot -1
+ *           still gets its q_out; a row with a bad position is left untouched, q_out included)
+ *  Strides in elements, multiples of 8 (PA_ERR_ALIGN) and at least the row's width (PA_ERR_SHAPE).
+ *  eps finite and >= 0.  head_dim 64, 96, 128 or 256.
+ */
+int pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                                   int64_t key_stride, const void* value, int64_t value_stride, const void* q_weight,
+                                   const void* k_weight, float eps, void* k_cache, void* v_cache,
+                                   const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin,
+                                   int64_t num_tokens, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                                   int64_t num_blocks, int64_t max_position, int dtype, void* stream);
+
+/*
+ * The paged latent cache.  A layer with latent attention caches one row a token for all its heads:
+ * latent_cache [num_blocks, block_size, latent_dim + rope_dim], row = [c, kr], c the token's
+ * (normalised) latent vector, kr the rotated key part the heads share.  latent_dim 256 or 512,
+ * rope_dim 64, up to 128 heads, block_size 8, 16, 32, 64 or 128.  Slots, block tables and lengths
+ * are those of the K/V caches.
+ *
+ * pa_latent_rope_and_cache -- writes the rows of new tokens and rotates the queries' rotary parts.
+ *
+ *  kv       [num_tokens, latent_dim + rope_dim], tokens kv_stride elements apart: the raw latent
+ *           vector, then the shared key part
+ *  weight   [latent_dim], dtype: c = kv[:latent_dim] * weight / sqrt(mean(kv[:latent_dim]^2) + eps);
+ *           NULL: c is kv[:latent_dim] unchanged
+ *  q_pe     [num_tokens, n_heads, rope_dim], strides in elements, or NULL (then q and n_heads are
+ *           not used); rotated into the last rope_dim columns of
+ *  q        [num_tokens, n_heads, latent_dim + rope_dim], contiguous; its other columns are not
+ *           touched.  q_pe may be those very columns of q; any other overlap is not allowed
+ *  cos_sin  [max_position, rope_dim] (pa_rope_table)
+ *  interleaved  0: pair i is columns (i, i + 32) of a rotary part, as pa_rope_reshape_and_cache;
+ *           1: columns (2 i, 2 i + 1)
+ *  slot_mapping, positions as pa_rope_reshape_and_cache (slot -1: q_pe is still rotated; a bad
+ *  position leaves the row untouched).  fp32 throughout, one rounding to dtype.  Strides multiples
+ *  of 8 (PA_ERR_ALIGN); kv_stride >= the row's width, q_pe's heads innermost and not overlapping
+ *  (PA_ERR_SHAPE).
+ */
+int pa_latent_rope_and_cache(void* q, const void* q_pe, int64_t q_pe_token_stride, int64_t q_pe_head_stride,
+                             const void* kv, int64_t kv_stride, const void* weight, float eps, void* latent_cache,
+                             const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin,
+                             int64_t num_tokens, int n_heads, int latent_dim, int rope_dim, int block_size,
+                             int64_t num_blocks, int64_t max_position, int interleaved, int dtype, void* stream);
+
+/*
+ * Workspace bytes of pa_latent_decode (max_q_len 1) and pa_latent_prefill_chunk: a descriptor and
+ * two fp32 partials for each of up to PA_LATENT_MAX_CTAS CTAs, whatever the batch and the lengths.
+ * 0 for shapes they do not support.  Caller-owned; nothing in it needs to start at any value.  Calls
+ * that can run at the same time on the GPU must not share one.
+ */
+#define PA_LATENT_MAX_CTAS 160
+size_t pa_latent_workspace_size(int n_heads, int latent_dim, int max_q_len);
+
+/*
+ * pa_latent_decode -- decode attention over the paged latent cache (absorbed form), one query token
+ * a sequence, on the tcgen05 tensor cores; the contexts are split over the SMs and joined.
+ *
+ *  out   [num_seqs, n_heads, latent_dim]              written
+ *  q     [num_seqs, n_heads, latent_dim + rope_dim]   read: a head's query times its key
+ *        up-projection, then its rotated rotary part
+ *  out[s, h] = sum_t softmax_t(scale * q[s, h] . row_t) row_t[:latent_dim] over t < context_lens[s].
+ *  block_tables, context_lens as pa_decode (0: zero output rows; a length out of range counts as 0
+ *  and sets PA_DEVERR_LENGTH).  scale: 1 / sqrt(the heads' own key width) usually.  Softmax weights
+ *  enter the second product rounded to dtype; sums are fp32.
+ */
+int pa_latent_decode(void* out, const void* q, const void* latent_cache, const int32_t* block_tables,
+                     int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int n_heads, int latent_dim,
+                     int rope_dim, int block_size, int64_t num_blocks, float scale, int dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * pa_latent_prefill_chunk -- the same over ragged chunks of new tokens (a prefill chunk, or the few
+ * drafted tokens of a verification step), bottom-right causal over the cached context.
+ *
+ *  out, q, query_start_loc, seq_lens, max_q_len as pa_prefill_chunk with the rows of
+ *  pa_latent_decode; total_q: rows of q and out.  A chunk whose rows are not inside [0, total_q), is
+ *  longer than max_q_len or than its seq_lens, or whose seq_lens is past the table is skipped (its
+ *  rows are not written) and sets PA_DEVERR_LENGTH.  Cached rows of tokens a query row does not see
+ *  must be finite where they share its unit (up to 64 / n_heads consecutive tokens of the chunk).
+ */
+int pa_latent_prefill_chunk(void* out, const void* q, const void* latent_cache, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* query_start_loc, const int32_t* seq_lens,
+                            int num_chunks, int max_q_len, int64_t total_q, int n_heads, int latent_dim, int rope_dim,
+                            int block_size, int64_t num_blocks, float scale, int dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
  * Reads (and with clear != 0, resets) the error word of the current device.
  * Synchronises the device first.  Returns the PA_DEVERR_* bits, or a negative
  * status if the CUDA calls fail.

@@ -25,6 +25,8 @@ EXPORTED = (
     "pa_decode_splitk", "pa_prefill_chunk", "pa_device_errors", "pa_status_string", "pa_version",
     "pa_decode_splitk_static", "pa_rope_table", "pa_rope_reshape_and_cache", "pa_decode_shared_prefix",
     "pa_decode_shared_prefix_workspace_size", "pa_prefill_chunk_small_m", "pa_decode_write",
+    "pa_norm_rope_reshape_and_cache", "pa_latent_rope_and_cache", "pa_latent_workspace_size", "pa_latent_decode",
+    "pa_latent_prefill_chunk",
 )
 STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -86,6 +88,19 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.pa_prefill_chunk.restype = i32
     L.pa_prefill_chunk_small_m.argtypes = L.pa_prefill_chunk.argtypes
     L.pa_prefill_chunk_small_m.restype = i32
+    L.pa_norm_rope_reshape_and_cache.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, vp, vp, vp, vp,
+                                                 i64, i32, i32, i32, i32, i64, i64, i32, vp]
+    L.pa_norm_rope_reshape_and_cache.restype = i32
+    L.pa_latent_rope_and_cache.argtypes = [vp, vp, i64, i64, vp, i64, vp, f32, vp, vp, vp, vp, i64, i32, i32, i32, i32,
+                                           i64, i64, i32, i32, vp]
+    L.pa_latent_rope_and_cache.restype = i32
+    L.pa_latent_workspace_size.argtypes = [i32, i32, i32]
+    L.pa_latent_workspace_size.restype = sz
+    L.pa_latent_decode.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, f32, i32, vp, sz, vp]
+    L.pa_latent_decode.restype = i32
+    L.pa_latent_prefill_chunk.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i32, i32, i32, i32, i64, f32, i32,
+                                          vp, sz, vp]
+    L.pa_latent_prefill_chunk.restype = i32
     L.pa_device_errors.argtypes = [i32]
     L.pa_device_errors.restype = i32
     L.pa_status_string.argtypes = [i32]
@@ -319,6 +334,158 @@ def pa_prefill_chunk(out, q, k_cache, v_cache, block_tables, query_start_loc, se
             _dev(seq_lens, "seq_lens", torch.int32), C, int(max_q_len), hq, hkv, d, bs, nb,
             float(scale), dt, _stream(stream, q.device))
     _check(st, "pa_prefill_chunk_small_m" if small_m else "pa_prefill_chunk")
+
+
+def _on_current(first, *others) -> None:
+    """The library launches on the current device: every tensor has to be on it."""
+    dev = _torch().cuda.current_device() if first.is_cuda else None
+    for t in (first, *others):
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _rows(t, name: str, dtype, shape):
+    """Pointer and token stride (elements) of t [N, heads, dim], whose heads and columns are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    n, h, d = shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be contiguous within a token")
+    return t.data_ptr(), (int(t.stride(0)) if n > 1 else h * d)
+
+
+def pa_norm_rope_reshape_and_cache(q, key, value, q_weight, k_weight, k_cache, v_cache, slot_mapping, positions,
+                                   cos_sin, eps: float = 1e-6, q_out=None, stream=None) -> None:
+    """RMS norm of every head of q [N, Hq, D] (weight q_weight [D]) and key [N, Hkv, D] (k_weight),
+    rotation by positions [N] (int64) with the cos_sin table [max_position, D] (float32), key and
+    value into the caches at slot_mapping [N] (int64, -1 skips), q into q_out (default: in place).
+    q, key, value and q_out may be slices of wider rows (contiguous within a token)."""
+    torch = _torch()
+    dt = _dtype_code(q)
+    nb, bs, hkv, d = _cache_dims(k_cache)
+    n, hq = int(q.shape[0]), int(q.shape[1])
+    if tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache / v_cache shapes differ")
+    if tuple(slot_mapping.shape) != (n,) or tuple(positions.shape) != (n,):
+        raise ValueError("slot_mapping / positions must hold one value per token")
+    if tuple(q_weight.shape) != (d,) or tuple(k_weight.shape) != (d,):
+        raise ValueError("q_weight / k_weight must be [head_dim]")
+    if cos_sin.dim() != 2 or int(cos_sin.shape[1]) != d:
+        raise ValueError("cos_sin must be [max_position, head_dim]")
+    _on_current(q, key, value, q_weight, k_weight, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
+    qp, qs = _rows(q, "q", q.dtype, (n, hq, d))
+    op, os_ = (qp, qs) if q_out is None else _rows(q_out, "q_out", q.dtype, (n, hq, d))
+    kp, ks = _rows(key, "key", q.dtype, (n, hkv, d))
+    vp, vs = _rows(value, "value", q.dtype, (n, hkv, d))
+    st = load().pa_norm_rope_reshape_and_cache(
+        op, os_, qp, qs, kp, ks, vp, vs, _dev(q_weight, "q_weight", q.dtype), _dev(k_weight, "k_weight", q.dtype),
+        float(eps), _dev(k_cache, "k_cache", q.dtype), _dev(v_cache, "v_cache", q.dtype),
+        _dev(slot_mapping, "slot_mapping", torch.int64), _dev(positions, "positions", torch.int64),
+        _dev(cos_sin, "cos_sin", torch.float32), n, hq, hkv, d, bs, nb, int(cos_sin.shape[0]), dt,
+        _stream(stream, q.device))
+    _check(st, "pa_norm_rope_reshape_and_cache")
+
+
+LATENT_ROPE_DIM = 64
+
+
+def _latent_dims(latent_cache):
+    if latent_cache.dim() != 3 or int(latent_cache.shape[2]) <= LATENT_ROPE_DIM:
+        raise ValueError("latent_cache must be [num_blocks, block_size, latent_dim + 64]")
+    nb, bs, row = (int(x) for x in latent_cache.shape)
+    return nb, bs, row - LATENT_ROPE_DIM
+
+
+def pa_latent_rope_and_cache(kv, latent_cache, slot_mapping, positions, cos_sin, weight=None, eps: float = 1e-6,
+                             q_pe=None, q=None, interleaved: bool = False, stream=None) -> None:
+    """New tokens' rows of a paged latent cache [NB, bs, DL + 64]: kv [N, DL + 64] (rows may be strided),
+    its first DL columns RMS-normalised with weight [DL] (None: unchanged), its last 64 rotated by
+    positions [N] with the cos_sin table [max_position, 64], at slot_mapping [N] (-1 skips).  q_pe
+    [N, H, 64] (any strides of whole rows), if given, is rotated into the last 64 columns of
+    q [N, H, DL + 64]; it may be that slice of q."""
+    torch = _torch()
+    dt = _dtype_code(kv)
+    nb, bs, dl = _latent_dims(latent_cache)
+    n, row = int(kv.shape[0]), dl + LATENT_ROPE_DIM
+    kvp, kvs = _rows(kv.unsqueeze(1), "kv", kv.dtype, (n, 1, row))
+    if tuple(slot_mapping.shape) != (n,) or tuple(positions.shape) != (n,):
+        raise ValueError("slot_mapping / positions must hold one value per token")
+    if weight is not None and tuple(weight.shape) != (dl,):
+        raise ValueError("weight must be [latent_dim]")
+    if cos_sin.dim() != 2 or int(cos_sin.shape[1]) != LATENT_ROPE_DIM:
+        raise ValueError("cos_sin must be [max_position, 64]")
+    _on_current(kv, latent_cache, slot_mapping, positions, cos_sin, weight, q_pe, q)
+    qp = pep = None
+    h = pts = phs = 0
+    if (q_pe is None) != (q is None):
+        raise ValueError("q_pe and q come together")
+    if q_pe is not None:
+        h = int(q_pe.shape[1])
+        if tuple(q_pe.shape) != (n, h, LATENT_ROPE_DIM) or tuple(q.shape) != (n, h, row):
+            raise ValueError("q_pe must be [N, H, 64] and q [N, H, latent_dim + 64]")
+        if not q_pe.is_cuda or q_pe.dtype != kv.dtype or q_pe.stride(2) != 1:
+            raise ValueError("q_pe must be a CUDA tensor of kv's type with contiguous columns")
+        qp, pep = _dev(q, "q", kv.dtype), q_pe.data_ptr()
+        phs = int(q_pe.stride(1)) if h > 1 else LATENT_ROPE_DIM
+        pts = int(q_pe.stride(0)) if n > 1 else (h - 1) * phs + LATENT_ROPE_DIM
+    st = load().pa_latent_rope_and_cache(
+        qp, pep, pts, phs, kvp, kvs, None if weight is None else _dev(weight, "weight", kv.dtype), float(eps),
+        _dev(latent_cache, "latent_cache", kv.dtype), _dev(slot_mapping, "slot_mapping", torch.int64),
+        _dev(positions, "positions", torch.int64), _dev(cos_sin, "cos_sin", torch.float32), n, h, dl, LATENT_ROPE_DIM,
+        bs, nb, int(cos_sin.shape[0]), int(bool(interleaved)), dt, _stream(stream, kv.device))
+    _check(st, "pa_latent_rope_and_cache")
+
+
+def pa_latent_workspace_size(n_heads: int, latent_dim: int, max_q_len: int = 1) -> int:
+    return int(load().pa_latent_workspace_size(n_heads, latent_dim, max_q_len))
+
+
+def _latent_common(out, q, latent_cache, block_tables, lens, workspace):
+    torch = _torch()
+    dt = _dtype_code(q)
+    nb, bs, dl = _latent_dims(latent_cache)
+    if q.dim() != 3 or int(q.shape[2]) != dl + LATENT_ROPE_DIM or tuple(out.shape) != (*q.shape[:2], dl):
+        raise ValueError("q must be [rows, H, latent_dim + 64] and out [rows, H, latent_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != lens.shape[0]:
+        raise ValueError("block_tables must hold one row per length")
+    _on_current(q, out, latent_cache, block_tables, lens, workspace)
+    ptrs = (_dev(out, "out", q.dtype), _dev(q, "q", q.dtype), _dev(latent_cache, "latent_cache", q.dtype),
+            _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]))
+    wp, wb = (_dev(workspace, "workspace"), workspace.numel() * workspace.element_size()) if workspace is not None \
+        else (None, 0)
+    return dt, nb, bs, dl, int(q.shape[0]), int(q.shape[1]), ptrs, wp, wb
+
+
+def pa_latent_decode(out, q, latent_cache, block_tables, context_lens, scale: float, workspace, stream=None) -> None:
+    """Decode over a paged latent cache: out [S, H, DL], q [S, H, DL + 64]; workspace of at least
+    pa_latent_workspace_size(H, DL) bytes."""
+    torch = _torch()
+    dt, nb, bs, dl, S, h, ptrs, wp, wb = _latent_common(out, q, latent_cache, block_tables, context_lens, workspace)
+    if int(context_lens.shape[0]) != S:
+        raise ValueError("context_lens must hold one length per row of q")
+    st = load().pa_latent_decode(*ptrs, _dev(context_lens, "context_lens", torch.int32), S, h, dl, LATENT_ROPE_DIM, bs,
+                                 nb, float(scale), dt, wp, wb, _stream(stream, q.device))
+    _check(st, "pa_latent_decode")
+
+
+def pa_latent_prefill_chunk(out, q, latent_cache, block_tables, query_start_loc, seq_lens, max_q_len: int, scale: float,
+                            workspace, stream=None) -> None:
+    """Ragged chunks (bottom-right causal over their cached context) on a paged latent cache: out
+    [T, H, DL], q [T, H, DL + 64], chunk c the rows query_start_loc[c] .. query_start_loc[c + 1];
+    workspace of at least pa_latent_workspace_size(H, DL, max_q_len) bytes."""
+    torch = _torch()
+    dt, nb, bs, dl, T, h, ptrs, wp, wb = _latent_common(out, q, latent_cache, block_tables, seq_lens, workspace)
+    C = int(seq_lens.shape[0])
+    if tuple(query_start_loc.shape) != (C + 1,):
+        raise ValueError("query_start_loc must hold num_chunks + 1 rows")
+    st = load().pa_latent_prefill_chunk(*ptrs, _dev(query_start_loc, "query_start_loc", torch.int32),
+                                        _dev(seq_lens, "seq_lens", torch.int32), C, int(max_q_len), T, h, dl,
+                                        LATENT_ROPE_DIM, bs, nb, float(scale), dt, wp, wb, _stream(stream, q.device))
+    _check(st, "pa_latent_prefill_chunk")
 
 
 def pa_device_errors(clear: bool = True) -> int:

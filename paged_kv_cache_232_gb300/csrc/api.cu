@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "kv_write.cuh"
+#include "norm_rope_write.cuh"
 #include "rope_write.cuh"
 #include "pa_launch.h"
 #include "pagedattn.h"
@@ -799,6 +800,248 @@ int pa_decode_shared_prefix(void* out, const void* q, const void* k_cache, const
     return decode_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                        num_seqs, n_q_heads, n_kv_heads, head_dim, block_size, num_blocks, scale, dtype,
                        which == 2 ? part : 0, ws2, ws2_bytes, static_cast<cudaStream_t>(stream), &pin);
+}
+
+// ---- per-head norms, rotation and KV write ------------------------------------------------------
+
+int pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                                   int64_t key_stride, const void* value, int64_t value_stride, const void* q_weight,
+                                   const void* k_weight, float eps, void* k_cache, void* v_cache,
+                                   const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin,
+                                   int64_t num_tokens, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                                   int64_t num_blocks, int64_t max_position, int dtype, void* stream) {
+    if (num_tokens < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
+        max_position <= 0 || !(eps >= 0.f) || !std::isfinite(eps))
+        return PA_ERR_SHAPE;
+    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)n_q_heads + 2 * (int64_t)n_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    const int64_t qw = (int64_t)n_q_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
+    if (q_stride < qw || q_out_stride < qw || key_stride < kw || value_stride < kw) return PA_ERR_SHAPE;
+    if ((q_stride | q_out_stride | key_stride | value_stride) % 8) return PA_ERR_ALIGN;
+    if (num_tokens == 0) return PA_OK;
+    if (!q_out || !q || !key || !value || !q_weight || !k_weight || !k_cache || !v_cache || !slot_mapping ||
+        !positions || !cos_sin)
+        return PA_ERR_NULL;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(key) || !aligned16(value) || !aligned16(q_weight) ||
+        !aligned16(k_weight) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(cos_sin))
+        return PA_ERR_ALIGN;
+    DeviceState* dev = nullptr;
+    int st = device_state(&dev);
+    if (st != PA_OK) return st;
+    pa::NormRopeParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.key = static_cast<const uint16_t*>(key);
+    p.value = static_cast<const uint16_t*>(value);
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.q_stride = q_stride;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.q_out_stride = q_out_stride;
+    p.q_weight = static_cast<const uint16_t*>(q_weight);
+    p.k_weight = static_cast<const uint16_t*>(k_weight);
+    p.k_cache = static_cast<uint16_t*>(k_cache);
+    p.v_cache = static_cast<uint16_t*>(v_cache);
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.num_tokens = num_tokens;
+    p.num_slots = num_blocks * block_size;
+    p.max_position = max_position;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.eps = eps;
+    p.err = dev->err;
+    const int rpw = head_dim == 64 ? 8 : head_dim == 256 ? 2 : 4;  // head rows per warp
+    const int64_t warps = num_tokens * ((n_q_heads + 2 * n_kv_heads + rpw - 1) / rpw);
+    const int grid = (int)std::min<int64_t>((warps + 7) / 8, INT32_MAX);
+    auto launch = [&](auto kern) { kern<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p); };
+    const bool bf = dtype == PA_BF16;
+    if (head_dim == 64) bf ? launch(pa::norm_rope_write_kernel<true, 64>) : launch(pa::norm_rope_write_kernel<false, 64>);
+    else if (head_dim == 96) bf ? launch(pa::norm_rope_write_kernel<true, 96>) : launch(pa::norm_rope_write_kernel<false, 96>);
+    else if (head_dim == 128) bf ? launch(pa::norm_rope_write_kernel<true, 128>) : launch(pa::norm_rope_write_kernel<false, 128>);
+    else bf ? launch(pa::norm_rope_write_kernel<true, 256>) : launch(pa::norm_rope_write_kernel<false, 256>);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// ---- the paged latent cache ---------------------------------------------------------------------
+
+static constexpr int kLatentRope = 64;
+
+static int check_latent(int n_heads, int latent_dim, int rope_dim, int block_size, int dtype) {
+    if (n_heads <= 0 || latent_dim <= 0 || rope_dim <= 0 || block_size <= 0) return PA_ERR_SHAPE;
+    if (n_heads > 128) return PA_ERR_UNSUPPORTED;
+    if ((latent_dim != 256 && latent_dim != 512) || rope_dim != kLatentRope) return PA_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
+        return PA_ERR_UNSUPPORTED;
+    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+int pa_latent_rope_and_cache(void* q, const void* q_pe, int64_t q_pe_token_stride, int64_t q_pe_head_stride,
+                             const void* kv, int64_t kv_stride, const void* weight, float eps, void* latent_cache,
+                             const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin,
+                             int64_t num_tokens, int n_heads, int latent_dim, int rope_dim, int block_size,
+                             int64_t num_blocks, int64_t max_position, int interleaved, int dtype, void* stream) {
+    if (num_tokens < 0 || num_blocks <= 0 || max_position <= 0 || !(eps >= 0.f) || !std::isfinite(eps))
+        return PA_ERR_SHAPE;
+    int st = check_latent(q_pe ? n_heads : 1, latent_dim, rope_dim, block_size, dtype);
+    if (st != PA_OK) return st;
+    const int row = latent_dim + rope_dim;
+    if (kv_stride < row || kv_stride % 8) return kv_stride < row ? PA_ERR_SHAPE : PA_ERR_ALIGN;
+    if (q_pe) {
+        // rows of 64 columns that do not overlap, heads innermost
+        if (q_pe_head_stride < rope_dim || q_pe_token_stride < (n_heads - 1) * q_pe_head_stride + rope_dim)
+            return PA_ERR_SHAPE;
+        if ((q_pe_head_stride | q_pe_token_stride) % 8) return PA_ERR_ALIGN;
+    }
+    if (num_tokens == 0) return PA_OK;
+    if (!kv || !latent_cache || !slot_mapping || !positions || !cos_sin || (q_pe && !q)) return PA_ERR_NULL;
+    if (!aligned16(kv) || !aligned16(latent_cache) || !aligned16(cos_sin) || (weight && !aligned16(weight)) ||
+        (q_pe && (!aligned16(q) || !aligned16(q_pe))))
+        return PA_ERR_ALIGN;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != PA_OK) return st;
+    pa::LatentWriteParams p{};
+    p.kv = static_cast<const uint16_t*>(kv);
+    p.weight = static_cast<const uint16_t*>(weight);
+    p.q_pe = static_cast<const uint16_t*>(q_pe);
+    p.q = static_cast<uint16_t*>(q);
+    p.cache = static_cast<uint16_t*>(latent_cache);
+    p.kv_stride = kv_stride;
+    p.pe_token_stride = q_pe_token_stride;
+    p.pe_head_stride = q_pe_head_stride;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.num_tokens = num_tokens;
+    p.num_slots = num_blocks * block_size;
+    p.max_position = max_position;
+    p.n_heads = n_heads;
+    p.interleaved = interleaved != 0;
+    p.eps = eps;
+    p.err = dev->err;
+    const int64_t warps = num_tokens * (1 + (1 + (q_pe ? n_heads : 0) + 7) / 8);
+    const int grid = (int)std::min<int64_t>((warps + 7) / 8, INT32_MAX);
+    auto launch = [&](auto kern) { kern<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p); };
+    const bool bf = dtype == PA_BF16;
+    if (latent_dim == 512) bf ? launch(pa::latent_write_kernel<true, 512>) : launch(pa::latent_write_kernel<false, 512>);
+    else bf ? launch(pa::latent_write_kernel<true, 256>) : launch(pa::latent_write_kernel<false, 256>);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// query rows per unit for n_heads and chunks of up to max_q_len tokens
+static int latent_rows(int n_heads, int max_q_len) {
+    if (n_heads > 64) return 64;
+    return pa::latent_unit_rows(n_heads * std::min(std::max(max_q_len, 1), 64 / n_heads));
+}
+
+struct LatentWs {
+    size_t desc_off, ml_off, o_off, total;
+};
+
+static LatentWs latent_ws(int unit_rows, int latent_dim) {
+    const size_t slots = 2 * (size_t)PA_LATENT_MAX_CTAS;
+    LatentWs w;
+    w.desc_off = 0;
+    w.ml_off = align256(PA_LATENT_MAX_CTAS * sizeof(int4));
+    w.o_off = w.ml_off + align256(slots * unit_rows * 2 * sizeof(float));
+    w.total = w.o_off + slots * unit_rows * latent_dim * sizeof(float);
+    return w;
+}
+
+size_t pa_latent_workspace_size(int n_heads, int latent_dim, int max_q_len) {
+    if (max_q_len < 0 || check_latent(n_heads, latent_dim, kLatentRope, 16, PA_BF16) != PA_OK) return 0;
+    return latent_ws(latent_rows(n_heads, max_q_len), latent_dim).total;
+}
+
+// Tensor map over [planes, rows, cols] 16-bit data: boxes of 64 columns x box_rows rows of one plane,
+// 128-byte swizzled; coordinates outside read zeros.  planes 0: a 2-D map [rows, cols].
+static int encode_latent_map(CUtensorMap* m, const void* base, int dtype, int64_t planes, int64_t rows, int cols,
+                             int box_rows) {
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)rows * cols * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          planes ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
+static int latent_impl(void* out, const void* q, const void* latent_cache, const int32_t* block_tables,
+                       int max_blocks_per_seq, const int32_t* q_loc, const int32_t* kv_lens, int num_chunks,
+                       int max_q_len, int64_t total_q, int n_heads, int latent_dim, int rope_dim, int block_size,
+                       int64_t num_blocks, float scale, int dtype, void* workspace, size_t workspace_bytes, void* stream,
+                       bool chunks) {
+    if (num_chunks < 0 || max_q_len < 0 || total_q < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0) return PA_ERR_SHAPE;
+    int st = check_latent(n_heads, latent_dim, rope_dim, block_size, dtype);
+    if (st != PA_OK) return st;
+    // token, block and query-row numbers are 32-bit in the kernel (tile ends included)
+    if (num_blocks >= INT32_MAX || (int64_t)max_blocks_per_seq * block_size > INT32_MAX - 1024 ||
+        total_q * n_heads > INT32_MAX - 1024)
+        return PA_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return PA_ERR_SHAPE;
+    if (num_chunks == 0 || max_q_len == 0 || total_q == 0) return PA_OK;
+    if (!out || !q || !latent_cache || !block_tables || !kv_lens || (chunks && !q_loc)) return PA_ERR_NULL;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(latent_cache)) return PA_ERR_ALIGN;
+    const int rows = latent_rows(n_heads, max_q_len);
+    const LatentWs w = latent_ws(rows, latent_dim);
+    if (!workspace || workspace_bytes < w.total) return PA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PA_ERR_ALIGN;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != PA_OK) return st;
+    char* base = static_cast<char*>(workspace);
+    pa::LatentParams p{};
+    p.out = out;
+    p.block_tables = block_tables;
+    p.q_loc = q_loc;
+    p.kv_lens = kv_lens;
+    p.err = dev->err;
+    p.num_chunks = num_chunks;
+    p.n_heads = n_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_blocks = (int)num_blocks;
+    p.block_size = block_size;
+    p.max_q_len = max_q_len;
+    p.total_q = (int)total_q;
+    p.hb = n_heads > 64 ? 2 : 1;
+    p.tb = p.hb == 2 ? 1 : rows / n_heads;
+    p.min_tiles = 2;
+    p.stream_once = (!chunks && p.hb == 1) ? 1 : 0;
+    p.qk_scale_log2 = scale * 1.4426950408889634f;
+    p.desc = reinterpret_cast<int4*>(base + w.desc_off);
+    p.part_ml = reinterpret_cast<float*>(base + w.ml_off);
+    p.part_o = reinterpret_cast<float*>(base + w.o_off);
+    CUtensorMap tc, tq;
+    const int row = latent_dim + rope_dim;
+    if ((st = encode_latent_map(&tc, latent_cache, dtype, num_blocks, block_size, row, std::min(block_size, 64))) != PA_OK)
+        return st;
+    if ((st = encode_latent_map(&tq, q, dtype, 0, total_q * n_heads, row, rows)) != PA_OK) return st;
+    const int grid = std::min(dev->sm_count, PA_LATENT_MAX_CTAS);
+    cudaError_t e = pa::launch_latent(dtype == PA_BF16, latent_dim, rows, p, tc, tq, grid,
+                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_latent_decode(void* out, const void* q, const void* latent_cache, const int32_t* block_tables,
+                     int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int n_heads, int latent_dim,
+                     int rope_dim, int block_size, int64_t num_blocks, float scale, int dtype, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    return latent_impl(out, q, latent_cache, block_tables, max_blocks_per_seq, nullptr, context_lens, num_seqs, 1,
+                       num_seqs, n_heads, latent_dim, rope_dim, block_size, num_blocks, scale, dtype, workspace,
+                       workspace_bytes, stream, false);
+}
+
+int pa_latent_prefill_chunk(void* out, const void* q, const void* latent_cache, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* query_start_loc, const int32_t* seq_lens,
+                            int num_chunks, int max_q_len, int64_t total_q, int n_heads, int latent_dim, int rope_dim,
+                            int block_size, int64_t num_blocks, float scale, int dtype, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    return latent_impl(out, q, latent_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens, num_chunks,
+                       max_q_len, total_q, n_heads, latent_dim, rope_dim, block_size, num_blocks, scale, dtype,
+                       workspace, workspace_bytes, stream, true);
 }
 
 }  // extern "C"

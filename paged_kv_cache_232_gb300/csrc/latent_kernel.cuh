@@ -1,0 +1,786 @@
+// latent_kernel.cuh -- attention over a paged cache of latent vectors (absorbed form), on the
+// tcgen05 tensor cores.
+//
+// A cache row of a token is [c (DL columns), kr (64 columns)]: its latent vector and the rotated
+// key part all heads share.  Every head's key is the whole row, its value the latent part:
+//     out[h] = sum_t softmax_t(scale * q[h] . row_t) c_t,
+// so the H heads of a token are H rows of one dense contraction over the same keys: each cache
+// row is read once for all of them.  Decode (one query token a sequence) and ragged chunks
+// (bottom-right causal) are one kernel: a unit is up to NR query rows (tokens x heads, 64 heads
+// at most) of one sequence over its keys.
+//
+// GB300 design:
+//  * Keys come in tiles of 64 tokens, as DL / 128 "pair" slots (two 64-column slabs of 64 rows,
+//    128-byte swizzled, 16 KB) and one rotary slot (8 KB).  Pair slots and rotary slots are two
+//    rings: a pair slot is released as soon as the PV product of its 128 columns is done, the
+//    rotary slot after the QK product, so loads stay in flight at a finer grain than whole tiles.
+//  * S = Q K^T: M = 64 query rows, N = 64 tokens, both operands K-major.  At M = 64 row r sits in
+//    TMEM lane (r mod 16) + 32 (r / 16), so one thread owns one row: the softmax needs no
+//    exchange between threads.  With NR < 64 the A operand's rows past NR read the shared memory
+//    behind the Q tile: rows of D are independent and those are never looked at.
+//  * O^T = C^T P^T: M = 128 latent columns (A: the pair slot read MN-major), N = NR query rows
+//    (B: the weights, K-major), so the accumulator takes DL / 128 x NR TMEM columns (256 at 64
+//    rows x 512; rows on M would take all 512 columns and leave none for S).
+//  * The running maximum is updated lazily: O and l are rescaled only when a row's maximum grows
+//    by more than 2^8; weights up to 2^8 above the reference are exact in fp32 and far from the
+//    16-bit formats' limits.  A weight enters the PV product rounded to the cache's 16-bit type
+//    (half a step is 2^-8 in bf16, 2^-11 in fp16, relative; the roundings of different keys are
+//    independent, so their sum stays about as large as the rounding of the output to that type,
+//    and a second product for the remainders would cost half the tensor work again), and l sums the
+//    rounded weights, so that they still sum to one.
+//  * The tiles of all units, laid end to end, are cut into equal ranges, one a CTA (one CTA per
+//    SM): units that end inside a range are written directly, the two that its ends cut leave fp32
+//    partials that latent_merge_kernel joins in a fixed order (no atomics).  The split needs no
+//    host-side lengths, and no workspace beyond two partials a CTA.
+//  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set, the roles leave their loops and
+//    TMEM is released.
+#pragma once
+
+#include "pa_launch.h"
+#include "tcgen05.cuh"
+
+namespace pa {
+namespace lat {
+
+constexpr int TK = 64;                  // tokens per tile
+constexpr int ROPE = 64;                // rotary columns of a cache row
+constexpr int SLAB = TK * 128;          // bytes of 64 tokens x 64 columns
+constexpr int PAIR = 2 * SLAB;
+constexpr int SOFTMAX_WARPS = 4, TMA_WARP = 4, MMA_WARP = 5, Q_WARP = 6;
+constexpr int THREADS = 7 * 32;
+constexpr int MAX_CTAS = 512;           // of the split: latent_merge_kernel gives every partial a thread
+
+template <int DL, int NR>
+struct Cfg {
+    static_assert(DL == 256 || DL == 512, "latent columns");
+    static_assert(NR == 16 || NR == 32 || NR == 64, "query rows per unit");
+    static constexpr int NB = DL / 128;                 // pair slots per tile = M blocks of O^T
+    static constexpr int QSLABS = DL / 64 + 1;
+    static constexpr int QSLAB = NR * 128;
+    // as many ring slots as fit next to the Q tile and the weights
+    static constexpr int NPAIR = DL == 512 ? (NR == 64 ? 8 : NR == 32 ? 10 : 11) : (NR == 64 ? 8 : 10);
+    static constexpr int NROPE = DL == 512 ? (NR == 64 ? 2 : 3) : (NR == 64 ? 4 : 5);
+    static constexpr int Q_OFF = 0;
+    static constexpr int P_OFF = QSLABS * QSLAB;
+    static constexpr int PAIR_OFF = P_OFF + NR * 128;
+    static constexpr int ROPE_OFF = PAIR_OFF + NPAIR * PAIR;
+    static constexpr int BAR_OFF = ROPE_OFF + NROPE * SLAB;
+    // barriers
+    static constexpr int PAIR_FULL = 0, PAIR_EMPTY = NPAIR, ROPE_FULL = 2 * NPAIR, ROPE_EMPTY = 2 * NPAIR + NROPE;
+    static constexpr int Q_FULL = 2 * (NPAIR + NROPE), Q_EMPTY = Q_FULL + 1, S_FULL = Q_FULL + 2, P_FULL = Q_FULL + 4,
+                         PV_DONE = Q_FULL + 5, O_FREE = Q_FULL + 6, DRAIN = Q_FULL + 7, NUM_BARS = Q_FULL + 8;
+    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;      // start record, TMEM address, scan scratch
+    static constexpr int ROW_OFF = MISC_OFF + 192;               // alpha [NR] and 1 / l [NR]
+    static constexpr int SMEM_BYTES = ROW_OFF + 2 * NR * 4 + 1024;  // + alignment slack
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    // the A operand of QK reads 64 rows of each Q slab, whatever NR is
+    static_assert((QSLABS - 1) * QSLAB + 64 * 128 <= BAR_OFF, "QK operand stays inside the tile area");
+    static constexpr uint32_t O_COL = 128;                       // two S buffers of 64 columns, then O^T
+    static constexpr uint32_t TMEM_COLS = 128 + NB * NR <= 256 ? 256 : 512;
+};
+
+// kind::f16 instruction descriptor with the A operand's major-ness (bit 15), see tc::idesc_f16
+__host__ __device__ constexpr uint32_t idesc(bool bf16, bool a_mn_major, int M, int N) {
+    return tc::idesc_f16(bf16, false, M, N) | ((a_mn_major ? 1u : 0u) << 15);
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// barrier of the four softmax warps that ORs a predicate over them
+__device__ __forceinline__ bool softmax_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// The warp waits through lane 0 alone; __syncwarp orders the other lanes behind its acquire.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok;
+}
+
+// ---- the split of all units' tiles over the CTAs ---------------------------------------------
+
+// One sequence's chunk: its first query row, query tokens and keys.  Decode: one token, the rows
+// in sequence order.  Lengths out of range: decode takes the sequence as empty (its rows become
+// zero), a chunk is skipped (q_len 0).
+struct Chunk {
+    int q0, q_len, kv_len;
+    bool bad;
+};
+
+__device__ __forceinline__ Chunk load_chunk(const LatentParams& p, int c) {
+    Chunk k;
+    const int cap = p.max_blocks_per_seq * p.block_size;
+    k.kv_len = __ldg(p.kv_lens + c);
+    if (p.q_loc == nullptr) {
+        k.q0 = c;
+        k.q_len = 1;
+        k.bad = k.kv_len < 0 || k.kv_len > cap;
+        if (k.bad) k.kv_len = 0;
+    } else {
+        k.q0 = __ldg(p.q_loc + c);
+        const int q1 = __ldg(p.q_loc + c + 1);
+        k.q_len = q1 - k.q0;
+        k.bad = k.q0 < 0 || q1 < k.q0 || q1 > p.total_q || k.q_len > p.max_q_len || k.kv_len < k.q_len ||
+                k.kv_len > cap;
+        if (k.bad) k.q_len = 0;
+    }
+    return k;
+}
+
+// keys that token block j of a chunk sees: up to its last token's limit
+__device__ __forceinline__ int keys_of(const LatentParams& p, const Chunk& k, int j) {
+    return k.kv_len - k.q_len + min((j + 1) * p.tb, k.q_len);
+}
+__device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + TK - 1) / TK); }
+
+// sum over i < n of floor((a i + b) / m), by the Euclidean reduction of the lattice-point count
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    unsigned long long s = 0;
+    while (true) {
+        if (a >= m) {
+            s += (unsigned long long)n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            s += (unsigned long long)n * (b / m);
+            b %= m;
+        }
+        const unsigned long long y = (unsigned long long)a * n + b;
+        if (y < m) return (long long)s;
+        n = (uint32_t)(y / m);
+        b = (uint32_t)(y % m);
+        const uint32_t t = m;
+        m = a;
+        a = t;
+    }
+}
+
+// tiles of token blocks 0 .. n - 1 of a chunk (n at most its number of blocks)
+__device__ __forceinline__ long long tiles_before(const LatentParams& p, const Chunk& k, int n) {
+    if (n == 0) return 0;
+    const int last = (k.q_len + p.tb - 1) / p.tb - 1;  // the last block may be short
+    const int full = min(n, last);
+    long long s = 0;
+    if (full > 0)  // block i: ceil((ctx + (i + 1) tb) / TK)
+        s = floor_sum((uint32_t)full, TK, (uint32_t)p.tb, (uint32_t)(k.kv_len - k.q_len + p.tb + TK - 1));
+    if (n > last) s += tiles_of(k.kv_len);
+    return s;
+}
+
+__device__ __forceinline__ long long tiles_in(const LatentParams& p, const Chunk& k) {
+    if (k.q_len == 0) return 0;
+    return p.hb * (p.q_loc == nullptr ? (long long)tiles_of(k.kv_len)
+                                      : tiles_before(p, k, (k.q_len + p.tb - 1) / p.tb));
+}
+
+// This CTA's range of tiles: where it starts (chunk, token block, half, tile) and how many.
+struct Start {
+    int c, j, half, tile, count, per;
+};
+
+// Every thread of the CTA calls it; all return the same record.
+__device__ __forceinline__ Start find_start(const LatentParams& p, long long* warp_sum, Start* rec) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int NW = THREADS / 32;
+    long long mine = 0;
+    for (int c = tid; c < p.num_chunks; c += THREADS) {
+        const Chunk k = load_chunk(p, c);
+        if (k.bad && blockIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
+        mine += tiles_in(p, k);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) warp_sum[warp] = mine;
+    if (tid == 0) rec->count = 0;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < NW; ++w) total += warp_sum[w];
+    const long long even = (total + gridDim.x - 1) / gridDim.x;
+    const int per = (int)max(even, (long long)p.min_tiles);
+    const long long lo = (long long)blockIdx.x * per;
+    __syncthreads();
+    if (lo < total) {
+        // the chunk that holds tile lo: prefix sums, THREADS chunks at a time
+        long long base = 0;
+        for (int c0 = 0; c0 < p.num_chunks; c0 += THREADS) {
+            const int c = c0 + tid;
+            Chunk k{0, 0, 0, false};
+            if (c < p.num_chunks) k = load_chunk(p, c);
+            const long long n = c < p.num_chunks ? tiles_in(p, k) : 0;
+            long long incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (lane == 31) warp_sum[warp] = incl;
+            __syncthreads();
+            long long before = base;
+            for (int w = 0; w < warp; ++w) before += warp_sum[w];
+            long long all = base;
+            for (int w = 0; w < NW; ++w) all += warp_sum[w];
+            const long long at = before + incl - n;
+            if (n > 0 && lo >= at && lo < at + n) {
+                long long rem = lo - at;
+                int j = 0;
+                if (p.q_loc != nullptr) {  // the last block whose first tile is at or before rem
+                    int hi = (k.q_len + p.tb - 1) / p.tb - 1;
+                    while (j < hi) {
+                        const int mid = (j + hi + 1) >> 1;
+                        if (p.hb * tiles_before(p, k, mid) <= rem) j = mid;
+                        else hi = mid - 1;
+                    }
+                    rem -= p.hb * tiles_before(p, k, j);
+                }
+                const int t = tiles_of(keys_of(p, k, j));
+                rec->c = c;
+                rec->j = j;
+                rec->half = (int)(rem / t);
+                rec->tile = (int)(rem % t);
+                rec->count = (int)min((long long)per, total - lo);
+            }
+            base = all;
+            __syncthreads();
+            if (base > lo) break;
+        }
+    }
+    __syncthreads();
+    Start s = *rec;
+    s.per = per;
+    return s;
+}
+
+// One segment of the CTA's range: tiles [tile, tile + n) of one unit's `tiles`.
+struct Segment {
+    int c, j, half;
+    int tile, n, tiles;
+    int ctx, keys;          // token jt of the block sees keys <= ctx + j tb + jt; the unit's tokens see [0, keys)
+    int rows;               // query rows of the unit
+    int row0;               // the first one's row of q and out, [total_q * n_heads]
+    int left;               // tiles of the CTA's range after this segment
+};
+
+template <typename F>
+__device__ __forceinline__ void for_each_segment(const LatentParams& p, const Start& s, F&& f) {
+    int c = s.c, j = s.j, half = s.half, tile = s.tile, left = s.count;
+    if (left <= 0) return;
+    Chunk k = load_chunk(p, c);
+    while (left > 0) {
+        Segment g;
+        g.c = c;
+        g.j = j;
+        g.half = half;
+        g.keys = keys_of(p, k, j);
+        g.tiles = tiles_of(g.keys);
+        g.tile = tile;
+        g.n = min(g.tiles - tile, left);
+        g.ctx = k.kv_len - k.q_len;
+        g.rows = p.hb == 2 ? (half == 0 ? 64 : p.n_heads - 64) : min(p.tb, k.q_len - j * p.tb) * p.n_heads;
+        g.row0 = (k.q0 + j * p.tb) * p.n_heads + half * 64;
+        left -= g.n;
+        g.left = left;
+        if (!f(g)) return;
+        if (left <= 0) return;
+        tile = 0;
+        if (++half < p.hb) continue;
+        half = 0;
+        if ((++j) * p.tb < k.q_len) continue;
+        j = 0;
+        do {
+            if (++c >= p.num_chunks) return;
+            k = load_chunk(p, c);
+        } while (k.q_len == 0);
+    }
+}
+
+}  // namespace lat
+
+template <bool BF16, int DL, int NR>
+__global__ void __launch_bounds__(lat::THREADS, 1)
+latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmQ) {
+    using namespace lat;
+    using C = Cfg<DL, NR>;
+    using F = F16x2<BF16>;
+    constexpr int NB = C::NB;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t sQ = sbase + C::Q_OFF, sP = sbase + C::P_OFF, sPair = sbase + C::PAIR_OFF, sRope = sbase + C::ROPE_OFF;
+    const uint32_t bars = sbase + C::BAR_OFF;
+    auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+    Start* rec = reinterpret_cast<Start*>(smem + C::MISC_OFF);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF + 32);
+    long long* warp_sum = reinterpret_cast<long long*>(smem + C::MISC_OFF + 64);
+    volatile float* alpha_s = reinterpret_cast<volatile float*>(smem + C::ROW_OFF);
+    volatile float* inv_s = alpha_s + NR;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NPAIR; ++i) {
+            mbar_init(bar(C::PAIR_FULL + i), 1);
+            mbar_init(bar(C::PAIR_EMPTY + i), 1);
+        }
+        for (int i = 0; i < C::NROPE; ++i) {
+            mbar_init(bar(C::ROPE_FULL + i), 1);
+            mbar_init(bar(C::ROPE_EMPTY + i), 1);
+        }
+        mbar_init(bar(C::Q_FULL), 1);
+        mbar_init(bar(C::Q_EMPTY), 1);
+        mbar_init(bar(C::S_FULL), 1);
+        mbar_init(bar(C::S_FULL + 1), 1);
+        mbar_init(bar(C::P_FULL), SOFTMAX_WARPS);
+        mbar_init(bar(C::PV_DONE), 1);
+        mbar_init(bar(C::O_FREE), SOFTMAX_WARPS);
+        mbar_init(bar(C::DRAIN), 1);
+        fence_barrier_init();
+    }
+    if (warp == MMA_WARP) {
+        tc::alloc(smem_addr(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
+        tc::relinquish();
+    }
+    // a programmatic dependent of the kernel before it: nothing is read before that one is complete;
+    // the merge may be set up now (it waits for this grid before it reads)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc::fence_before();
+    const Start start = find_start(p, warp_sum, rec);  // (synchronises the CTA)
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < SOFTMAX_WARPS) {
+        // ------------------------------------------------------------ softmax, rescale, epilogue
+        const int r = lane < 16 ? 16 * warp + lane : -1;  // this thread's query row of the unit
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const uint32_t tS = tmem + lane_base, tO = tmem + lane_base + C::O_COL;
+        const bool row_warp = 16 * warp < NR;             // the warp holds rows of S at all
+        const float sc = p.qk_scale_log2;
+        int i = 0;             // tile number over the CTA's range
+        int pv_seen = 0;       // PV_DONE phases this warp has waited for
+        int seg = 0, pair0 = 0;  // segment number; ring position of the tile's first pair slot
+        bool ok = true;
+        int desc_parts = 0, desc_rows = 0, desc_row0 = 0, desc_slot = 0;
+        auto wait_pv = [&](int n) {  // PVs of tiles 0 .. n - 1 complete
+            while (pv_seen < n) {
+                ok = lat::warp_wait(bar(C::PV_DONE), (uint32_t)(pv_seen & 1), p.err) && ok;
+                ++pv_seen;
+            }
+        };
+        for_each_segment(p, start, [&](const Segment& g) -> bool {
+            const bool valid = r >= 0 && r < g.rows;
+            const int tok = p.hb == 2 ? 0 : (valid ? r / p.n_heads : 0);
+            const int lim = valid ? g.ctx + g.j * p.tb + tok : -1;  // the row sees keys <= lim
+            const int lim_min = g.ctx + g.j * p.tb;                 // the smallest limit in the unit
+            float m_ref = -INFINITY, l = 0.f;
+            for (int u = 0; u < g.n; ++u, ++i) {
+                const int kbase = (g.tile + u) * TK;
+                const uint32_t tSb = tS + (uint32_t)((i & 1) * 64);
+                float x[64];
+                float mx = -INFINITY;
+                if (row_warp) {
+                    ok = lat::warp_wait(bar(C::S_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), p.err) && ok;
+                    tc::fence_after();
+                    uint32_t s[64];
+                    tc::ld64(tSb, s);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(s[e]) * sc;
+                    if (kbase + TK - 1 > lim_min || g.rows < NR || lane >= 16) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (kbase + e > lim) x[e] = -INFINITY;
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[e]);
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                }
+                const bool first = u == 0;
+                if (first) m_ref = mx;  // no O yet: the first tile's own maximum is the reference
+                if (softmax_or(!ok || mx > m_ref + 8.f)) {
+                    if (softmax_or(!ok)) {  // some warp's wait ran out: all four leave together
+                        ok = false;
+                        return false;
+                    }
+                    float alpha = 1.f;
+                    if (mx > m_ref) {
+                        alpha = m_ref == -INFINITY ? 1.f : ex2(m_ref - mx);
+                        m_ref = mx;
+                        l *= alpha;
+                    }
+                    if (valid) alpha_s[r] = alpha;
+                    else if (r >= 0 && r < NR) alpha_s[r] = 1.f;
+                    wait_pv(i);  // O holds every tile before this one
+                    softmax_sync();
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int q = 0; q < NB * NR / 16; ++q) {
+                        uint32_t o[16];
+                        tc::ld16(tO + 16 * q, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_s[(16 * q + e) & (NR - 1)]);
+                        tc::st16(tO + 16 * q, o);
+                    }
+                    tc::wait_st();
+                }
+                if (row_warp) {
+                    const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                    uint32_t w[32];
+                    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        w[e] = F::pack_rn(ex2(x[2 * e] - mu), ex2(x[2 * e + 1] - mu));
+                        const float2 b = F::unpack(w[e]);
+                        l0 += b.x;
+                        l1 += b.y;
+                    }
+                    l += l0 + l1;
+                    wait_pv(i);  // the weights' buffer is free
+                    if (r >= 0) {
+#pragma unroll
+                        for (int ch = 0; ch < 8; ++ch)
+                            sts128(sP + swz128(r, ch), make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]));
+                    }
+                } else {
+                    wait_pv(i);  // in step with PV_DONE's phases, one a tile
+                }
+                if (kbase + TK > g.keys) {
+                    // rows past the keys may hold anything (their weights are 0, but 0 * NaN is NaN): zero them
+                    // (this tile's S, which also read them, is complete: the warps with rows have seen it
+                    // before the vote above)
+                    const int z = max(g.keys - kbase, 0), nz = (TK - z) * 8;
+                    for (int b = 0; b < 2 * NB; ++b) {
+                        const int slot = (pair0 + (b >> 1)) % C::NPAIR;
+                        const uint32_t dst = sPair + slot * PAIR + (b & 1) * SLAB + z * 128;
+                        for (int e = threadIdx.x; e < nz; e += 128) sts128(dst + e * 16, make_uint4(0u, 0u, 0u, 0u));
+                    }
+                }
+                pair0 = (pair0 + NB) % C::NPAIR;
+                tc::fence_async_smem();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::P_FULL));
+            }
+            // the segment's end: O^T / l, or the partial
+            const bool whole = g.tile == 0 && g.n == g.tiles;
+            const int slot = 2 * (int)blockIdx.x + (seg == 0 ? 0 : 1);
+            if (r >= 0 && r < NR) {
+                inv_s[r] = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+                if (!whole && valid) {
+                    p.part_ml[((size_t)slot * NR + r) * 2] = m_ref;
+                    p.part_ml[((size_t)slot * NR + r) * 2 + 1] = l;
+                }
+            }
+            wait_pv(i);
+            if (softmax_or(!ok)) {
+                ok = false;
+                return false;
+            }
+            tc::fence_after();
+            const int col = warp * 32 + lane;  // this thread's latent column within a block of 128
+            constexpr int W = NR < 32 ? NR : 32;
+#pragma unroll 1
+            for (int q = 0; q < NB * NR / W; ++q) {
+                uint32_t o[W];
+                if constexpr (W == 16) tc::ld16(tO + W * q, o);
+                else tc::ld32(tO + W * q, o);
+                tc::wait_ld();
+                if (q == NB * NR / W - 1) {  // O^T read: the next segment's first PV may overwrite it
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::O_FREE));
+                }
+                const int blk = (W * q) / NR, h0 = (W * q) & (NR - 1);
+                if (whole) {
+                    uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(g.row0 + h0) * DL + blk * 128 + (col & ~1);
+#pragma unroll
+                    for (int e = 0; e < W; e += 2) {
+                        // lanes 2k and 2k + 1 hold columns 2k, 2k + 1 of rows e and e + 1: after the exchange the
+                        // even lane has both of row e, the odd lane both of row e + 1
+                        const float a = __uint_as_float(o[e]) * inv_s[h0 + e], b = __uint_as_float(o[e + 1]) * inv_s[h0 + e + 1];
+                        const float y = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+                        const int row = e + (lane & 1);
+                        if (h0 + row < g.rows)
+                            *reinterpret_cast<uint32_t*>(dst + (size_t)row * DL) =
+                                (lane & 1) ? F::pack_rn(y, b) : F::pack_rn(a, y);
+                    }
+                } else {
+                    float* dst = p.part_o + ((size_t)slot * NR + h0) * DL + blk * 128 + col;
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        if (h0 + e < g.rows) dst[(size_t)e * DL] = __uint_as_float(o[e]);
+                }
+            }
+            if (!whole && g.tile == 0) {  // the unit starts here and goes on in the CTAs behind
+                const long long f0 = (long long)blockIdx.x * start.per + (start.count - g.left - g.n);
+                desc_parts = (int)((f0 + g.tiles - 1) / start.per) - (int)blockIdx.x + 1;
+                desc_rows = g.rows;
+                desc_row0 = g.row0;
+                desc_slot = slot;
+            }
+            ++seg;
+            return true;
+        });
+        if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(ok ? desc_parts : 0, desc_rows, desc_row0, desc_slot);
+    } else if (warp == TMA_WARP) {
+        // ------------------------------------------------------------ cache rows into the rings
+        if (lane == 0) tma_prefetch_desc(&tmC);
+        const uint64_t pol = p.stream_once ? l2_policy_evict_first() : l2_policy_evict_last();
+        const int br = min(p.block_size, TK), nbox = TK / br;  // rows per box, boxes per slab
+        const int box = lane % nbox, sl = lane / nbox;
+        int np = 0, nr = 0;  // slots filled so far
+        bool ok = true;
+        for_each_segment(p, start, [&](const Segment& g) -> bool {
+            const int32_t* bt = p.block_tables + (size_t)g.c * p.max_blocks_per_seq;
+            auto entry = [&](int tile) {  // block id of this lane's box; past the keys or invalid: zero fill
+                const int t = tile * TK + box * br;
+                if (t >= g.keys) return p.num_blocks;
+                const int b = __ldg(bt + t / p.block_size);
+                if (b < 0 || b >= p.num_blocks) {
+                    flag_error(p.err, PA_DEVERR_BLOCK);
+                    return p.num_blocks;
+                }
+                return b;
+            };
+            int blk = entry(g.tile);
+            for (int u = 0; u < g.n; ++u) {
+                const int tile = g.tile + u;
+                const int nxt = u + 1 < g.n ? entry(tile + 1) : 0;
+                const int row = (tile * TK + box * br) % p.block_size;
+#pragma unroll 1
+                for (int b = 0; b < NB; ++b, ++np) {
+                    const int slot = np % C::NPAIR, use = np / C::NPAIR;
+                    if (lane == 0) {
+                        if (use > 0) ok = mbar_wait(bar(C::PAIR_EMPTY + slot), (uint32_t)((use - 1) & 1), p.err);
+                        if (ok) mbar_arrive_expect_tx(bar(C::PAIR_FULL + slot), PAIR);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) return false;
+                    if (sl < 2)
+                        tma_load_3d(sPair + slot * PAIR + sl * SLAB + box * br * 128, &tmC, (2 * b + sl) * 64, row, blk,
+                                    bar(C::PAIR_FULL + slot), pol);
+                }
+                {
+                    const int slot = nr % C::NROPE, use = nr / C::NROPE;
+                    if (lane == 0) {
+                        if (use > 0) ok = mbar_wait(bar(C::ROPE_EMPTY + slot), (uint32_t)((use - 1) & 1), p.err);
+                        if (ok) mbar_arrive_expect_tx(bar(C::ROPE_FULL + slot), SLAB);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) return false;
+                    if (sl < 1)
+                        tma_load_3d(sRope + slot * SLAB + box * br * 128, &tmC, DL, row, blk, bar(C::ROPE_FULL + slot), pol);
+                    ++nr;
+                }
+                blk = nxt;
+            }
+            return true;
+        });
+        if (!ok && lane == 0) {  // leave no copy in flight behind
+            for (int k = max(0, np - C::NPAIR); k < np; ++k)
+                (void)mbar_wait(bar(C::PAIR_FULL + k % C::NPAIR), (uint32_t)((k / C::NPAIR) & 1), p.err);
+            for (int k = max(0, nr - C::NROPE); k < nr; ++k)
+                (void)mbar_wait(bar(C::ROPE_FULL + k % C::NROPE), (uint32_t)((k / C::NROPE) & 1), p.err);
+        }
+        __syncwarp();
+    } else if (warp == Q_WARP && lane == 0) {
+        // ------------------------------------------------------------ the units' query rows
+        tma_prefetch_desc(&tmQ);
+        int seg = 0;
+        bool pending = false;
+        for_each_segment(p, start, [&](const Segment& g) -> bool {
+            if (seg > 0 && !mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err)) return false;
+            mbar_arrive_expect_tx(bar(C::Q_FULL), C::QSLABS * C::QSLAB);
+#pragma unroll 1
+            for (int s = 0; s < C::QSLABS; ++s) tma_load_2d(sQ + s * C::QSLAB, &tmQ, s * 64, g.row0, bar(C::Q_FULL));
+            ++seg;
+            pending = true;
+            return true;
+        });
+        if (pending) (void)mbar_wait(bar(C::Q_FULL), (uint32_t)((seg - 1) & 1), p.err);
+    } else if (warp == MMA_WARP && lane == 0) {
+        // ------------------------------------------------------------ MMA issue (one thread)
+        constexpr uint32_t ID_QK = idesc(BF16, false, 64, TK);
+        constexpr uint32_t ID_PV = idesc(BF16, true, 128, NR);
+        const uint64_t dq = tc::sdesc_sw128(sQ, 16, 1024), dkp = tc::sdesc_sw128(sPair, 16, 1024),
+                       dkr = tc::sdesc_sw128(sRope, 16, 1024), dp = tc::sdesc_sw128(sP, 16, 1024),
+                       dv = tc::sdesc_sw128(sPair, SLAB, 1024);
+        const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), kp_lo = (uint32_t)dkp, kp_hi = (uint32_t)(dkp >> 32);
+        const uint32_t kr_lo = (uint32_t)dkr, kr_hi = (uint32_t)(dkr >> 32), p_lo = (uint32_t)dp, p_hi = (uint32_t)(dp >> 32);
+        const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+        int i = 0, seg = 0, nk = 0, nr = 0, nv = 0;  // tiles, segments; slots read by QK (pair, rope) and by PV
+        bool ok = true, issued = false;
+        // O^T += C^T P^T for tile t (the t-th of the range); fresh: the first of its segment s
+        auto issue_pv = [&](int t, bool fresh, int s) -> bool {
+            if (!mbar_wait(bar(C::P_FULL), (uint32_t)(t & 1), p.err)) return false;
+            if (fresh && s > 0 && !mbar_wait(bar(C::O_FREE), (uint32_t)((s - 1) & 1), p.err)) return false;
+            tc::fence_after();
+#pragma unroll 1
+            for (int b = 0; b < NB; ++b, ++nv) {
+                const int slot = nv % C::NPAIR;
+#pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    tc::mma_f16_ss_w(tmem + C::O_COL + b * NR, v_lo + (uint32_t)((slot * PAIR + kk * 2048) >> 4), v_hi,
+                                     p_lo + (uint32_t)((kk * 32) >> 4), p_hi, ID_PV, !(fresh && kk == 0));
+                tc::commit(bar(C::PAIR_EMPTY + slot));
+            }
+            tc::commit(bar(C::PV_DONE));
+            return true;
+        };
+        bool prev_fresh = false;
+        int prev_seg = 0;
+        for_each_segment(p, start, [&](const Segment& g) -> bool {
+            for (int u = 0; u < g.n; ++u, ++i) {
+                if (u == 0) {
+                    // a new unit: its rows may still be on their way, so the previous unit's last PV goes first
+                    if (i > 0 && !(ok = issue_pv(i - 1, prev_fresh, prev_seg))) return false;
+                    if (!(ok = mbar_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err))) return false;
+                }
+                const uint32_t dS = tmem + (uint32_t)((i & 1) * 64);
+#pragma unroll 1
+                for (int b = 0; b < NB; ++b, ++nk) {
+                    const int slot = nk % C::NPAIR;
+                    if (!(ok = mbar_wait(bar(C::PAIR_FULL + slot), (uint32_t)((nk / C::NPAIR) & 1), p.err))) return false;
+                    tc::fence_after();
+                    issued = true;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc::mma_f16_ss_w(dS, q_lo + (uint32_t)(((2 * b + (kk >> 2)) * C::QSLAB + (kk & 3) * 32) >> 4), q_hi,
+                                         kp_lo + (uint32_t)((slot * PAIR + (kk >> 2) * SLAB + (kk & 3) * 32) >> 4), kp_hi,
+                                         ID_QK, b > 0 || kk > 0);
+                }
+                const int rs = nr % C::NROPE;
+                if (!(ok = mbar_wait(bar(C::ROPE_FULL + rs), (uint32_t)((nr / C::NROPE) & 1), p.err))) return false;
+                tc::fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_f16_ss_w(dS, q_lo + (uint32_t)(((C::QSLABS - 1) * C::QSLAB + kk * 32) >> 4), q_hi,
+                                     kr_lo + (uint32_t)((rs * SLAB + kk * 32) >> 4), kr_hi, ID_QK, 1u);
+                ++nr;
+                tc::commit(bar(C::S_FULL + (i & 1)));
+                tc::commit(bar(C::ROPE_EMPTY + rs));
+                if (u == g.n - 1) tc::commit(bar(C::Q_EMPTY));
+                if (u > 0 && !(ok = issue_pv(i - 1, prev_fresh, prev_seg))) return false;
+                prev_fresh = u == 0;
+                prev_seg = seg;
+            }
+            ++seg;
+            return true;
+        });
+        if (ok && i > 0) ok = issue_pv(i - 1, prev_fresh, prev_seg);
+        if (issued) {  // every MMA must be complete before TMEM is released
+            tc::commit(bar(C::DRAIN));
+            (void)mbar_wait(bar(C::DRAIN), 0, p.err);
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc::fence_after();
+        tc::dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Joins the partials of the units that the ranges' ends cut.  Block (b, y): the unit that starts in CTA
+// b's range and goes on behind it, query rows y, y + gridDim.y, ...; each of the block's groups of
+// DL / 4 threads sums every KG-th partial, weighted by 2^(m - max m), then the groups' sums are added
+// in order.
+template <bool BF16, int DL, int NR>
+__global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p) {
+    using F = F16x2<BF16>;
+    constexpr int TG = DL / 4, KG = 512 / TG;
+    __shared__ float4 acc[512];
+    __shared__ float wt[lat::MAX_CTAS];
+    __shared__ float red[16], l_s[1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d = __ldcg(p.desc + blockIdx.x);
+    const int parts = d.x, tid = threadIdx.x;
+    if (parts == 0) return;
+    auto slot_of = [&](int k) { return k == 0 ? d.w : 2 * ((int)blockIdx.x + k); };
+    for (int row = blockIdx.y; row < d.y; row += gridDim.y) {
+        float m = -INFINITY, l = 0.f;
+        if (tid < parts) {
+            const float* ml = p.part_ml + ((size_t)slot_of(tid) * NR + row) * 2;
+            m = __ldcg(ml);
+            l = __ldcg(ml + 1);
+        }
+        float mx = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if ((tid & 31) == 0) red[tid >> 5] = mx;
+        __syncthreads();
+        mx = red[0];
+        for (int w = 1; w < 16; ++w) mx = fmaxf(mx, red[w]);
+        const float w = m == -INFINITY ? 0.f : ex2(m - mx);
+        if (tid < parts) wt[tid] = w;
+        float lw = tid < parts && l != 0.f ? l * w : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+        __syncthreads();
+        if ((tid & 31) == 0) red[tid >> 5] = lw;
+        __syncthreads();
+        if (tid == 0) {
+            float t = 0.f;
+            for (int k = 0; k < 16; ++k) t += red[k];
+            l_s[0] = t;
+        }
+        const int gidx = tid / TG, t = tid % TG;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = gidx; k < parts; k += KG) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_of(k) * NR + row) * DL) + t);
+            const float f = wt[k];
+            if (f != 0.f) {
+                a.x = fmaf(v.x, f, a.x);
+                a.y = fmaf(v.y, f, a.y);
+                a.z = fmaf(v.z, f, a.z);
+                a.w = fmaf(v.w, f, a.w);
+            }
+        }
+        acc[tid] = a;
+        __syncthreads();
+        if (tid < TG) {
+            for (int k = 1; k < KG; ++k) {
+                const float4 v = acc[k * TG + tid];
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            const float lt = l_s[0], inv = lt != 0.f ? 1.f / lt : 0.f;
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(d.z + row) * DL + 4 * tid) =
+                make_uint2(F::pack_rn(a.x * inv, a.y * inv), F::pack_rn(a.z * inv, a.w * inv));
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace pa

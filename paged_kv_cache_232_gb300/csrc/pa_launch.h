@@ -114,4 +114,28 @@ cudaError_t launch_prefill_small(int bf16, int head_dim, int group, const Prefil
 cudaError_t launch_prefix(int bf16, int head_dim, int group, const PrefillParams& params, const CUtensorMap& tmK,
                           const CUtensorMap& tmV, cudaStream_t stream);
 
+// Attention over a paged cache of latent vectors (latent_kernel.cuh).
+struct LatentParams {
+    void* out;                  // [total_q, n_heads, DL]
+    const int32_t* block_tables;
+    const int32_t* q_loc;       // [num_chunks + 1] first query row of each chunk; null: one query token a sequence
+    const int32_t* kv_lens;     // [num_chunks]
+    unsigned* err;
+    int num_chunks, n_heads, max_blocks_per_seq, num_blocks, block_size, max_q_len, total_q;
+    int tb;                     // tokens per unit of query rows
+    int hb;                     // units per token (2 above 64 heads)
+    int min_tiles;              // least tiles of a CTA's range
+    int stream_once;            // 1: every cache row is read by one unit (L2 evict-first)
+    float qk_scale_log2;
+    float* part_o;              // [2 * CTAs][NR][DL]
+    float* part_ml;             // [2 * CTAs][NR][2]: reference (base 2) and exp-sum
+    int4* desc;                 // [CTAs]: partials, rows, first row of out, first slot of the unit cut at the range's end
+};
+
+// Query rows per unit the kernel is built for (16, 32 or 64): the least that holds `rows`.
+inline int latent_unit_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+cudaError_t launch_latent(int bf16, int latent_dim, int unit_rows, const LatentParams& params, const CUtensorMap& tmC,
+                          const CUtensorMap& tmQ, int grid, cudaStream_t stream);
+
 }  // namespace pa

@@ -96,11 +96,6 @@ constexpr uint32_t O_COL = 256;         // S_t buffers at columns 128 t + 64 b, 
 
 }  // namespace pf
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
 // Key tiles a unit (a pair of query tiles: tokens [j0, j0 + span) of chunk c) streams.
 __device__ __forceinline__ int unit_cost(const int* qsl, const int* kvl, int c, int pair, int span, int cap,
                                          int max_q_len) {
