@@ -336,26 +336,37 @@ def pa_prefill_chunk(out, q, k_cache, v_cache, block_tables, query_start_loc, se
     _check(st, "pa_prefill_chunk_small_m" if small_m else "pa_prefill_chunk")
 
 
-def _on_current(first, *others) -> None:
+def _on_current(*tensors) -> int:
     """The library launches on the current device: every tensor has to be on it."""
-    dev = _torch().cuda.current_device() if first.is_cuda else None
-    for t in (first, *others):
-        if t is not None and t.is_cuda and t.device.index != dev:
+    if not tensors[0].is_cuda:
+        raise ValueError("every tensor must be a CUDA tensor")
+    dev = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
 
 
 def _rows(t, name: str, dtype, shape):
     """Pointer and token stride (elements) of t [N, heads, dim], whose heads and columns are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     n, h, d = shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
         raise ValueError(f"{name} must be contiguous within a token")
-    return t.data_ptr(), (int(t.stride(0)) if n > 1 else h * d)
+    return t.data_ptr(), (s[0] if n > 1 else h * d)
+
+
+def _flat(t, name: str, dtype, shape):
+    """Pointer of a contiguous tensor of this type and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
 def pa_norm_rope_reshape_and_cache(q, key, value, q_weight, k_weight, k_cache, v_cache, slot_mapping, positions,
@@ -365,29 +376,20 @@ def pa_norm_rope_reshape_and_cache(q, key, value, q_weight, k_weight, k_cache, v
     value into the caches at slot_mapping [N] (int64, -1 skips), q into q_out (default: in place).
     q, key, value and q_out may be slices of wider rows (contiguous within a token)."""
     torch = _torch()
-    dt = _dtype_code(q)
-    nb, bs, hkv, d = _cache_dims(k_cache)
-    n, hq = int(q.shape[0]), int(q.shape[1])
-    if tuple(v_cache.shape) != tuple(k_cache.shape):
-        raise ValueError("k_cache / v_cache shapes differ")
-    if tuple(slot_mapping.shape) != (n,) or tuple(positions.shape) != (n,):
-        raise ValueError("slot_mapping / positions must hold one value per token")
-    if tuple(q_weight.shape) != (d,) or tuple(k_weight.shape) != (d,):
-        raise ValueError("q_weight / k_weight must be [head_dim]")
-    if cos_sin.dim() != 2 or int(cos_sin.shape[1]) != d:
-        raise ValueError("cos_sin must be [max_position, head_dim]")
-    _on_current(q, key, value, q_weight, k_weight, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
-    qp, qs = _rows(q, "q", q.dtype, (n, hq, d))
-    op, os_ = (qp, qs) if q_out is None else _rows(q_out, "q_out", q.dtype, (n, hq, d))
-    kp, ks = _rows(key, "key", q.dtype, (n, hkv, d))
-    vp, vs = _rows(value, "value", q.dtype, (n, hkv, d))
-    st = load().pa_norm_rope_reshape_and_cache(
-        op, os_, qp, qs, kp, ks, vp, vs, _dev(q_weight, "q_weight", q.dtype), _dev(k_weight, "k_weight", q.dtype),
-        float(eps), _dev(k_cache, "k_cache", q.dtype), _dev(v_cache, "v_cache", q.dtype),
-        _dev(slot_mapping, "slot_mapping", torch.int64), _dev(positions, "positions", torch.int64),
-        _dev(cos_sin, "cos_sin", torch.float32), n, hq, hkv, d, bs, nb, int(cos_sin.shape[0]), dt,
-        _stream(stream, q.device))
-    _check(st, "pa_norm_rope_reshape_and_cache")
+    ty, dt = q.dtype, _dtype_code(q)
+    nb, bs, hkv, d = k_cache.shape
+    n, hq, _ = q.shape
+    mp = cos_sin.shape[0]
+    qp, qs = _rows(q, "q", ty, (n, hq, d))
+    op, os_ = (qp, qs) if q_out is None else _rows(q_out, "q_out", ty, (n, hq, d))
+    kp, ks = _rows(key, "key", ty, (n, hkv, d))
+    vp, vs = _rows(value, "value", ty, (n, hkv, d))
+    args = (op, os_, qp, qs, kp, ks, vp, vs, _flat(q_weight, "q_weight", ty, (d,)), _flat(k_weight, "k_weight", ty, (d,)),
+            eps, _flat(k_cache, "k_cache", ty, (nb, bs, hkv, d)), _flat(v_cache, "v_cache", ty, (nb, bs, hkv, d)),
+            _flat(slot_mapping, "slot_mapping", torch.int64, (n,)), _flat(positions, "positions", torch.int64, (n,)),
+            _flat(cos_sin, "cos_sin", torch.float32, (mp, d)), n, hq, hkv, d, bs, nb, mp, dt)
+    dev = _on_current(q, key, value, q_weight, k_weight, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
+    _check(load().pa_norm_rope_reshape_and_cache(*args, _stream(stream, dev)), "pa_norm_rope_reshape_and_cache")
 
 
 LATENT_ROPE_DIM = 64
@@ -408,36 +410,30 @@ def pa_latent_rope_and_cache(kv, latent_cache, slot_mapping, positions, cos_sin,
     [N, H, 64] (any strides of whole rows), if given, is rotated into the last 64 columns of
     q [N, H, DL + 64]; it may be that slice of q."""
     torch = _torch()
-    dt = _dtype_code(kv)
+    ty, dt = kv.dtype, _dtype_code(kv)
     nb, bs, dl = _latent_dims(latent_cache)
-    n, row = int(kv.shape[0]), dl + LATENT_ROPE_DIM
-    kvp, kvs = _rows(kv.unsqueeze(1), "kv", kv.dtype, (n, 1, row))
-    if tuple(slot_mapping.shape) != (n,) or tuple(positions.shape) != (n,):
-        raise ValueError("slot_mapping / positions must hold one value per token")
-    if weight is not None and tuple(weight.shape) != (dl,):
-        raise ValueError("weight must be [latent_dim]")
-    if cos_sin.dim() != 2 or int(cos_sin.shape[1]) != LATENT_ROPE_DIM:
-        raise ValueError("cos_sin must be [max_position, 64]")
-    _on_current(kv, latent_cache, slot_mapping, positions, cos_sin, weight, q_pe, q)
-    qp = pep = None
-    h = pts = phs = 0
+    n, row, mp = kv.shape[0], dl + LATENT_ROPE_DIM, cos_sin.shape[0]
+    if kv.shape != (n, row) or kv.dim() != 2 or kv.stride(1) != 1:
+        raise ValueError("kv must be [N, latent_dim + 64] with contiguous rows")
     if (q_pe is None) != (q is None):
         raise ValueError("q_pe and q come together")
+    qp = pep = None
+    h = pts = phs = 0
     if q_pe is not None:
-        h = int(q_pe.shape[1])
-        if tuple(q_pe.shape) != (n, h, LATENT_ROPE_DIM) or tuple(q.shape) != (n, h, row):
-            raise ValueError("q_pe must be [N, H, 64] and q [N, H, latent_dim + 64]")
-        if not q_pe.is_cuda or q_pe.dtype != kv.dtype or q_pe.stride(2) != 1:
-            raise ValueError("q_pe must be a CUDA tensor of kv's type with contiguous columns")
-        qp, pep = _dev(q, "q", kv.dtype), q_pe.data_ptr()
-        phs = int(q_pe.stride(1)) if h > 1 else LATENT_ROPE_DIM
-        pts = int(q_pe.stride(0)) if n > 1 else (h - 1) * phs + LATENT_ROPE_DIM
-    st = load().pa_latent_rope_and_cache(
-        qp, pep, pts, phs, kvp, kvs, None if weight is None else _dev(weight, "weight", kv.dtype), float(eps),
-        _dev(latent_cache, "latent_cache", kv.dtype), _dev(slot_mapping, "slot_mapping", torch.int64),
-        _dev(positions, "positions", torch.int64), _dev(cos_sin, "cos_sin", torch.float32), n, h, dl, LATENT_ROPE_DIM,
-        bs, nb, int(cos_sin.shape[0]), int(bool(interleaved)), dt, _stream(stream, kv.device))
-    _check(st, "pa_latent_rope_and_cache")
+        h = q_pe.shape[1]
+        if q_pe.shape != (n, h, LATENT_ROPE_DIM) or q_pe.dtype != ty or q_pe.stride(2) != 1:
+            raise ValueError("q_pe must be [N, H, 64] of kv's type with contiguous columns")
+        qp, pep = _flat(q, "q", ty, (n, h, row)), q_pe.data_ptr()
+        phs = q_pe.stride(1) if h > 1 else LATENT_ROPE_DIM
+        pts = q_pe.stride(0) if n > 1 else (h - 1) * phs + LATENT_ROPE_DIM
+    args = (qp, pep, pts, phs, kv.data_ptr(), kv.stride(0) if n > 1 else row,
+            None if weight is None else _flat(weight, "weight", ty, (dl,)), eps,
+            _flat(latent_cache, "latent_cache", ty, (nb, bs, row)),
+            _flat(slot_mapping, "slot_mapping", torch.int64, (n,)), _flat(positions, "positions", torch.int64, (n,)),
+            _flat(cos_sin, "cos_sin", torch.float32, (mp, LATENT_ROPE_DIM)), n, h, dl, LATENT_ROPE_DIM, bs, nb, mp,
+            1 if interleaved else 0, dt)
+    dev = _on_current(kv, latent_cache, slot_mapping, positions, cos_sin, weight, q_pe, q)
+    _check(load().pa_latent_rope_and_cache(*args, _stream(stream, dev)), "pa_latent_rope_and_cache")
 
 
 def pa_latent_workspace_size(n_heads: int, latent_dim: int, max_q_len: int = 1) -> int:
@@ -446,30 +442,30 @@ def pa_latent_workspace_size(n_heads: int, latent_dim: int, max_q_len: int = 1) 
 
 def _latent_common(out, q, latent_cache, block_tables, lens, workspace):
     torch = _torch()
-    dt = _dtype_code(q)
+    ty, dt = q.dtype, _dtype_code(q)
     nb, bs, dl = _latent_dims(latent_cache)
-    if q.dim() != 3 or int(q.shape[2]) != dl + LATENT_ROPE_DIM or tuple(out.shape) != (*q.shape[:2], dl):
-        raise ValueError("q must be [rows, H, latent_dim + 64] and out [rows, H, latent_dim]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != lens.shape[0]:
-        raise ValueError("block_tables must hold one row per length")
-    _on_current(q, out, latent_cache, block_tables, lens, workspace)
-    ptrs = (_dev(out, "out", q.dtype), _dev(q, "q", q.dtype), _dev(latent_cache, "latent_cache", q.dtype),
-            _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]))
-    wp, wb = (_dev(workspace, "workspace"), workspace.numel() * workspace.element_size()) if workspace is not None \
-        else (None, 0)
-    return dt, nb, bs, dl, int(q.shape[0]), int(q.shape[1]), ptrs, wp, wb
+    rows, h, k = q.shape
+    if k != dl + LATENT_ROPE_DIM:
+        raise ValueError("q must be [rows, H, latent_dim + 64]")
+    n, mb = block_tables.shape
+    args = (_flat(out, "out", ty, (rows, h, dl)), _flat(q, "q", ty, (rows, h, k)),
+            _flat(latent_cache, "latent_cache", ty, (nb, bs, k)),
+            _flat(block_tables, "block_tables", torch.int32, (n, mb)), mb)
+    lp = _flat(lens, "lengths", torch.int32, (n,))
+    wp = wb = 0
+    if workspace is not None:
+        wp, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    dev = _on_current(q, out, latent_cache, block_tables, lens, workspace)
+    return args, lp, rows, n, (h, dl, LATENT_ROPE_DIM, bs, nb), dt, wp, wb, dev
 
 
 def pa_latent_decode(out, q, latent_cache, block_tables, context_lens, scale: float, workspace, stream=None) -> None:
     """Decode over a paged latent cache: out [S, H, DL], q [S, H, DL + 64]; workspace of at least
     pa_latent_workspace_size(H, DL) bytes."""
-    torch = _torch()
-    dt, nb, bs, dl, S, h, ptrs, wp, wb = _latent_common(out, q, latent_cache, block_tables, context_lens, workspace)
-    if int(context_lens.shape[0]) != S:
-        raise ValueError("context_lens must hold one length per row of q")
-    st = load().pa_latent_decode(*ptrs, _dev(context_lens, "context_lens", torch.int32), S, h, dl, LATENT_ROPE_DIM, bs,
-                                 nb, float(scale), dt, wp, wb, _stream(stream, q.device))
-    _check(st, "pa_latent_decode")
+    args, lp, rows, n, dims, dt, wp, wb, dev = _latent_common(out, q, latent_cache, block_tables, context_lens, workspace)
+    if n != rows:
+        raise ValueError("block_tables and context_lens must hold one row per row of q")
+    _check(load().pa_latent_decode(*args, lp, rows, *dims, scale, dt, wp, wb, _stream(stream, dev)), "pa_latent_decode")
 
 
 def pa_latent_prefill_chunk(out, q, latent_cache, block_tables, query_start_loc, seq_lens, max_q_len: int, scale: float,
@@ -477,15 +473,11 @@ def pa_latent_prefill_chunk(out, q, latent_cache, block_tables, query_start_loc,
     """Ragged chunks (bottom-right causal over their cached context) on a paged latent cache: out
     [T, H, DL], q [T, H, DL + 64], chunk c the rows query_start_loc[c] .. query_start_loc[c + 1];
     workspace of at least pa_latent_workspace_size(H, DL, max_q_len) bytes."""
-    torch = _torch()
-    dt, nb, bs, dl, T, h, ptrs, wp, wb = _latent_common(out, q, latent_cache, block_tables, seq_lens, workspace)
-    C = int(seq_lens.shape[0])
-    if tuple(query_start_loc.shape) != (C + 1,):
-        raise ValueError("query_start_loc must hold num_chunks + 1 rows")
-    st = load().pa_latent_prefill_chunk(*ptrs, _dev(query_start_loc, "query_start_loc", torch.int32),
-                                        _dev(seq_lens, "seq_lens", torch.int32), C, int(max_q_len), T, h, dl,
-                                        LATENT_ROPE_DIM, bs, nb, float(scale), dt, wp, wb, _stream(stream, q.device))
-    _check(st, "pa_latent_prefill_chunk")
+    args, lp, rows, n, dims, dt, wp, wb, dev = _latent_common(out, q, latent_cache, block_tables, seq_lens, workspace)
+    loc = _flat(query_start_loc, "query_start_loc", _torch().int32, (n + 1,))
+    _on_current(q, query_start_loc)
+    _check(load().pa_latent_prefill_chunk(*args, loc, lp, n, max_q_len, rows, *dims, scale, dt, wp, wb,
+                                          _stream(stream, dev)), "pa_latent_prefill_chunk")
 
 
 def pa_device_errors(clear: bool = True) -> int:

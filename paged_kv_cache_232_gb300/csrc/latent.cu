@@ -11,7 +11,7 @@ static cudaError_t launch_latent_t(const LatentParams& p, const CUtensorMap& tmC
     static std::atomic<unsigned long long> s_done{0};
     cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, s_done);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, (unsigned)grid, lat::THREADS, C::SMEM_BYTES, st, p, tmC, tmQ);
+    e = launch_dependent(kern, (unsigned)grid, C::THREADS, C::SMEM_BYTES, st, p, tmC, tmQ);
     if (e != cudaSuccess) return e;
     // the merge: 16 blocks a cut unit, each every 16th query row
     cudaLaunchConfig_t cfg = {};

@@ -46,8 +46,9 @@ constexpr int TK = 64;                  // tokens per tile
 constexpr int ROPE = 64;                // rotary columns of a cache row
 constexpr int SLAB = TK * 128;          // bytes of 64 tokens x 64 columns
 constexpr int PAIR = 2 * SLAB;
-constexpr int SOFTMAX_WARPS = 4, TMA_WARP = 4, MMA_WARP = 5, Q_WARP = 6;
-constexpr int THREADS = 7 * 32;
+// warps 0..3: softmax; then the two MMA issuers, the Q loader, and the cache row loaders (one a pair slot of a tile, one
+// for the rotary slot)
+constexpr int SOFTMAX_WARPS = 4, QK_WARP = 4, PV_WARP = 5, Q_WARP = 6, TMA_WARP = 7;
 constexpr int MAX_CTAS = 512;           // of the split: latent_merge_kernel gives every partial a thread
 
 template <int DL, int NR>
@@ -55,6 +56,7 @@ struct Cfg {
     static_assert(DL == 256 || DL == 512, "latent columns");
     static_assert(NR == 16 || NR == 32 || NR == 64, "query rows per unit");
     static constexpr int NB = DL / 128;                 // pair slots per tile = M blocks of O^T
+    static constexpr int THREADS = (TMA_WARP + NB + 1) * 32;
     static constexpr int QSLABS = DL / 64 + 1;
     static constexpr int QSLAB = NR * 128;
     // as many ring slots as fit next to the Q tile and the weights
@@ -68,11 +70,13 @@ struct Cfg {
     // barriers
     static constexpr int PAIR_FULL = 0, PAIR_EMPTY = NPAIR, ROPE_FULL = 2 * NPAIR, ROPE_EMPTY = 2 * NPAIR + NROPE;
     static constexpr int Q_FULL = 2 * (NPAIR + NROPE), Q_EMPTY = Q_FULL + 1, S_FULL = Q_FULL + 2, P_FULL = Q_FULL + 4,
-                         PV_DONE = Q_FULL + 5, O_FREE = Q_FULL + 6, DRAIN = Q_FULL + 7, NUM_BARS = Q_FULL + 8;
-    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;      // start record, TMEM address, scan scratch
+                         PV_DONE = Q_FULL + 5, O_FREE = Q_FULL + 6, DRAIN = Q_FULL + 7, S_EMPTY = Q_FULL + 9,
+                         NUM_BARS = Q_FULL + 11;
+    static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch
     static constexpr int ROW_OFF = MISC_OFF + 192;               // alpha [NR] and 1 / l [NR]
     static constexpr int SMEM_BYTES = ROW_OFF + 2 * NR * 4 + 1024;  // + alignment slack
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert(ROW_OFF % 16 == 0, "1 / l is read 16 bytes at a time");
     // the A operand of QK reads 64 rows of each Q slab, whatever NR is
     static_assert((QSLABS - 1) * QSLAB + 64 * 128 <= BAR_OFF, "QK operand stays inside the tile area");
     static constexpr uint32_t O_COL = 128;                       // two S buffers of 64 columns, then O^T
@@ -114,6 +118,20 @@ __device__ __forceinline__ bool softmax_or(bool v) {
     return r != 0;
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // The warp waits through lane 0 alone; __syncwarp orders the other lanes behind its acquire.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
@@ -206,6 +224,7 @@ struct Start {
 };
 
 // Every thread of the CTA calls it; all return the same record.
+template <int THREADS>
 __device__ __forceinline__ Start find_start(const LatentParams& p, long long* warp_sum, Start* rec) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = THREADS / 32;
@@ -323,7 +342,7 @@ __device__ __forceinline__ void for_each_segment(const LatentParams& p, const St
 }  // namespace lat
 
 template <bool BF16, int DL, int NR>
-__global__ void __launch_bounds__(lat::THREADS, 1)
+__global__ void __launch_bounds__(lat::Cfg<DL, NR>::THREADS, 1)
 latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmQ) {
     using namespace lat;
     using C = Cfg<DL, NR>;
@@ -338,8 +357,8 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
     Start* rec = reinterpret_cast<Start*>(smem + C::MISC_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF + 32);
     long long* warp_sum = reinterpret_cast<long long*>(smem + C::MISC_OFF + 64);
-    volatile float* alpha_s = reinterpret_cast<volatile float*>(smem + C::ROW_OFF);
-    volatile float* inv_s = alpha_s + NR;
+    float* alpha_s = reinterpret_cast<float*>(smem + C::ROW_OFF);
+    float* inv_s = alpha_s + NR;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -359,9 +378,12 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         mbar_init(bar(C::PV_DONE), 1);
         mbar_init(bar(C::O_FREE), SOFTMAX_WARPS);
         mbar_init(bar(C::DRAIN), 1);
+        mbar_init(bar(C::DRAIN + 1), 1);
+        mbar_init(bar(C::S_EMPTY), NR / 16);
+        mbar_init(bar(C::S_EMPTY + 1), NR / 16);
         fence_barrier_init();
     }
-    if (warp == MMA_WARP) {
+    if (warp == QK_WARP) {
         tc::alloc(smem_addr(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
         tc::relinquish();
     }
@@ -370,7 +392,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before();
-    const Start start = find_start(p, warp_sum, rec);  // (synchronises the CTA)
+    const Start start = find_start<C::THREADS>(p, warp_sum, rec);  // (synchronises the CTA)
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -409,6 +431,9 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                     uint32_t s[64];
                     tc::ld64(tSb, s);
                     tc::wait_ld();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::S_EMPTY + (i & 1)));
 #pragma unroll
                     for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(s[e]) * sc;
                     if (kbase + TK - 1 > lim_min || g.rows < NR || lane >= 16) {
@@ -428,14 +453,14 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                         ok = false;
                         return false;
                     }
-                    float alpha = 1.f;
+                    const uint32_t alpha = smem_addr(alpha_s);
+                    float a = 1.f;
                     if (mx > m_ref) {
-                        alpha = m_ref == -INFINITY ? 1.f : ex2(m_ref - mx);
+                        a = m_ref == -INFINITY ? 1.f : ex2(m_ref - mx);
                         m_ref = mx;
-                        l *= alpha;
+                        l *= a;
                     }
-                    if (valid) alpha_s[r] = alpha;
-                    else if (r >= 0 && r < NR) alpha_s[r] = 1.f;
+                    if (r >= 0 && r < NR) alpha_s[r] = a;
                     wait_pv(i);  // O holds every tile before this one
                     softmax_sync();
                     tc::fence_after();
@@ -446,7 +471,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                         tc::wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_s[(16 * q + e) & (NR - 1)]);
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * lds_f32(alpha + (uint32_t)(((16 * q + e) & (NR - 1)) * 4)));
                         tc::st16(tO + 16 * q, o);
                     }
                     tc::wait_st();
@@ -520,17 +545,20 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 }
                 const int blk = (W * q) / NR, h0 = (W * q) & (NR - 1);
                 if (whole) {
-                    uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(g.row0 + h0) * DL + blk * 128 + (col & ~1);
+                    // 2-byte stores, 64 bytes a warp and row: pairing lanes by shuffles to store 4 bytes was
+                    // slower (shuffles share the path to shared memory with the MMA operands)
+                    uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(g.row0 + h0) * DL + blk * 128 + col;
+                    const uint32_t inv = smem_addr(inv_s) + (uint32_t)(h0 * 4);
+                    uint4 iv[W / 4];
+#pragma unroll
+                    for (int e = 0; e < W / 4; ++e) iv[e] = lds128(inv + e * 16);
 #pragma unroll
                     for (int e = 0; e < W; e += 2) {
-                        // lanes 2k and 2k + 1 hold columns 2k, 2k + 1 of rows e and e + 1: after the exchange the
-                        // even lane has both of row e, the odd lane both of row e + 1
-                        const float a = __uint_as_float(o[e]) * inv_s[h0 + e], b = __uint_as_float(o[e + 1]) * inv_s[h0 + e + 1];
-                        const float y = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
-                        const int row = e + (lane & 1);
-                        if (h0 + row < g.rows)
-                            *reinterpret_cast<uint32_t*>(dst + (size_t)row * DL) =
-                                (lane & 1) ? F::pack_rn(y, b) : F::pack_rn(a, y);
+                        const float a = __uint_as_float(e & 2 ? iv[e / 4].z : iv[e / 4].x);
+                        const float b = __uint_as_float(e & 2 ? iv[e / 4].w : iv[e / 4].y);
+                        const uint32_t v = F::pack_rn(__uint_as_float(o[e]) * a, __uint_as_float(o[e + 1]) * b);
+                        if (h0 + e < g.rows) dst[(size_t)e * DL] = (uint16_t)v;
+                        if (h0 + e + 1 < g.rows) dst[(size_t)(e + 1) * DL] = (uint16_t)(v >> 16);
                     }
                 } else {
                     float* dst = p.part_o + ((size_t)slot * NR + h0) * DL + blk * 128 + col;
@@ -550,67 +578,63 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
             return true;
         });
         if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(ok ? desc_parts : 0, desc_rows, desc_row0, desc_slot);
-    } else if (warp == TMA_WARP) {
-        // ------------------------------------------------------------ cache rows into the rings
+    } else if (warp >= TMA_WARP) {
+        // ------------------------------------------------------------ cache rows into the rings.  One warp a
+        // pair slot of the tile and one for the rotary slot: a box of 16 rows moves 2 KB, so at small cache
+        // blocks the issue of boxes, not the copies, would set the pace of a single warp (GB300: 36 boxes a
+        // tile took one warp ~4000 cycles).  An elected lane issues from warp-uniform operands, as for the MMAs
         if (lane == 0) tma_prefetch_desc(&tmC);
         const uint64_t pol = p.stream_once ? l2_policy_evict_first() : l2_policy_evict_last();
-        const int br = min(p.block_size, TK), nbox = TK / br;  // rows per box, boxes per slab
-        const int box = lane % nbox, sl = lane / nbox;
-        int np = 0, nr = 0;  // slots filled so far
+        const int b = warp - TMA_WARP;                          // pair of the tile; NB: the rotary slot
+        const bool rope = b == NB;
+        const int br = min(p.block_size, TK), nbox = TK / br;   // rows per box, boxes per slab
+        const int slabs = rope ? 1 : 2, slots = rope ? C::NROPE : C::NPAIR;
+        const int full0 = rope ? C::ROPE_FULL : C::PAIR_FULL, empty0 = rope ? C::ROPE_EMPTY : C::PAIR_EMPTY;
+        const uint32_t bytes = (uint32_t)(slabs * SLAB), ring = rope ? sRope : sPair;
+        int n = rope ? 0 : b;    // slot number of this warp's next load, over the whole range
+        const int step = rope ? 1 : NB;
+        int done = 0;
         bool ok = true;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             const int32_t* bt = p.block_tables + (size_t)g.c * p.max_blocks_per_seq;
-            auto entry = [&](int tile) {  // block id of this lane's box; past the keys or invalid: zero fill
-                const int t = tile * TK + box * br;
-                if (t >= g.keys) return p.num_blocks;
-                const int b = __ldg(bt + t / p.block_size);
-                if (b < 0 || b >= p.num_blocks) {
+            auto entry = [&](int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
+                const int t = tile * TK + lane * br;
+                if (lane >= nbox || t >= g.keys) return p.num_blocks;
+                const int e = __ldg(bt + t / p.block_size);
+                if (e < 0 || e >= p.num_blocks) {
                     flag_error(p.err, PA_DEVERR_BLOCK);
                     return p.num_blocks;
                 }
-                return b;
+                return e;
             };
             int blk = entry(g.tile);
-            for (int u = 0; u < g.n; ++u) {
+            for (int u = 0; u < g.n; ++u, n += step, ++done) {
                 const int tile = g.tile + u;
                 const int nxt = u + 1 < g.n ? entry(tile + 1) : 0;
-                const int row = (tile * TK + box * br) % p.block_size;
-#pragma unroll 1
-                for (int b = 0; b < NB; ++b, ++np) {
-                    const int slot = np % C::NPAIR, use = np / C::NPAIR;
-                    if (lane == 0) {
-                        if (use > 0) ok = mbar_wait(bar(C::PAIR_EMPTY + slot), (uint32_t)((use - 1) & 1), p.err);
-                        if (ok) mbar_arrive_expect_tx(bar(C::PAIR_FULL + slot), PAIR);
+                const int slot = (int)uniform((uint32_t)(n % slots)), use = n / slots;
+                if (use > 0 && !(ok = lat::warp_wait(bar(empty0 + slot), (uint32_t)((use - 1) & 1), p.err))) return false;
+                const uint32_t full = bar(full0 + slot), dst = ring + (uint32_t)slot * bytes;
+                if (elect_one()) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                for (int x = 0; x < nbox; ++x) {
+                    const int row = (int)uniform((uint32_t)((tile * TK + x * br) % p.block_size));
+                    const int e = __shfl_sync(0xffffffffu, blk, x);
+                    if (elect_one()) {
+                        tma_load_3d(dst + x * br * 128, &tmC, b * 128, row, e, full, pol);
+                        if (!rope) tma_load_3d(dst + SLAB + x * br * 128, &tmC, b * 128 + 64, row, e, full, pol);
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) return false;
-                    if (sl < 2)
-                        tma_load_3d(sPair + slot * PAIR + sl * SLAB + box * br * 128, &tmC, (2 * b + sl) * 64, row, blk,
-                                    bar(C::PAIR_FULL + slot), pol);
-                }
-                {
-                    const int slot = nr % C::NROPE, use = nr / C::NROPE;
-                    if (lane == 0) {
-                        if (use > 0) ok = mbar_wait(bar(C::ROPE_EMPTY + slot), (uint32_t)((use - 1) & 1), p.err);
-                        if (ok) mbar_arrive_expect_tx(bar(C::ROPE_FULL + slot), SLAB);
-                    }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) return false;
-                    if (sl < 1)
-                        tma_load_3d(sRope + slot * SLAB + box * br * 128, &tmC, DL, row, blk, bar(C::ROPE_FULL + slot), pol);
-                    ++nr;
+                    __syncwarp();
                 }
                 blk = nxt;
             }
             return true;
         });
-        if (!ok && lane == 0) {  // leave no copy in flight behind
-            for (int k = max(0, np - C::NPAIR); k < np; ++k)
-                (void)mbar_wait(bar(C::PAIR_FULL + k % C::NPAIR), (uint32_t)((k / C::NPAIR) & 1), p.err);
-            for (int k = max(0, nr - C::NROPE); k < nr; ++k)
-                (void)mbar_wait(bar(C::ROPE_FULL + k % C::NROPE), (uint32_t)((k / C::NROPE) & 1), p.err);
+        if (!ok) {  // leave no copy in flight behind
+            for (int k = max(0, done - slots); k < done; ++k) {
+                const int m = (rope ? 0 : b) + k * step;
+                (void)lat::warp_wait(bar(full0 + m % slots), (uint32_t)((m / slots) & 1), p.err);
+            }
         }
-        __syncwarp();
     } else if (warp == Q_WARP && lane == 0) {
         // ------------------------------------------------------------ the units' query rows
         tma_prefetch_desc(&tmQ);
@@ -626,84 +650,104 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
             return true;
         });
         if (pending) (void)mbar_wait(bar(C::Q_FULL), (uint32_t)((seg - 1) & 1), p.err);
-    } else if (warp == MMA_WARP && lane == 0) {
-        // ------------------------------------------------------------ MMA issue (one thread)
+    } else if (warp == QK_WARP) {
+        // ------------------------------------------------------------ QK issue.  QK and PV have an issuer
+        // each: a tile's PV frees the ring for the tile after the next, so it must not queue behind the
+        // next tile's QK, which waits for that tile's loads.  The whole warp walks the loop and one elected
+        // lane issues, from descriptors that a shuffle makes warp-uniform: the instruction takes them from
+        // uniform registers, and moving divergent ones there costs ~90 cycles an MMA
         constexpr uint32_t ID_QK = idesc(BF16, false, 64, TK);
-        constexpr uint32_t ID_PV = idesc(BF16, true, 128, NR);
         const uint64_t dq = tc::sdesc_sw128(sQ, 16, 1024), dkp = tc::sdesc_sw128(sPair, 16, 1024),
-                       dkr = tc::sdesc_sw128(sRope, 16, 1024), dp = tc::sdesc_sw128(sP, 16, 1024),
-                       dv = tc::sdesc_sw128(sPair, SLAB, 1024);
-        const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), kp_lo = (uint32_t)dkp, kp_hi = (uint32_t)(dkp >> 32);
-        const uint32_t kr_lo = (uint32_t)dkr, kr_hi = (uint32_t)(dkr >> 32), p_lo = (uint32_t)dp, p_hi = (uint32_t)(dp >> 32);
-        const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
-        int i = 0, seg = 0, nk = 0, nr = 0, nv = 0;  // tiles, segments; slots read by QK (pair, rope) and by PV
-        bool ok = true, issued = false;
-        // O^T += C^T P^T for tile t (the t-th of the range); fresh: the first of its segment s
-        auto issue_pv = [&](int t, bool fresh, int s) -> bool {
-            if (!mbar_wait(bar(C::P_FULL), (uint32_t)(t & 1), p.err)) return false;
-            if (fresh && s > 0 && !mbar_wait(bar(C::O_FREE), (uint32_t)((s - 1) & 1), p.err)) return false;
-            tc::fence_after();
-#pragma unroll 1
-            for (int b = 0; b < NB; ++b, ++nv) {
-                const int slot = nv % C::NPAIR;
-#pragma unroll
-                for (int kk = 0; kk < TK / 16; ++kk)
-                    tc::mma_f16_ss_w(tmem + C::O_COL + b * NR, v_lo + (uint32_t)((slot * PAIR + kk * 2048) >> 4), v_hi,
-                                     p_lo + (uint32_t)((kk * 32) >> 4), p_hi, ID_PV, !(fresh && kk == 0));
-                tc::commit(bar(C::PAIR_EMPTY + slot));
-            }
-            tc::commit(bar(C::PV_DONE));
-            return true;
-        };
-        bool prev_fresh = false;
-        int prev_seg = 0;
+                       dkr = tc::sdesc_sw128(sRope, 16, 1024);
+        int i = 0, seg = 0, nk = 0, nr = 0;  // tiles, segments, pair and rotary slots read
+        bool issued = false, ok = true;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
+            if (!(ok = mbar_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err))) return false;
             for (int u = 0; u < g.n; ++u, ++i) {
-                if (u == 0) {
-                    // a new unit: its rows may still be on their way, so the previous unit's last PV goes first
-                    if (i > 0 && !(ok = issue_pv(i - 1, prev_fresh, prev_seg))) return false;
-                    if (!(ok = mbar_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err))) return false;
-                }
-                const uint32_t dS = tmem + (uint32_t)((i & 1) * 64);
-#pragma unroll 1
+                if (i >= 2 && !(ok = mbar_wait(bar(C::S_EMPTY + (i & 1)), (uint32_t)(((i >> 1) - 1) & 1), p.err)))
+                    return false;
+                const uint32_t dS = uniform(tmem + (uint32_t)((i & 1) * 64));
+#pragma unroll
                 for (int b = 0; b < NB; ++b, ++nk) {
                     const int slot = nk % C::NPAIR;
                     if (!(ok = mbar_wait(bar(C::PAIR_FULL + slot), (uint32_t)((nk / C::NPAIR) & 1), p.err))) return false;
                     tc::fence_after();
                     issued = true;
+                    const uint64_t dk = dkp + uniform((uint32_t)((slot * PAIR) >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_f16_ss_w(dS, q_lo + (uint32_t)(((2 * b + (kk >> 2)) * C::QSLAB + (kk & 3) * 32) >> 4), q_hi,
-                                         kp_lo + (uint32_t)((slot * PAIR + (kk >> 2) * SLAB + (kk & 3) * 32) >> 4), kp_hi,
-                                         ID_QK, b > 0 || kk > 0);
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_f16_ss(dS, dq + (uint32_t)(((2 * b + (kk >> 2)) * C::QSLAB + (kk & 3) * 32) >> 4),
+                                           dk + (uint32_t)(((kk >> 2) * SLAB + (kk & 3) * 32) >> 4), ID_QK, b > 0 || kk > 0);
+                    }
+                    __syncwarp();
                 }
                 const int rs = nr % C::NROPE;
                 if (!(ok = mbar_wait(bar(C::ROPE_FULL + rs), (uint32_t)((nr / C::NROPE) & 1), p.err))) return false;
                 tc::fence_after();
+                const uint64_t dk = dkr + uniform((uint32_t)((rs * SLAB) >> 4));
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_f16_ss_w(dS, q_lo + (uint32_t)(((C::QSLABS - 1) * C::QSLAB + kk * 32) >> 4), q_hi,
-                                     kr_lo + (uint32_t)((rs * SLAB + kk * 32) >> 4), kr_hi, ID_QK, 1u);
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_f16_ss(dS, dq + (uint32_t)(((C::QSLABS - 1) * C::QSLAB + kk * 32) >> 4),
+                                       dk + (uint32_t)((kk * 32) >> 4), ID_QK, 1u);
+                    tc::commit(bar(C::S_FULL + (i & 1)));
+                    tc::commit(bar(C::ROPE_EMPTY + rs));
+                    if (u == g.n - 1) tc::commit(bar(C::Q_EMPTY));
+                }
+                __syncwarp();
                 ++nr;
-                tc::commit(bar(C::S_FULL + (i & 1)));
-                tc::commit(bar(C::ROPE_EMPTY + rs));
-                if (u == g.n - 1) tc::commit(bar(C::Q_EMPTY));
-                if (u > 0 && !(ok = issue_pv(i - 1, prev_fresh, prev_seg))) return false;
-                prev_fresh = u == 0;
-                prev_seg = seg;
             }
             ++seg;
             return true;
         });
-        if (ok && i > 0) ok = issue_pv(i - 1, prev_fresh, prev_seg);
         if (issued) {  // every MMA must be complete before TMEM is released
-            tc::commit(bar(C::DRAIN));
+            if (elect_one()) tc::commit(bar(C::DRAIN));
+            __syncwarp();
             (void)mbar_wait(bar(C::DRAIN), 0, p.err);
+        }
+    } else if (warp == PV_WARP) {
+        // ------------------------------------------------------------ PV issue: O^T += C^T P^T
+        constexpr uint32_t ID_PV = idesc(BF16, true, 128, NR);
+        const uint64_t dp = tc::sdesc_sw128(sP, 16, 1024), dv0 = tc::sdesc_sw128(sPair, SLAB, 1024);
+        const uint32_t dO = uniform(tmem + C::O_COL);
+        int i = 0, seg = 0, nv = 0;
+        bool issued = false;
+        for_each_segment(p, start, [&](const Segment& g) -> bool {
+            // O^T of the segment before must have been read before the first product overwrites it
+            if (seg > 0 && !mbar_wait(bar(C::O_FREE), (uint32_t)((seg - 1) & 1), p.err)) return false;
+            for (int u = 0; u < g.n; ++u, ++i) {
+                if (!mbar_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err)) return false;
+                tc::fence_after();
+                issued = true;
+                const uint32_t acc = uniform(u > 0);
+#pragma unroll
+                for (int b = 0; b < NB; ++b, ++nv) {
+                    const int slot = nv % C::NPAIR;
+                    const uint64_t dv = dv0 + uniform((uint32_t)((slot * PAIR) >> 4));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < TK / 16; ++kk)
+                            tc::mma_f16_ss(dO + b * NR, dv + (uint32_t)((kk * 2048) >> 4), dp + (uint32_t)((kk * 32) >> 4), ID_PV,
+                                           kk > 0 ? 1u : acc);
+                        tc::commit(bar(C::PAIR_EMPTY + slot));
+                        if (b == NB - 1) tc::commit(bar(C::PV_DONE));
+                    }
+                    __syncwarp();
+                }
+            }
+            ++seg;
+            return true;
+        });
+        if (issued) {
+            if (elect_one()) tc::commit(bar(C::DRAIN + 1));
+            __syncwarp();
+            (void)mbar_wait(bar(C::DRAIN + 1), 0, p.err);
         }
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == MMA_WARP) {
+    if (warp == QK_WARP) {
         tc::fence_after();
         tc::dealloc(tmem, C::TMEM_COLS);
     }
