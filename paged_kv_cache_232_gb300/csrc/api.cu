@@ -932,8 +932,7 @@ int pa_latent_rope_and_cache(void* q, const void* q_pe, int64_t q_pe_token_strid
 
 // query rows per unit for n_heads and chunks of up to max_q_len tokens
 static int latent_rows(int n_heads, int max_q_len) {
-    if (n_heads > 64) return 64;
-    return pa::latent_unit_rows(n_heads * std::min(std::max(max_q_len, 1), 64 / n_heads));
+    return pa::latent_unit_rows((int)std::min<int64_t>((int64_t)n_heads * std::max(max_q_len, 1), 128));
 }
 
 struct LatentWs {
@@ -941,7 +940,7 @@ struct LatentWs {
 };
 
 static LatentWs latent_ws(int unit_rows, int latent_dim) {
-    const size_t slots = 2 * (size_t)PA_LATENT_MAX_CTAS;
+    const size_t slots = 2 * (size_t)PA_LATENT_MAX_CTAS / (unit_rows == 128 ? 2 : 1);  // two a range
     LatentWs w;
     w.desc_off = 0;
     w.ml_off = align256(PA_LATENT_MAX_CTAS * sizeof(int4));
@@ -1006,10 +1005,11 @@ static int latent_impl(void* out, const void* q, const void* latent_cache, const
     p.block_size = block_size;
     p.max_q_len = max_q_len;
     p.total_q = (int)total_q;
-    p.hb = n_heads > 64 ? 2 : 1;
-    p.tb = p.hb == 2 ? 1 : rows / n_heads;
-    p.min_tiles = 2;
-    p.stream_once = (!chunks && p.hb == 1) ? 1 : 0;
+    p.tb = rows / n_heads;
+    p.tile_log2 = rows == 128 ? 7 : 6;
+    p.unit_cost = 1;
+    p.min_tiles = 3;
+    p.stream_once = n_heads * (int64_t)max_q_len <= 128 ? 1 : 0;  // one unit a sequence
     p.qk_scale_log2 = scale * 1.4426950408889634f;
     p.desc = reinterpret_cast<int4*>(base + w.desc_off);
     p.part_ml = reinterpret_cast<float*>(base + w.ml_off);
@@ -1018,9 +1018,9 @@ static int latent_impl(void* out, const void* q, const void* latent_cache, const
     const int row = latent_dim + rope_dim;
     if ((st = encode_latent_map(&tc, latent_cache, dtype, num_blocks, block_size, row, std::min(block_size, 64))) != PA_OK)
         return st;
-    if ((st = encode_latent_map(&tq, q, dtype, 0, total_q * n_heads, row, rows)) != PA_OK) return st;
-    const int grid = std::min(dev->sm_count, PA_LATENT_MAX_CTAS);
-    cudaError_t e = pa::launch_latent(dtype == PA_BF16, latent_dim, rows, p, tc, tq, grid,
+    if ((st = encode_latent_map(&tq, q, dtype, 0, total_q * n_heads, row, std::min(rows, 64))) != PA_OK) return st;
+    const int ctas = std::min(dev->sm_count, PA_LATENT_MAX_CTAS) & ~1;
+    cudaError_t e = pa::launch_latent(dtype == PA_BF16, latent_dim, rows, p, tc, tq, ctas,
                                       static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -7,7 +7,7 @@
 // so the H heads of a token are H rows of one dense contraction over the same keys: each cache
 // row is read once for all of them.  Decode (one query token a sequence) and ragged chunks
 // (bottom-right causal) are one kernel: a unit is up to NR query rows (tokens x heads, 64 heads
-// at most) of one sequence over its keys.
+// at most) of one sequence over its keys (more rows: latent_pair_kernel.cuh).
 //
 // GB300 design:
 //  * Keys come in tiles of 64 tokens, as DL / 128 "pair" slots (two 64-column slabs of 64 rows,
@@ -133,11 +133,14 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// The warp waits through lane 0 alone; __syncwarp orders the other lanes behind its acquire.
+// The warp waits, all lanes polling (one request); the polling loop stays out of line, so that the waits'
+// usual path is a few instructions (the roles' code competes for the instruction cache).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned* err) {
+    return mbar_wait(bar, parity, err);
+}
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = wait_slow(bar, parity, err);
     __syncwarp();
     return ok;
 }
@@ -176,7 +179,9 @@ __device__ __forceinline__ Chunk load_chunk(const LatentParams& p, int c) {
 __device__ __forceinline__ int keys_of(const LatentParams& p, const Chunk& k, int j) {
     return k.kv_len - k.q_len + min((j + 1) * p.tb, k.q_len);
 }
-__device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + TK - 1) / TK); }
+__device__ __forceinline__ int tiles_of(const LatentParams& p, int keys) {
+    return max(1, (keys + (1 << p.tile_log2) - 1) >> p.tile_log2);
+}
 
 // sum over i < n of floor((a i + b) / m), by the Euclidean reduction of the lattice-point count
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
@@ -200,32 +205,35 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
     }
 }
 
-// tiles of token blocks 0 .. n - 1 of a chunk (n at most its number of blocks)
+// The ranges are cut in units of cost: a unit (a token block of a chunk) counts unit_cost for its start and
+// its output, then one a tile.
+// cost of token blocks 0 .. n - 1 of a chunk (n at most its number of blocks)
 __device__ __forceinline__ long long tiles_before(const LatentParams& p, const Chunk& k, int n) {
     if (n == 0) return 0;
     const int last = (k.q_len + p.tb - 1) / p.tb - 1;  // the last block may be short
     const int full = min(n, last);
     long long s = 0;
-    if (full > 0)  // block i: ceil((ctx + (i + 1) tb) / TK)
-        s = floor_sum((uint32_t)full, TK, (uint32_t)p.tb, (uint32_t)(k.kv_len - k.q_len + p.tb + TK - 1));
-    if (n > last) s += tiles_of(k.kv_len);
-    return s;
+    if (full > 0)  // block i: ceil((ctx + (i + 1) tb) / tile)
+        s = floor_sum((uint32_t)full, 1u << p.tile_log2, (uint32_t)p.tb,
+                      (uint32_t)(k.kv_len - k.q_len + p.tb + (1 << p.tile_log2) - 1));
+    if (n > last) s += tiles_of(p, k.kv_len);
+    return s + (long long)n * p.unit_cost;
 }
 
 __device__ __forceinline__ long long tiles_in(const LatentParams& p, const Chunk& k) {
     if (k.q_len == 0) return 0;
-    return p.hb * (p.q_loc == nullptr ? (long long)tiles_of(k.kv_len)
-                                      : tiles_before(p, k, (k.q_len + p.tb - 1) / p.tb));
+    return p.q_loc == nullptr ? (long long)tiles_of(p, k.kv_len) + p.unit_cost
+                              : tiles_before(p, k, (k.q_len + p.tb - 1) / p.tb);
 }
 
-// This CTA's range of tiles: where it starts (chunk, token block, half, tile) and how many.
+// A range: where it starts (chunk, token block, cost into that block) and its cost.
 struct Start {
-    int c, j, half, tile, count, per;
+    int c, j, at, count, per;
 };
 
-// Every thread of the CTA calls it; all return the same record.
+// Range `range` of `ranges`.  Every thread of the CTA calls it; all return the same record.
 template <int THREADS>
-__device__ __forceinline__ Start find_start(const LatentParams& p, long long* warp_sum, Start* rec) {
+__device__ __forceinline__ Start find_start(const LatentParams& p, int range, int ranges, long long* warp_sum, Start* rec) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = THREADS / 32;
     long long mine = 0;
@@ -241,9 +249,9 @@ __device__ __forceinline__ Start find_start(const LatentParams& p, long long* wa
     __syncthreads();
     long long total = 0;
     for (int w = 0; w < NW; ++w) total += warp_sum[w];
-    const long long even = (total + gridDim.x - 1) / gridDim.x;
+    const long long even = (total + ranges - 1) / ranges;
     const int per = (int)max(even, (long long)p.min_tiles);
-    const long long lo = (long long)blockIdx.x * per;
+    const long long lo = (long long)range * per;
     __syncthreads();
     if (lo < total) {
         // the chunk that holds tile lo: prefix sums, THREADS chunks at a time
@@ -273,16 +281,14 @@ __device__ __forceinline__ Start find_start(const LatentParams& p, long long* wa
                     int hi = (k.q_len + p.tb - 1) / p.tb - 1;
                     while (j < hi) {
                         const int mid = (j + hi + 1) >> 1;
-                        if (p.hb * tiles_before(p, k, mid) <= rem) j = mid;
+                        if (tiles_before(p, k, mid) <= rem) j = mid;
                         else hi = mid - 1;
                     }
-                    rem -= p.hb * tiles_before(p, k, j);
+                    rem -= tiles_before(p, k, j);
                 }
-                const int t = tiles_of(keys_of(p, k, j));
                 rec->c = c;
                 rec->j = j;
-                rec->half = (int)(rem / t);
-                rec->tile = (int)(rem % t);
+                rec->at = (int)rem;
                 rec->count = (int)min((long long)per, total - lo);
             }
             base = all;
@@ -296,40 +302,40 @@ __device__ __forceinline__ Start find_start(const LatentParams& p, long long* wa
     return s;
 }
 
-// One segment of the CTA's range: tiles [tile, tile + n) of one unit's `tiles`.
+// One segment of a range: tiles [tile, tile + n) of one unit's `tiles`.
 struct Segment {
-    int c, j, half;
+    int c, j;
     int tile, n, tiles;
     int ctx, keys;          // token jt of the block sees keys <= ctx + j tb + jt; the unit's tokens see [0, keys)
     int rows;               // query rows of the unit
     int row0;               // the first one's row of q and out, [total_q * n_heads]
-    int left;               // tiles of the CTA's range after this segment
+    int parts;              // where the unit starts here and goes on behind the range: ranges it spans; else 0
 };
 
 template <typename F>
 __device__ __forceinline__ void for_each_segment(const LatentParams& p, const Start& s, F&& f) {
-    int c = s.c, j = s.j, half = s.half, tile = s.tile, left = s.count;
+    int c = s.c, j = s.j, at = s.at, left = s.count;
     if (left <= 0) return;
     Chunk k = load_chunk(p, c);
     while (left > 0) {
         Segment g;
         g.c = c;
         g.j = j;
-        g.half = half;
         g.keys = keys_of(p, k, j);
-        g.tiles = tiles_of(g.keys);
-        g.tile = tile;
-        g.n = min(g.tiles - tile, left);
+        g.tiles = tiles_of(p, g.keys);
+        const int n = min(g.tiles + p.unit_cost - at, left);  // cost of the unit in this range
+        left -= n;
+        g.tile = max(0, at - p.unit_cost);
+        g.n = max(0, at + n - p.unit_cost) - g.tile;
+        // (left is 0 when the unit goes on: what is behind this range starts a full range further)
+        const int rest = g.tiles - g.tile - g.n;
+        g.parts = (g.tile == 0 && rest > 0) ? 1 + (rest + s.per - 1) / s.per : 0;
         g.ctx = k.kv_len - k.q_len;
-        g.rows = p.hb == 2 ? (half == 0 ? 64 : p.n_heads - 64) : min(p.tb, k.q_len - j * p.tb) * p.n_heads;
-        g.row0 = (k.q0 + j * p.tb) * p.n_heads + half * 64;
-        left -= g.n;
-        g.left = left;
-        if (!f(g)) return;
+        g.rows = min(p.tb, k.q_len - j * p.tb) * p.n_heads;
+        g.row0 = (k.q0 + j * p.tb) * p.n_heads;
+        if (g.n > 0 && !f(g)) return;
         if (left <= 0) return;
-        tile = 0;
-        if (++half < p.hb) continue;
-        half = 0;
+        at = 0;
         if ((++j) * p.tb < k.q_len) continue;
         j = 0;
         do {
@@ -392,7 +398,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before();
-    const Start start = find_start<C::THREADS>(p, warp_sum, rec);  // (synchronises the CTA)
+    const Start start = find_start<C::THREADS>(p, (int)blockIdx.x, (int)gridDim.x, warp_sum, rec);  // (synchronises the CTA)
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -410,13 +416,13 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         int desc_parts = 0, desc_rows = 0, desc_row0 = 0, desc_slot = 0;
         auto wait_pv = [&](int n) {  // PVs of tiles 0 .. n - 1 complete
             while (pv_seen < n) {
-                ok = lat::warp_wait(bar(C::PV_DONE), (uint32_t)(pv_seen & 1), p.err) && ok;
+                ok = warp_wait(bar(C::PV_DONE), (uint32_t)(pv_seen & 1), p.err) && ok;
                 ++pv_seen;
             }
         };
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             const bool valid = r >= 0 && r < g.rows;
-            const int tok = p.hb == 2 ? 0 : (valid ? r / p.n_heads : 0);
+            const int tok = valid ? r / p.n_heads : 0;
             const int lim = valid ? g.ctx + g.j * p.tb + tok : -1;  // the row sees keys <= lim
             const int lim_min = g.ctx + g.j * p.tb;                 // the smallest limit in the unit
             float m_ref = -INFINITY, l = 0.f;
@@ -426,7 +432,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 float x[64];
                 float mx = -INFINITY;
                 if (row_warp) {
-                    ok = lat::warp_wait(bar(C::S_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), p.err) && ok;
+                    ok = warp_wait(bar(C::S_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), p.err) && ok;
                     tc::fence_after();
                     uint32_t s[64];
                     tc::ld64(tSb, s);
@@ -567,9 +573,8 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                         if (h0 + e < g.rows) dst[(size_t)e * DL] = __uint_as_float(o[e]);
                 }
             }
-            if (!whole && g.tile == 0) {  // the unit starts here and goes on in the CTAs behind
-                const long long f0 = (long long)blockIdx.x * start.per + (start.count - g.left - g.n);
-                desc_parts = (int)((f0 + g.tiles - 1) / start.per) - (int)blockIdx.x + 1;
+            if (g.parts) {
+                desc_parts = g.parts;
                 desc_rows = g.rows;
                 desc_row0 = g.row0;
                 desc_slot = slot;
@@ -612,7 +617,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 const int tile = g.tile + u;
                 const int nxt = u + 1 < g.n ? entry(tile + 1) : 0;
                 const int slot = (int)uniform((uint32_t)(n % slots)), use = n / slots;
-                if (use > 0 && !(ok = lat::warp_wait(bar(empty0 + slot), (uint32_t)((use - 1) & 1), p.err))) return false;
+                if (use > 0 && !(ok = warp_wait(bar(empty0 + slot), (uint32_t)((use - 1) & 1), p.err))) return false;
                 const uint32_t full = bar(full0 + slot), dst = ring + (uint32_t)slot * bytes;
                 if (elect_one()) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
@@ -632,7 +637,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         if (!ok) {  // leave no copy in flight behind
             for (int k = max(0, done - slots); k < done; ++k) {
                 const int m = (rope ? 0 : b) + k * step;
-                (void)lat::warp_wait(bar(full0 + m % slots), (uint32_t)((m / slots) & 1), p.err);
+                (void)warp_wait(bar(full0 + m % slots), (uint32_t)((m / slots) & 1), p.err);
             }
         }
     } else if (warp == Q_WARP && lane == 0) {

@@ -123,19 +123,22 @@ struct LatentParams {
     unsigned* err;
     int num_chunks, n_heads, max_blocks_per_seq, num_blocks, block_size, max_q_len, total_q;
     int tb;                     // tokens per unit of query rows
-    int hb;                     // units per token (2 above 64 heads)
-    int min_tiles;              // least tiles of a CTA's range
+    int tile_log2;              // log2 of the tokens per tile
+    int unit_cost;              // what a unit's start and output cost, in tiles (evens out the ranges)
+    int min_tiles;              // least cost of a range
     int stream_once;            // 1: every cache row is read by one unit (L2 evict-first)
     float qk_scale_log2;
-    float* part_o;              // [2 * CTAs][NR][DL]
-    float* part_ml;             // [2 * CTAs][NR][2]: reference (base 2) and exp-sum
-    int4* desc;                 // [CTAs]: partials, rows, first row of out, first slot of the unit cut at the range's end
+    float* part_o;              // [2 * ranges][NR][DL]
+    float* part_ml;             // [2 * ranges][NR][2]: reference (base 2) and exp-sum
+    int4* desc;                 // [ranges]: partials, rows, first row of out, first slot of the unit cut at the range's end
 };
 
-// Query rows per unit the kernel is built for (16, 32 or 64): the least that holds `rows`.
-inline int latent_unit_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Query rows per unit the kernels are built for: the least that holds `rows`.  16, 32 and 64: one CTA a
+// range of tiles (latent_kernel); 128: a pair of CTAs (latent_pair_kernel).
+inline int latent_unit_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
+// ctas: CTAs to run (a multiple of 2 for unit_rows 128)
 cudaError_t launch_latent(int bf16, int latent_dim, int unit_rows, const LatentParams& params, const CUtensorMap& tmC,
-                          const CUtensorMap& tmQ, int grid, cudaStream_t stream);
+                          const CUtensorMap& tmQ, int ctas, cudaStream_t stream);
 
 }  // namespace pa

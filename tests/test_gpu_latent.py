@@ -65,10 +65,11 @@ def test_decode_splits_long_contexts(ty, h, bs):
     _check_decode(ty, h, 512, bs, [9000, 12345, 17], seed=2)
 
 
-def test_decode_many_sequences():
+@pytest.mark.parametrize("h", [16, 70])
+def test_decode_many_sequences(h):
     """More sequences than threads of a CTA and than CTAs, empty ones among them."""
     lens = [(37 * i) % 150 for i in range(701)]
-    _check_decode("fp16", 16, 512, 16, lens, seed=3)
+    _check_decode("fp16", h, 512, 16, lens, seed=3)
 
 
 @pytest.mark.parametrize("h,dl", [(16, 512), (64, 512), (128, 512), (32, 256)])
@@ -90,9 +91,11 @@ def test_decode_finds_each_token(h, dl):
     assert (err <= half_step(dt) * want.abs() + 2.0 ** -12 * 8 + 2.0 ** -25).all()
 
 
-def test_decode_rising_scores_rescale():
-    """Scores that grow along the context by far more than the lazy rescale's 2^8, and a row that falls."""
-    dt, dl, h, L = torch.float16, 512, 16, 1000
+@pytest.mark.parametrize("h", [16, 40, 128])
+def test_decode_rising_scores_rescale(h):
+    """Scores that grow along the context by far more than the lazy rescale's 2^8, others that fall: heads of
+    both kinds, in both halves of a pair."""
+    dt, dl, L = torch.float16, 512, 1000
     g = gen(9)
     cache, bt, rows = paged(g, [L], 16, dl, dt)
     r = rows[0].clone()
@@ -121,15 +124,16 @@ def attend_sign(q, rows, sc):
     return (-q, -sc) if sc < 0 else (q, sc)
 
 
-def test_decode_nonfinite_rows_stay_in_their_sequence():
+@pytest.mark.parametrize("h", [16, 128])
+def test_decode_nonfinite_rows_stay_in_their_sequence(h):
     g = gen(5)
     lens = [100, 90, 80]
     cache, bt, rows = paged(g, lens, 16, 512, torch.bfloat16)
-    q = randn(g, (3, 16, 576), torch.bfloat16)
+    q = randn(g, (3, h, 576), torch.bfloat16)
     q[1, 3, 0] = float("nan")
     out = _decode(q, cache, bt, lens)
     assert torch.isnan(out[1, 3]).all()
-    keep = torch.ones(16, dtype=torch.bool, device="cuda")
+    keep = torch.ones(h, dtype=torch.bool, device="cuda")
     keep[3] = False
     assert torch.isfinite(out[1, keep]).all()
     for s in (0, 2):
@@ -139,11 +143,12 @@ def test_decode_nonfinite_rows_stay_in_their_sequence():
     assert torch.isnan(out2[0]).any() and torch.equal(out2[2], out[2])
 
 
-def test_decode_bad_lengths_and_blocks_are_flagged():
+@pytest.mark.parametrize("h", [8, 100])
+def test_decode_bad_lengths_and_blocks_are_flagged(h):
     g = gen(6)
     lens = [100, 90, 80]
     cache, bt, rows = paged(g, lens, 16, 512, torch.bfloat16)
-    q = randn(g, (3, 8, 576), torch.bfloat16)
+    q = randn(g, (3, h, 576), torch.bfloat16)
     pa.pa_device_errors(clear=True)
     out = _decode(q, cache, bt, [100, -5, bt.shape[1] * 16 + 1])
     assert pa.pa_device_errors(clear=True) == pa.PA_DEVERR_LENGTH
@@ -159,12 +164,13 @@ def test_decode_bad_lengths_and_blocks_are_flagged():
     check_attend(out[2:], q[2:], rows[2], SCALE, 512, 1, "the good one")
 
 
-def test_decode_repeats_bit_for_bit():
+@pytest.mark.parametrize("h", [16, 128])
+def test_decode_repeats_bit_for_bit(h):
     g = gen(7)
     lens = [3000, 17, 5000]
     cache, bt, rows = paged(g, lens, 16, 512, torch.bfloat16)
-    q = randn(g, (3, 16, 576), torch.bfloat16)
-    ws = _ws(16, 512)
+    q = randn(g, (3, h, 576), torch.bfloat16)
+    ws = _ws(h, 512)
     first = _decode(q, cache, bt, lens, ws=ws)
     for _ in range(5):
         assert torch.equal(_decode(q, cache, bt, lens, ws=ws), first)
