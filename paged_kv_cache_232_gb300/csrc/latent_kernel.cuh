@@ -88,12 +88,14 @@ __host__ __device__ constexpr uint32_t idesc(bool bf16, bool a_mn_major, int M, 
     return tc::idesc_f16(bf16, false, M, N) | ((a_mn_major ? 1u : 0u) << 15);
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar,
-                                            uint64_t policy) {
+__device__ __forceinline__ void tma_load_3d(uint32_t el, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            uint32_t bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy), "r"(el)
         : "memory");
 }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
@@ -101,6 +103,26 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
             dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// Issue, commits and loads are predicated on `el` (the warp's elected lane) rather than branched around: the
+// issuing warp stays converged, so that descriptors are formed once for the warp.
+__device__ __forceinline__ void mma(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t el, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(el)
         : "memory");
 }
 
@@ -424,7 +446,8 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
             const bool valid = r >= 0 && r < g.rows;
             const int tok = valid ? r / p.n_heads : 0;
             const int lim = valid ? g.ctx + g.j * p.tb + tok : -1;  // the row sees keys <= lim
-            const int lim_min = g.ctx + g.j * p.tb;                 // the smallest limit in the unit
+            // the smallest limit in the warp (its lanes without a row of S never matter: see below)
+            const int lim_min = g.rows < NR ? -1 : g.ctx + g.j * p.tb;
             float m_ref = -INFINITY, l = 0.f;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int kbase = (g.tile + u) * TK;
@@ -441,8 +464,12 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::S_EMPTY + (i & 1)));
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(s[e]) * sc;
-                    if (kbase + TK - 1 > lim_min || g.rows < NR || lane >= 16) {
+                    for (int e = 0; e < 64; e += 2) {
+                        const float2 v = __fmul2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(sc, sc));
+                        x[e] = v.x;
+                        x[e + 1] = v.y;
+                    }
+                    if (kbase + TK - 1 > lim_min) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
                             if (kbase + e > lim) x[e] = -INFINITY;
@@ -450,7 +477,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[e]);
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    mx = lane < 16 ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
                 }
                 const bool first = u == 0;
                 if (first) m_ref = mx;  // no O yet: the first tile's own maximum is the reference
@@ -485,15 +512,14 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 if (row_warp) {
                     const float mu = m_ref == -INFINITY ? 0.f : m_ref;
                     uint32_t w[32];
-                    float l0 = 0.f, l1 = 0.f;
+                    float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        w[e] = F::pack_rn(ex2(x[2 * e] - mu), ex2(x[2 * e + 1] - mu));
-                        const float2 b = F::unpack(w[e]);
-                        l0 += b.x;
-                        l1 += b.y;
+                        const float2 v = fadd2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(-mu, -mu));
+                        w[e] = F::pack_rn(ex2(v.x), ex2(v.y));
+                        ls = fadd2(ls, F::unpack(w[e]));
                     }
-                    l += l0 + l1;
+                    l += ls.x + ls.y;
                     wait_pv(i);  // the weights' buffer is free
                     if (r >= 0) {
 #pragma unroll
@@ -595,6 +621,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         const int br = min(p.block_size, TK), nbox = TK / br;   // rows per box, boxes per slab
         const int slabs = rope ? 1 : 2, slots = rope ? C::NROPE : C::NPAIR;
         const int full0 = rope ? C::ROPE_FULL : C::PAIR_FULL, empty0 = rope ? C::ROPE_EMPTY : C::PAIR_EMPTY;
+        const uint32_t el = elect_one();
         const uint32_t bytes = (uint32_t)(slabs * SLAB), ring = rope ? sRope : sPair;
         int n = rope ? 0 : b;    // slot number of this warp's next load, over the whole range
         const int step = rope ? 1 : NB;
@@ -619,16 +646,14 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 const int slot = (int)uniform((uint32_t)(n % slots)), use = n / slots;
                 if (use > 0 && !(ok = warp_wait(bar(empty0 + slot), (uint32_t)((use - 1) & 1), p.err))) return false;
                 const uint32_t full = bar(full0 + slot), dst = ring + (uint32_t)slot * bytes;
-                if (elect_one()) mbar_arrive_expect_tx(full, bytes);
+                const int first = (int)uniform((uint32_t)(tile * TK));
+                if (el) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
                 for (int x = 0; x < nbox; ++x) {
-                    const int row = (int)uniform((uint32_t)((tile * TK + x * br) % p.block_size));
+                    const int row = (first + x * br) % p.block_size;
                     const int e = __shfl_sync(0xffffffffu, blk, x);
-                    if (elect_one()) {
-                        tma_load_3d(dst + x * br * 128, &tmC, b * 128, row, e, full, pol);
-                        if (!rope) tma_load_3d(dst + SLAB + x * br * 128, &tmC, b * 128 + 64, row, e, full, pol);
-                    }
-                    __syncwarp();
+                    tma_load_3d(el, dst + x * br * 128, &tmC, b * 128, row, e, full, pol);
+                    if (!rope) tma_load_3d(el, dst + SLAB + x * br * 128, &tmC, b * 128 + 64, row, e, full, pol);
                 }
                 blk = nxt;
             }
@@ -664,90 +689,81 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         constexpr uint32_t ID_QK = idesc(BF16, false, 64, TK);
         const uint64_t dq = tc::sdesc_sw128(sQ, 16, 1024), dkp = tc::sdesc_sw128(sPair, 16, 1024),
                        dkr = tc::sdesc_sw128(sRope, 16, 1024);
+        const uint32_t el = elect_one(), tS = uniform(tmem);
         int i = 0, seg = 0, nk = 0, nr = 0;  // tiles, segments, pair and rotary slots read
-        bool issued = false, ok = true;
+        bool issued = false;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
-            if (!(ok = mbar_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err))) return false;
+            if (!warp_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err)) return false;
             for (int u = 0; u < g.n; ++u, ++i) {
-                if (i >= 2 && !(ok = mbar_wait(bar(C::S_EMPTY + (i & 1)), (uint32_t)(((i >> 1) - 1) & 1), p.err)))
-                    return false;
-                const uint32_t dS = uniform(tmem + (uint32_t)((i & 1) * 64));
+                const uint32_t dS = tS + uniform((uint32_t)(i & 1)) * 64;
+                if (i >= 2 && !warp_wait(bar(C::S_EMPTY + (i & 1)), (uint32_t)(((i >> 1) - 1) & 1), p.err)) return false;
 #pragma unroll
                 for (int b = 0; b < NB; ++b, ++nk) {
-                    const int slot = nk % C::NPAIR;
-                    if (!(ok = mbar_wait(bar(C::PAIR_FULL + slot), (uint32_t)((nk / C::NPAIR) & 1), p.err))) return false;
+                    const int slot = (int)uniform((uint32_t)(nk % C::NPAIR));
+                    const uint64_t dk = dkp + (uint32_t)((slot * PAIR) >> 4);
+                    if (!warp_wait(bar(C::PAIR_FULL + slot), (uint32_t)((nk / C::NPAIR) & 1), p.err)) return false;
                     tc::fence_after();
                     issued = true;
-                    const uint64_t dk = dkp + uniform((uint32_t)((slot * PAIR) >> 4));
-                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_f16_ss(dS, dq + (uint32_t)(((2 * b + (kk >> 2)) * C::QSLAB + (kk & 3) * 32) >> 4),
-                                           dk + (uint32_t)(((kk >> 2) * SLAB + (kk & 3) * 32) >> 4), ID_QK, b > 0 || kk > 0);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma(el, dS, dq + (uint32_t)(((2 * b + (kk >> 2)) * C::QSLAB + (kk & 3) * 32) >> 4),
+                            dk + (uint32_t)(((kk >> 2) * SLAB + (kk & 3) * 32) >> 4), ID_QK, b > 0 || kk > 0);
                 }
-                const int rs = nr % C::NROPE;
-                if (!(ok = mbar_wait(bar(C::ROPE_FULL + rs), (uint32_t)((nr / C::NROPE) & 1), p.err))) return false;
+                const int rs = (int)uniform((uint32_t)(nr % C::NROPE));
+                const uint64_t dk = dkr + (uint32_t)((rs * SLAB) >> 4);
+                if (!warp_wait(bar(C::ROPE_FULL + rs), (uint32_t)((nr / C::NROPE) & 1), p.err)) return false;
                 tc::fence_after();
-                const uint64_t dk = dkr + uniform((uint32_t)((rs * SLAB) >> 4));
-                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f16_ss(dS, dq + (uint32_t)(((C::QSLABS - 1) * C::QSLAB + kk * 32) >> 4),
-                                       dk + (uint32_t)((kk * 32) >> 4), ID_QK, 1u);
-                    tc::commit(bar(C::S_FULL + (i & 1)));
-                    tc::commit(bar(C::ROPE_EMPTY + rs));
-                    if (u == g.n - 1) tc::commit(bar(C::Q_EMPTY));
-                }
-                __syncwarp();
+                for (int kk = 0; kk < 4; ++kk)
+                    mma(el, dS, dq + (uint32_t)(((C::QSLABS - 1) * C::QSLAB + kk * 32) >> 4), dk + (uint32_t)((kk * 32) >> 4),
+                        ID_QK, 1u);
+                commit(el, bar(C::S_FULL + (i & 1)));
+                commit(el, bar(C::ROPE_EMPTY + rs));
+                if (u == g.n - 1) commit(el, bar(C::Q_EMPTY));
                 ++nr;
             }
             ++seg;
             return true;
         });
         if (issued) {  // every MMA must be complete before TMEM is released
-            if (elect_one()) tc::commit(bar(C::DRAIN));
-            __syncwarp();
-            (void)mbar_wait(bar(C::DRAIN), 0, p.err);
+            commit(el, bar(C::DRAIN));
+            (void)warp_wait(bar(C::DRAIN), 0, p.err);
         }
     } else if (warp == PV_WARP) {
         // ------------------------------------------------------------ PV issue: O^T += C^T P^T
         constexpr uint32_t ID_PV = idesc(BF16, true, 128, NR);
         const uint64_t dp = tc::sdesc_sw128(sP, 16, 1024), dv0 = tc::sdesc_sw128(sPair, SLAB, 1024);
-        const uint32_t dO = uniform(tmem + C::O_COL);
+        const uint32_t el = elect_one(), dO = uniform(tmem + C::O_COL);
         int i = 0, seg = 0, nv = 0;
         bool issued = false;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             // O^T of the segment before must have been read before the first product overwrites it
-            if (seg > 0 && !mbar_wait(bar(C::O_FREE), (uint32_t)((seg - 1) & 1), p.err)) return false;
+            if (seg > 0 && !warp_wait(bar(C::O_FREE), (uint32_t)((seg - 1) & 1), p.err)) return false;
             for (int u = 0; u < g.n; ++u, ++i) {
-                if (!mbar_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err)) return false;
+                const uint32_t acc = uniform(u > 0);
+                const int slot0 = (int)uniform((uint32_t)(nv % C::NPAIR));
+                if (!warp_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err)) return false;
                 tc::fence_after();
                 issued = true;
-                const uint32_t acc = uniform(u > 0);
 #pragma unroll
-                for (int b = 0; b < NB; ++b, ++nv) {
-                    const int slot = nv % C::NPAIR;
-                    const uint64_t dv = dv0 + uniform((uint32_t)((slot * PAIR) >> 4));
-                    if (elect_one()) {
+                for (int b = 0; b < NB; ++b) {
+                    const int slot = slot0 + b < C::NPAIR ? slot0 + b : slot0 + b - C::NPAIR;
+                    const uint64_t dv = dv0 + (uint32_t)((slot * PAIR) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < TK / 16; ++kk)
-                            tc::mma_f16_ss(dO + b * NR, dv + (uint32_t)((kk * 2048) >> 4), dp + (uint32_t)((kk * 32) >> 4), ID_PV,
-                                           kk > 0 ? 1u : acc);
-                        tc::commit(bar(C::PAIR_EMPTY + slot));
-                        if (b == NB - 1) tc::commit(bar(C::PV_DONE));
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < TK / 16; ++kk)
+                        mma(el, dO + b * NR, dv + (uint32_t)((kk * 2048) >> 4), dp + (uint32_t)((kk * 32) >> 4), ID_PV,
+                            kk > 0 ? 1u : acc);
+                    commit(el, bar(C::PAIR_EMPTY + slot));
                 }
+                commit(el, bar(C::PV_DONE));
+                nv += NB;
             }
             ++seg;
             return true;
         });
         if (issued) {
-            if (elect_one()) tc::commit(bar(C::DRAIN + 1));
-            __syncwarp();
-            (void)mbar_wait(bar(C::DRAIN + 1), 0, p.err);
+            commit(el, bar(C::DRAIN + 1));
+            (void)warp_wait(bar(C::DRAIN + 1), 0, p.err);
         }
     }
     tc::fence_before();
