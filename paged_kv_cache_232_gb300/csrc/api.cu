@@ -1007,8 +1007,8 @@ static int latent_impl(void* out, const void* q, const void* latent_cache, const
     p.total_q = (int)total_q;
     p.tb = rows / n_heads;
     p.tile_log2 = rows == 128 ? 7 : 6;
-    p.unit_cost = 1;
-    p.min_tiles = 3;
+    p.unit_cost = rows == 128 ? 2 : 1;
+    p.min_tiles = p.unit_cost + 2;
     p.stream_once = n_heads * (int64_t)max_q_len <= 128 ? 1 : 0;  // one unit a sequence
     p.qk_scale_log2 = scale * 1.4426950408889634f;
     p.desc = reinterpret_cast<int4*>(base + w.desc_off);

@@ -206,6 +206,7 @@ __device__ __forceinline__ int tiles_of(const LatentParams& p, int keys) {
 }
 
 // sum over i < n of floor((a i + b) / m), by the Euclidean reduction of the lattice-point count
+// (a, m at most 128: from the first reduction of b on, a n + b fits 32 bits for n below 2^24)
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     unsigned long long s = 0;
     while (true) {
@@ -217,10 +218,10 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
             s += (unsigned long long)n * (b / m);
             b %= m;
         }
-        const unsigned long long y = (unsigned long long)a * n + b;
+        const uint32_t y = a * n + b;
         if (y < m) return (long long)s;
-        n = (uint32_t)(y / m);
-        b = (uint32_t)(y % m);
+        n = y / m;
+        b = y % m;
         const uint32_t t = m;
         m = a;
         a = t;
@@ -250,72 +251,99 @@ __device__ __forceinline__ long long tiles_in(const LatentParams& p, const Chunk
 
 // A range: where it starts (chunk, token block, cost into that block) and its cost.
 struct Start {
+    long long rem;  // (while it is looked for: the cost into the chunk)
     int c, j, at, count, per;
 };
+static_assert(sizeof(Start) <= 32, "record area");
 
-// Range `range` of `ranges`.  Every thread of the CTA calls it; all return the same record.
+// Range `range` of `ranges`.  Every thread of the CTA calls it; all return the same record.  One pass over the
+// sequences' lengths where they are at most as many as threads, two otherwise.
 template <int THREADS>
 __device__ __forceinline__ Start find_start(const LatentParams& p, int range, int ranges, long long* warp_sum, Start* rec) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = THREADS / 32;
-    long long mine = 0;
-    for (int c = tid; c < p.num_chunks; c += THREADS) {
-        const Chunk k = load_chunk(p, c);
-        if (k.bad && blockIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
-        mine += tiles_in(p, k);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) warp_sum[warp] = mine;
     if (tid == 0) rec->count = 0;
+    Chunk k{0, 0, 0, false};
+    long long mine = 0, n = 0;  // cost of this thread's sequences, of the one in k
+    for (int c = tid; c < p.num_chunks; c += THREADS) {
+        k = load_chunk(p, c);
+        if (k.bad && blockIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
+        n = tiles_in(p, k);
+        mine += n;
+    }
+    const bool one = p.num_chunks <= THREADS;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < NW; ++w) total += warp_sum[w];
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const long long x = warp_sum[w];
+        if (w < warp) before += x;
+        total += x;
+    }
     const long long even = (total + ranges - 1) / ranges;
     const int per = (int)max(even, (long long)p.min_tiles);
     const long long lo = (long long)range * per;
-    __syncthreads();
     if (lo < total) {
-        // the chunk that holds tile lo: prefix sums, THREADS chunks at a time
-        long long base = 0;
-        for (int c0 = 0; c0 < p.num_chunks; c0 += THREADS) {
-            const int c = c0 + tid;
-            Chunk k{0, 0, 0, false};
-            if (c < p.num_chunks) k = load_chunk(p, c);
-            const long long n = c < p.num_chunks ? tiles_in(p, k) : 0;
-            long long incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (lane == 31) warp_sum[warp] = incl;
-            __syncthreads();
-            long long before = base;
-            for (int w = 0; w < warp; ++w) before += warp_sum[w];
-            long long all = base;
-            for (int w = 0; w < NW; ++w) all += warp_sum[w];
-            const long long at = before + incl - n;
-            if (n > 0 && lo >= at && lo < at + n) {
-                long long rem = lo - at;
-                int j = 0;
-                if (p.q_loc != nullptr) {  // the last block whose first tile is at or before rem
-                    int hi = (k.q_len + p.tb - 1) / p.tb - 1;
-                    while (j < hi) {
-                        const int mid = (j + hi + 1) >> 1;
-                        if (tiles_before(p, k, mid) <= rem) j = mid;
-                        else hi = mid - 1;
-                    }
-                    rem -= tiles_before(p, k, j);
-                }
+        auto found = [&](int c, const Chunk& q, long long at, long long cost) {
+            if (cost > 0 && lo >= at && lo < at + cost) {
                 rec->c = c;
-                rec->j = j;
-                rec->at = (int)rem;
+                rec->j = 0;
+                rec->at = (int)(lo - at);
+                rec->rem = lo - at;
                 rec->count = (int)min((long long)per, total - lo);
             }
-            base = all;
+        };
+        if (one) {
+            found(tid, k, before + incl - n, n);
+        } else {
+            // prefix sums, THREADS sequences at a time
+            long long base = 0;
+            for (int c0 = 0; c0 < p.num_chunks && base <= lo; c0 += THREADS) {
+                __syncthreads();
+                const int c = c0 + tid;
+                Chunk q{0, 0, 0, false};
+                if (c < p.num_chunks) q = load_chunk(p, c);
+                const long long m = c < p.num_chunks ? tiles_in(p, q) : 0;
+                long long in = m;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, in, o);
+                    if (lane >= o) in += y;
+                }
+                if (lane == 31) warp_sum[warp] = in;
+                __syncthreads();
+                long long all = base, bef = base;
+                for (int w = 0; w < NW; ++w) {
+                    if (w < warp) bef += warp_sum[w];
+                    all += warp_sum[w];
+                }
+                found(c, q, bef + in - m, m);
+                base = all;
+            }
+        }
+        if (p.q_loc != nullptr) {
+            // the last token block of the chunk whose cost starts at or before the range, THREADS candidates a round
             __syncthreads();
-            if (base > lo) break;
+            const Start r = *rec;
+            const Chunk q = load_chunk(p, r.c);
+            int j0 = 0, m = (q.q_len + p.tb - 1) / p.tb;  // it is in [j0, j0 + m)
+            while (m > 1) {
+                const int step = (m + THREADS - 1) / THREADS, j = j0 + tid * step;
+                const int hit = __syncthreads_count(tid * step < m && tiles_before(p, q, j) <= r.rem);  // (j0 itself: always)
+                j0 += (hit - 1) * step;
+                m = min(step, m - (hit - 1) * step);
+            }
+            if (tid == 0) {
+                rec->j = j0;
+                rec->at = (int)(r.rem - tiles_before(p, q, j0));
+            }
         }
     }
     __syncthreads();
@@ -774,33 +802,125 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
     }
 }
 
-// Joins the partials of the units that the ranges' ends cut.  Block (b, y): the unit that starts in CTA
-// b's range and goes on behind it, query rows y, y + gridDim.y, ...; each of the block's groups of
-// DL / 4 threads sums every KG-th partial, weighted by 2^(m - max m), then the groups' sums are added
-// in order.
+// Joins the partials of the units that the ranges' ends cut: out = sum_k 2^(m_k - max m) o_k / sum_k 2^(m_k - max m) l_k.
+// The rows of all cut units are dealt out evenly.  With few partials a row (the usual cut: two) a warp takes a row,
+// DL / 32 columns a lane; with many (few long contexts) a block takes a row, its groups of DL / 4 threads every KG-th
+// partial each, their sums added in order.  Fixed orders: the same inputs give the same bits.
 template <bool BF16, int DL, int NR>
-__global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p) {
+__global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p, int ranges) {
     using F = F16x2<BF16>;
-    constexpr int TG = DL / 4, KG = 512 / TG;
+    constexpr int TG = DL / 4, KG = 512 / TG, CV = DL / 128;
+    constexpr int kFew = 8;
     __shared__ float4 acc[512];
     __shared__ float wt[lat::MAX_CTAS];
     __shared__ float red[16], l_s[1];
+    __shared__ int4 desc[lat::MAX_CTAS];
+    __shared__ int row_end[lat::MAX_CTAS];   // rows of the cut units up to and with range b's
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 d = __ldcg(p.desc + blockIdx.x);
-    const int parts = d.x, tid = threadIdx.x;
-    if (parts == 0) return;
-    auto slot_of = [&](int k) { return k == 0 ? d.w : 2 * ((int)blockIdx.x + k); };
-    for (int row = blockIdx.y; row < d.y; row += gridDim.y) {
+    int4 d = make_int4(0, 0, 0, 0);
+    if (tid < ranges) d = __ldcg(p.desc + tid);
+    const bool many = __syncthreads_or(d.x > kFew);
+    {
+        const int rows = d.x ? d.y : 0;
+        int incl = rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        int* sums = reinterpret_cast<int*>(red);
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += sums[w];
+        if (tid < ranges) {
+            row_end[tid] = incl;
+            desc[tid] = d;
+        }
+        __syncthreads();
+    }
+    const int total = ranges > 0 ? row_end[ranges - 1] : 0;
+    auto unit_of = [&](int item) {  // the range whose cut unit holds row `item`
+        int lo = 0, hi = ranges - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (row_end[mid] > item) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    };
+    if (!many) {
+        for (int item = (int)blockIdx.x * 16 + warp; item < total; item += (int)gridDim.x * 16) {
+            const int b = unit_of(item);
+            const int4 u = desc[b];
+            const int row = item - (row_end[b] - u.y);
+            const int mine = lane == 0 ? u.w : 2 * (b + lane);  // the slot of partial `lane`
+            float m = -INFINITY, l = 0.f;
+            if (lane < u.x) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)mine * NR + row);
+                m = ml.x;
+                l = ml.y;
+            }
+            float4 a[CV] = {};
+            // the partials, loaded before their weights are known
+            float4 v[2][CV];
+            auto fetch = [&](int k, float4 (&x)[CV]) {
+                const int slot = k == 0 ? u.w : 2 * (b + k);
+#pragma unroll
+                for (int c = 0; c < CV; ++c)
+                    x[c] = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * NR + row) * DL) + lane + 32 * c);
+            };
+            fetch(0, v[0]);
+            fetch(1, v[1]);
+            float mx = m;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = __shfl_sync(0xffffffffu, mx, 0);
+            const float w = m == -INFINITY ? 0.f : ex2(m - mx);
+            float lw = l != 0.f ? l * w : 0.f;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+            lw = __shfl_sync(0xffffffffu, lw, 0);
+            auto add = [&](int k, const float4 (&x)[CV]) {
+                const float f = __shfl_sync(0xffffffffu, w, k);
+                if (f == 0.f) return;
+#pragma unroll
+                for (int c = 0; c < CV; ++c) {
+                    a[c].x = fmaf(x[c].x, f, a[c].x);
+                    a[c].y = fmaf(x[c].y, f, a[c].y);
+                    a[c].z = fmaf(x[c].z, f, a[c].z);
+                    a[c].w = fmaf(x[c].w, f, a[c].w);
+                }
+            };
+            add(0, v[0]);
+            add(1, v[1]);
+            for (int k = 2; k < u.x; ++k) {
+                fetch(k, v[0]);
+                add(k, v[0]);
+            }
+            const float inv = lw != 0.f ? 1.f / lw : 0.f;
+            uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(u.z + row) * DL);
+#pragma unroll
+            for (int c = 0; c < CV; ++c)
+                dst[lane + 32 * c] = make_uint2(F::pack_rn(a[c].x * inv, a[c].y * inv), F::pack_rn(a[c].z * inv, a[c].w * inv));
+        }
+        return;
+    }
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        const int b = unit_of(item);
+        const int4 u = desc[b];
+        const int row = item - (row_end[b] - u.y), parts = u.x;
+        auto slot_of = [&](int k) { return k == 0 ? u.w : 2 * (b + k); };
         float m = -INFINITY, l = 0.f;
         if (tid < parts) {
-            const float* ml = p.part_ml + ((size_t)slot_of(tid) * NR + row) * 2;
-            m = __ldcg(ml);
-            l = __ldcg(ml + 1);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot_of(tid) * NR + row);
+            m = ml.x;
+            l = ml.y;
         }
         float mx = m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
+        if (lane == 0) red[warp] = mx;
         __syncthreads();
         mx = red[0];
         for (int w = 1; w < 16; ++w) mx = fmaxf(mx, red[w]);
@@ -810,7 +930,7 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
         __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = lw;
+        if (lane == 0) red[warp] = lw;
         __syncthreads();
         if (tid == 0) {
             float t = 0.f;
@@ -819,7 +939,7 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p)
         }
         const int gidx = tid / TG, t = tid % TG;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int k = gidx; k < parts; k += KG) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_of(k) * NR + row) * DL) + t);
             const float f = wt[k];
@@ -841,7 +961,7 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p)
                 a.w += v.w;
             }
             const float lt = l_s[0], inv = lt != 0.f ? 1.f / lt : 0.f;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(d.z + row) * DL + 4 * tid) =
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(u.z + row) * DL + 4 * tid) =
                 make_uint2(F::pack_rn(a.x * inv, a.y * inv), F::pack_rn(a.z * inv, a.w * inv));
         }
         __syncthreads();
