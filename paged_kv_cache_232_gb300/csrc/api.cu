@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -852,10 +853,12 @@ int pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_stride, const void
     p.n_kv_heads = n_kv_heads;
     p.eps = eps;
     p.err = dev->err;
-    const int rpw = head_dim == 64 ? 8 : head_dim == 256 ? 2 : 4;  // head rows per warp
-    const int64_t warps = num_tokens * ((n_q_heads + 2 * n_kv_heads + rpw - 1) / rpw);
-    const int grid = (int)std::min<int64_t>((warps + 7) / 8, INT32_MAX);
-    auto launch = [&](auto kern) { kern<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p); };
+    const int gl = head_dim == 64 ? 4 : head_dim == 256 ? 16 : 8;  // lanes a head row
+    const int lanes = (n_q_heads + 2 * n_kv_heads) * gl;
+    const int threads = std::min((lanes + 31) / 32 * 32, 512);
+    const int64_t max_grid = (int64_t)dev->sm_count * (2048 / threads);
+    const int grid = (int)std::min<int64_t>(num_tokens, max_grid);
+    auto launch = [&](auto kern) { kern<<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p); };
     const bool bf = dtype == PA_BF16;
     if (head_dim == 64) bf ? launch(pa::norm_rope_write_kernel<true, 64>) : launch(pa::norm_rope_write_kernel<false, 64>);
     else if (head_dim == 96) bf ? launch(pa::norm_rope_write_kernel<true, 96>) : launch(pa::norm_rope_write_kernel<false, 96>);
@@ -921,9 +924,12 @@ int pa_latent_rope_and_cache(void* q, const void* q_pe, int64_t q_pe_token_strid
     p.interleaved = interleaved != 0;
     p.eps = eps;
     p.err = dev->err;
-    const int64_t warps = num_tokens * (1 + (1 + (q_pe ? n_heads : 0) + 7) / 8);
-    const int grid = (int)std::min<int64_t>((warps + 7) / 8, INT32_MAX);
-    auto launch = [&](auto kern) { kern<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p); };
+    const int tasks = 1 + (1 + (q_pe ? n_heads : 0) + 7) / 8;   // warps a token
+    const int per_block = std::max(1, 8 / tasks);
+    const int parts = tasks <= 8 ? 1 : (tasks + 7) / 8;         // blocks a token
+    const int64_t max_grid = std::max(1, dev->sm_count * 8 / parts);
+    const dim3 grid((unsigned)std::min<int64_t>((num_tokens + per_block - 1) / per_block, max_grid), (unsigned)parts);
+    auto launch = [&](auto kern) { kern<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p, tasks, per_block); };
     const bool bf = dtype == PA_BF16;
     if (latent_dim == 512) bf ? launch(pa::latent_write_kernel<true, 512>) : launch(pa::latent_write_kernel<false, 512>);
     else bf ? launch(pa::latent_write_kernel<true, 256>) : launch(pa::latent_write_kernel<false, 256>);

@@ -11,17 +11,38 @@
 
 namespace pa {
 
-template <bool BF16, int N>
-__device__ __forceinline__ float sum_sq(const uint4 (&v)[N], float scale) {
-    float s = 0.f;
+template <bool BF16>
+__device__ __forceinline__ float sum_sq(const uint4& v, float scale) {
+    float f[8], s = 0.f;
+    unpack8<BF16>(v, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(f[e] * scale, f[e] * scale, s);
+    return s;
+}
+
+// The rare case of inv_rms, out of line: the row scaled by (a power of two near 1 /) its largest value.
+template <bool BF16, int GL, int D, int N>
+__device__ __noinline__ float inv_rms_scaled(uint4 v0, uint4 v1, float eps, float ss, float r, bool lost) {
+    const uint4 v[2] = {v0, v1};
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float f[8];
         unpack8<BF16>(v[i], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(f[e] * scale, f[e] * scale, s);
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
     }
-    return s;
+#pragma unroll
+    for (int o = GL / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float k = exp2f(-(float)min(max(ilogbf(m), -126), 126));
+    float st = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) st += sum_sq<BF16>(v[i], k);
+#pragma unroll
+    for (int o = GL / 2; o > 0; o >>= 1) st += __shfl_xor_sync(0xffffffffu, st, o);
+    // an infinite value leaves the finite ones 0 and itself NaN (0 * inf), as the formula does
+    if (lost && m > 0.f) r = m == INFINITY ? 0.f : k * rsqrtf(st * (1.f / D) + fminf(eps * k * k, 1e37f));
+    return ss != ss ? ss : r;
 }
 
 // 1 / sqrt(mean(x^2) + eps) of a row of D values that GL neighbouring lanes hold (N 16-byte chunks
@@ -29,31 +50,14 @@ __device__ __forceinline__ float sum_sq(const uint4 (&v)[N], float scale) {
 // squares overflows fp32 (or, next to a tiny eps, vanishes), the row is scaled by its largest value first.
 template <bool BF16, int GL, int D, int N>
 __device__ __forceinline__ float inv_rms(const uint4 (&v)[N], float eps) {
-    float ss = sum_sq<BF16>(v, 1.f);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss += sum_sq<BF16>(v[i], 1.f);
 #pragma unroll
     for (int o = GL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     float r = rsqrtf(ss * (1.f / D) + eps);
     const bool lost = !(ss <= 1e37f) || (eps < 1e-30f && ss < 1e-25f);
-    if (__any_sync(0xffffffffu, lost)) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float f[8];
-            unpack8<BF16>(v[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-        }
-#pragma unroll
-        for (int o = GL / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // a power of two near 1 / m, so that scaling is exact
-        const float k = exp2f(-(float)min(max(ilogbf(m), -126), 126));
-        float st = sum_sq<BF16>(v, k);
-#pragma unroll
-        for (int o = GL / 2; o > 0; o >>= 1) st += __shfl_xor_sync(0xffffffffu, st, o);
-        // an infinite value leaves the finite ones 0 and itself NaN (0 * inf), as the formula does
-        if (lost && m > 0.f) r = m == INFINITY ? 0.f : k * rsqrtf(st * (1.f / D) + fminf(eps * k * k, 1e37f));
-        if (ss != ss) r = ss;
-    }
+    if (__any_sync(0xffffffffu, lost)) r = inv_rms_scaled<BF16, GL, D, N>(v[0], v[N - 1], eps, ss, r, lost);
     return r;
 }
 
@@ -102,62 +106,69 @@ struct NormRopeParams {
 };
 
 // A head row takes GL lanes, each the 16-byte chunks c and c + D / 16 of it (both halves of eight
-// rotations), so the sum of squares is a shuffle over GL lanes.  A warp takes 32 / GL head rows of
-// one token; the warps of the grid walk (token, group of head rows) items.
+// rotations), so the sum of squares is a shuffle over GL lanes.  A thread keeps its head row and its
+// weights and walks tokens, the next token's loads in flight while it works on one.
 template <bool BF16, int D>
-__global__ void __launch_bounds__(256) norm_rope_write_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(512, 2) norm_rope_write_kernel(const NormRopeParams p) {
     constexpr int PAIRS = D / 16;
     constexpr int GL = D == 64 ? 4 : D == 256 ? 16 : 8;  // 96 columns: 6 of 8 lanes
-    constexpr int RPW = 32 / GL;
     // the next kernel of the step may start its launch; it waits for this grid before reading anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, c = lane % GL;
+    const int c = threadIdx.x % GL;
     const int heads = p.n_q_heads + 2 * p.n_kv_heads;
-    const int groups = (heads + RPW - 1) / RPW;
-    const int64_t items = p.num_tokens * groups;
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
-        const int64_t t = it / groups;
-        const int gr = (int)(it - t * groups);
-        const int h = gr * RPW + lane / GL;
-        const int64_t pos = __ldg(p.positions + t);
-        int64_t slot = __ldg(p.slot_mapping + t);
-        if (pos < 0 || pos >= p.max_position) {  // the row is left untouched
-            if (gr == 0 && lane == 0) flag_error(p.err, PA_DEVERR_POSITION);
-            continue;
-        }
-        if (slot < -1 || slot >= p.num_slots) {
-            if (gr == 0 && lane == 0) flag_error(p.err, PA_DEVERR_SLOT);
-            slot = -1;
-        }
+    // (whole warps take part in the shuffles: the head loop runs to a multiple of the block's head rows)
+    for (int h0 = 0; h0 < heads; h0 += (int)blockDim.x / GL) {
+        const int h = h0 + (int)threadIdx.x / GL;
         const int kind = h < p.n_q_heads ? 0 : h < p.n_q_heads + p.n_kv_heads ? 1 : 2;
         const int hh = kind == 0 ? h : kind == 1 ? h - p.n_q_heads : h - p.n_q_heads - p.n_kv_heads;
-        const bool act = h < heads && c < PAIRS && (kind == 0 || slot >= 0);
-        uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        uint4 &lo = x[0], &hi = x[1];
-        if (act) {
-            const uint16_t* src = kind == 0 ? p.q + t * p.q_stride : kind == 1 ? p.key + t * p.key_stride
-                                                                              : p.value + t * p.value_stride;
-            const uint4* row = reinterpret_cast<const uint4*>(src + (int64_t)hh * D);
-            lo = row[c];
-            hi = row[c + PAIRS];
+        const bool mine = h < heads && c < PAIRS;
+        const uint16_t* src = (kind == 0 ? p.q : kind == 1 ? p.key : p.value) + (int64_t)hh * D + 8 * c;
+        uint16_t* dst = (kind == 0 ? p.q_out : kind == 1 ? p.k_cache : p.v_cache) + (int64_t)hh * D + 8 * c;
+        const int64_t in_stride = kind == 0 ? p.q_stride : kind == 1 ? p.key_stride : p.value_stride;
+        const int64_t out_stride = kind == 0 ? p.q_out_stride : (int64_t)p.n_kv_heads * D;
+        const uint4* weight = reinterpret_cast<const uint4*>(kind == 0 ? p.q_weight : p.k_weight) + c;
+        uint4 nxt[2];
+        int64_t npos = 0, nslot = -1;
+        auto fetch = [&](int64_t t) {
+            nxt[0] = nxt[1] = make_uint4(0u, 0u, 0u, 0u);
+            if (t >= p.num_tokens) return;
+            npos = __ldg(p.positions + t);
+            nslot = __ldg(p.slot_mapping + t);
+            if (mine) {
+                const uint4* row = reinterpret_cast<const uint4*>(src + t * in_stride);
+                nxt[0] = row[0];
+                nxt[1] = row[PAIRS];
+            }
+        };
+        fetch(blockIdx.x);
+        for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
+            uint4 x[2] = {nxt[0], nxt[1]};
+            const int64_t pos = npos;
+            int64_t slot = nslot;
+            // (the row in flight is another token's: also where q is rewritten in place)
+            fetch(t + gridDim.x);
+            const float r = inv_rms<BF16, GL, D>(x, p.eps);
+            if (pos < 0 || pos >= p.max_position) {  // the row is left untouched
+                if (threadIdx.x == 0 && h0 == 0) flag_error(p.err, PA_DEVERR_POSITION);
+                continue;
+            }
+            if (slot < -1 || slot >= p.num_slots) {
+                if (threadIdx.x == 0 && h0 == 0) flag_error(p.err, PA_DEVERR_SLOT);
+                slot = -1;
+            }
+            if (!mine || (kind != 0 && slot < 0)) continue;
+            uint4* out = reinterpret_cast<uint4*>(dst + (kind == 0 ? t : slot) * out_stride);
+            if (kind < 2) {
+                float a[8], b[8];
+                norm8<BF16>(x[0], __ldg(weight), r, a);
+                norm8<BF16>(x[1], __ldg(weight + PAIRS), r, b);
+                turn8(a, b, p.cos_sin + pos * D, 8 * c, D / 2);
+                x[0] = pack8<BF16>(a);
+                x[1] = pack8<BF16>(b);
+            }
+            out[0] = x[0];
+            out[PAIRS] = x[1];
         }
-        const float r = inv_rms<BF16, GL, D>(x, p.eps);
-        if (!act) continue;
-        uint4* dst;
-        if (kind == 0) dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + (int64_t)hh * D);
-        else dst = reinterpret_cast<uint4*>((kind == 1 ? p.k_cache : p.v_cache) + (slot * p.n_kv_heads + hh) * D);
-        if (kind < 2) {
-            const uint4* w = reinterpret_cast<const uint4*>(kind == 0 ? p.q_weight : p.k_weight);
-            float a[8], b[8];
-            norm8<BF16>(lo, __ldg(w + c), r, a);
-            norm8<BF16>(hi, __ldg(w + c + PAIRS), r, b);
-            turn8(a, b, p.cos_sin + pos * D, 8 * c, D / 2);
-            lo = pack8<BF16>(a);
-            hi = pack8<BF16>(b);
-        }
-        dst[c] = lo;
-        dst[c + PAIRS] = hi;
     }
 }
 
@@ -176,62 +187,82 @@ struct LatentWriteParams {
     unsigned* err;
 };
 
-// A warp takes one token's latent columns (item 0: DL / 32 columns a lane, the sum of squares over
-// the warp) or eight of its 64-column rotary rows (four lanes each: the shared key part, then the
-// query heads').  A lane holds the 16-byte chunks c and c + 4 of its rotary row: the rotate-half
-// pairs of eight angles, or (interleaved) the neighbours of four angles in each chunk.
+// A warp keeps one task of a token and walks tokens, the next token's loads in flight: task 0 its latent
+// columns (DL / 32 a lane, the sum of squares over the warp), task 1 .. eight of its 64-column rotary rows
+// (four lanes each: the shared key part, then the query heads').  A lane holds the 16-byte chunks c and
+// c + 4 of its rotary row: the rotate-half pairs of eight angles, or (interleaved) the neighbours of four
+// angles in each chunk.  A block's eight warps hold the tasks of `per_block` tokens (up to eight tasks a
+// token), or eight of one token's tasks (blockIdx.y: which eight).
 template <bool BF16, int DL>
-__global__ void __launch_bounds__(256) latent_write_kernel(const LatentWriteParams p) {
+__global__ void __launch_bounds__(256, 4) latent_write_kernel(const LatentWriteParams p, int tasks, int per_block) {
     constexpr int ROW = DL + 64, CH = DL / 256;  // 16-byte chunks of the latent columns per lane
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, c = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3;
+    const int task = tasks <= 8 ? warp % tasks : (int)blockIdx.y * 8 + warp;
+    if (task >= tasks || warp >= tasks * per_block) return;
     const int rows = 1 + (p.q_pe ? p.n_heads : 0);
-    const int groups = 1 + (rows + 7) / 8;
-    const int64_t items = p.num_tokens * groups;
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
-        const int64_t t = it / groups;
-        const int gr = (int)(it - t * groups);
-        const int64_t pos = __ldg(p.positions + t);
-        int64_t slot = __ldg(p.slot_mapping + t);
+    const int rr = (task - 1) * 8 + (lane >> 2);  // rotary row: 0 the key part, 1 .. query head rr - 1
+    const bool mine = task == 0 || rr < rows;
+    const int hop = task == 0 ? (CH - 1) * 32 : 4;  // chunks between this lane's two (none: one chunk, read twice)
+    const uint16_t* src = task == 0 ? p.kv + 8 * lane
+                          : rr == 0 ? p.kv + DL + 8 * c
+                                    : p.q_pe + (int64_t)(rr - 1) * p.pe_head_stride + 8 * c;
+    const int64_t in_stride = rr <= 0 ? p.kv_stride : p.pe_token_stride;
+    const int64_t step = (int64_t)gridDim.x * per_block;
+    uint4 nxt[2];
+    int64_t npos = 0, nslot = -1;
+    auto fetch = [&](int64_t t) {
+        nxt[0] = nxt[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (t >= p.num_tokens) return;
+        npos = __ldg(p.positions + t);
+        nslot = __ldg(p.slot_mapping + t);
+        if (mine) {
+            const uint4* row = reinterpret_cast<const uint4*>(src + t * in_stride);
+            nxt[0] = row[0];
+            nxt[1] = row[hop];
+        }
+    };
+    int64_t t = (int64_t)blockIdx.x * per_block + (tasks <= 8 ? warp / tasks : 0);
+    fetch(t);
+    for (; t < p.num_tokens; t += step) {
+        uint4 x[2] = {nxt[0], nxt[1]};
+        const int64_t pos = npos;
+        int64_t slot = nslot;
+        fetch(t + step);
         if (pos < 0 || pos >= p.max_position) {  // the row is left untouched
-            if (gr == 0 && lane == 0) flag_error(p.err, PA_DEVERR_POSITION);
+            if (task == 0 && lane == 0) flag_error(p.err, PA_DEVERR_POSITION);
             continue;
         }
         if (slot < -1 || slot >= p.num_slots) {
-            if (gr == 0 && lane == 0) flag_error(p.err, PA_DEVERR_SLOT);
+            if (task == 0 && lane == 0) flag_error(p.err, PA_DEVERR_SLOT);
             slot = -1;
         }
-        if (gr == 0) {
-            if (slot < 0) continue;
-            const uint4* src = reinterpret_cast<const uint4*>(p.kv + t * p.kv_stride);
-            uint4* dst = reinterpret_cast<uint4*>(p.cache + slot * ROW);
-            uint4 v[CH];
-#pragma unroll
-            for (int i = 0; i < CH; ++i) v[i] = src[lane + 32 * i];
+        if (task == 0) {
+            if (slot < 0) continue;  // (the same in the whole warp)
             if (p.weight) {
+                const uint4* w = reinterpret_cast<const uint4*>(p.weight) + lane;
+                uint4 v[CH];
+#pragma unroll
+                for (int e = 0; e < CH; ++e) v[e] = x[e];
                 const float r = inv_rms<BF16, 32, DL>(v, p.eps);
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    float y[8];
-                    norm8<BF16>(v[i], __ldg(reinterpret_cast<const uint4*>(p.weight) + lane + 32 * i), r, y);
-                    v[i] = pack8<BF16>(y);
+                for (int e = 0; e < CH; ++e) {
+                    float f[8];
+                    norm8<BF16>(x[e], __ldg(w + 32 * e), r, f);
+                    x[e] = pack8<BF16>(f);
                 }
             }
+            uint4* dst = reinterpret_cast<uint4*>(p.cache + slot * ROW) + lane;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) dst[lane + 32 * i] = v[i];
+            for (int e = 0; e < CH; ++e) dst[32 * e] = x[e];
             continue;
         }
-        const int rr = (gr - 1) * 8 + (lane >> 2);  // 0: the key part, 1 ..: query head rr - 1
-        if (rr >= rows || (rr == 0 && slot < 0)) continue;
-        const uint16_t* src = rr == 0 ? p.kv + t * p.kv_stride + DL
-                                      : p.q_pe + t * p.pe_token_stride + (int64_t)(rr - 1) * p.pe_head_stride;
+        if (!mine || (rr == 0 && slot < 0)) continue;
         uint16_t* dst = rr == 0 ? p.cache + slot * ROW + DL : p.q + (t * p.n_heads + rr - 1) * ROW + DL;
-        const uint4 lo = reinterpret_cast<const uint4*>(src)[c], hi = reinterpret_cast<const uint4*>(src)[c + 4];
         const float* cs = p.cos_sin + pos * 64;
         float a[8], b[8];
-        unpack8<BF16>(lo, a);
-        unpack8<BF16>(hi, b);
+        unpack8<BF16>(x[0], a);
+        unpack8<BF16>(x[1], b);
         if (!p.interleaved) {
             turn8(a, b, cs, 8 * c, 32);
         } else {
