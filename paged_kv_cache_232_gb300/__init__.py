@@ -336,37 +336,52 @@ def pa_prefill_chunk(out, q, k_cache, v_cache, block_tables, query_start_loc, se
     _check(st, "pa_prefill_chunk_small_m" if small_m else "pa_prefill_chunk")
 
 
-def _on_current(*tensors) -> int:
-    """The library launches on the current device: every tensor has to be on it."""
-    if not tensors[0].is_cuda:
+# The calls below run for microseconds on the GPU, so their checks are one pass over the tensors.
+
+
+def _device(t) -> int:
+    """Index of the device a call runs on: t's, which has to be the current one (the library launches there)."""
+    if not t.is_cuda:
         raise ValueError("every tensor must be a CUDA tensor")
     dev = _torch().cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     return dev
 
 
-def _rows(t, name: str, dtype, shape):
-    """Pointer and token stride (elements) of t [N, heads, dim], whose heads and columns are contiguous."""
+def _refuse(t, name: str, dtype, shape, dev, what: str):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev} like the other tensors, got {t.device}")
+    raise ValueError(f"{name} must be {what}")
+
+
+def _rows(t, name: str, dtype, shape, dev):
+    """Pointer and token stride (elements) of t [N, heads, dim], whose heads and columns are contiguous."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev, "")
     n, h, d = shape
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
-        raise ValueError(f"{name} must be contiguous within a token")
-    return t.data_ptr(), (s[0] if n > 1 else h * d)
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        _refuse(t, name, dtype, shape, dev, "contiguous within a token")
+    return t.data_ptr(), (s0 if n > 1 else h * d)
 
 
-def _flat(t, name: str, dtype, shape):
+def _flat(t, name: str, dtype, shape, dev):
     """Pointer of a contiguous tensor of this type and shape."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev, "contiguous")
     return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """cudaStream_t of the given stream, or of the device's current one."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream, dev)
 
 
 def pa_norm_rope_reshape_and_cache(q, key, value, q_weight, k_weight, k_cache, v_cache, slot_mapping, positions,
@@ -380,16 +395,17 @@ def pa_norm_rope_reshape_and_cache(q, key, value, q_weight, k_weight, k_cache, v
     nb, bs, hkv, d = k_cache.shape
     n, hq, _ = q.shape
     mp = cos_sin.shape[0]
-    qp, qs = _rows(q, "q", ty, (n, hq, d))
-    op, os_ = (qp, qs) if q_out is None else _rows(q_out, "q_out", ty, (n, hq, d))
-    kp, ks = _rows(key, "key", ty, (n, hkv, d))
-    vp, vs = _rows(value, "value", ty, (n, hkv, d))
-    args = (op, os_, qp, qs, kp, ks, vp, vs, _flat(q_weight, "q_weight", ty, (d,)), _flat(k_weight, "k_weight", ty, (d,)),
-            eps, _flat(k_cache, "k_cache", ty, (nb, bs, hkv, d)), _flat(v_cache, "v_cache", ty, (nb, bs, hkv, d)),
-            _flat(slot_mapping, "slot_mapping", torch.int64, (n,)), _flat(positions, "positions", torch.int64, (n,)),
-            _flat(cos_sin, "cos_sin", torch.float32, (mp, d)), n, hq, hkv, d, bs, nb, mp, dt)
-    dev = _on_current(q, key, value, q_weight, k_weight, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
-    _check(load().pa_norm_rope_reshape_and_cache(*args, _stream(stream, dev)), "pa_norm_rope_reshape_and_cache")
+    dev = _device(q)
+    qp, qs = _rows(q, "q", ty, (n, hq, d), dev)
+    op, os_ = (qp, qs) if q_out is None else _rows(q_out, "q_out", ty, (n, hq, d), dev)
+    kp, ks = _rows(key, "key", ty, (n, hkv, d), dev)
+    vp, vs = _rows(value, "value", ty, (n, hkv, d), dev)
+    _check(load().pa_norm_rope_reshape_and_cache(
+        op, os_, qp, qs, kp, ks, vp, vs, _flat(q_weight, "q_weight", ty, (d,), dev),
+        _flat(k_weight, "k_weight", ty, (d,), dev), eps, _flat(k_cache, "k_cache", ty, (nb, bs, hkv, d), dev),
+        _flat(v_cache, "v_cache", ty, (nb, bs, hkv, d), dev), _flat(slot_mapping, "slot_mapping", torch.int64, (n,), dev),
+        _flat(positions, "positions", torch.int64, (n,), dev), _flat(cos_sin, "cos_sin", torch.float32, (mp, d), dev),
+        n, hq, hkv, d, bs, nb, mp, dt, _raw_stream(stream, dev)), "pa_norm_rope_reshape_and_cache")
 
 
 LATENT_ROPE_DIM = 64
@@ -413,7 +429,8 @@ def pa_latent_rope_and_cache(kv, latent_cache, slot_mapping, positions, cos_sin,
     ty, dt = kv.dtype, _dtype_code(kv)
     nb, bs, dl = _latent_dims(latent_cache)
     n, row, mp = kv.shape[0], dl + LATENT_ROPE_DIM, cos_sin.shape[0]
-    if kv.shape != (n, row) or kv.dim() != 2 or kv.stride(1) != 1:
+    dev = _device(kv)
+    if kv.shape != (n, row) or kv.stride(1) != 1:
         raise ValueError("kv must be [N, latent_dim + 64] with contiguous rows")
     if (q_pe is None) != (q is None):
         raise ValueError("q_pe and q come together")
@@ -421,19 +438,21 @@ def pa_latent_rope_and_cache(kv, latent_cache, slot_mapping, positions, cos_sin,
     h = pts = phs = 0
     if q_pe is not None:
         h = q_pe.shape[1]
-        if q_pe.shape != (n, h, LATENT_ROPE_DIM) or q_pe.dtype != ty or q_pe.stride(2) != 1:
-            raise ValueError("q_pe must be [N, H, 64] of kv's type with contiguous columns")
-        qp, pep = _flat(q, "q", ty, (n, h, row)), q_pe.data_ptr()
-        phs = q_pe.stride(1) if h > 1 else LATENT_ROPE_DIM
-        pts = q_pe.stride(0) if n > 1 else (h - 1) * phs + LATENT_ROPE_DIM
-    args = (qp, pep, pts, phs, kv.data_ptr(), kv.stride(0) if n > 1 else row,
-            None if weight is None else _flat(weight, "weight", ty, (dl,)), eps,
-            _flat(latent_cache, "latent_cache", ty, (nb, bs, row)),
-            _flat(slot_mapping, "slot_mapping", torch.int64, (n,)), _flat(positions, "positions", torch.int64, (n,)),
-            _flat(cos_sin, "cos_sin", torch.float32, (mp, LATENT_ROPE_DIM)), n, h, dl, LATENT_ROPE_DIM, bs, nb, mp,
-            1 if interleaved else 0, dt)
-    dev = _on_current(kv, latent_cache, slot_mapping, positions, cos_sin, weight, q_pe, q)
-    _check(load().pa_latent_rope_and_cache(*args, _stream(stream, dev)), "pa_latent_rope_and_cache")
+        pts, phs, one = q_pe.stride()
+        if q_pe.dtype != ty or q_pe.shape != (n, h, LATENT_ROPE_DIM) or one != 1 or q_pe.get_device() != dev:
+            _refuse(q_pe, "q_pe", ty, (n, h, LATENT_ROPE_DIM), dev, "contiguous in its columns")
+        qp, pep = _flat(q, "q", ty, (n, h, row), dev), q_pe.data_ptr()
+        if h == 1:
+            phs = LATENT_ROPE_DIM
+        if n == 1:
+            pts = (h - 1) * phs + LATENT_ROPE_DIM
+    _check(load().pa_latent_rope_and_cache(
+        qp, pep, pts, phs, kv.data_ptr(), kv.stride(0) if n > 1 else row,
+        None if weight is None else _flat(weight, "weight", ty, (dl,), dev), eps,
+        _flat(latent_cache, "latent_cache", ty, (nb, bs, row), dev),
+        _flat(slot_mapping, "slot_mapping", torch.int64, (n,), dev), _flat(positions, "positions", torch.int64, (n,), dev),
+        _flat(cos_sin, "cos_sin", torch.float32, (mp, LATENT_ROPE_DIM), dev), n, h, dl, LATENT_ROPE_DIM, bs, nb, mp,
+        1 if interleaved else 0, dt, _raw_stream(stream, dev)), "pa_latent_rope_and_cache")
 
 
 def pa_latent_workspace_size(n_heads: int, latent_dim: int, max_q_len: int = 1) -> int:
@@ -448,15 +467,14 @@ def _latent_common(out, q, latent_cache, block_tables, lens, workspace):
     if k != dl + LATENT_ROPE_DIM:
         raise ValueError("q must be [rows, H, latent_dim + 64]")
     n, mb = block_tables.shape
-    args = (_flat(out, "out", ty, (rows, h, dl)), _flat(q, "q", ty, (rows, h, k)),
-            _flat(latent_cache, "latent_cache", ty, (nb, bs, k)),
-            _flat(block_tables, "block_tables", torch.int32, (n, mb)), mb)
-    lp = _flat(lens, "lengths", torch.int32, (n,))
+    dev = _device(q)
     wp = wb = 0
     if workspace is not None:
-        wp, wb = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    dev = _on_current(q, out, latent_cache, block_tables, lens, workspace)
-    return args, lp, rows, n, (h, dl, LATENT_ROPE_DIM, bs, nb), dt, wp, wb, dev
+        wp, wb = _flat(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.nbytes
+    return ((_flat(out, "out", ty, (rows, h, dl), dev), _flat(q, "q", ty, (rows, h, k), dev),
+             _flat(latent_cache, "latent_cache", ty, (nb, bs, k), dev),
+             _flat(block_tables, "block_tables", torch.int32, (n, mb), dev), mb),
+            _flat(lens, "lengths", torch.int32, (n,), dev), rows, n, (h, dl, LATENT_ROPE_DIM, bs, nb), dt, wp, wb, dev)
 
 
 def pa_latent_decode(out, q, latent_cache, block_tables, context_lens, scale: float, workspace, stream=None) -> None:
@@ -465,7 +483,8 @@ def pa_latent_decode(out, q, latent_cache, block_tables, context_lens, scale: fl
     args, lp, rows, n, dims, dt, wp, wb, dev = _latent_common(out, q, latent_cache, block_tables, context_lens, workspace)
     if n != rows:
         raise ValueError("block_tables and context_lens must hold one row per row of q")
-    _check(load().pa_latent_decode(*args, lp, rows, *dims, scale, dt, wp, wb, _stream(stream, dev)), "pa_latent_decode")
+    _check(load().pa_latent_decode(*args, lp, rows, *dims, scale, dt, wp, wb, _raw_stream(stream, dev)),
+           "pa_latent_decode")
 
 
 def pa_latent_prefill_chunk(out, q, latent_cache, block_tables, query_start_loc, seq_lens, max_q_len: int, scale: float,
@@ -474,10 +493,9 @@ def pa_latent_prefill_chunk(out, q, latent_cache, block_tables, query_start_loc,
     [T, H, DL], q [T, H, DL + 64], chunk c the rows query_start_loc[c] .. query_start_loc[c + 1];
     workspace of at least pa_latent_workspace_size(H, DL, max_q_len) bytes."""
     args, lp, rows, n, dims, dt, wp, wb, dev = _latent_common(out, q, latent_cache, block_tables, seq_lens, workspace)
-    loc = _flat(query_start_loc, "query_start_loc", _torch().int32, (n + 1,))
-    _on_current(q, query_start_loc)
+    loc = _flat(query_start_loc, "query_start_loc", _torch().int32, (n + 1,), dev)
     _check(load().pa_latent_prefill_chunk(*args, loc, lp, n, max_q_len, rows, *dims, scale, dt, wp, wb,
-                                          _stream(stream, dev)), "pa_latent_prefill_chunk")
+                                          _raw_stream(stream, dev)), "pa_latent_prefill_chunk")
 
 
 def pa_device_errors(clear: bool = True) -> int:

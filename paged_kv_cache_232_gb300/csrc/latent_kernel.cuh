@@ -818,6 +818,8 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p,
     __shared__ int row_end[lat::MAX_CTAS];   // rows of the cut units up to and with range b's
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the next kernel of the step may start its launch; it waits for this grid before reading anything
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int4 d = make_int4(0, 0, 0, 0);
     if (tid < ranges) d = __ldcg(p.desc + tid);
     const bool many = __syncthreads_or(d.x > kFew);
@@ -862,16 +864,18 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p,
                 l = ml.y;
             }
             float4 a[CV] = {};
-            // the partials, loaded before their weights are known
-            float4 v[2][CV];
-            auto fetch = [&](int k, float4 (&x)[CV]) {
-                const int slot = k == 0 ? u.w : 2 * (b + k);
+            float4 v[4][CV];
+            auto fetch4 = [&](int k0) {
 #pragma unroll
-                for (int c = 0; c < CV; ++c)
-                    x[c] = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * NR + row) * DL) + lane + 32 * c);
+                for (int k = 0; k < 4; ++k) {
+                    if (k0 + k >= u.x) break;
+                    const int slot = k0 + k == 0 ? u.w : 2 * (b + k0 + k);
+#pragma unroll
+                    for (int c = 0; c < CV; ++c)
+                        v[k][c] = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * NR + row) * DL) + lane + 32 * c);
+                }
             };
-            fetch(0, v[0]);
-            fetch(1, v[1]);
+            fetch4(0);  // in flight before their weights are known
             float mx = m;
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -881,22 +885,21 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p,
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
             lw = __shfl_sync(0xffffffffu, lw, 0);
-            auto add = [&](int k, const float4 (&x)[CV]) {
-                const float f = __shfl_sync(0xffffffffu, w, k);
-                if (f == 0.f) return;
+            for (int k0 = 0; k0 < u.x; k0 += 4) {
+                if (k0 > 0) fetch4(k0);
 #pragma unroll
-                for (int c = 0; c < CV; ++c) {
-                    a[c].x = fmaf(x[c].x, f, a[c].x);
-                    a[c].y = fmaf(x[c].y, f, a[c].y);
-                    a[c].z = fmaf(x[c].z, f, a[c].z);
-                    a[c].w = fmaf(x[c].w, f, a[c].w);
+                for (int k = 0; k < 4; ++k) {
+                    if (k0 + k >= u.x) break;
+                    const float f = __shfl_sync(0xffffffffu, w, k0 + k);
+                    if (f == 0.f) continue;
+#pragma unroll
+                    for (int c = 0; c < CV; ++c) {
+                        a[c].x = fmaf(v[k][c].x, f, a[c].x);
+                        a[c].y = fmaf(v[k][c].y, f, a[c].y);
+                        a[c].z = fmaf(v[k][c].z, f, a[c].z);
+                        a[c].w = fmaf(v[k][c].w, f, a[c].w);
+                    }
                 }
-            };
-            add(0, v[0]);
-            add(1, v[1]);
-            for (int k = 2; k < u.x; ++k) {
-                fetch(k, v[0]);
-                add(k, v[0]);
             }
             const float inv = lw != 0.f ? 1.f / lw : 0.f;
             uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(u.z + row) * DL);
