@@ -429,8 +429,8 @@ int pa_latent_rope_and_cache(void* q, const void* q_pe, int64_t q_pe_token_strid
                              int64_t num_blocks, int64_t max_position, int interleaved, int dtype, void* stream);
 
 /*
- * Workspace bytes of pa_latent_decode (max_q_len 1) and pa_latent_prefill_chunk: a descriptor and
- * two fp32 partials for each of up to PA_LATENT_MAX_CTAS CTAs, whatever the batch and the lengths.
+ * Workspace bytes of pa_latent_decode (max_q_len 1) and pa_latent_prefill_chunk: two descriptors
+ * and two fp32 partials for each of up to PA_LATENT_MAX_CTAS CTAs, whatever the batch and the lengths.
  * 0 for shapes they do not support.  Caller-owned; nothing in it needs to start at any value.  Calls
  * that can run at the same time on the GPU must not share one.
  */

@@ -949,7 +949,7 @@ static LatentWs latent_ws(int unit_rows, int latent_dim) {
     const size_t slots = 2 * (size_t)PA_LATENT_MAX_CTAS / (unit_rows == 128 ? 2 : 1);  // two a range
     LatentWs w;
     w.desc_off = 0;
-    w.ml_off = align256(PA_LATENT_MAX_CTAS * sizeof(int4));
+    w.ml_off = align256(2 * PA_LATENT_MAX_CTAS * sizeof(int4));
     w.o_off = w.ml_off + align256(slots * unit_rows * 2 * sizeof(float));
     w.total = w.o_off + slots * unit_rows * latent_dim * sizeof(float);
     return w;
@@ -1015,7 +1015,6 @@ static int latent_impl(void* out, const void* q, const void* latent_cache, const
     p.tile_log2 = rows == 128 ? 7 : 6;
     p.unit_cost = rows == 128 ? 2 : 1;
     p.min_tiles = p.unit_cost + 2;
-    p.stream_once = n_heads * (int64_t)max_q_len <= 128 ? 1 : 0;  // one unit a sequence
     p.qk_scale_log2 = scale * 1.4426950408889634f;
     p.desc = reinterpret_cast<int4*>(base + w.desc_off);
     p.part_ml = reinterpret_cast<float*>(base + w.ml_off);

@@ -1,6 +1,4 @@
 // latent.cu -- instantiations of the latent-cache attention kernels.
-#include <algorithm>
-
 #include "latent_pair_kernel.cuh"
 
 namespace pa {
@@ -22,11 +20,17 @@ static cudaError_t launch_latent_t(const LatentParams& p, const CUtensorMap& tmC
         e = launch_dependent(kern, (unsigned)ctas, C::THREADS, C::SMEM_BYTES, st, p, tmC, tmQ);
     }
     if (e != cudaSuccess) return e;
-    // the merge: up to a block an SM, a warp a row of the units that may be cut (one a range at most)
-    const int ranges = NR == 128 ? ctas / 2 : ctas;
-    const int64_t rows = std::min<int64_t>((int64_t)ranges * NR, (int64_t)p.total_q * p.n_heads);
-    const int blocks = (int)std::min<int64_t>(ctas, rows);
-    return launch_dependent(latent_merge_kernel<BF16, DL, NR>, (unsigned)blocks, 512, 0, st, p, ranges);
+    // the merge: a block for 16 query rows of each range
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(NR == 128 ? ctas / 2 : ctas), NR / 16);
+    cfg.blockDim = dim3(lat::MERGE_THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<BF16, DL, NR>, p);
 }
 
 template <bool BF16, int DL>

@@ -49,7 +49,9 @@ constexpr int PAIR = 2 * SLAB;
 // warps 0..3: softmax; then the two MMA issuers, the Q loader, and the cache row loaders (one a pair slot of a tile, one
 // for the rotary slot)
 constexpr int SOFTMAX_WARPS = 4, QK_WARP = 4, PV_WARP = 5, Q_WARP = 6, TMA_WARP = 7;
-constexpr int MAX_CTAS = 512;           // of the split: latent_merge_kernel gives every partial a thread
+constexpr int MERGE_THREADS = 256;
+constexpr int MAX_CTAS = 256;           // of the split: latent_merge_kernel gives every partial a thread
+static_assert(MAX_CTAS <= MERGE_THREADS && PA_LATENT_MAX_CTAS <= MAX_CTAS, "partials of a unit");
 
 template <int DL, int NR>
 struct Cfg {
@@ -359,8 +361,16 @@ struct Segment {
     int ctx, keys;          // token jt of the block sees keys <= ctx + j tb + jt; the unit's tokens see [0, keys)
     int rows;               // query rows of the unit
     int row0;               // the first one's row of q and out, [total_q * n_heads]
-    int parts;              // where the unit starts here and goes on behind the range: ranges it spans; else 0
+    int parts, back;        // ranges the unit's tiles span (0: this one alone), and how many of them are before this one
 };
+
+// A cut unit's partials: the range it starts in writes slot 2 range + 1, those behind it slot 2 range.
+__device__ __forceinline__ int slot_of(const Segment& g, int range) { return 2 * range + (g.tile == 0 ? 1 : 0); }
+
+// What the merge needs to know of a cut unit, from each range it spans
+__device__ __forceinline__ int4 cut_of(const Segment& g, int range) {
+    return make_int4(g.parts, g.rows, g.row0, range - g.back);
+}
 
 template <typename F>
 __device__ __forceinline__ void for_each_segment(const LatentParams& p, const Start& s, F&& f) {
@@ -377,9 +387,9 @@ __device__ __forceinline__ void for_each_segment(const LatentParams& p, const St
         left -= n;
         g.tile = max(0, at - p.unit_cost);
         g.n = max(0, at + n - p.unit_cost) - g.tile;
-        // (left is 0 when the unit goes on: what is behind this range starts a full range further)
-        const int rest = g.tiles - g.tile - g.n;
-        g.parts = (g.tile == 0 && rest > 0) ? 1 + (rest + s.per - 1) / s.per : 0;
+        const int rest = g.tiles - g.tile - g.n;  // behind this range, and g.tile before it: whole ranges but for the ends
+        g.back = (g.tile + s.per - 1) / s.per;
+        g.parts = (g.tile > 0 || rest > 0) ? g.back + 1 + (rest + s.per - 1) / s.per : 0;
         g.ctx = k.kv_len - k.q_len;
         g.rows = min(p.tb, k.q_len - j * p.tb) * p.n_heads;
         g.row0 = (k.q0 + j * p.tb) * p.n_heads;
@@ -461,9 +471,9 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         const float sc = p.qk_scale_log2;
         int i = 0;             // tile number over the CTA's range
         int pv_seen = 0;       // PV_DONE phases this warp has waited for
-        int seg = 0, pair0 = 0;  // segment number; ring position of the tile's first pair slot
+        int pair0 = 0;         // ring position of the tile's first pair slot
         bool ok = true;
-        int desc_parts = 0, desc_rows = 0, desc_row0 = 0, desc_slot = 0;
+        int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
         auto wait_pv = [&](int n) {  // PVs of tiles 0 .. n - 1 complete
             while (pv_seen < n) {
                 ok = warp_wait(bar(C::PV_DONE), (uint32_t)(pv_seen & 1), p.err) && ok;
@@ -575,8 +585,8 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 if (lane == 0) mbar_arrive(bar(C::P_FULL));
             }
             // the segment's end: O^T / l, or the partial
-            const bool whole = g.tile == 0 && g.n == g.tiles;
-            const int slot = 2 * (int)blockIdx.x + (seg == 0 ? 0 : 1);
+            const bool whole = g.parts == 0;
+            const int slot = slot_of(g, (int)blockIdx.x);
             if (r >= 0 && r < NR) {
                 inv_s[r] = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
                 if (!whole && valid) {
@@ -627,23 +637,21 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                         if (h0 + e < g.rows) dst[(size_t)e * DL] = __uint_as_float(o[e]);
                 }
             }
-            if (g.parts) {
-                desc_parts = g.parts;
-                desc_rows = g.rows;
-                desc_row0 = g.row0;
-                desc_slot = slot;
-            }
-            ++seg;
+            if (!whole) (g.tile == 0 ? begins : goes_on) = cut_of(g, (int)blockIdx.x);
             return true;
         });
-        if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(ok ? desc_parts : 0, desc_rows, desc_row0, desc_slot);
+        if (threadIdx.x == 0) {
+            if (!ok) begins = goes_on = make_int4(0, 0, 0, 0);
+            p.desc[blockIdx.x] = begins;
+            p.desc[gridDim.x + blockIdx.x] = goes_on;
+        }
     } else if (warp >= TMA_WARP) {
         // ------------------------------------------------------------ cache rows into the rings.  One warp a
         // pair slot of the tile and one for the rotary slot: a box of 16 rows moves 2 KB, so at small cache
         // blocks the issue of boxes, not the copies, would set the pace of a single warp (GB300: 36 boxes a
         // tile took one warp ~4000 cycles).  An elected lane issues from warp-uniform operands, as for the MMAs
         if (lane == 0) tma_prefetch_desc(&tmC);
-        const uint64_t pol = p.stream_once ? l2_policy_evict_first() : l2_policy_evict_last();
+        const uint64_t pol = l2_policy_evict_first();  // one unit a sequence: every row is read once
         const int b = warp - TMA_WARP;                          // pair of the tile; NB: the rotary slot
         const bool rope = b == NB;
         const int br = min(p.block_size, TK), nbox = TK / br;   // rows per box, boxes per slab
@@ -803,171 +811,140 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
 }
 
 // Joins the partials of the units that the ranges' ends cut: out = sum_k 2^(m_k - max m) o_k / sum_k 2^(m_k - max m) l_k.
-// The rows of all cut units are dealt out evenly.  With few partials a row (the usual cut: two) a warp takes a row,
-// DL / 32 columns a lane; with many (few long contexts) a block takes a row, its groups of DL / 4 threads every KG-th
-// partial each, their sums added in order.  Fixed orders: the same inputs give the same bits.
+// A unit of few partials (the usual cut: two) is joined by the blocks of the range it starts in, a warp a row, DL / 32
+// columns a lane.  One of many (few long contexts) by the blocks of all the ranges it spans, a block a row: its
+// groups of DL / 4 threads every KG-th partial each, their sums added in order.  Fixed orders: the same inputs give
+// the same bits.
 template <bool BF16, int DL, int NR>
-__global__ void __launch_bounds__(512) latent_merge_kernel(const LatentParams p, int ranges) {
+__global__ void __launch_bounds__(lat::MERGE_THREADS) latent_merge_kernel(const LatentParams p) {
     using F = F16x2<BF16>;
-    constexpr int TG = DL / 4, KG = 512 / TG, CV = DL / 128;
+    constexpr int TH = lat::MERGE_THREADS, NW = TH / 32, TG = DL / 4, KG = TH / TG, CV = DL / 128;
     constexpr int kFew = 8;
-    __shared__ float4 acc[512];
+    __shared__ float4 acc[TH];
     __shared__ float wt[lat::MAX_CTAS];
-    __shared__ float red[16], l_s[1];
-    __shared__ int4 desc[lat::MAX_CTAS];
-    __shared__ int row_end[lat::MAX_CTAS];   // rows of the cut units up to and with range b's
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ float red[NW], l_s[1];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, range = (int)blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // the next kernel of the step may start its launch; it waits for this grid before reading anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int4 d = make_int4(0, 0, 0, 0);
-    if (tid < ranges) d = __ldcg(p.desc + tid);
-    const bool many = __syncthreads_or(d.x > kFew);
-    {
-        const int rows = d.x ? d.y : 0;
-        int incl = rows;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        int* sums = reinterpret_cast<int*>(red);
-        if (lane == 31) sums[warp] = incl;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) incl += sums[w];
-        if (tid < ranges) {
-            row_end[tid] = incl;
-            desc[tid] = d;
-        }
-        __syncthreads();
-    }
-    const int total = ranges > 0 ? row_end[ranges - 1] : 0;
-    auto unit_of = [&](int item) {  // the range whose cut unit holds row `item`
-        int lo = 0, hi = ranges - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (row_end[mid] > item) hi = mid;
-            else lo = mid + 1;
-        }
-        return lo;
-    };
-    if (!many) {
-        for (int item = (int)blockIdx.x * 16 + warp; item < total; item += (int)gridDim.x * 16) {
-            const int b = unit_of(item);
-            const int4 u = desc[b];
-            const int row = item - (row_end[b] - u.y);
-            const int mine = lane == 0 ? u.w : 2 * (b + lane);  // the slot of partial `lane`
-            float m = -INFINITY, l = 0.f;
-            if (lane < u.x) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)mine * NR + row);
-                m = ml.x;
-                l = ml.y;
-            }
-            float4 a[CV] = {};
-            float4 v[4][CV];
-            auto fetch4 = [&](int k0) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k0 + k >= u.x) break;
-                    const int slot = k0 + k == 0 ? u.w : 2 * (b + k0 + k);
-#pragma unroll
-                    for (int c = 0; c < CV; ++c)
-                        v[k][c] = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * NR + row) * DL) + lane + 32 * c);
-                }
-            };
-            fetch4(0);  // in flight before their weights are known
-            float mx = m;
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = __shfl_sync(0xffffffffu, mx, 0);
-            const float w = m == -INFINITY ? 0.f : ex2(m - mx);
-            float lw = l != 0.f ? l * w : 0.f;
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-            lw = __shfl_sync(0xffffffffu, lw, 0);
-            for (int k0 = 0; k0 < u.x; k0 += 4) {
-                if (k0 > 0) fetch4(k0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k0 + k >= u.x) break;
-                    const float f = __shfl_sync(0xffffffffu, w, k0 + k);
-                    if (f == 0.f) continue;
-#pragma unroll
-                    for (int c = 0; c < CV; ++c) {
-                        a[c].x = fmaf(v[k][c].x, f, a[c].x);
-                        a[c].y = fmaf(v[k][c].y, f, a[c].y);
-                        a[c].z = fmaf(v[k][c].z, f, a[c].z);
-                        a[c].w = fmaf(v[k][c].w, f, a[c].w);
-                    }
-                }
-            }
-            const float inv = lw != 0.f ? 1.f / lw : 0.f;
-            uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(u.z + row) * DL);
-#pragma unroll
-            for (int c = 0; c < CV; ++c)
-                dst[lane + 32 * c] = make_uint2(F::pack_rn(a[c].x * inv, a[c].y * inv), F::pack_rn(a[c].z * inv, a[c].w * inv));
-        }
-        return;
-    }
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        const int b = unit_of(item);
-        const int4 u = desc[b];
-        const int row = item - (row_end[b] - u.y), parts = u.x;
-        auto slot_of = [&](int k) { return k == 0 ? u.w : 2 * (b + k); };
+    const int4 cut[2] = {__ldcg(p.desc + range), __ldcg(p.desc + gridDim.x + range)};
+    const int4 few = cut[0].x <= kFew ? cut[0] : make_int4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int row = (int)blockIdx.y * 16 + warp; row < min(few.y, ((int)blockIdx.y + 1) * 16); row += NW) {
+        const int4 u = few;
         float m = -INFINITY, l = 0.f;
-        if (tid < parts) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot_of(tid) * NR + row);
+        if (lane < u.x) {
+            const int slot = 2 * (range + lane) + (lane == 0);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot * NR + row);
             m = ml.x;
             l = ml.y;
         }
+        float4 a[CV] = {};
+        float4 v[4][CV];
+        auto fetch4 = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= u.x) break;
+                const int slot = 2 * (range + k0 + k) + (k0 + k == 0);
+#pragma unroll
+                for (int c = 0; c < CV; ++c)
+                    v[k][c] = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * NR + row) * DL) + lane + 32 * c);
+            }
+        };
+        fetch4(0);  // in flight before their weights are known
         float mx = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 0) red[warp] = mx;
-        __syncthreads();
-        mx = red[0];
-        for (int w = 1; w < 16; ++w) mx = fmaxf(mx, red[w]);
+        for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = __shfl_sync(0xffffffffu, mx, 0);
         const float w = m == -INFINITY ? 0.f : ex2(m - mx);
-        if (tid < parts) wt[tid] = w;
-        float lw = tid < parts && l != 0.f ? l * w : 0.f;
+        float lw = l != 0.f ? l * w : 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-        __syncthreads();
-        if (lane == 0) red[warp] = lw;
-        __syncthreads();
-        if (tid == 0) {
-            float t = 0.f;
-            for (int k = 0; k < 16; ++k) t += red[k];
-            l_s[0] = t;
+        for (int o = 4; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+        lw = __shfl_sync(0xffffffffu, lw, 0);
+        for (int k0 = 0; k0 < u.x; k0 += 4) {
+            if (k0 > 0) fetch4(k0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= u.x) break;
+                const float f = __shfl_sync(0xffffffffu, w, k0 + k);
+                if (f == 0.f) continue;
+#pragma unroll
+                for (int c = 0; c < CV; ++c) {
+                    a[c].x = fmaf(v[k][c].x, f, a[c].x);
+                    a[c].y = fmaf(v[k][c].y, f, a[c].y);
+                    a[c].z = fmaf(v[k][c].z, f, a[c].z);
+                    a[c].w = fmaf(v[k][c].w, f, a[c].w);
+                }
+            }
         }
-        const int gidx = tid / TG, t = tid % TG;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float inv = lw != 0.f ? 1.f / lw : 0.f;
+        uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(u.z + row) * DL);
+#pragma unroll
+        for (int c = 0; c < CV; ++c)
+            dst[lane + 32 * c] = make_uint2(F::pack_rn(a[c].x * inv, a[c].y * inv), F::pack_rn(a[c].z * inv, a[c].w * inv));
+    }
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int4 u = which == 0 ? cut[0] : cut[1];
+        const int parts = u.x, b = u.w;
+        if (parts <= kFew) continue;
+        auto slot_at = [&](int k) { return 2 * (b + k) + (k == 0); };
+        for (int row = (range - b) * (int)gridDim.y + (int)blockIdx.y; row < u.y; row += parts * (int)gridDim.y) {
+            float m = -INFINITY, l = 0.f;
+            if (tid < parts) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot_at(tid) * NR + row);
+                m = ml.x;
+                l = ml.y;
+            }
+            float mx = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane == 0) red[warp] = mx;
+            __syncthreads();
+            mx = red[0];
+            for (int w = 1; w < NW; ++w) mx = fmaxf(mx, red[w]);
+            const float w = m == -INFINITY ? 0.f : ex2(m - mx);
+            if (tid < parts) wt[tid] = w;
+            float lw = tid < parts && l != 0.f ? l * w : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+            __syncthreads();
+            if (lane == 0) red[warp] = lw;
+            __syncthreads();
+            if (tid == 0) {
+                float t = 0.f;
+                for (int k = 0; k < NW; ++k) t += red[k];
+                l_s[0] = t;
+            }
+            const int gidx = tid / TG, t = tid % TG;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int k = gidx; k < parts; k += KG) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_of(k) * NR + row) * DL) + t);
-            const float f = wt[k];
-            if (f != 0.f) {
-                a.x = fmaf(v.x, f, a.x);
-                a.y = fmaf(v.y, f, a.y);
-                a.z = fmaf(v.z, f, a.z);
-                a.w = fmaf(v.w, f, a.w);
+            for (int k = gidx; k < parts; k += KG) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_at(k) * NR + row) * DL) + t);
+                const float f = wt[k];
+                if (f != 0.f) {
+                    a.x = fmaf(v.x, f, a.x);
+                    a.y = fmaf(v.y, f, a.y);
+                    a.z = fmaf(v.z, f, a.z);
+                    a.w = fmaf(v.w, f, a.w);
+                }
             }
-        }
-        acc[tid] = a;
-        __syncthreads();
-        if (tid < TG) {
-            for (int k = 1; k < KG; ++k) {
-                const float4 v = acc[k * TG + tid];
-                a.x += v.x;
-                a.y += v.y;
-                a.z += v.z;
-                a.w += v.w;
+            acc[tid] = a;
+            __syncthreads();
+            if (tid < TG) {
+                for (int k = 1; k < KG; ++k) {
+                    const float4 v = acc[k * TG + tid];
+                    a.x += v.x;
+                    a.y += v.y;
+                    a.z += v.z;
+                    a.w += v.w;
+                }
+                const float lt = l_s[0], inv = lt != 0.f ? 1.f / lt : 0.f;
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(u.z + row) * DL + 4 * tid) =
+                    make_uint2(F::pack_rn(a.x * inv, a.y * inv), F::pack_rn(a.z * inv, a.w * inv));
             }
-            const float lt = l_s[0], inv = lt != 0.f ? 1.f / lt : 0.f;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)(u.z + row) * DL + 4 * tid) =
-                make_uint2(F::pack_rn(a.x * inv, a.y * inv), F::pack_rn(a.z * inv, a.w * inv));
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 

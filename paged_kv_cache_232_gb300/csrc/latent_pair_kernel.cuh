@@ -236,7 +236,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         };
         int i = 0, pv_seen = 0, seg = 0;
         bool ok = true;
-        int desc_parts = 0, desc_rows = 0, desc_row0 = 0, desc_slot = 0;
+        int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
         auto wait_pv = [&](int n) {
             while (pv_seen < n) {
                 ok = warp_wait(bar(C::PV_DONE), (uint32_t)(pv_seen & 1), p.err) && ok;
@@ -334,8 +334,8 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                 if (lane == 0) arrive_at(p_full);
             }
             // the segment's end: the rows' sums to the rescale warps of both CTAs, which write the output
-            const bool whole = g.tile == 0 && g.n == g.tiles;
-            const int slot = 2 * range + (seg == 0 ? 0 : 1);
+            const bool whole = g.parts == 0;
+            const int slot = lat::slot_of(g, range);
             softmax_sync();  // (exch: the last tile's maxima have been read)
             exch[part * 64 + hr] = l;
             softmax_sync();
@@ -352,16 +352,15 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     p.part_ml[((size_t)slot * NR + R) * 2 + 1] = lr;
                 }
             }
-            if (g.parts) {
-                desc_parts = g.parts;
-                desc_rows = g.rows;
-                desc_row0 = g.row0;
-                desc_slot = slot;
-            }
+            if (!whole) (g.tile == 0 ? begins : goes_on) = lat::cut_of(g, range);
             ++seg;
             return true;
         });
-        if (threadIdx.x == 0 && rank == 0) p.desc[range] = make_int4(ok ? desc_parts : 0, desc_rows, desc_row0, desc_slot);
+        if (threadIdx.x == 0 && rank == 0) {
+            if (!ok) begins = goes_on = make_int4(0, 0, 0, 0);
+            p.desc[range] = begins;
+            p.desc[ranges + range] = goes_on;
+        }
     } else if (warp < CORR_WARP + 4) {
         // ------------------------------------------------------------ rescale of O^T and the output: lane = latent
         // column.  Commands come from the PV issuer: CMD_END (or'ed flags: which CTAs' rows to rescale by tile parity)
@@ -400,8 +399,8 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                 __syncwarp();
                 if (lane == 0) arrive_at(corr);
             }
-            const bool whole = g.tile == 0 && g.n == g.tiles;
-            const int slot = 2 * range + (seg == 0 ? 0 : 1);
+            const bool whole = g.parts == 0;
+            const int slot = lat::slot_of(g, range);
             i += g.n;
             if (!(ok = warp_wait(bar(C::F_FULL + (seg & 1)), (uint32_t)((seg >> 1) & 1), p.err))) return false;
             if (!(ok = warp_wait(bar(C::PV_DONE), (uint32_t)((i - 1) & 1), p.err))) return false;
@@ -445,7 +444,9 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         // 2 k + 1 of this CTA's 64 tokens, then their rotary part (ROPE_WARP); X_WARP: after a tile's S, this CTA's columns
         // of the peer's tokens
         if (lane == 0) tma_prefetch_desc(&tmC);
-        const uint64_t pol = p.stream_once ? l2_policy_evict_first() : l2_policy_evict_last();
+        // both CTAs read each row's values: evict-first would lose them in between (decode of 128 sequences at 128 heads
+        // 174 us, 167 with this)
+        const uint64_t pol = l2_policy_evict_last();
         const uint32_t el = elect_one();
         const int br = min(p.block_size, 64), nbox = 64 / br;
         const bool extra = warp == X_WARP, rope = warp == ROPE_WARP;

@@ -126,11 +126,11 @@ struct LatentParams {
     int tile_log2;              // log2 of the tokens per tile
     int unit_cost;              // what a unit's start and output cost, in tiles (evens out the ranges)
     int min_tiles;              // least cost of a range
-    int stream_once;            // 1: every cache row is read by one unit (L2 evict-first)
     float qk_scale_log2;
     float* part_o;              // [2 * ranges][NR][DL]
     float* part_ml;             // [2 * ranges][NR][2]: reference (base 2) and exp-sum
-    int4* desc;                 // [ranges]: partials, rows, first row of out, first slot of the unit cut at the range's end
+    int4* desc;                 // [2][ranges]: the units cut at a range's end and at its start (partials, query rows,
+                                // first row of out, range they start in)
 };
 
 // Query rows per unit the kernels are built for: the least that holds `rows`.  16, 32 and 64: one CTA a

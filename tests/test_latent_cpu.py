@@ -79,9 +79,9 @@ def test_latent_attention_refusals(lib):
 
 
 def test_latent_workspace_size():
-    """A descriptor, the exp-sum pairs and the partials of two units a CTA."""
+    """Descriptors, the exp-sum pairs and the partials of two units a CTA."""
     def want(rows, dl):
-        return 160 * 16 + 2 * 160 * rows * 8 + 2 * 160 * rows * dl * 4
+        return 2 * 160 * 16 + 2 * 160 * rows * 8 + 2 * 160 * rows * dl * 4
     size = pa.pa_latent_workspace_size
     assert size(16, 512) == size(1, 512, 5) == want(16, 512)
     assert size(17, 512) == size(16, 512, 2) == want(32, 512)
