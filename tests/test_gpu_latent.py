@@ -204,6 +204,67 @@ def test_chunk_matches_formula(ty, h, dl, bs, ql, ctx):
     assert (out[T:] == 7).all(), "rows behind the last chunk"
 
 
+@pytest.mark.parametrize("ty,h,dl,ql,ctx", [("fp16", 128, 256, 1500, 3), ("bf16", 3, 256, 2100, 40), ("fp16", 30, 512, 1000, 0)])
+def test_chunk_long(ty, h, dl, ql, ctx):
+    """More units in a chunk than threads look for a range's start, units of one token, of 42 and of 4."""
+    g = gen(ql)
+    cache, bt, rows = paged(g, [ql + ctx, 5], 64, dl, TYPES[ty])
+    q = randn(g, (ql + 2, h, dl + ROPE), TYPES[ty])
+    out = torch.full((ql + 2, h, dl), float("nan"), device="cuda", dtype=TYPES[ty])
+    pa.pa_device_errors(clear=True)
+    pa.pa_latent_prefill_chunk(out, q, cache, bt, torch.tensor([0, ql, ql + 2], device="cuda", dtype=torch.int32),
+                               torch.tensor([ql + ctx, 5], device="cuda", dtype=torch.int32), ql, SCALE, _ws(h, dl, ql))
+    assert pa.pa_device_errors(clear=True) == 0
+    for j0 in list(range(0, ql, 97)) + [ql - 1]:      # rows spread over the chunk, each over its own prefix
+        check_attend(out[j0:j0 + 1], q[j0:j0 + 1], rows[0][:ctx + j0 + 1], SCALE, dl, 1, f"token {j0}")
+    check_attend(out[ql:], q[ql:], rows[1], SCALE, dl, 2, "the short chunk")
+    assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("h", [4, 20])
+def test_chunk_many_chunks(h):
+    """More chunks than threads of a CTA, empty ones among them."""
+    n, dl = 900, 256
+    ql = [(5 * i) % 4 for i in range(n)]
+    kl = [a + (13 * i) % 200 for i, a in enumerate(ql)]
+    g = gen(31)
+    cache, bt, rows = paged(g, kl, 16, dl, torch.float16)
+    loc = [sum(ql[:i]) for i in range(n + 1)]
+    q = randn(g, (loc[-1], h, dl + ROPE), torch.float16)
+    out = torch.full((loc[-1], h, dl), float("nan"), device="cuda", dtype=torch.float16)
+    pa.pa_latent_prefill_chunk(out, q, cache, bt, torch.tensor(loc, device="cuda", dtype=torch.int32),
+                               torch.tensor(kl, device="cuda", dtype=torch.int32), 3, SCALE, _ws(h, dl, 3))
+    assert pa.pa_device_errors(clear=True) == 0
+    for c in range(n):
+        if ql[c]:
+            check_attend(out[loc[c]:loc[c + 1]], q[loc[c]:loc[c + 1]], rows[c], SCALE, dl, ql[c], f"chunk {c}")
+
+
+@pytest.mark.parametrize("h", [16, 128])
+def test_cache_past_32_bit_offsets(h):
+    """Blocks whose rows lie past 2^31 elements (and 2^32 bytes) of the cache: written, then attended."""
+    dt, dl, bs = torch.bfloat16, 512, 64
+    nb = (2 ** 31 // ((dl + ROPE) * bs)) + 40
+    cache = torch.empty((nb, bs, dl + ROPE), device="cuda", dtype=dt)
+    L = 300
+    blocks = torch.arange(nb - 1, nb - 7, -1, device="cuda", dtype=torch.int32)
+    bt = blocks[None].contiguous()
+    cache[blocks.long()] = float("nan")
+    g = gen(41)
+    kv = randn(g, (L, dl + ROPE), dt)
+    pos = torch.arange(L, device="cuda")
+    slots = bt[0, pos // bs].long() * bs + pos % bs
+    assert int(slots.min()) * (dl + ROPE) > 2 ** 31
+    pa.pa_device_errors(clear=True)
+    pa.pa_latent_rope_and_cache(kv, cache, slots, torch.zeros_like(pos), table(1, ROPE))     # position 0: unturned
+    rows = cache[bt[0, pos // bs].long(), pos % bs]
+    assert torch.equal(rows, kv)
+    q = randn(g, (1, h, dl + ROPE), dt)
+    out = _decode(q, cache, bt, [L])
+    assert pa.pa_device_errors(clear=True) == 0
+    check_attend(out, q, rows, SCALE, dl, 1, "far blocks")
+
+
 def test_chunk_of_single_tokens_equals_decode():
     """q_len 1 everywhere: the decode call's result bit for bit when the units are the same size."""
     g = gen(8)

@@ -186,3 +186,39 @@ def test_writes_on_a_side_stream():
                                       a["cs"], eps=EPS, q_out=out, stream=st)
     torch.cuda.current_stream().wait_stream(st)
     _check_norm_rope(a, q0, kc0, vc0, out)
+
+
+def test_norm_rope_feeds_decode():
+    """A decode step as a user runs it: norm + rotation + write, then pa_decode over contexts that include the new
+    rows; against attention in 64 bits over the written cache and queries."""
+    g = gen(17)
+    dt, S, hq, hkv, d, bs = torch.bfloat16, 5, 16, 8, 128, 16
+    lens = [40, 1, 129, 16, 300]
+    mb = 20
+    bt = torch.randperm(S * mb, generator=g, device="cuda").to(torch.int32).view(S, mb).contiguous()
+    kc, vc = (randn(g, (S * mb, bs, hkv, d), dt) for _ in range(2))
+    qkv = randn(g, (S, (hq + 2 * hkv) * d), dt)
+    q, k, v = (qkv[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in ((0, hq), (hq, hq + hkv), (hq + hkv, hq + 2 * hkv)))
+    qw, kw = (randn(g, (d,), torch.float32, 0.2).add_(1).to(dt) for _ in range(2))
+    cl = torch.tensor(lens, device="cuda", dtype=torch.int32)
+    pos = cl.long() - 1
+    slots = bt[torch.arange(S, device="cuda"), pos // bs].long() * bs + pos % bs
+    cs = table(400, d)
+    qr, out = torch.empty((S, hq, d), device="cuda", dtype=dt), torch.empty((S, hq, d), device="cuda", dtype=dt)
+    pa.pa_device_errors(clear=True)
+    pa.pa_norm_rope_reshape_and_cache(q, k, v, qw, kw, kc, vc, slots, pos, cs, q_out=qr)
+    ws = torch.empty(max(16, pa.pa_decode_workspace_size(S, hq, d, max(lens))), device="cuda", dtype=torch.uint8)
+    pa.pa_decode(out, qr, kc, vc, bt, cl, max(lens), d ** -0.5, ws)
+    assert pa.pa_device_errors(clear=True) == 0
+    check_write(qr, *turn64(norm64(q, qw, EPS), cs[pos]), "q")
+    kn = kc.flatten(0, 1)[slots]
+    check_write(kn, *turn64(norm64(k, kw, EPS), cs[pos]), "k")
+    for s, L in enumerate(lens):
+        t = torch.arange(L, device="cuda")
+        at = bt[s, t // bs].long() * bs + t % bs
+        kk = kc.flatten(0, 1)[at].double().repeat_interleave(hq // hkv, 1)
+        vv = vc.flatten(0, 1)[at].double().repeat_interleave(hq // hkv, 1)
+        w = torch.softmax(torch.einsum("hd,thd->ht", qr[s].double(), kk) * d ** -0.5, -1)
+        want, mag = torch.einsum("ht,thd->hd", w, vv), torch.einsum("ht,thd->hd", w, vv.abs())
+        # fp32 sums: the allowance pa_decode's own tests use, and one rounding to the type
+        assert ((out[s].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-4 * mag + 1e-6).all(), f"sequence {s}"
