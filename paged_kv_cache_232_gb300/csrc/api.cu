@@ -1000,6 +1000,7 @@ static int latent_impl(void* out, const void* q, const void* latent_cache, const
     char* base = static_cast<char*>(workspace);
     pa::LatentParams p{};
     p.out = out;
+    p.cache = latent_cache;
     p.block_tables = block_tables;
     p.q_loc = q_loc;
     p.kv_lens = kv_lens;
@@ -1015,6 +1016,7 @@ static int latent_impl(void* out, const void* q, const void* latent_cache, const
     p.tile_log2 = rows == 128 ? 7 : 6;
     p.unit_cost = rows == 128 ? 2 : 1;
     p.min_tiles = p.unit_cost + 2;
+    p.stream_once = (int64_t)n_heads * max_q_len <= rows ? 1 : 0;
     p.qk_scale_log2 = scale * 1.4426950408889634f;
     p.desc = reinterpret_cast<int4*>(base + w.desc_off);
     p.part_ml = reinterpret_cast<float*>(base + w.ml_off);

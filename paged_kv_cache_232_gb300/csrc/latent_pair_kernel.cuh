@@ -106,6 +106,10 @@ __device__ __forceinline__ void load_3d(uint32_t el, uint32_t dst, const CUtenso
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy), "r"(el)
         : "memory");
 }
+// rows of the cache into L2 (16-byte aligned, a multiple of 16 bytes)
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
@@ -466,10 +470,10 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                 }
                 return e;
             };
-            int blk = entry(g.tile);
+            int blk = entry(g.tile), nxt = g.n > 1 ? entry(g.tile + 1) : p.num_blocks;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int tile = g.tile + u;
-                const int nxt = u + 1 < g.n ? entry(tile + 1) : 0;
+                const int nxt2 = u + 2 < g.n ? entry(tile + 2) : p.num_blocks;
                 const uint32_t buf = uniform((uint32_t)(i & 1)), dst = sBuf + buf * (NP * PAIR);
                 const int first = (int)uniform((uint32_t)(tile * TK + half * 64));  // of the 64 tokens
                 // boxes of `n` slabs from column c0, `to` onwards, counted on barrier fb
@@ -502,6 +506,13 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                         __syncwarp();
                         if (lane == 0) arrive_at(lead(C::X_FULL + buf));
                     }
+                    // these tokens of the tile after the next into L2 (the two CTAs' loaders cover both halves): its loads
+                    // start once this tile's PV is done, and their DRAM latency would be on the way from tile to tile
+                    if (p.stream_once && nxt2 < p.num_blocks)
+                        prefetch_l2(static_cast<const uint16_t*>(p.cache) +
+                                        ((int64_t)nxt2 * p.block_size + (first + 2 * TK + lane * br) % p.block_size) * (DL + lat::ROPE),
+                                    (uint32_t)(br * (DL + lat::ROPE) * 2));
+                    __syncwarp();
                 } else if (rope) {
                     if (i > 0 && !(ok = warp_wait(bar(C::ROPE_EMPTY), (uint32_t)((i - 1) & 1), p.err))) return false;
                     if (rank == 0 && el) mbar_arrive_expect_tx(bar(C::ROPE_FULL), 2 * SLAB);  // both CTAs'
@@ -514,6 +525,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     load(dst + (uint32_t)(k0 * PAIR), 128 * k0, 4, lead(C::FULL + buf));
                 }
                 blk = nxt;
+                nxt = nxt2;
             }
             return true;
         });

@@ -117,6 +117,7 @@ cudaError_t launch_prefix(int bf16, int head_dim, int group, const PrefillParams
 // Attention over a paged cache of latent vectors (latent_kernel.cuh).
 struct LatentParams {
     void* out;                  // [total_q, n_heads, DL]
+    const void* cache;          // [num_blocks, block_size, DL + 64]
     const int32_t* block_tables;
     const int32_t* q_loc;       // [num_chunks + 1] first query row of each chunk; null: one query token a sequence
     const int32_t* kv_lens;     // [num_chunks]
@@ -126,6 +127,7 @@ struct LatentParams {
     int tile_log2;              // log2 of the tokens per tile
     int unit_cost;              // what a unit's start and output cost, in tiles (evens out the ranges)
     int min_tiles;              // least cost of a range
+    int stream_once;            // 1: one unit a sequence, its rows come from DRAM
     float qk_scale_log2;
     float* part_o;              // [2 * ranges][NR][DL]
     float* part_ml;             // [2 * ranges][NR][2]: reference (base 2) and exp-sum
