@@ -1014,6 +1014,7 @@ static int latent_impl(void* out, const void* q, const void* latent_cache, const
     p.total_q = (int)total_q;
     p.tb = rows / n_heads;
     p.tile_log2 = rows == 128 ? 7 : 6;
+    p.block_log2 = 4 + cpb_log2_of(block_size);
     p.unit_cost = rows == 128 ? 2 : 1;
     p.min_tiles = p.unit_cost + 2;
     p.stream_once = (int64_t)n_heads * max_q_len <= rows ? 1 : 0;

@@ -668,7 +668,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
             auto entry = [&](int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
                 const int t = tile * TK + lane * br;
                 if (lane >= nbox || t >= g.keys) return p.num_blocks;
-                const int e = __ldg(bt + t / p.block_size);
+                const int e = __ldg(bt + (t >> p.block_log2));
                 if (e < 0 || e >= p.num_blocks) {
                     flag_error(p.err, PA_DEVERR_BLOCK);
                     return p.num_blocks;
@@ -682,11 +682,11 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 const int slot = (int)uniform((uint32_t)(n % slots)), use = n / slots;
                 if (use > 0 && !(ok = warp_wait(bar(empty0 + slot), (uint32_t)((use - 1) & 1), p.err))) return false;
                 const uint32_t full = bar(full0 + slot), dst = ring + (uint32_t)slot * bytes;
-                const int first = (int)uniform((uint32_t)(tile * TK));
+                const int row = nbox == 1 ? (int)uniform((uint32_t)(tile * TK)) & (p.block_size - 1) : 0;  // a whole block, or 64 rows
                 if (el) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
+#pragma unroll 1
                 for (int x = 0; x < nbox; ++x) {
-                    const int row = (first + x * br) % p.block_size;
                     const int e = __shfl_sync(0xffffffffu, blk, x);
                     tma_load_3d(el, dst + x * br * 128, &tmC, b * 128, row, e, full, pol);
                     if (!rope) tma_load_3d(el, dst + SLAB + x * br * 128, &tmC, b * 128 + 64, row, e, full, pol);

@@ -65,6 +65,11 @@ struct Cfg {
     static constexpr uint32_t TMEM_COLS = 512;
 };
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -463,7 +468,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             auto entry = [&](int tile) {
                 const int t = tile * TK + half * 64 + lane * br;
                 if (lane >= nbox || t >= g.keys) return p.num_blocks;
-                const int e = __ldg(bt + t / p.block_size);
+                const int e = __ldg(bt + (t >> p.block_log2));
                 if (e < 0 || e >= p.num_blocks) {
                     flag_error(p.err, PA_DEVERR_BLOCK);
                     return p.num_blocks;
@@ -476,14 +481,16 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                 const int nxt2 = u + 2 < g.n ? entry(tile + 2) : p.num_blocks;
                 const uint32_t buf = uniform((uint32_t)(i & 1)), dst = sBuf + buf * (NP * PAIR);
                 const int first = (int)uniform((uint32_t)(tile * TK + half * 64));  // of the 64 tokens
-                // boxes of `n` slabs from column c0, `to` onwards, counted on barrier fb
-                auto load = [&](uint32_t to, int c0, int n, uint32_t fb) {
-                    for (int x = 0; x < nbox; ++x) {
-                        const int row = (first + x * br) % p.block_size;
-                        const int e = __shfl_sync(0xffffffffu, blk, x);
+                const int row = nbox == 1 ? first & (p.block_size - 1) : 0;  // a box is a whole block, or 64 rows of one
+                // boxes of N slabs from column c0, `to` onwards, counted on barrier fb
+                auto load = [&](auto slabs, uint32_t to, int c0, uint32_t fb) {
+                    constexpr int N = decltype(slabs)::value;
 #pragma unroll 1
-                        for (int s = 0; s < n; ++s)
-                            load_3d(el, to + s * SLAB + x * br * 128, &tmC, c0 + 64 * s, row, e, fb, pol);
+                    for (int x = 0; x < nbox; ++x) {
+                        const int e = __shfl_sync(0xffffffffu, blk, x);
+                        const uint32_t at = to + (uint32_t)(x * br * 128);
+#pragma unroll
+                        for (int s = 0; s < N; ++s) load_3d(el, at + s * SLAB, &tmC, c0 + 64 * s, row, e, fb, pol);
                     }
                 };
                 if (extra) {
@@ -494,7 +501,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     if (!(ok = warp_wait(bar(C::S_FULL + buf), (uint32_t)((i >> 1) & 1), p.err))) return false;
                     if (el) arrive_expect_at(fb, NB * PAIR);
                     __syncwarp();
-                    load(to, (int)rank * (DL / 2), 2 * NB, fb);
+                    load(Int<2 * NB>{}, to, (int)rank * (DL / 2), fb);
                     if (tail) {
                         if (!(ok = warp_wait(bar(C::X_TAIL), (uint32_t)(tails & 1), p.err))) return false;
                         ++tails;
@@ -510,19 +517,19 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     // start once this tile's PV is done, and their DRAM latency would be on the way from tile to tile
                     if (p.stream_once && nxt2 < p.num_blocks)
                         prefetch_l2(static_cast<const uint16_t*>(p.cache) +
-                                        ((int64_t)nxt2 * p.block_size + (first + 2 * TK + lane * br) % p.block_size) * (DL + lat::ROPE),
+                                        ((int64_t)nxt2 * p.block_size + row) * (DL + lat::ROPE),
                                     (uint32_t)(br * (DL + lat::ROPE) * 2));
                     __syncwarp();
                 } else if (rope) {
                     if (i > 0 && !(ok = warp_wait(bar(C::ROPE_EMPTY), (uint32_t)((i - 1) & 1), p.err))) return false;
                     if (rank == 0 && el) mbar_arrive_expect_tx(bar(C::ROPE_FULL), 2 * SLAB);  // both CTAs'
                     __syncwarp();
-                    load(sRope, DL, 1, lead(C::ROPE_FULL));
+                    load(Int<1>{}, sRope, DL, lead(C::ROPE_FULL));
                 } else {
                     if (i > 1 && !(ok = warp_wait(bar(C::EMPTY + buf), (uint32_t)(((i >> 1) - 1) & 1), p.err))) return false;
                     if (rank == 0 && el) mbar_arrive_expect_tx(bar(C::FULL + buf), 2 * 2 * PAIR);  // two pairs, both CTAs'
                     __syncwarp();
-                    load(dst + (uint32_t)(k0 * PAIR), 128 * k0, 4, lead(C::FULL + buf));
+                    load(Int<4>{}, dst + (uint32_t)(k0 * PAIR), 128 * k0, lead(C::FULL + buf));
                 }
                 blk = nxt;
                 nxt = nxt2;

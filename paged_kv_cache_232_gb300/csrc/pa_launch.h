@@ -124,7 +124,7 @@ struct LatentParams {
     unsigned* err;
     int num_chunks, n_heads, max_blocks_per_seq, num_blocks, block_size, max_q_len, total_q;
     int tb;                     // tokens per unit of query rows
-    int tile_log2;              // log2 of the tokens per tile
+    int tile_log2, block_log2;  // log2 of the tokens per tile, per cache block
     int unit_cost;              // what a unit's start and output cost, in tiles (evens out the ranges)
     int min_tiles;              // least cost of a range
     int stream_once;            // 1: one unit a sequence, its rows come from DRAM
