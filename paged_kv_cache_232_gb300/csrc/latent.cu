@@ -23,7 +23,7 @@ static cudaError_t launch_latent_t(const LatentParams& p, const CUtensorMap& tmC
     // the merge: a block for 16 query rows of each range
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(NR == 128 ? ctas / 2 : ctas), NR / 16);
-    cfg.blockDim = dim3(lat::MERGE_THREADS);
+    cfg.blockDim = dim3(lat::merge_threads(NR));
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -49,9 +49,10 @@ constexpr int PAIR = 2 * SLAB;
 // warps 0..3: softmax; then the two MMA issuers, the Q loader, and the cache row loaders (one a pair slot of a tile, one
 // for the rotary slot)
 constexpr int SOFTMAX_WARPS = 4, QK_WARP = 4, PV_WARP = 5, Q_WARP = 6, TMA_WARP = 7;
-constexpr int MERGE_THREADS = 256;
-constexpr int MAX_CTAS = 256;           // of the split: latent_merge_kernel gives every partial a thread
-static_assert(MAX_CTAS <= MERGE_THREADS && PA_LATENT_MAX_CTAS <= MAX_CTAS, "partials of a unit");
+// threads of a merge block (16 rows): a warp a row where the blocks then still run at once
+constexpr int merge_threads(int nr) { return nr <= 32 ? 512 : 256; }
+constexpr int MAX_CTAS = 256;           // of the split: the merge gives every partial a thread
+static_assert(MAX_CTAS <= merge_threads(128) && PA_LATENT_MAX_CTAS <= MAX_CTAS, "partials of a unit");
 
 template <int DL, int NR>
 struct Cfg {
@@ -484,8 +485,9 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
             const bool valid = r >= 0 && r < g.rows;
             const int tok = valid ? r / p.n_heads : 0;
             const int lim = valid ? g.ctx + g.j * p.tb + tok : -1;  // the row sees keys <= lim
-            // the smallest limit in the warp (its lanes without a row of S never matter: see below)
-            const int lim_min = g.rows < NR ? -1 : g.ctx + g.j * p.tb;
+            // the smallest limit of the unit's rows.  Lanes without one (and rows past them: other tokens' queries) are
+            // not masked: rows are independent in both products, theirs are never written and never ask for a rescale
+            const int lim_min = g.ctx + g.j * p.tb;
             float m_ref = -INFINITY, l = 0.f;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int kbase = (g.tile + u) * TK;
@@ -515,7 +517,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[e]);
-                    mx = lane < 16 ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
+                    mx = valid ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
                 }
                 const bool first = u == 0;
                 if (first) m_ref = mx;  // no O yet: the first tile's own maximum is the reference
@@ -816,9 +818,9 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
 // groups of DL / 4 threads every KG-th partial each, their sums added in order.  Fixed orders: the same inputs give
 // the same bits.
 template <bool BF16, int DL, int NR>
-__global__ void __launch_bounds__(lat::MERGE_THREADS) latent_merge_kernel(const LatentParams p) {
+__global__ void __launch_bounds__(lat::merge_threads(NR)) latent_merge_kernel(const LatentParams p) {
     using F = F16x2<BF16>;
-    constexpr int TH = lat::MERGE_THREADS, NW = TH / 32, TG = DL / 4, KG = TH / TG, CV = DL / 128;
+    constexpr int TH = lat::merge_threads(NR), NW = TH / 32, TG = DL / 4, KG = TH / TG, CV = DL / 128;
     constexpr int kFew = 8;
     __shared__ float4 acc[TH];
     __shared__ float wt[lat::MAX_CTAS];

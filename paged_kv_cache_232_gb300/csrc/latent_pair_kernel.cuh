@@ -255,7 +255,9 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             const bool valid = R < g.rows;
             const int lim = valid ? g.ctx + g.j * p.tb + R / p.n_heads : -1;
-            const int lim_min = g.rows < NR ? -1 : g.ctx + g.j * p.tb;
+            // the smallest limit of the unit's rows.  Rows past them (other tokens' queries) are not masked: rows are
+            // independent in both products, theirs are never written and never ask for a rescale
+            const int lim_min = g.ctx + g.j * p.tb;
             float m_ref = -INFINITY, l = 0.f;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int kbase = (g.tile + u) * TK + 64 * th + 32 * ch;
@@ -284,7 +286,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[e]);
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const float mx = valid ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) : -INFINITY;
                 const bool first = u == 0;
                 uint32_t rescale = 0;
                 if (softmax_or(!ok || first || mx > m_ref + 8.f)) {
