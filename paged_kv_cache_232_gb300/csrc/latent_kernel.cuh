@@ -247,13 +247,20 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 __device__ __forceinline__ long long tiles_before(const LatentParams& p, const Chunk& k, int n) {
     if (n == 0) return 0;
     const int last = (k.q_len + p.tb - 1) / p.tb - 1;  // the last block may be short
-    const int full = min(n, last);
-    long long s = 0;
-    if (full > 0)  // block i: ceil((ctx + (i + 1) tb) / tile)
-        s = floor_sum((uint32_t)full, 1u << p.tile_log2, (uint32_t)p.tb,
-                      (uint32_t)(k.kv_len - k.q_len + p.tb + (1 << p.tile_log2) - 1));
+    const int full = min(n, last), ctx = k.kv_len - k.q_len, round = (1 << p.tile_log2) - 1;
+    long long s = (long long)n * p.unit_cost;
+    if (full > 0) {  // block i: ceil((ctx + (i + 1) tb) / tile) tiles
+        const int lo = (ctx + p.tb + round) >> p.tile_log2, hi = (ctx + full * p.tb + round) >> p.tile_log2;
+        if (hi - lo <= 8) {
+            // few different counts: the blocks with more than t tiles are those from floor((t tile - ctx) / tb) on
+            s += (long long)full * lo;
+            for (int t = lo; t < hi; ++t) s += full - ((t << p.tile_log2) - ctx) / p.tb;
+        } else {
+            s += floor_sum((uint32_t)full, 1u << p.tile_log2, (uint32_t)p.tb, (uint32_t)(ctx + p.tb + round));
+        }
+    }
     if (n > last) s += tiles_of(p, k.kv_len);
-    return s + (long long)n * p.unit_cost;
+    return s;
 }
 
 __device__ __forceinline__ long long tiles_in(const LatentParams& p, const Chunk& k) {
@@ -309,7 +316,7 @@ __device__ __forceinline__ Start find_start(const LatentParams& p, int range, in
                 rec->c = c;
                 rec->j = 0;
                 rec->at = (int)(lo - at);
-                rec->rem = lo - at;
+                rec->rem = p.q_loc != nullptr && q.q_len > p.tb ? lo - at : -1;  // -1: one token block, nothing to look for
                 rec->count = (int)min((long long)per, total - lo);
             }
         };
@@ -345,17 +352,20 @@ __device__ __forceinline__ Start find_start(const LatentParams& p, int range, in
             // the last token block of the chunk whose cost starts at or before the range, THREADS candidates a round
             __syncthreads();
             const Start r = *rec;
-            const Chunk q = load_chunk(p, r.c);
-            int j0 = 0, m = (q.q_len + p.tb - 1) / p.tb;  // it is in [j0, j0 + m)
-            while (m > 1) {
-                const int step = (m + THREADS - 1) / THREADS, j = j0 + tid * step;
-                const int hit = __syncthreads_count(tid * step < m && tiles_before(p, q, j) <= r.rem);  // (j0 itself: always)
-                j0 += (hit - 1) * step;
-                m = min(step, m - (hit - 1) * step);
-            }
-            if (tid == 0) {
-                rec->j = j0;
-                rec->at = (int)(r.rem - tiles_before(p, q, j0));
+            if (r.rem >= 0) {
+                const Chunk q = load_chunk(p, r.c);
+                int j0 = 0, m = (q.q_len + p.tb - 1) / p.tb;  // it is in [j0, j0 + m)
+                do {
+                    const int step = (m + THREADS - 1) / THREADS, j = j0 + tid * step;
+                    const long long at = tid * step < m ? tiles_before(p, q, j) : 0;
+                    const int hit = __syncthreads_count(tid * step < m && at <= r.rem);  // (j0 itself: always)
+                    if (tid == hit - 1) {
+                        rec->j = j;
+                        rec->at = (int)(r.rem - at);
+                    }
+                    j0 += (hit - 1) * step;
+                    m = min(step, m - (hit - 1) * step);
+                } while (m > 1);
             }
         }
     }

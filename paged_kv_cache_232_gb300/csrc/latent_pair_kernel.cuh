@@ -42,7 +42,7 @@ using lat::SLAB;
 constexpr int TK = 128;                 // tokens per tile
 constexpr int NR = 128;                 // query rows per unit
 constexpr int SOFTMAX_WARPS = 8, CORR_WARP = 8, QK_WARP = 12, PV_WARP = 13, Q_WARP = 14, X_WARP = 15, ROPE_WARP = 16,
-              TMA_WARP = 17;
+              TMA_WARP = 17, LOADERS = 2;
 constexpr uint32_t CMD_END = 8;         // to the rescale warps: a segment's last PV is issued
 
 template <int DL>
@@ -50,7 +50,8 @@ struct Cfg {
     static_assert(DL == 256 || DL == 512, "latent columns");
     static constexpr int NP = DL / 128;                 // pair slots of a tile buffer
     static constexpr int NB = DL / 256;                 // blocks of 128 latent columns a CTA accumulates
-    static constexpr int THREADS = (TMA_WARP + NP / 2) * 32;
+    static constexpr int THREADS = (TMA_WARP + LOADERS) * 32;
+    static constexpr int SLABS_EACH = 2 * NP / LOADERS;   // slabs of a tile a loader warp brings
     static constexpr int QSLABS = DL / 64 + 1;
     static constexpr int Q_OFF = 0;                     // 64 rows x 9 (5) slabs
     static constexpr int P_OFF = QSLABS * SLAB;         // two slabs: 64 rows x 64 tokens of T_0, of T_1
@@ -210,7 +211,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         for (int i = 0; i < C::NUM_BARS; ++i) {
             const int n = i == C::S_EMPTY || i == C::S_EMPTY + 1 || i == C::P_FULL ? 2 * SOFTMAX_WARPS
                           : i == C::CORR || i == C::O_FREE                         ? 8
-                          : i == C::FULL || i == C::FULL + 1                       ? NP / 2
+                          : i == C::FULL || i == C::FULL + 1                       ? LOADERS
                           : (i >= C::T_FULL && i < C::CMD) || i == C::X_FULL || i == C::X_FULL + 1 ? 2
                                                                                    : 1;
             mbar_init(bar(i), n);
@@ -461,8 +462,8 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             return true;
         });
     } else if (warp >= X_WARP) {
-        // ------------------------------------------------------------ cache rows.  Warps TMA_WARP + k: pairs 2 k and
-        // 2 k + 1 of this CTA's 64 tokens, then their rotary part (ROPE_WARP); X_WARP: after a tile's S, this CTA's columns
+        // ------------------------------------------------------------ cache rows.  Warps TMA_WARP + k: the k-th half
+        // of the slabs of this CTA's 64 tokens; ROPE_WARP: their rotary part; X_WARP: after a tile's S, this CTA's columns
         // of the peer's tokens
         if (lane == 0) tma_prefetch_desc(&tmC);
         // both CTAs read each row's values: evict-first would lose them in between (decode of 128 sequences at 128 heads
@@ -471,7 +472,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         const uint32_t el = elect_one();
         const int br = min(p.block_size, 64), nbox = 64 / br;
         const bool extra = warp == X_WARP, rope = warp == ROPE_WARP;
-        const int k0 = 2 * (warp - TMA_WARP);                // first pair of this warp
+        const int slab0 = C::SLABS_EACH * (warp - TMA_WARP); // first slab of this warp
         const int half = extra ? (int)peer : (int)rank;      // whose tokens
         int i = 0, tails = 0;
         bool ok = true;
@@ -539,9 +540,9 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     load(Int<1>{}, sRope, DL, lead(C::ROPE_FULL));
                 } else {
                     if (i > 1 && !(ok = warp_wait(bar(C::EMPTY + buf), (uint32_t)(((i >> 1) - 1) & 1), p.err))) return false;
-                    if (rank == 0 && el) mbar_arrive_expect_tx(bar(C::FULL + buf), 2 * 2 * PAIR);  // two pairs, both CTAs'
+                    if (rank == 0 && el) mbar_arrive_expect_tx(bar(C::FULL + buf), 2 * C::SLABS_EACH * SLAB);  // both CTAs'
                     __syncwarp();
-                    load(Int<4>{}, dst + (uint32_t)(k0 * PAIR), 128 * k0, lead(C::FULL + buf));
+                    load(Int<C::SLABS_EACH>{}, dst + (uint32_t)(slab0 * SLAB), 64 * slab0, lead(C::FULL + buf));
                 }
                 blk = nxt;
                 nxt = nxt2;
