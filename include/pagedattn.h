@@ -461,8 +461,9 @@ int pa_latent_decode(void* out, const void* q, const void* latent_cache, const i
  *  out, q, query_start_loc, seq_lens, max_q_len as pa_prefill_chunk with the rows of
  *  pa_latent_decode; total_q: rows of q and out.  A chunk whose rows are not inside [0, total_q), is
  *  longer than max_q_len or than its seq_lens, or whose seq_lens is past the table is skipped (its
- *  rows are not written) and sets PA_DEVERR_LENGTH.  Cached rows of tokens a query row does not see
- *  must be finite where they share its unit (up to 64 / n_heads consecutive tokens of the chunk).
+ *  rows are not written) and sets PA_DEVERR_LENGTH.  Query rows are worked in units of consecutive
+ *  tokens, 128 / n_heads of them at most: a row's weight for a later token of its unit is 0, and that
+ *  token's cached row must be finite (0 * NaN is NaN); rows past the unit may hold anything.
  */
 int pa_latent_prefill_chunk(void* out, const void* q, const void* latent_cache, const int32_t* block_tables,
                             int max_blocks_per_seq, const int32_t* query_start_loc, const int32_t* seq_lens,

@@ -402,7 +402,7 @@ def pa_norm_rope_reshape_and_cache(q, key, value, q_weight, k_weight, k_cache, v
     vp, vs = _rows(value, "value", ty, (n, hkv, d), dev)
     _check(load().pa_norm_rope_reshape_and_cache(
         op, os_, qp, qs, kp, ks, vp, vs, _flat(q_weight, "q_weight", ty, (d,), dev),
-        _flat(k_weight, "k_weight", ty, (d,), dev), eps, _flat(k_cache, "k_cache", ty, (nb, bs, hkv, d), dev),
+        _flat(k_weight, "k_weight", ty, (d,), dev), float(eps), _flat(k_cache, "k_cache", ty, (nb, bs, hkv, d), dev),
         _flat(v_cache, "v_cache", ty, (nb, bs, hkv, d), dev), _flat(slot_mapping, "slot_mapping", torch.int64, (n,), dev),
         _flat(positions, "positions", torch.int64, (n,), dev), _flat(cos_sin, "cos_sin", torch.float32, (mp, d), dev),
         n, hq, hkv, d, bs, nb, mp, dt, _raw_stream(stream, dev)), "pa_norm_rope_reshape_and_cache")
@@ -448,7 +448,7 @@ def pa_latent_rope_and_cache(kv, latent_cache, slot_mapping, positions, cos_sin,
             pts = (h - 1) * phs + LATENT_ROPE_DIM
     _check(load().pa_latent_rope_and_cache(
         qp, pep, pts, phs, kv.data_ptr(), kv.stride(0) if n > 1 else row,
-        None if weight is None else _flat(weight, "weight", ty, (dl,), dev), eps,
+        None if weight is None else _flat(weight, "weight", ty, (dl,), dev), float(eps),
         _flat(latent_cache, "latent_cache", ty, (nb, bs, row), dev),
         _flat(slot_mapping, "slot_mapping", torch.int64, (n,), dev), _flat(positions, "positions", torch.int64, (n,), dev),
         _flat(cos_sin, "cos_sin", torch.float32, (mp, LATENT_ROPE_DIM), dev), n, h, dl, LATENT_ROPE_DIM, bs, nb, mp,
@@ -483,7 +483,7 @@ def pa_latent_decode(out, q, latent_cache, block_tables, context_lens, scale: fl
     args, lp, rows, n, dims, dt, wp, wb, dev = _latent_common(out, q, latent_cache, block_tables, context_lens, workspace)
     if n != rows:
         raise ValueError("block_tables and context_lens must hold one row per row of q")
-    _check(load().pa_latent_decode(*args, lp, rows, *dims, scale, dt, wp, wb, _raw_stream(stream, dev)),
+    _check(load().pa_latent_decode(*args, lp, rows, *dims, float(scale), dt, wp, wb, _raw_stream(stream, dev)),
            "pa_latent_decode")
 
 
@@ -494,7 +494,7 @@ def pa_latent_prefill_chunk(out, q, latent_cache, block_tables, query_start_loc,
     workspace of at least pa_latent_workspace_size(H, DL, max_q_len) bytes."""
     args, lp, rows, n, dims, dt, wp, wb, dev = _latent_common(out, q, latent_cache, block_tables, seq_lens, workspace)
     loc = _flat(query_start_loc, "query_start_loc", _torch().int32, (n + 1,), dev)
-    _check(load().pa_latent_prefill_chunk(*args, loc, lp, n, max_q_len, rows, *dims, scale, dt, wp, wb,
+    _check(load().pa_latent_prefill_chunk(*args, loc, lp, n, int(max_q_len), rows, *dims, float(scale), dt, wp, wb,
                                           _raw_stream(stream, dev)), "pa_latent_prefill_chunk")
 
 

@@ -56,6 +56,10 @@ constexpr int TK = 64;                  // tokens per tile
 constexpr int ROPE = 64;                // rotary columns of a cache row
 constexpr int SLAB = TK * 128;          // bytes of 64 tokens x 64 columns
 constexpr int PAIR = 2 * SLAB;
+// Weights are 2^(score - reference + kShift): in fp16 up to 2^15 (the reference may lag by 2^8), so that weights of
+// 2^-21 of the largest are still normal numbers -- many equal small weights would all round the same way as subnormals
+template <bool BF16>
+constexpr float kShift = BF16 ? 0.f : 7.f;
 // warps 0..3: softmax; then the two MMA issuers, the Q loader, and the cache row loaders (one a pair slot of a tile, one
 // for the rotary slot)
 constexpr int SOFTMAX_WARPS = 4, QK_WARP = 4, PV_WARP = 5, Q_WARP = 6, TMA_WARP = 7;
@@ -570,7 +574,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                     tc::wait_st();
                 }
                 if (row_warp) {
-                    const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                    const float mu = m_ref == -INFINITY ? 0.f : m_ref - kShift<BF16>;
                     uint32_t w[32];
                     float2 ls = make_float2(0.f, 0.f);
 #pragma unroll

@@ -326,7 +326,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     send(flag_a + (uint32_t)(((i & 1) * 2 + (int)rank) * 4), rescale, b);
                 }
                 __syncwarp();
-                const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                const float mu = m_ref == -INFINITY ? 0.f : m_ref - lat::kShift<BF16>;
                 uint32_t w[16];
                 float2 ls = make_float2(0.f, 0.f);
 #pragma unroll

@@ -109,6 +109,28 @@ def test_decode_rising_scores_rescale(h):
     check_attend(out, q, r, 1.0, dl, 1, "rising scores")
 
 
+@pytest.mark.parametrize("ty", ["fp16", "bf16"])
+@pytest.mark.parametrize("h", [16, 128])
+def test_decode_many_small_equal_weights(h, ty):
+    """One token far above 40,000 equal ones of 2^-22 its weight each (1 % together): their common rounding must not
+    show, so the weights may not be fp16 subnormals."""
+    dt, dl, L = TYPES[ty], 512, 40001
+    g = gen(15)
+    cache, bt, rows = paged(g, [L], 64, dl, dt)
+    r = rows[0]
+    r[:] = 0
+    r[1:, :dl] = 1.0
+    r[:, dl] = 0.75
+    r[7, dl], r[7, :dl], r[0, :dl] = 16.0, 0.0, 1.0
+    blocks = bt[0, :-(-L // 64)].long()
+    t = torch.arange(L, device="cuda")
+    cache[blocks[t // 64], t % 64] = r
+    q = torch.zeros((1, h, dl + ROPE), device="cuda", dtype=dt)
+    q[..., dl] = 1.0
+    out = _decode(q, cache, bt, [L], scale=1.0)
+    check_attend(out, q, r, 1.0, dl, 1, "small weights")
+
+
 def test_decode_negative_and_zero_scale():
     g = gen(4)
     cache, bt, rows = paged(g, [333], 16, 512, torch.float16)
