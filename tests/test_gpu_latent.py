@@ -327,14 +327,15 @@ def test_chunk_bad_lengths_are_flagged_and_skipped():
     assert err == 0 and (out == 7).all()
 
 
-def test_two_streams_with_their_own_workspaces():
+@pytest.mark.parametrize("heads", [(16, 16), (128, 16), (128, 100)])
+def test_two_streams_with_their_own_workspaces(heads):
     g = gen(12)
     lens = [4000, 2500]
     cache, bt, rows = paged(g, lens, 16, 512, torch.bfloat16)
-    qs = [randn(g, (2, 16, 576), torch.bfloat16) for _ in range(2)]
+    qs = [randn(g, (2, h, 576), torch.bfloat16) for h in heads]
     want = [_decode(q, cache, bt, lens) for q in qs]
     cl = torch.tensor(lens, device="cuda", dtype=torch.int32)
-    outs, wss = [torch.empty_like(want[0]) for _ in qs], [_ws(16, 512) for _ in qs]
+    outs, wss = [torch.empty_like(w) for w in want], [_ws(h, 512) for h in heads]
     streams = [torch.cuda.Stream() for _ in qs]
     torch.cuda.synchronize()
     for _ in range(8):
@@ -345,11 +346,35 @@ def test_two_streams_with_their_own_workspaces():
         assert torch.equal(o, w)
 
 
-def test_step_graph_replay():
+def test_two_captured_graphs_share_a_workspace():
+    """Replayed one after the other on one stream: the second's call does not see what the first's left."""
+    g = gen(14)
+    cases = []
+    ws = _ws(128, 512)
+    for h, lens in ((128, [3000, 40]), (100, [900, 2222])):
+        cache, bt, _ = paged(g, lens, 16, 512, torch.bfloat16)
+        q, cl = randn(g, (2, h, 576), torch.bfloat16), torch.tensor(lens, device="cuda", dtype=torch.int32)
+        out = torch.zeros((2, h, 512), device="cuda", dtype=torch.bfloat16)
+        want = _decode(q, cache, bt, lens)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pa.pa_latent_decode(out, q, cache, bt, cl, SCALE, ws)
+        cases.append((graph, out, want, (cache, bt, q, cl)))
+    for _ in range(3):
+        for graph, out, _, _ in cases:
+            out.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _ in cases:
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("h", [16, 128])
+def test_step_graph_replay(h):
     """A captured write + decode step, replayed on new inputs, equals the eager step bit for bit."""
     g = gen(13)
     lens = [200, 1, 77, 640]
-    dt, dl, h, bs = torch.bfloat16, 512, 16, 16
+    dt, dl, bs = torch.bfloat16, 512, 16
     cache, bt, _ = paged(g, lens, bs, dl, dt, fill=0.0)
     cl = torch.tensor(lens, device="cuda", dtype=torch.int32)
     pos = cl.long() - 1
