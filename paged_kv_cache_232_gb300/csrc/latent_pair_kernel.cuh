@@ -25,7 +25,7 @@
 // tensor work an SM and ~2750 of operand reads and tile writes; measured ~2970 a tile, 870 us for 4 chunks of
 // 512 tokens at 128 heads over 0..4096 cached ones (1.31 PFLOP: 1.5 PFLOP/s, 0.77 of the measured burst rate,
 // 0.87 of the sustained).  Decode at 128 heads is balanced between memory and tensor cores: ~3200 cycles a
-// tile in steady state (the copy rate), 141 us for 128 sequences of 1K..8K tokens (0.74 of the floor).  Steps on the way
+// tile in steady state (the copy rate), 140 us for 128 sequences of 1K..8K tokens (0.74 of the floor).  Steps on the way
 // (prefill / decode): two independent CTAs of 64 rows 3360 / 322 us; this pair with cluster-scope
 // arrivals and waits, 10500 cycles a tile, 3750 / 397; without them, MMA issue predicated in a converged
 // warp, two waits a role and tile, 1081 / 188; ranges evened by the units' own cost 875 / 174; rows kept in
