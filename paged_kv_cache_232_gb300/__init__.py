@@ -423,7 +423,7 @@ def pa_latent_rope_and_cache(kv, latent_cache, slot_mapping, positions, cos_sin,
     """New tokens' rows of a paged latent cache [NB, bs, DL + 64]: kv [N, DL + 64] (rows may be strided),
     its first DL columns RMS-normalised with weight [DL] (None: unchanged), its last 64 rotated by
     positions [N] with the cos_sin table [max_position, 64], at slot_mapping [N] (-1 skips).  q_pe
-    [N, H, 64] (any strides of whole rows), if given, is rotated into the last 64 columns of
+    [N, H, 64] (strided rows, a token's heads before the next token's), if given, is rotated into the last 64 columns of
     q [N, H, DL + 64]; it may be that slice of q."""
     torch = _torch()
     ty, dt = kv.dtype, _dtype_code(kv)
