@@ -43,7 +43,9 @@ constexpr int TK = 128;                 // tokens per tile
 constexpr int NR = 128;                 // query rows per unit
 constexpr int SOFTMAX_WARPS = 8, CORR_WARP = 8, QK_WARP = 12, PV_WARP = 13, Q_WARP = 14, X_WARP = 15, ROPE_WARP = 16,
               TMA_WARP = 17, LOADERS = 2;
-constexpr uint32_t CMD_END = 8;         // to the rescale warps: a segment's last PV is issued
+// To the rescale warps: a segment's last PV is issued; or (below it) bits 0, 1: whose rows to rescale, bit 2: the
+// tile's parity, bit 3: its phase on T_FULL
+constexpr uint32_t CMD_END = 16;
 
 template <int DL>
 struct Cfg {
@@ -59,12 +61,12 @@ struct Cfg {
     static constexpr int ROPE_OFF = BUF_OFF + 2 * NP * PAIR;  // one slot: it is free again after the first MMAs of S
     static constexpr int BAR_OFF = ROPE_OFF + SLAB;
     // barriers (buffer, tile or segment parity where there are two).  On the leader alone: FULL (a tile's own rows, both
-    // CTAs'), ROPE_FULL, X_FULL (the reloaded ones), Q_FULL, S_EMPTY, P_FULL, CORR (a rescale is done), O_FREE, DRAIN; on
-    // both: the others.  T_FULL: a tile's rescale flags and factors are there; F_FULL: a segment's 1 / l; CMD: the next
-    // command to the rescale warps; X_TAIL: see the loaders
+    // CTAs'), ROPE_FULL, X_FULL (the reloaded ones), Q_FULL, S_EMPTY, P_FULL, CORR (a rescale is done), O_FREE, SEEN (the
+    // peer's T_FULL is complete), DRAIN; on both: the others.  T_FULL: a tile's rescale flags and factors are there;
+    // F_FULL: a segment's 1 / l; CMD: the next command to the rescale warps; X_TAIL: see the loaders
     static constexpr int FULL = 0, X_FULL = 2, EMPTY = 4, ROPE_FULL = 6, ROPE_EMPTY = 7, Q_FULL = 8, Q_EMPTY = 9,
                          S_FULL = 10, S_EMPTY = 12, P_FULL = 14, PV_DONE = 15, CORR = 16, O_FREE = 17, T_FULL = 18,
-                         F_FULL = 20, CMD = 22, X_TAIL = 23, DRAIN = 24, NUM_BARS = 26;
+                         F_FULL = 20, CMD = 22, X_TAIL = 23, SEEN = 24, DRAIN = 26, NUM_BARS = 28;
     static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, rescale flags, command
     static constexpr int EXCH_OFF = MISC_OFF + 80;                        // [4][64] row maxima or sums; scan scratch before
     static constexpr int ALPHA_OFF = EXCH_OFF + 4 * 64 * 4;               // [2][128] by tile parity
@@ -98,7 +100,19 @@ __device__ __forceinline__ void cluster_sync() {
 // Arrivals and waits keep the default CTA scope: cluster-scope release and acquire cost ~700 cycles each here,
 // several a tile.  What crosses the pair does not need them: the weights are behind a proxy fence and read by
 // the tensor cores, TMEM accesses are behind tcgen05 fences, and values the peer's threads read travel by
-// st.async, whose completion on the barrier follows the data.
+// st.async, whose completion on the barrier follows the data, for a reader that waits for that barrier.  So every
+// reader waits for the barrier of its own CTA that counts what it reads:
+//  * flags: the PV issuer, T_FULL of the tile.  alpha: the rescale warps, T_FULL of the tile that the command names.
+//    1 / l: the rescale warps, F_FULL of the segment.  The command: CMD.
+// and no barrier is used again before its phase is known to be complete in both CTAs, nor its data overwritten
+// before they are read:
+//  * T_FULL and alpha of a tile are next used two tiles on, by softmax warps that have seen this tile's PV.  The PV
+//    was issued behind T_FULL of the leader, behind SEEN, which a warp of the peer gives once its own T_FULL is
+//    complete (on tiles without a rescale nobody else there waits for it), and behind the rescale (CORR).
+//  * 1 / l and F_FULL of a segment: the next segment's first PV is issued behind O_FREE, which the rescale warps give
+//    once they have read; the softmax warps see a PV of the next segment before they send again.
+//  * CMD: the next command follows CORR or O_FREE.
+// Nothing is in flight when a CTA ends: its T_FULL, F_FULL and CMD have all been waited for there.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -385,7 +399,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         }
     } else if (warp < CORR_WARP + 4) {
         // ------------------------------------------------------------ rescale of O^T and the output: lane = latent
-        // column.  Commands come from the PV issuer: CMD_END (or'ed flags: which CTAs' rows to rescale by tile parity)
+        // column.  Commands come from the PV issuer: see CMD_END
         const int quarter = warp & 3;
         const uint32_t tO = tmem + ((uint32_t)(quarter * 32) << 16) + C::O_COL;
         const uint32_t corr = lead(C::CORR), o_free = lead(C::O_FREE);
@@ -398,8 +412,10 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                 ++cmds;
                 const uint32_t cmd = *cmd_s;
                 if (cmd == CMD_END) break;
+                const int par = (int)((cmd >> 2) & 1);
+                // this CTA's copies of the factors: the leader's command says nothing about the peer's
+                if (!(ok = warp_wait(bar(C::T_FULL + par), (cmd >> 3) & 1, p.err))) return false;
                 tc::fence_after();
-                const int par = (int)(cmd >> 2);
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     if (!((cmd >> c) & 1)) continue;
@@ -639,11 +655,12 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                 const uint32_t flags = flag_s[2 * buf] | (flag_s[2 * buf + 1] << 1);
                 if (flags) {  // O^T is rescaled once it holds every tile before this one
                     if (!warp_wait(bar(C::PV_DONE), (uint32_t)((i - 1) & 1), p.err)) return false;
-                    command(flags | (buf << 2));
+                    command(flags | (buf << 2) | ((uint32_t)((i >> 1) & 1) << 3));
                     if (!warp_wait(bar(C::CORR), (uint32_t)(corrs & 1), p.err)) return false;
                     ++corrs;
                 }
                 if (!warp_wait(bar(C::X_FULL + buf), (uint32_t)((i >> 1) & 1), p.err)) return false;
+                if (!warp_wait(bar(C::SEEN + buf), (uint32_t)((i >> 1) & 1), p.err)) return false;
                 if (!warp_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err)) return false;
                 tc::fence_after();
                 issued = true;
@@ -664,6 +681,17 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             commit1(el, bar(C::DRAIN + 1));
             (void)warp_wait(bar(C::DRAIN + 1), 0, p.err);
         }
+    } else if (warp == PV_WARP) {
+        // ------------------------------------------------------------ the peer's T_FULL, seen tile by tile for the leader
+        int i = 0;
+        for_each_segment(p, start, [&](const Segment& g) -> bool {
+            for (int u = 0; u < g.n; ++u, ++i) {
+                if (!warp_wait(bar(C::T_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), p.err)) return false;
+                if (lane == 0) arrive_at(lead(C::SEEN + (i & 1)));
+                __syncwarp();
+            }
+            return true;
+        });
     }
     __syncwarp();
     tc::fence_before();

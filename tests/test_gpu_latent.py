@@ -109,6 +109,72 @@ def test_decode_rising_scores_rescale(h):
     check_attend(out, q, r, 1.0, dl, 1, "rising scores")
 
 
+def _rising(g, q, rows, cache, bt, dl, bs, seqs):
+    """Scores that grow along each sequence for the query rows [n, H] with a positive column dl of q, and fall for the
+    others: by sequence the rows that rise are all, the first 64 of a unit, those behind them, or a mixed set, so that the
+    two CTAs of a pair rescale in the same tiles, in different ones, or not at all."""
+    for s in seqs:
+        r, at = rows[s], q[s]
+        if not len(r):
+            continue
+        r[:, dl] = torch.linspace(-8, 8, len(r), device="cuda").to(r.dtype)
+        t = torch.arange(len(r), device="cuda")
+        cache[bt[s, t // bs].long(), t % bs] = r
+        n = at.shape[0] * at.shape[1]
+        up = torch.arange(n, device="cuda")
+        up = (up >= 0, up % 128 < 64, up % 128 >= 64, up % 3 == 0, up < 0)[s % 5].view(at.shape[:2])
+        size = torch.linspace(20, 60, n, device="cuda").view(at.shape[:2])
+        at[..., dl] = torch.where(up, size, -size).to(q[s].dtype)
+
+
+@pytest.mark.parametrize("ty", ["fp16", "bf16"])
+@pytest.mark.parametrize("h,dl", [(65, 512), (100, 256), (100, 512), (128, 256), (128, 512)])
+def test_decode_rescales_in_many_tiles_of_several_units(h, dl, ty):
+    """Three units a pair and more, of one to six tiles, whose rows outgrow their reference in most tiles: the factors
+    of every tile reach both CTAs of the pair in time (both parities, across the units' ends)."""
+    g = gen(61 + h)
+    lens = [1 + (97 * i) % 700 for i in range(240)]
+    bs = 16
+    cache, bt, rows = paged(g, lens, bs, dl, TYPES[ty])
+    q = randn(g, (len(lens), 1, h, dl + ROPE), TYPES[ty], 0.05)
+    _rising(g, q, rows, cache, bt, dl, bs, range(len(lens)))
+    q = q[:, 0]
+    pa.pa_device_errors(clear=True)
+    out = _decode(q, cache, bt, lens, scale=1.0)
+    for _ in range(10):
+        assert torch.equal(_decode(q, cache, bt, lens, scale=1.0), out)
+    assert pa.pa_device_errors(clear=True) == 0
+    for s, r in enumerate(rows):
+        check_attend(out[s:s + 1], q[s:s + 1], r, 1.0, dl, 1, f"sequence {s} of {lens[s]}")
+
+
+@pytest.mark.parametrize("ty", ["fp16", "bf16"])
+@pytest.mark.parametrize("h,dl,n", [(16, 512, 8), (48, 256, 5), (128, 512, 3)])
+def test_chunk_rescales_in_many_tiles_of_several_units(h, dl, n, ty):
+    """The same over chunks of a few tokens, in units of 128, 96 and 128 rows (one to three units a chunk)."""
+    g = gen(71 + h)
+    lens = [n + (89 * i) % 600 for i in range(110)]
+    bs, C = 32, 110
+    cache, bt, rows = paged(g, lens, bs, dl, TYPES[ty])
+    q = randn(g, (C, n, h, dl + ROPE), TYPES[ty], 0.05)
+    _rising(g, q, rows, cache, bt, dl, bs, range(C))
+    q = q.flatten(0, 1)
+
+    def call():
+        out = torch.full((C * n, h, dl), float("nan"), device="cuda", dtype=TYPES[ty])
+        pa.pa_latent_prefill_chunk(out, q, cache, bt, torch.arange(0, C * n + 1, n, device="cuda", dtype=torch.int32),
+                                   torch.tensor(lens, device="cuda", dtype=torch.int32), n, 1.0, _ws(h, dl, n))
+        return out
+
+    pa.pa_device_errors(clear=True)
+    out = call()
+    for _ in range(10):
+        assert torch.equal(call(), out)
+    assert pa.pa_device_errors(clear=True) == 0
+    for c, r in enumerate(rows):
+        check_attend(out[c * n:(c + 1) * n], q[c * n:(c + 1) * n], r, 1.0, dl, n, f"chunk {c} of {lens[c]}")
+
+
 @pytest.mark.parametrize("ty", ["fp16", "bf16"])
 @pytest.mark.parametrize("h", [16, 128])
 def test_decode_many_small_equal_weights(h, ty):
