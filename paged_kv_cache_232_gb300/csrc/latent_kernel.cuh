@@ -173,15 +173,15 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // The warp waits, all lanes polling (one request); the polling loop stays out of line, so that the waits'
-// usual path is a few instructions (the roles' code competes for the instruction cache).
+// usual path is a few instructions (the roles' code competes for the instruction cache).  The result is the
+// warp's, false as soon as one lane's wait ran out: the lanes keep their own clocks, and a role that went on in
+// some of its lanes would meet its next warp-wide instruction without the others.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned* err) {
-    return mbar_wait(bar, parity, err);
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) ok = wait_slow(bar, parity, err);
-    __syncwarp();
-    return ok;
+    if (__any_sync(0xffffffffu, !mbar_try_wait(bar, parity))) return wait_slow(bar, parity, err);
+    return true;
 }
 
 // ---- the split of all units' tiles over the CTAs ---------------------------------------------
