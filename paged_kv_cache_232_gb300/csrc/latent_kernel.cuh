@@ -486,6 +486,8 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
     const Start start = find_start<C::THREADS>(p, (int)blockIdx.x, (int)gridDim.x, warp_sum, rec);  // (synchronises the CTA)
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
+    bool ok = true;    // none of this thread's waits has run out
+    int done = 0;      // loader warps: tiles loaded
 
     if (warp < SOFTMAX_WARPS) {
         // ------------------------------------------------------------ softmax, rescale, epilogue
@@ -497,7 +499,6 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         int i = 0;             // tile number over the CTA's range
         int pv_seen = 0;       // PV_DONE phases this warp has waited for
         int pair0 = 0;         // ring position of the tile's first pair slot
-        bool ok = true;
         int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
         auto wait_pv = [&](int n) {  // PVs of tiles 0 .. n - 1 complete
             while (pv_seen < n) {
@@ -687,8 +688,6 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         const uint32_t bytes = (uint32_t)(slabs * SLAB), ring = rope ? sRope : sPair;
         int n = rope ? 0 : b;    // slot number of this warp's next load, over the whole range
         const int step = rope ? 1 : NB;
-        int done = 0;
-        bool ok = true;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             const int32_t* bt = p.block_tables + (size_t)g.c * p.max_blocks_per_seq;
             auto entry = [&](int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
@@ -721,19 +720,13 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
             }
             return true;
         });
-        if (!ok) {  // leave no copy in flight behind
-            for (int k = max(0, done - slots); k < done; ++k) {
-                const int m = (rope ? 0 : b) + k * step;
-                (void)warp_wait(bar(full0 + m % slots), (uint32_t)((m / slots) & 1), p.err);
-            }
-        }
     } else if (warp == Q_WARP && lane == 0) {
         // ------------------------------------------------------------ the units' query rows
         tma_prefetch_desc(&tmQ);
         int seg = 0;
         bool pending = false;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
-            if (seg > 0 && !mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err)) return false;
+            if (seg > 0 && !(ok = mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err))) return false;
             mbar_arrive_expect_tx(bar(C::Q_FULL), C::QSLABS * C::QSLAB);
 #pragma unroll 1
             for (int s = 0; s < C::QSLABS; ++s) tma_load_2d(sQ + s * C::QSLAB, &tmQ, s * 64, g.row0, bar(C::Q_FULL));
@@ -755,15 +748,15 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         int i = 0, seg = 0, nk = 0, nr = 0;  // tiles, segments, pair and rotary slots read
         bool issued = false;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
-            if (!warp_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err)) return false;
+            if (!(ok = warp_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err))) return false;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const uint32_t dS = tS + uniform((uint32_t)(i & 1)) * 64;
-                if (i >= 2 && !warp_wait(bar(C::S_EMPTY + (i & 1)), (uint32_t)(((i >> 1) - 1) & 1), p.err)) return false;
+                if (i >= 2 && !(ok = warp_wait(bar(C::S_EMPTY + (i & 1)), (uint32_t)(((i >> 1) - 1) & 1), p.err))) return false;
 #pragma unroll
                 for (int b = 0; b < NB; ++b, ++nk) {
                     const int slot = (int)uniform((uint32_t)(nk % C::NPAIR));
                     const uint64_t dk = dkp + (uint32_t)((slot * PAIR) >> 4);
-                    if (!warp_wait(bar(C::PAIR_FULL + slot), (uint32_t)((nk / C::NPAIR) & 1), p.err)) return false;
+                    if (!(ok = warp_wait(bar(C::PAIR_FULL + slot), (uint32_t)((nk / C::NPAIR) & 1), p.err))) return false;
                     tc::fence_after();
                     issued = true;
 #pragma unroll
@@ -773,7 +766,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
                 }
                 const int rs = (int)uniform((uint32_t)(nr % C::NROPE));
                 const uint64_t dk = dkr + (uint32_t)((rs * SLAB) >> 4);
-                if (!warp_wait(bar(C::ROPE_FULL + rs), (uint32_t)((nr / C::NROPE) & 1), p.err)) return false;
+                if (!(ok = warp_wait(bar(C::ROPE_FULL + rs), (uint32_t)((nr / C::NROPE) & 1), p.err))) return false;
                 tc::fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -800,11 +793,11 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         bool issued = false;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             // O^T of the segment before must have been read before the first product overwrites it
-            if (seg > 0 && !warp_wait(bar(C::O_FREE), (uint32_t)((seg - 1) & 1), p.err)) return false;
+            if (seg > 0 && !(ok = warp_wait(bar(C::O_FREE), (uint32_t)((seg - 1) & 1), p.err))) return false;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const uint32_t acc = uniform(u > 0);
                 const int slot0 = (int)uniform((uint32_t)(nv % C::NPAIR));
-                if (!warp_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err)) return false;
+                if (!(ok = warp_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err))) return false;
                 tc::fence_after();
                 issued = true;
 #pragma unroll
@@ -829,7 +822,16 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
         }
     }
     tc::fence_before();
-    __syncthreads();
+    // Every load is behind a wait of the QK issuer, every weight behind one of the PV issuer.  If all went well nothing is
+    // in flight now; if some role's wait ran out, no copy may be left behind: the last ones of each ring
+    if (__syncthreads_or(!ok) && warp >= TMA_WARP) {
+        const bool rope = warp == TMA_WARP + NB;
+        const int slots = rope ? C::NROPE : C::NPAIR, step = rope ? 1 : NB, full0 = rope ? C::ROPE_FULL : C::PAIR_FULL;
+        for (int k = max(0, done - (slots + step - 1) / step); k < done; ++k) {
+            const int m = (rope ? 0 : warp - TMA_WARP) + k * step;
+            (void)warp_wait(bar(full0 + m % slots), (uint32_t)((m / slots) & 1), p.err);
+        }
+    }
     if (warp == QK_WARP) {
         tc::fence_after();
         tc::dealloc(tmem, C::TMEM_COLS);

@@ -249,6 +249,9 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
     cluster_sync();  // both CTAs' barriers and TMEM are ready
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
+    bool ok = true;          // none of this thread's waits has run out
+    int loaded = 0;          // loader warps: tiles loaded
+    bool tail_out = false;   // X_WARP: copies counted on X_TAIL are in flight
 
     if (warp < SOFTMAX_WARPS) {
         // ------------------------------------------------------------ softmax: thread = (row, 32 tokens)
@@ -269,7 +272,6 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             send_u32(map_to(addr, peer), v, map_to(bar(b), peer));
         };
         int i = 0, pv_seen = 0, seg = 0;
-        bool ok = true;
         int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
         auto wait_pv = [&](int n) {
             while (pv_seen < n) {
@@ -405,7 +407,6 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         const uint32_t corr = lead(C::CORR), o_free = lead(C::O_FREE);
         const int col = (int)rank * (DL / 2) + quarter * 32 + lane;  // of block 0
         int i = 0, cmds = 0, seg = 0;
-        bool ok = true;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             while (true) {
                 if (!(ok = warp_wait(bar(C::CMD), (uint32_t)(cmds & 1), p.err))) return false;
@@ -491,7 +492,6 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         const int slab0 = C::SLABS_EACH * (warp - TMA_WARP); // first slab of this warp
         const int half = extra ? (int)peer : (int)rank;      // whose tokens
         int i = 0, tails = 0;
-        bool ok = true;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             const int32_t* bt = p.block_tables + (size_t)g.c * p.max_blocks_per_seq;
             auto entry = [&](int tile) {
@@ -528,12 +528,14 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     // with rows past the keys: wait for the copies here, zero those rows, then hand over
                     const uint32_t fb = tail ? map_to(bar(C::X_TAIL), rank) : lead(C::X_FULL + buf);
                     if (!(ok = warp_wait(bar(C::S_FULL + buf), (uint32_t)((i >> 1) & 1), p.err))) return false;
+                    tail_out = tail;
                     if (el) arrive_expect_at(fb, NB * PAIR);
                     __syncwarp();
                     load(Int<2 * NB>{}, to, (int)rank * (DL / 2), fb);
                     if (tail) {
                         if (!(ok = warp_wait(bar(C::X_TAIL), (uint32_t)(tails & 1), p.err))) return false;
                         ++tails;
+                        tail_out = false;
                         const int z = max(g.keys - first, 0), nz = (64 - z) * 8;
                         for (int b2 = 0; b2 < 2 * NB; ++b2)
                             for (int e = lane; e < nz; e += 32)
@@ -565,19 +567,15 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             }
             return true;
         });
-        if (!ok && rank == 0) {  // leave no copy in flight behind: the last ones of each buffer, both CTAs'
-            for (int k = max(0, i - (rope ? 1 : 2)); k < i; ++k) {
-                if (rope) (void)warp_wait(bar(C::ROPE_FULL), (uint32_t)(k & 1), p.err);
-                else (void)warp_wait(bar((extra ? C::X_FULL : C::FULL) + (k & 1)), (uint32_t)((k >> 1) & 1), p.err);
-            }
-        }
+        if (tail_out) (void)warp_wait(bar(C::X_TAIL), (uint32_t)(tails & 1), p.err);  // ran out: once more
+        loaded = i;
     } else if (warp == Q_WARP) {
         // ------------------------------------------------------------ this CTA's 64 query rows of the unit
         if (lane == 0) tma_prefetch_desc(&tmQ);
         int seg = 0;
         bool pending = false;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
-            if (seg > 0 && !warp_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err)) return false;
+            if (seg > 0 && !(ok = warp_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err))) return false;
             const uint32_t full = lead(C::Q_FULL);
             if (rank == 0 && elect_one()) mbar_arrive_expect_tx(bar(C::Q_FULL), (uint32_t)(2 * C::QSLABS * SLAB));
             __syncwarp();
@@ -602,12 +600,12 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         int i = 0, seg = 0;
         bool issued = false;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
-            if (!warp_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err)) return false;
+            if (!(ok = warp_wait(bar(C::Q_FULL), (uint32_t)(seg & 1), p.err))) return false;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const uint32_t buf = uniform((uint32_t)(i & 1)), dS = tS + buf * 64;
                 const uint64_t dk = dk0 + ((buf * (NP * PAIR)) >> 4);
-                if (i >= 2 && !warp_wait(bar(C::S_EMPTY + buf), (uint32_t)(((i >> 1) - 1) & 1), p.err)) return false;
-                if (!warp_wait(bar(C::ROPE_FULL), (uint32_t)(i & 1), p.err)) return false;
+                if (i >= 2 && !(ok = warp_wait(bar(C::S_EMPTY + buf), (uint32_t)(((i >> 1) - 1) & 1), p.err))) return false;
+                if (!(ok = warp_wait(bar(C::ROPE_FULL), (uint32_t)(i & 1), p.err))) return false;
                 tc::fence_after();
                 issued = true;
 #pragma unroll
@@ -615,7 +613,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
                     mma(el, dS, dq + (uint32_t)(((C::QSLABS - 1) * SLAB + kk * 32) >> 4), dkr + (uint32_t)((kk * 32) >> 4), ID_QK,
                         kk > 0);
                 commit2(el, bar(C::ROPE_EMPTY));
-                if (!warp_wait(bar(C::FULL + buf), (uint32_t)((i >> 1) & 1), p.err)) return false;
+                if (!(ok = warp_wait(bar(C::FULL + buf), (uint32_t)((i >> 1) & 1), p.err))) return false;
                 tc::fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4 * (C::QSLABS - 1); ++kk)
@@ -647,21 +645,21 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             __syncwarp();
         };
         for_each_segment(p, start, [&](const Segment& g) -> bool {
-            if (seg > 0 && !warp_wait(bar(C::O_FREE), (uint32_t)((seg - 1) & 1), p.err)) return false;
+            if (seg > 0 && !(ok = warp_wait(bar(C::O_FREE), (uint32_t)((seg - 1) & 1), p.err))) return false;
             for (int u = 0; u < g.n; ++u, ++i) {
                 const uint32_t acc = uniform(u > 0), buf = uniform((uint32_t)(i & 1));
                 const uint64_t dv = dv0 + ((buf * (NP * PAIR)) >> 4);
-                if (!warp_wait(bar(C::T_FULL + buf), (uint32_t)((i >> 1) & 1), p.err)) return false;
+                if (!(ok = warp_wait(bar(C::T_FULL + buf), (uint32_t)((i >> 1) & 1), p.err))) return false;
                 const uint32_t flags = flag_s[2 * buf] | (flag_s[2 * buf + 1] << 1);
                 if (flags) {  // O^T is rescaled once it holds every tile before this one
-                    if (!warp_wait(bar(C::PV_DONE), (uint32_t)((i - 1) & 1), p.err)) return false;
+                    if (!(ok = warp_wait(bar(C::PV_DONE), (uint32_t)((i - 1) & 1), p.err))) return false;
                     command(flags | (buf << 2) | ((uint32_t)((i >> 1) & 1) << 3));
-                    if (!warp_wait(bar(C::CORR), (uint32_t)(corrs & 1), p.err)) return false;
+                    if (!(ok = warp_wait(bar(C::CORR), (uint32_t)(corrs & 1), p.err))) return false;
                     ++corrs;
                 }
-                if (!warp_wait(bar(C::X_FULL + buf), (uint32_t)((i >> 1) & 1), p.err)) return false;
-                if (!warp_wait(bar(C::SEEN + buf), (uint32_t)((i >> 1) & 1), p.err)) return false;
-                if (!warp_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err)) return false;
+                if (!(ok = warp_wait(bar(C::X_FULL + buf), (uint32_t)((i >> 1) & 1), p.err))) return false;
+                if (!(ok = warp_wait(bar(C::SEEN + buf), (uint32_t)((i >> 1) & 1), p.err))) return false;
+                if (!(ok = warp_wait(bar(C::P_FULL), (uint32_t)(i & 1), p.err))) return false;
                 tc::fence_after();
                 issued = true;
 #pragma unroll
@@ -686,7 +684,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
         int i = 0;
         for_each_segment(p, start, [&](const Segment& g) -> bool {
             for (int u = 0; u < g.n; ++u, ++i) {
-                if (!warp_wait(bar(C::T_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), p.err)) return false;
+                if (!(ok = warp_wait(bar(C::T_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), p.err))) return false;
                 if (lane == 0) arrive_at(lead(C::SEEN + (i & 1)));
                 __syncwarp();
             }
@@ -695,6 +693,16 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
     }
     __syncwarp();
     tc::fence_before();
+    // Every load of both CTAs is behind a wait of the leader's issuers.  If those went well nothing is in flight now; if
+    // a wait ran out (one in the peer makes one of the leader's run out, or had nothing left to load), no copy may be left
+    // behind: the last ones of each buffer, both CTAs'
+    if (__syncthreads_or(!ok) && rank == 0 && warp >= X_WARP) {
+        const bool rope = warp == ROPE_WARP;
+        for (int k = max(0, loaded - (rope ? 1 : 2)); k < loaded; ++k) {
+            if (rope) (void)warp_wait(bar(C::ROPE_FULL), (uint32_t)(k & 1), p.err);
+            else (void)warp_wait(bar((warp == X_WARP ? C::X_FULL : C::FULL) + (k & 1)), (uint32_t)((k >> 1) & 1), p.err);
+        }
+    }
     cluster_sync();  // every MMA and every access to the peer's shared memory is complete
     if (warp == QK_WARP) {
         tc::fence_after();
