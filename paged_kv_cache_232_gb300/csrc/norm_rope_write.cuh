@@ -27,9 +27,14 @@ __device__ __forceinline__ float sum_sq(const uint4& v, float scale) {
     return s;
 }
 
-// The rare case of inv_rms, out of line: the row scaled by (a power of two near 1 /) its largest value.
+// The rare case of inv_rms, out of line: the row scaled by k, a power of two near 1 / its largest value m.  Returns
+// r and the factor that the row's values take before they are multiplied by r:
+//   1 / sqrt(mean(x^2) + eps) = k / sqrt(mean((k x)^2) + eps k^2).
+// Large rows (k < 1): r = k / sqrt(..), at least 2^-128.  Tiny ones: k stays with the values, for k / sqrt(..) may be past
+// fp32 (one value of 2^-126 in 256 columns: 2^130).  Where eps k^2 is past 1e30 the row is nothing beside eps (mean((k x)^2)
+// is at most 4), so the unscaled r was right; m is then so small that eps k^2 itself may be past fp32.
 template <bool BF16, int GL, int D, int N>
-__device__ __noinline__ float inv_rms_scaled(uint4 v0, uint4 v1, float eps, float ss, float r, bool lost) {
+__device__ __noinline__ float2 inv_rms_scaled(uint4 v0, uint4 v1, float eps, float ss, float r, bool lost) {
     const uint4 v[2] = {v0, v1};
     float m = 0.f;
 #pragma unroll
@@ -41,41 +46,46 @@ __device__ __noinline__ float inv_rms_scaled(uint4 v0, uint4 v1, float eps, floa
     }
 #pragma unroll
     for (int o = GL / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float k = exp2f(-(float)min(max(ilogbf(m), -126), 126));
+    const float k = __int_as_float((127 - min(max(ilogbf(m), -126), 126)) << 23);
     float st = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) st += sum_sq<BF16>(v[i], k);
 #pragma unroll
     for (int o = GL / 2; o > 0; o >>= 1) st += __shfl_xor_sync(0xffffffffu, st, o);
+    if (ss != ss) return make_float2(ss, 1.f);
     // an infinite value leaves the finite ones 0 and itself NaN (0 * inf), as the formula does
-    if (lost && m > 0.f) r = m == INFINITY ? 0.f : k * rsqrtf(st * (1.f / D) + fminf(eps * k * k, 1e37f));
-    return ss != ss ? ss : r;
+    if (lost && m == INFINITY) return make_float2(0.f, 1.f);
+    const float ek = eps * k * k;
+    if (!lost || m == 0.f || !(ek <= 1e30f)) return make_float2(r, 1.f);
+    const float t = rsqrtf(st * (1.f / D) + ek);
+    return k < 1.f ? make_float2(k * t, 1.f) : make_float2(t, k);
 }
 
 // 1 / sqrt(mean(x^2) + eps) of a row of D values that GL neighbouring lanes hold (N 16-byte chunks
-// each, zeros where a lane holds none).  The whole warp calls it.  bf16 reaches 2^128: where a sum of
-// squares overflows fp32 (or, next to a tiny eps, vanishes), the row is scaled by its largest value first.
+// each, zeros where a lane holds none).  The whole warp calls it.  bf16 reaches 2^128 and down to 2^-133: where a
+// sum of squares overflows fp32 (or, next to a tiny eps, vanishes), the row is scaled by its largest value first.  In
+// two factors (usually 1 / sqrt and 1), the second, a power of two, for the values before the first.
 template <bool BF16, int GL, int D, int N>
-__device__ __forceinline__ float inv_rms(const uint4 (&v)[N], float eps) {
+__device__ __forceinline__ float2 inv_rms(const uint4 (&v)[N], float eps) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) ss += sum_sq<BF16>(v[i], 1.f);
 #pragma unroll
     for (int o = GL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    float r = rsqrtf(ss * (1.f / D) + eps);
+    float2 r = make_float2(rsqrtf(ss * (1.f / D) + eps), 1.f);
     const bool lost = !(ss <= 1e37f) || (eps < 1e-30f && ss < 1e-25f);
-    if (__any_sync(0xffffffffu, lost)) r = inv_rms_scaled<BF16, GL, D, N>(v[0], v[N - 1], eps, ss, r, lost);
+    if (__any_sync(0xffffffffu, lost)) r = inv_rms_scaled<BF16, GL, D, N>(v[0], v[N - 1], eps, ss, r.x, lost);
     return r;
 }
 
-// eight values x * r * w, rounded by the caller's next step only: kept as floats
+// eight values x * r * w (r of inv_rms), rounded by the caller's next step only: kept as floats
 template <bool BF16>
-__device__ __forceinline__ void norm8(const uint4& x, const uint4& w, float r, float* y) {
+__device__ __forceinline__ void norm8(const uint4& x, const uint4& w, float2 r, float* y) {
     float a[8], b[8];
     unpack8<BF16>(x, a);
     unpack8<BF16>(w, b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = a[e] * r * b[e];
+    for (int e = 0; e < 8; ++e) y[e] = a[e] * r.y * r.x * b[e];
 }
 
 template <bool BF16>
@@ -154,7 +164,7 @@ __global__ void __launch_bounds__(512, 2) norm_rope_write_kernel(const NormRopeP
             int64_t slot = nslot;
             // (the row in flight is another token's: also where q is rewritten in place)
             fetch(t + gridDim.x);
-            const float r = inv_rms<BF16, GL, D>(x, p.eps);
+            const float2 r = inv_rms<BF16, GL, D>(x, p.eps);
             if (pos < 0 || pos >= p.max_position) {  // the row is left untouched
                 if (threadIdx.x == 0 && h0 == 0) flag_error(p.err, PA_DEVERR_POSITION);
                 continue;
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(256, 4) latent_write_kernel(const LatentWriteP
                 uint4 v[CH];
 #pragma unroll
                 for (int e = 0; e < CH; ++e) v[e] = x[e];
-                const float r = inv_rms<BF16, 32, DL>(v, p.eps);
+                const float2 r = inv_rms<BF16, 32, DL>(v, p.eps);
 #pragma unroll
                 for (int e = 0; e < CH; ++e) {
                     float f[8];

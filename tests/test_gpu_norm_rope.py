@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_232_gb300 as pa
-from latent_testutil import ROPE, TYPES, check_write, gen, norm64, randn, table, turn64
+from latent_testutil import ROPE, TYPES, check_write, gen, half_step, norm64, randn, table, turn64
 
 pytestmark = pytest.mark.gpu
 
@@ -98,6 +98,52 @@ def test_norm_rope_without_eps_and_a_nan_row():
     assert torch.isnan(out[2, 1]).all() and torch.isfinite(out[keep]).all()      # a head's row stays its own
     want, mag = turn64(norm64(q0, a["qw"], 0.0), a["cs"][a["pos"]])
     check_write(out[keep], want[keep], mag[keep], "the other rows")
+
+
+# bf16 rows at the ends of the format: all values alike, one value alone, and a mixed row
+_ENDS = [lambda r: r.fill_(1e-20), lambda r: r.fill_(1e-36), lambda r: r.fill_(-2.0 ** -133), lambda r: r.fill_(3.0e38),
+         lambda r: r.zero_()[..., 5].fill_(2.0 ** -126), lambda r: r.zero_()[..., 9].fill_(2.0 ** -133),
+         lambda r: r.zero_()[..., 3].fill_(3.0e38), lambda r: r.mul_(1e-25), lambda r: r.mul_(1e-37), lambda r: r.mul_(1e37)]
+
+
+def _check_ends(got, want, mag, what):
+    """check_write's bound, and half the smallest step of bf16 (2^-133): these rows' results reach down there."""
+    d = 2.0 ** -19 * mag
+    bad = (got.double() - want).abs() > half_step(got.dtype) * (want.abs() + d) + d + 2.0 ** -134
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} values off"
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-38, 1e-31, 1e-29, 1e-6])
+def test_norm_rope_rows_at_the_ends_of_the_format(d, eps):
+    """eps of any size next to rows whose squares leave fp32, each beside ordinary rows of the same warp; values are
+    copied whatever their size."""
+    eps = torch.tensor(eps, dtype=torch.float32).item()
+    n = len(_ENDS)
+    a = _norm_rope(torch.bfloat16, n, 4, 3, d, 16, False, 0, seed=12, eps=eps)
+    for i, make in enumerate(_ENDS):
+        make(a["q"][i, i % 4])
+        make(a["k"][i, i % 3])
+        make(a["v"][i, (i + 1) % 3])
+    out = torch.empty_like(a["q"])
+    q0 = a["q"].clone()
+    _run_norm_rope(a, out)
+    cs = a["cs"][a["pos"]]
+    _check_ends(out, *turn64(norm64(q0, a["qw"], eps), cs), "q")
+    _check_ends(a["kc"].flatten(0, 1)[a["slots"]], *turn64(norm64(a["k"], a["kw"], eps), cs), "k_cache")
+    assert torch.equal(a["vc"].flatten(0, 1)[a["slots"]], a["v"]), "v_cache"
+
+
+@pytest.mark.parametrize("dl", [256, 512])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-38, 1e-31, 1e-29, 1e-6])
+def test_latent_write_rows_at_the_ends_of_the_format(dl, eps):
+    eps = torch.tensor(eps, dtype=torch.float32).item()
+    a = _latent(torch.bfloat16, len(_ENDS) + 2, 0, dl, 16, 0, True, seed=13)
+    for i, make in enumerate(_ENDS):
+        make(a["kv"][i, :dl])
+    pa.pa_latent_rope_and_cache(a["kv"], a["cache"], a["slots"], a["pos"], a["cs"], weight=a["w"], eps=eps)
+    want = norm64(a["kv"][:, :dl], a["w"], eps)
+    _check_ends(a["cache"].flatten(0, 1)[a["slots"]][:, :dl], want, want.abs(), "latent part")
 
 
 def test_norm_rope_bad_rows_are_flagged_and_left():
