@@ -359,6 +359,13 @@ def _refuse(t, name: str, dtype, shape, dev, what: str):
     raise ValueError(f"{name} must be {what}")
 
 
+def _dims(t, name: str, shape: str, n: int):
+    """t's sizes, n of them (shape: what the message calls them)."""
+    if t.dim() != n:
+        raise ValueError(f"{name} must be {shape}, got {list(t.shape)}")
+    return t.shape
+
+
 def _rows(t, name: str, dtype, shape, dev):
     """Pointer and token stride (elements) of t [N, heads, dim], whose heads and columns are contiguous."""
     if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
@@ -392,9 +399,9 @@ def pa_norm_rope_reshape_and_cache(q, key, value, q_weight, k_weight, k_cache, v
     q, key, value and q_out may be slices of wider rows (contiguous within a token)."""
     torch = _torch()
     ty, dt = q.dtype, _dtype_code(q)
-    nb, bs, hkv, d = k_cache.shape
-    n, hq, _ = q.shape
-    mp = cos_sin.shape[0]
+    nb, bs, hkv, d = _dims(k_cache, "k_cache", "[num_blocks, block_size, Hkv, D]", 4)
+    n, hq, _ = _dims(q, "q", "[N, Hq, D]", 3)
+    mp, _ = _dims(cos_sin, "cos_sin", "[max_position, D]", 2)
     dev = _device(q)
     qp, qs = _rows(q, "q", ty, (n, hq, d), dev)
     op, os_ = (qp, qs) if q_out is None else _rows(q_out, "q_out", ty, (n, hq, d), dev)
@@ -428,12 +435,16 @@ def pa_latent_rope_and_cache(kv, latent_cache, slot_mapping, positions, cos_sin,
     torch = _torch()
     ty, dt = kv.dtype, _dtype_code(kv)
     nb, bs, dl = _latent_dims(latent_cache)
-    n, row, mp = kv.shape[0], dl + LATENT_ROPE_DIM, cos_sin.shape[0]
+    n, _ = _dims(kv, "kv", "[N, latent_dim + 64]", 2)
+    mp, _ = _dims(cos_sin, "cos_sin", "[max_position, 64]", 2)
+    row = dl + LATENT_ROPE_DIM
+    if (q_pe is None) != (q is None):
+        raise ValueError("q_pe and q come together")
+    if q_pe is not None:
+        _dims(q_pe, "q_pe", "[N, H, 64]", 3)
     dev = _device(kv)
     if kv.shape != (n, row) or kv.stride(1) != 1:
         raise ValueError("kv must be [N, latent_dim + 64] with contiguous rows")
-    if (q_pe is None) != (q is None):
-        raise ValueError("q_pe and q come together")
     qp = pep = None
     h = pts = phs = 0
     if q_pe is not None:
@@ -463,10 +474,10 @@ def _latent_common(out, q, latent_cache, block_tables, lens, workspace):
     torch = _torch()
     ty, dt = q.dtype, _dtype_code(q)
     nb, bs, dl = _latent_dims(latent_cache)
-    rows, h, k = q.shape
+    rows, h, k = _dims(q, "q", "[rows, H, latent_dim + 64]", 3)
     if k != dl + LATENT_ROPE_DIM:
         raise ValueError("q must be [rows, H, latent_dim + 64]")
-    n, mb = block_tables.shape
+    n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
     dev = _device(q)
     wp = wb = 0
     if workspace is not None:

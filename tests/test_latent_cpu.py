@@ -119,3 +119,34 @@ def test_bindings_check_shapes_first():
     with pytest.raises(ValueError):
         pa.pa_latent_rope_and_cache(c[:, 0], c, torch.zeros(4, dtype=torch.int64), torch.zeros(4, dtype=torch.int64),
                                     torch.zeros(9, 64), q_pe=q[..., 512:])
+
+
+def test_bindings_refuse_other_numbers_of_dimensions():
+    """By name and with the shape that was meant, not by an unpacking error."""
+    bf, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+    c, q, kv = torch.zeros(4, 16, 576, dtype=bf), torch.zeros(2, 16, 576, dtype=bf), torch.zeros(2, 576, dtype=bf)
+    bt, cl, sl, cs = torch.zeros(2, 4, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(2, dtype=i64), torch.zeros(9, 64)
+    out = torch.zeros(2, 16, 512, dtype=bf)
+
+    def write(**kw):
+        a = dict(kv=kv, latent_cache=c, slot_mapping=sl, positions=sl, cos_sin=cs)
+        pa.pa_latent_rope_and_cache(**{**a, **kw})
+    for name, bad in (("q_pe", torch.zeros(2, 16 * 64, dtype=bf)), ("q_pe", torch.zeros(64, dtype=bf)),
+                      ("q_pe", torch.zeros(2, 4, 4, 64, dtype=bf)), ("kv", kv[0]), ("kv", kv[None]), ("kv", kv[0, 0]),
+                      ("cos_sin", cs[0]), ("cos_sin", cs[0, 0]), ("latent_cache", c[0])):
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            write(**({"q_pe": bad, "q": q} if name == "q_pe" else {name: bad}))
+    with pytest.raises(ValueError, match="come together"):
+        write(q_pe=q[..., 512:])
+    for name, args in (("q", (out, q[0], c, bt, cl)), ("q", (out, q[None], c, bt, cl)), ("block_tables", (out, q, c, bt[0], cl)),
+                       ("block_tables", (out, q, c, bt[None], cl)), ("latent_cache", (out, q, c[0], bt, cl))):
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            pa.pa_latent_decode(*args, 0.1, None)
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            pa.pa_latent_prefill_chunk(*args[:4], cl, args[4], 1, 0.1, None)
+    k, kc, w = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(4, 16, 8, 64, dtype=bf), torch.zeros(64, dtype=bf)
+    for name, kw in (("q", dict(q=k[0])), ("q", dict(q=k[None])), ("k_cache", dict(k_cache=kc[0])),
+                     ("k_cache", dict(k_cache=kc[None])), ("cos_sin", dict(cos_sin=cs[0])), ("cos_sin", dict(cos_sin=cs[0, 0]))):
+        a = dict(q=k, key=k, value=k, q_weight=w, k_weight=w, k_cache=kc, v_cache=kc, slot_mapping=sl, positions=sl, cos_sin=cs)
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            pa.pa_norm_rope_reshape_and_cache(**{**a, **kw})
