@@ -60,6 +60,7 @@ extern "C" {
 #define PA_DEVERR_LENGTH 4u  /* a context / kv length outside its allowed range */
 #define PA_DEVERR_TIMEOUT 8u /* a pipeline wait in a kernel exceeded its time limit; the kernel gave up */
 #define PA_DEVERR_POSITION 16u /* a rotary-embedding position outside [0, max_position) */
+#define PA_DEVERR_SMEM 32u   /* a kernel's shared memory started at an address it cannot work from; it wrote nothing */
 
 /* split-K piece length the pages use (mini_engine, "Custom CUDA kernels", v2) */
 #define PA_DEFAULT_PARTITION_TOKENS 256

@@ -17,6 +17,7 @@ from . import _build
 PA_F16, PA_BF16 = 0, 1
 PA_OK = 0
 PA_DEVERR_SLOT, PA_DEVERR_BLOCK, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION = 1, 2, 4, 8, 16
+PA_DEVERR_SMEM = 32
 DEFAULT_PARTITION_TOKENS = 256
 
 # names the header declares; the CPU test checks that the library exports each one

@@ -71,8 +71,10 @@ struct Cfg {
     static constexpr int EXCH_OFF = MISC_OFF + 80;                        // [4][64] row maxima or sums; scan scratch before
     static constexpr int ALPHA_OFF = EXCH_OFF + 4 * 64 * 4;               // [2][128] by tile parity
     static constexpr int INV_OFF = ALPHA_OFF + 2 * NR * 4;                // [128]
-    static constexpr int SMEM_BYTES = INV_OFF + NR * 4;
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static constexpr int USED_BYTES = INV_OFF + NR * 4;
+    static_assert(USED_BYTES <= 227 * 1024, "shared memory per CTA");
+    // + alignment slack, as far as it goes (512 latent columns: 208 bytes)
+    static constexpr int SMEM_BYTES = USED_BYTES + 1024 <= 227 * 1024 ? USED_BYTES + 1024 : 227 * 1024;
     static_assert(EXCH_OFF % 16 == 0 && THREADS / 32 * 8 <= 1024, "scratch");
     static constexpr uint32_t O_COL = 128;              // two S buffers of 64 columns, then NB x 128 of O^T
     static constexpr uint32_t TMEM_COLS = 512;
@@ -205,7 +207,12 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
     using C = Cfg<DL>;
     using F = F16x2<BF16>;
     constexpr int NB = C::NB, NP = C::NP;
-    extern __shared__ __align__(1024) unsigned char smem[];
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    // The tiles' swizzle and the operand descriptors need a base of 1024 bytes' alignment.  The launch gives one (the kernel
+    // has no static shared memory); should that change, the base moves up, or the kernel gives up where it cannot
+    const uint32_t skip = (0u - smem_addr(smem_raw)) & 1023u;
+    const bool aligned = skip + C::USED_BYTES <= C::SMEM_BYTES;
+    unsigned char* smem = smem_raw + (aligned ? skip : 0u);
     const uint32_t sbase = smem_addr(smem);
     const uint32_t sQ = sbase + C::Q_OFF, sP = sbase + C::P_OFF, sBuf = sbase + C::BUF_OFF, sRope = sbase + C::ROPE_OFF;
     auto bar = [&](int i) { return sbase + C::BAR_OFF + 8u * (uint32_t)i; };
@@ -231,8 +238,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             mbar_init(bar(i), n);
         }
         fence_barrier_init();
-        // the tiles' swizzle and the operand descriptors need this alignment; the launch gives it
-        if (sbase & 1023u) flag_error(p.err, PA_DEVERR_TIMEOUT);
+        if (!aligned) flag_error(p.err, PA_DEVERR_SMEM);
     }
     if (warp == QK_WARP) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -244,7 +250,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Start start = lat::find_start<C::THREADS>(p, range, ranges, reinterpret_cast<long long*>(exch), rec);
-    if (sbase & 1023u) start.count = 0;
+    if (!aligned) start.count = 0;
     tc::fence_before();
     cluster_sync();  // both CTAs' barriers and TMEM are ready
     tc::fence_after();

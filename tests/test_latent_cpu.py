@@ -1,11 +1,14 @@
 """Host-side refusals and sizes of the norm + rotary write and the latent-cache entry points (no GPU:
 every refusal comes before any device call)."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 
 import paged_kv_cache_232_gb300 as pa
+from paged_kv_cache_232_gb300 import _build
 
 
 @pytest.fixture(scope="module")
@@ -150,3 +153,11 @@ def test_bindings_refuse_other_numbers_of_dimensions():
         a = dict(q=k, key=k, value=k, q_weight=w, k_weight=w, k_cache=kc, v_cache=kc, slot_mapping=sl, positions=sl, cos_sin=cs)
         with pytest.raises(ValueError, match=f"{name} must be"):
             pa.pa_norm_rope_reshape_and_cache(**{**a, **kw})
+
+
+def test_device_error_bits_match_the_header():
+    """Every cause has a bit of its own, under the same name in the header and the package."""
+    with open(os.path.join(_build.INCLUDE, "pagedattn.h")) as f:
+        bits = {m[1]: int(m[2]) for m in re.finditer(r"#define (PA_DEVERR_[A-Z]+) (\d+)u", f.read())}
+    assert bits == {k: v for k, v in vars(pa).items() if k.startswith("PA_DEVERR_")}
+    assert sorted(bits.values()) == [1 << i for i in range(len(bits))] and "PA_DEVERR_SMEM" in bits
