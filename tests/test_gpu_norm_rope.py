@@ -73,6 +73,22 @@ def test_norm_rope_matches_formula(ty, n, hq, hkv, d, bs, fused, pad):
     assert pa.pa_device_errors(clear=True) == 0
 
 
+@pytest.mark.parametrize("ty", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,hq,hkv,d", [(3, 64, 8, 256), (700, 25, 4, 256), (9, 64, 16, 128), (2, 61, 2, 96), (5, 128, 3, 64)])
+def test_norm_rope_more_head_rows_than_a_block_holds(ty, n, hq, hkv, d):
+    """A block of 512 threads holds 32 head rows of 256 columns, 64 of 96 or 128, 128 of 64: the others in further
+    passes over the tokens (the last one partly filled), q rewritten in place too."""
+    a = _norm_rope(TYPES[ty], n, hq, hkv, d, 16, True, n // 3, seed=n + hq)
+    q0, kc0, vc0 = a["q"].clone(), a["kc"].clone(), a["vc"].clone()
+    pa.pa_device_errors(clear=True)
+    out = torch.full((n, hq, d), float("nan"), device="cuda", dtype=TYPES[ty])
+    _run_norm_rope(a, out)
+    _check_norm_rope(a, q0, kc0, vc0, out)
+    _run_norm_rope(a, None)
+    assert torch.equal(a["q"], out)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
 def test_norm_rope_extremes():
     """Rows of zeros (eps alone under the root), of the largest values and of tiny ones."""
     a = _norm_rope(torch.bfloat16, 4, 4, 2, 128, 16, False, 0, seed=5)
