@@ -23,11 +23,16 @@
 //    rows x 512; rows on M would take all 512 columns and leave none for S).
 //  * The running maximum is updated lazily: O and l are rescaled only when a row's maximum grows
 //    by more than 2^8; weights up to 2^8 above the reference are exact in fp32 and far from the
-//    16-bit formats' limits.  A weight enters the PV product rounded to the cache's 16-bit type
-//    (half a step is 2^-8 in bf16, 2^-11 in fp16, relative; the roundings of different keys are
-//    independent, so their sum stays about as large as the rounding of the output to that type,
-//    and a second product for the remainders would cost half the tensor work again), and l sums the
-//    rounded weights, so that they still sum to one.
+//    16-bit formats' limits.
+//  * A weight enters the PV product rounded once to the cache's 16-bit type (half a step is 2^-8 in
+//    bf16, 2^-11 in fp16, relative), and l sums the rounded weights, so that they still sum to one.
+//    The roundings of different keys are independent, so their sum stays below the rounding of the
+//    output to that type.  Both sides measured: root-mean-square error against 64 bits, relative to
+//    the output, 0.0019..0.0020 in bf16 (weights of 32 bits: 0.0016..0.0017) and 0.00022..0.00027 in
+//    fp16 (0.00020..0.00021), the most for one short context; the remainders as a second product, as
+//    prefill_kernel.cuh has them, cost by their MMAs alone (the product issued twice) 25.7 -> 27.3 us
+//    for 64 x 100..2048 tokens at 16 heads, 134 -> 162 us for 128 x 1K..8K at 128 heads and 905 -> 1196
+//    us for a prefill at 128 heads, where shared memory has no place for them either (16 KB, 0.2 are left).
 //  * All units, laid end to end and measured in cost (a unit's start and output, then its tiles), are
 //    cut into equal ranges, one a CTA (one CTA per SM): units that end inside a range are written
 //    directly, the two that its ends cut leave fp32 partials that latent_merge_kernel joins in a fixed
@@ -41,8 +46,8 @@
 // cycles at 16 rows and ~3450 at 64 (GB300, 256 sequences of 1K..2K tokens): 6.9 and 6.3 TB/s over the
 // 152 SMs, about the copy rate.  What is left is fixed: ~6 us to the first S (lengths, block table, first
 // rows from DRAM, each waiting for the one before), 1..3 us for output or partials, ~4 us for the merge.
-// Whole calls: 64 sequences of 100..2048 tokens at 16 heads 26 us (12 us of bytes at the copy rate), 4 of
-// 32K at 64 heads 41 us (22).  Steps on the way: one MMA issuer for QK and PV 38 and 67 us (the PV that frees
+// Whole calls: 64 sequences of 100..2048 tokens at 16 heads 25.7 us (12 us of bytes at the copy rate), 4 of
+// 32K at 64 heads 40.8 us (22).  Steps on the way: one MMA issuer for QK and PV 38 and 67 us (the PV that frees
 // the ring queued behind the next tile's QK); descriptors formed in a divergent lane ~90 cycles an MMA.
 #pragma once
 

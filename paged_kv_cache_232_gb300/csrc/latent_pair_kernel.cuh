@@ -22,14 +22,16 @@
 //    more warps apply them and write the output, beside the next unit's softmax.
 //
 // What bounds it.  Prefill (rows from L2): shared-memory bandwidth.  A tile's products are 2176 cycles of
-// tensor work an SM and ~2750 of operand reads and tile writes; measured ~2970 a tile, 870 us for 4 chunks of
-// 512 tokens at 128 heads over 0..4096 cached ones (1.31 PFLOP: 1.5 PFLOP/s, 0.77 of the measured burst rate,
-// 0.87 of the sustained).  Decode at 128 heads is balanced between memory and tensor cores: ~3200 cycles a
-// tile in steady state (the copy rate), 140 us for 128 sequences of 1K..8K tokens (0.74 of the floor).  Steps on the way
-// (prefill / decode): two independent CTAs of 64 rows 3360 / 322 us; this pair with cluster-scope
-// arrivals and waits, 10500 cycles a tile, 3750 / 397; without them, MMA issue predicated in a converged
-// warp, two waits a role and tile, 1081 / 188; ranges evened by the units' own cost 875 / 174; rows kept in
-// L2 for the second read 875 / 164; the tile after the next prefetched into L2 870 / 143.
+// tensor work an SM and ~2750 of operand reads and tile writes; measured ~3000 a tile, 890..945 us (by box) for 4
+// chunks of 512 tokens at 128 heads over 0..4096 cached ones (1.31 PFLOP: 1.39..1.47 PFLOP/s, 0.71..0.75 of the
+// measured burst rate, 0.81..0.85 of the sustained).  Decode at 128 heads is balanced between memory and tensor
+// cores: ~3200 cycles a tile in steady state (the copy rate), 136..148 us for 128 sequences of 1K..8K tokens (0.70..0.76
+// of the floor): ~104 us of tiles, ~12 of start and merge; the rest is not accounted for (units' ends, most likely: no
+// load looks past one).  Steps on the way (prefill / decode, us, each of its own build): two independent CTAs of 64
+// rows 3360 / 322; this pair with cluster-scope arrivals and waits, 10500 cycles a tile, 3750 / 397; without them, MMA
+// issue predicated in a converged warp, two waits a role and tile, 1081 / 188; ranges cut by cost and rows kept in
+// L2 for the second read 875 / 164; the tile after the next prefetched into L2 870 / 143.  Taken out of this build:
+// the units' own cost in the cut, 905 -> 1413 / 136 -> 138.
 #pragma once
 
 #include "latent_kernel.cuh"

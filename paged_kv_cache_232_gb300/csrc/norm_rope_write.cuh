@@ -10,8 +10,9 @@
 // the next one's loads issued ahead.  GB300, 64K rows of 16 q / 8 KV heads x 128: a warp an item with a
 // division each 246 us, four tokens unrolled 320 (registers cost occupancy), one 199, one ahead 180 (1.09 GB:
 // 0.89 of the measured copy bandwidth); 42 or fewer registers spill (330 and more).  32K latent rows with 16
-// heads: 59 -> 45 us (0.68; 128-byte pieces at strides of 384 and 1152 bytes; two tokens ahead, other
-// grids and register limits no better).
+// heads: 59 -> 47.5 us (0.68; two tokens ahead, other grids and register limits no better).  Part of what is left
+// there: the key part is the first of a token's rotary rows, so at a multiple of 8 heads the token's last warp
+// holds one row in 4 of its 32 lanes (one warp in four at 16 heads) and keeps few bytes in flight.
 #pragma once
 
 #include "rope_write.cuh"
