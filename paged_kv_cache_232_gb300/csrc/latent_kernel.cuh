@@ -29,10 +29,11 @@
 //    The roundings of different keys are independent, so their sum stays below the rounding of the
 //    output to that type.  Both sides measured: root-mean-square error against 64 bits, relative to
 //    the output, 0.0019..0.0020 in bf16 (weights of 32 bits: 0.0016..0.0017) and 0.00022..0.00027 in
-//    fp16 (0.00020..0.00021), the most for one short context; the remainders as a second product, as
-//    prefill_kernel.cuh has them, cost by their MMAs alone (the product issued twice) 25.7 -> 27.3 us
-//    for 64 x 100..2048 tokens at 16 heads, 134 -> 162 us for 128 x 1K..8K at 128 heads and 905 -> 1196
-//    us for a prefill at 128 heads, where shared memory has no place for them either (16 KB, 0.2 are left).
+//    fp16 (0.00020..0.00021), the most for one short context.  The remainders as further columns of the
+//    operand or (64 rows x 512) as a second product, as prefill_kernel.cuh has them: built and timed in
+//    turn, 64 x 100..2048 tokens at 16 heads 25.6 -> 27.0 us, 4 x 32K at 64 heads 40.7 -> 44.0, 64 x 1K..8K
+//    at 64 heads 81 -> 88.  For pairs their MMAs alone (the product issued twice): 128 x 1K..8K at 128 heads
+//    134 -> 162 us, prefill 905 -> 1196, and shared memory has no place for them (16 KB, 0.2 are left).
 //  * All units, laid end to end and measured in cost (a unit's start and output, then its tiles), are
 //    cut into equal ranges, one a CTA (one CTA per SM): units that end inside a range are written
 //    directly, the two that its ends cut leave fp32 partials that latent_merge_kernel joins in a fixed
