@@ -61,6 +61,10 @@ extern "C" {
 #define PA_DEVERR_TIMEOUT 8u /* a pipeline wait in a kernel exceeded its time limit; the kernel gave up */
 #define PA_DEVERR_POSITION 16u /* a rotary-embedding position outside [0, max_position) */
 #define PA_DEVERR_SMEM 32u   /* a kernel's shared memory started at an address it cannot work from; it wrote nothing */
+#define PA_DEVERR_PATH 64u   /* an accepted path that does not rise within its tree; none of its rows were moved */
+#define PA_DEVERR_FORK 128u  /* a fork from or to a sequence that cannot be forked; it was skipped */
+#define PA_DEVERR_PAGES 256u /* the free list held too few pages for a sequence, which kept its length */
+#define PA_DEVERR_COUNT 512u /* a page's count, the free list or its length contradicts the tables */
 
 /* split-K piece length the pages use (mini_engine, "Custom CUDA kernels", v2) */
 #define PA_DEFAULT_PARTITION_TOKENS 256
@@ -471,6 +475,137 @@ int pa_latent_prefill_chunk(void* out, const void* q, const void* latent_cache, 
                             int num_chunks, int max_q_len, int64_t total_q, int n_heads, int latent_dim, int rope_dim,
                             int block_size, int64_t num_blocks, float scale, int dtype, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/*
+ * Trees of drafted tokens.  A verification step scores several continuations of a sequence at once: its n
+ * drafted tokens form a tree, each a continuation of its parent.  Their K/V rows are written behind the ctx
+ * cached tokens like any new tokens (slots of positions ctx .. ctx + n - 1 in the order of the tree, rotated
+ * by ctx + depth), pa_tree_decode attends, and after the accepted path is known pa_tree_commit moves its rows
+ * to the front and pa_resize_pages gives back the pages that are left over.
+ *
+ * pa_tree_mask -- the mask and the depths of a tree (HOST function, no GPU).
+ *
+ *  parents  HOST [num_tokens]: token j continues parents[j] < j, or the context (-1)
+ *  mask     HOST [num_tokens, mask_words], written: bit k (bit k % 64 of word k / 64) of row j is set when
+ *           token k is j or one of its ancestors
+ *  depth    HOST [num_tokens] or NULL, written: number of ancestors (position ctx + depth)
+ *  Returns PA_ERR_SHAPE for 64 mask_words < num_tokens, PA_ERR_BOUNDS for a parent that is not before its child.
+ */
+int pa_tree_mask(int64_t* mask, int32_t* depth, const int32_t* parents, int num_tokens, int mask_words);
+
+/*
+ * Workspace bytes of pa_tree_decode: two descriptors and two fp32 partials for each of up to
+ * PA_TREE_MAX_CTAS CTAs, whatever the batch and the lengths.  0 for shapes it does not support.
+ * Caller-owned; nothing in it needs to start at any value.  Calls that can run at the same time on the GPU
+ * must not share one.
+ */
+#define PA_TREE_MAX_CTAS 160
+size_t pa_tree_workspace_size(int n_q_heads, int n_kv_heads, int head_dim, int max_q_len);
+
+/*
+ * pa_tree_decode -- attention of trees of drafted tokens over the paged cache, on the tcgen05 tensor cores.
+ *
+ *  out, q [total_q, n_q_heads, head_dim]; sequence s owns rows [query_start_loc[s], query_start_loc[s + 1]),
+ *         n_s of them (0 allowed); rows of no sequence are left as they are
+ *  seq_lens [num_seqs] int32: tokens in the cache, the drafted ones included (ctx = seq_lens[s] - n_s)
+ *  tree_mask [total_q, mask_words] int64, 64 mask_words >= max_q_len: drafted token j of a sequence sees every
+ *         token t < ctx, and drafted token k (at ctx + k) where bit k of its row is set (its own bit too: nothing is
+ *         implied); bits from n_s on are ignored.  A row that sees nothing is zero.
+ *  out[j, h] = sum_t softmax_t(scale * q[j, h] . K_t) V_t over the tokens that j sees, head h of KV head h / G.
+ *  Any group size G = n_q_heads / n_kv_heads up to 16; head_dim 64, 96, 128 or 256; block_size 8 .. 128; trees of
+ *  any size (a sequence longer than max_q_len or its table, shorter than its tree, or with rows outside
+ *  [0, total_q) is skipped and sets PA_DEVERR_LENGTH).
+ *  Cache rows of drafted tokens may hold anything for rows that do not see them (a padded token's slot is
+ *  never written); a row that sees a V row which is not finite becomes NaN throughout.  Softmax weights enter
+ *  the second product rounded to dtype; sums are fp32.
+ */
+int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                   int max_blocks_per_seq, const int32_t* query_start_loc, const int32_t* seq_lens, const int64_t* tree_mask,
+                   int mask_words, int num_seqs, int max_q_len, int64_t total_q, int n_q_heads, int n_kv_heads, int head_dim,
+                   int block_size, int64_t num_blocks, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * Pages.  The calls below move, share, take and free the pages (cache blocks) of sequences between forward
+ * passes, on the device, so that what follows from a verification needs no answer on the host.  They treat the
+ * caches of all layers at once:
+ *
+ *  k_cache, v_cache [num_layers, num_blocks, block_size, row] contiguous, row_bytes a token's row (n_kv_heads *
+ *         head_dim * 2; a multiple of 16), num_layers 1 for one layer's cache; v_cache NULL for caches of one
+ *         array a layer (the latent cache).  Data are copied bit by bit, whatever their type.
+ *  block_tables [num_seqs, max_blocks_per_seq], seq_lens [num_seqs] as for attention: sequence s holds
+ *         ceil(seq_lens[s] / block_size) pages.
+ *
+ * pa_tree_commit -- the rows of the accepted drafted tokens moved to the front of the drafted ones.
+ *
+ *  query_start_loc, seq_lens  as pa_tree_decode
+ *  path [num_seqs, max_path] int32: accepted tokens of s by their number in the tree, rising;
+ *         num_accepted [num_seqs] of them (entries behind are not read)
+ *  Row ctx + path[s][i] of every layer goes to ctx + i (i < num_accepted[s]), as if all were read before any is
+ *  written, and new_lens[s] (int32, written; must not overlap the inputs) = ctx + num_accepted[s].
+ *  A path that does not rise within [0, n_s), or with more entries than max_path or n_s: no row is moved, new_lens[s] =
+ *  ctx, PA_DEVERR_PATH.  Lengths out of range: nothing is moved, new_lens[s] = seq_lens[s], PA_DEVERR_LENGTH.  A row
+ *  whose page is not in the pool stays, PA_DEVERR_BLOCK.  Rows that are moved must lie in pages of their sequence
+ *  alone (pa_resize_pages sees to that for the tokens that it adds).
+ */
+int pa_tree_commit(void* k_cache, void* v_cache, int num_layers, const int32_t* block_tables, int max_blocks_per_seq,
+                   const int32_t* query_start_loc, const int32_t* seq_lens, const int32_t* path, int max_path,
+                   const int32_t* num_accepted, int32_t* new_lens, int num_seqs, int64_t row_bytes, int block_size,
+                   int64_t num_blocks, void* stream);
+
+/*
+ * pa_copy_pages -- pages copied to other pages in all layers (copy on write or relocation decided on the host).
+ *
+ *  pairs [num_pairs, 2] int32: page pairs[i][0] is copied to page pairs[i][1]; -1 in either: skipped.  The pages
+ *         written must be distinct and none of those read.  Ids outside [0, num_blocks): skipped, PA_DEVERR_BLOCK.
+ */
+int pa_copy_pages(void* k_cache, void* v_cache, int num_layers, const int32_t* pairs, int64_t num_pairs, int64_t row_bytes,
+                  int block_size, int64_t num_blocks, void* stream);
+
+/*
+ * The page ledger of pa_fork_pages and pa_resize_pages, all int32 on the device and owned by the caller:
+ *
+ *  ref_counts [num_blocks]: in how many sequences' tables a page is (0: free)
+ *  free_list [num_blocks], free_count [1]: the free pages are free_list[0 .. free_count - 1], the last one is taken first
+ *
+ * pa_fork_pages -- sequences that share the tokens of others, with no data copied.
+ *
+ *  parents [num_seqs] int32: sequence s (which must be empty) becomes a fork of parents[s]: its table row starts
+ *         with the same pages, whose counts rise by one, and seq_lens[s] = seq_lens[parents[s]]; -1: s stays as it
+ *         is.  A parent out of range or that is itself to become a fork in this call, or a sequence with tokens:
+ *         skipped, PA_DEVERR_FORK.
+ */
+int pa_fork_pages(int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_lens, const int32_t* parents, int num_seqs,
+                  int32_t* ref_counts, int block_size, int64_t num_blocks, void* stream);
+
+/*
+ * pa_resize_pages -- sequences to new lengths: pages taken for those that grow, dropped by those that shrink
+ * (to 0: the sequence is freed), and the last page of a growing sequence made its own.
+ *
+ *  new_lens [num_seqs] int32 (must not overlap the ledger or the tables); -1: s stays as it is
+ *  seq_lens [num_seqs], updated to new_lens
+ *  A sequence that grows gets ceil(new / block_size) - ceil(old / block_size) pages into its table; one more where
+ *  its last page is partly filled and had a count above 1 when the call began: the page's rows in use are
+ *  copied to the new page in all layers, which takes its place (all sequences that share a page and grow in
+ *  one call get their own).  One that shrinks drops the pages behind its new last one (table entries become -1).  A
+ *  dropped page's count falls by one; at 0 the page is free.
+ *  Pages are taken in the order of the sequences, the last of the free list first, as long as the list as it was
+ *  before the call holds all that a sequence needs; that one and every later one that needs pages keep their
+ *  length (seq_lens[s] != new_lens[s]) and PA_DEVERR_PAGES is set.  Pages that get free are put on the list behind
+ *  those not taken, in the order of their numbers: the same call gives the same tables and list every time.
+ *  Entries of free_list from the new free_count on are left as they were.
+ *  Lengths outside the table: skipped, PA_DEVERR_LENGTH.  Ids outside the pool: PA_DEVERR_BLOCK.  A count that would
+ *  fall below 0 stays; a page taken that has a count, or is not in the pool (its table entry becomes -1), a free_count
+ *  outside [0, num_blocks] (then nothing is done): PA_DEVERR_COUNT.
+ *  workspace: pa_resize_workspace_size(num_seqs, num_blocks) bytes, caller-owned; nothing in it needs to start at
+ *  any value.  Calls that can run at the same time on the GPU must not share one, nor a ledger.
+ */
+size_t pa_resize_workspace_size(int num_seqs, int64_t num_blocks);
+
+int pa_resize_pages(void* k_cache, void* v_cache, int num_layers, int32_t* block_tables, int max_blocks_per_seq,
+                    int32_t* seq_lens, const int32_t* new_lens, int num_seqs, int32_t* ref_counts, int32_t* free_list,
+                    int32_t* free_count, int64_t row_bytes, int block_size, int64_t num_blocks, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /*
  * Reads (and with clear != 0, resets) the error word of the current device.

@@ -18,6 +18,7 @@ PA_F16, PA_BF16 = 0, 1
 PA_OK = 0
 PA_DEVERR_SLOT, PA_DEVERR_BLOCK, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION = 1, 2, 4, 8, 16
 PA_DEVERR_SMEM = 32
+PA_DEVERR_PATH, PA_DEVERR_FORK, PA_DEVERR_PAGES, PA_DEVERR_COUNT = 64, 128, 256, 512
 DEFAULT_PARTITION_TOKENS = 256
 
 # names the header declares; the CPU test checks that the library exports each one
@@ -27,7 +28,8 @@ EXPORTED = (
     "pa_decode_splitk_static", "pa_rope_table", "pa_rope_reshape_and_cache", "pa_decode_shared_prefix",
     "pa_decode_shared_prefix_workspace_size", "pa_prefill_chunk_small_m", "pa_decode_write",
     "pa_norm_rope_reshape_and_cache", "pa_latent_rope_and_cache", "pa_latent_workspace_size", "pa_latent_decode",
-    "pa_latent_prefill_chunk",
+    "pa_latent_prefill_chunk", "pa_tree_mask", "pa_tree_workspace_size", "pa_tree_decode", "pa_tree_commit",
+    "pa_copy_pages", "pa_fork_pages", "pa_resize_workspace_size", "pa_resize_pages",
 )
 STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -102,6 +104,23 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.pa_latent_prefill_chunk.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i32, i32, i32, i32, i64, f32, i32,
                                           vp, sz, vp]
     L.pa_latent_prefill_chunk.restype = i32
+    L.pa_tree_mask.argtypes = [vp, vp, vp, i32, i32]
+    L.pa_tree_mask.restype = i32
+    L.pa_tree_workspace_size.argtypes = [i32, i32, i32, i32]
+    L.pa_tree_workspace_size.restype = sz
+    L.pa_tree_decode.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i64, i32, i32, i32, i32, i64, f32, i32,
+                                 vp, sz, vp]
+    L.pa_tree_decode.restype = i32
+    L.pa_tree_commit.argtypes = [vp, vp, i32, vp, i32, vp, vp, vp, i32, vp, vp, i32, i64, i32, i64, vp]
+    L.pa_tree_commit.restype = i32
+    L.pa_copy_pages.argtypes = [vp, vp, i32, vp, i64, i64, i32, i64, vp]
+    L.pa_copy_pages.restype = i32
+    L.pa_fork_pages.argtypes = [vp, i32, vp, vp, i32, vp, i32, i64, vp]
+    L.pa_fork_pages.restype = i32
+    L.pa_resize_workspace_size.argtypes = [i32, i64]
+    L.pa_resize_workspace_size.restype = sz
+    L.pa_resize_pages.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, vp, vp, vp, i64, i32, i64, vp, sz, vp]
+    L.pa_resize_pages.restype = i32
     L.pa_device_errors.argtypes = [i32]
     L.pa_device_errors.restype = i32
     L.pa_status_string.argtypes = [i32]
@@ -508,6 +527,126 @@ def pa_latent_prefill_chunk(out, q, latent_cache, block_tables, query_start_loc,
     loc = _flat(query_start_loc, "query_start_loc", _torch().int32, (n + 1,), dev)
     _check(load().pa_latent_prefill_chunk(*args, loc, lp, n, int(max_q_len), rows, *dims, float(scale), dt, wp, wb,
                                           _raw_stream(stream, dev)), "pa_latent_prefill_chunk")
+
+
+def tree_mask(parents, mask_words: int = 0):
+    """(mask, depth) of a tree of drafted tokens as host numpy arrays: mask [n, words] int64 with the bits of each
+    token and its ancestors (words: at least mask_words and enough for n), depth [n] int32.  parents[j] < j, or -1
+    for a token that continues the context."""
+    import numpy as np
+    up = np.ascontiguousarray(parents, dtype=np.int32)
+    if up.ndim != 1:
+        raise ValueError(f"parents must be [num_tokens], got {list(up.shape)}")
+    n = up.shape[0]
+    words = max(int(mask_words), -(-n // 64))
+    mask, depth = np.zeros((n, words), dtype=np.int64), np.zeros(n, dtype=np.int32)
+    _check(load().pa_tree_mask(mask.ctypes.data, depth.ctypes.data, up.ctypes.data, n, words), "pa_tree_mask")
+    return mask, depth
+
+
+def pa_tree_workspace_size(n_q_heads: int, n_kv_heads: int, head_dim: int, max_q_len: int) -> int:
+    return int(load().pa_tree_workspace_size(n_q_heads, n_kv_heads, head_dim, max_q_len))
+
+
+def pa_tree_decode(out, q, k_cache, v_cache, block_tables, query_start_loc, seq_lens, tree_mask, max_q_len: int, scale: float,
+                   workspace, stream=None) -> None:
+    """Attention of trees of drafted tokens over the paged cache: out, q [T, Hq, D], sequence s the rows
+    query_start_loc[s] .. query_start_loc[s + 1], seq_lens [S] with the drafted tokens, tree_mask [T, words] int64 (bit k
+    of a row: it sees the k-th drafted token); workspace of at least pa_tree_workspace_size(Hq, Hkv, D, max_q_len) bytes."""
+    torch = _torch()
+    ty, dt = q.dtype, _dtype_code(q)
+    nb, bs, hkv, d = _dims(k_cache, "k_cache", "[num_blocks, block_size, Hkv, D]", 4)
+    rows, hq, _ = _dims(q, "q", "[T, Hq, D]", 3)
+    n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
+    _, words = _dims(tree_mask, "tree_mask", "[T, words]", 2)
+    dev = _device(q)
+    wp, wb = _workspace(workspace, dev)
+    _check(load().pa_tree_decode(
+        _flat(out, "out", ty, (rows, hq, d), dev), _flat(q, "q", ty, (rows, hq, d), dev),
+        _flat(k_cache, "k_cache", ty, (nb, bs, hkv, d), dev), _flat(v_cache, "v_cache", ty, (nb, bs, hkv, d), dev),
+        _flat(block_tables, "block_tables", torch.int32, (n, mb), dev), mb,
+        _flat(query_start_loc, "query_start_loc", torch.int32, (n + 1,), dev), _flat(seq_lens, "seq_lens", torch.int32, (n,), dev),
+        _flat(tree_mask, "tree_mask", torch.int64, (rows, words), dev), words, n, int(max_q_len), rows, hq, hkv, d, bs, nb,
+        float(scale), dt, wp, wb, _raw_stream(stream, dev)), "pa_tree_decode")
+
+
+def _workspace(workspace, dev):
+    if workspace is None:
+        return 0, 0
+    return _flat(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.nbytes
+
+
+def _planes(k_cache, v_cache):
+    """(k pointer, v pointer, layers, row bytes, block_size, num_blocks, device) of caches [NB, bs, Hkv, D] or, of all
+    layers, [L, NB, bs, Hkv, D]; v_cache None: of one array a layer, [NB, bs, row] or [L, NB, bs, row]."""
+    inner = 2 if v_cache is not None else 1
+    if k_cache.dim() not in (2 + inner, 3 + inner):
+        raise ValueError("k_cache must be " + ("[num_blocks, block_size, Hkv, D]" if inner == 2 else "[num_blocks, block_size, row]")
+                         + f" (layers before it where there are several), got {list(k_cache.shape)}")
+    _dtype_code(k_cache)
+    dev, shape = _device(k_cache), k_cache.shape
+    layers = shape[0] if len(shape) == 3 + inner else 1
+    nb, bs = shape[-2 - inner], shape[-1 - inner]
+    row = shape[-1] * (shape[-2] if inner == 2 else 1) * 2
+    kp = _flat(k_cache, "k_cache", k_cache.dtype, shape, dev)
+    vp = None if v_cache is None else _flat(v_cache, "v_cache", k_cache.dtype, shape, dev)
+    return kp, vp, layers, row, bs, nb, dev
+
+
+def pa_tree_commit(k_cache, v_cache, block_tables, query_start_loc, seq_lens, path, num_accepted, new_lens, stream=None) -> None:
+    """The accepted drafted tokens' rows moved to the front: row ctx + path[s][i] of every layer to ctx + i for i <
+    num_accepted[s] (path [S, P] int32, rising), new_lens [S] = ctx + num_accepted.  Caches [NB, bs, Hkv, D] or, of all
+    layers, [L, NB, bs, Hkv, D]; v_cache None with k_cache a latent cache [NB, bs, row] or [L, NB, bs, row]."""
+    i32 = _torch().int32
+    kp, vp, layers, row, bs, nb, dev = _planes(k_cache, v_cache)
+    n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
+    _, most = _dims(path, "path", "[sequences, max_path]", 2)
+    _check(load().pa_tree_commit(
+        kp, vp, layers, _flat(block_tables, "block_tables", i32, (n, mb), dev), mb,
+        _flat(query_start_loc, "query_start_loc", i32, (n + 1,), dev), _flat(seq_lens, "seq_lens", i32, (n,), dev),
+        _flat(path, "path", i32, (n, most), dev), most, _flat(num_accepted, "num_accepted", i32, (n,), dev),
+        _flat(new_lens, "new_lens", i32, (n,), dev), n, row, bs, nb, _raw_stream(stream, dev)), "pa_tree_commit")
+
+
+def pa_copy_pages(k_cache, v_cache, pairs, stream=None) -> None:
+    """Page pairs[i][0] copied to page pairs[i][1] (int32 [N, 2]; -1 skips) in all layers of the caches (as
+    pa_tree_commit)."""
+    kp, vp, layers, row, bs, nb, dev = _planes(k_cache, v_cache)
+    n, _ = _dims(pairs, "pairs", "[N, 2]", 2)
+    _check(load().pa_copy_pages(kp, vp, layers, _flat(pairs, "pairs", _torch().int32, (n, 2), dev), n, row, bs, nb,
+                                _raw_stream(stream, dev)), "pa_copy_pages")
+
+
+def pa_fork_pages(block_tables, seq_lens, parents, ref_counts, block_size: int, stream=None) -> None:
+    """Empty sequences s with parents[s] >= 0 become forks of them: the same pages (counts + 1) and length."""
+    i32 = _torch().int32
+    n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
+    nb, = _dims(ref_counts, "ref_counts", "[num_blocks]", 1)
+    dev = _device(block_tables)
+    _check(load().pa_fork_pages(
+        _flat(block_tables, "block_tables", i32, (n, mb), dev), mb, _flat(seq_lens, "seq_lens", i32, (n,), dev),
+        _flat(parents, "parents", i32, (n,), dev), n, _flat(ref_counts, "ref_counts", i32, (nb,), dev), int(block_size), nb,
+        _raw_stream(stream, dev)), "pa_fork_pages")
+
+
+def pa_resize_workspace_size(num_seqs: int, num_blocks: int) -> int:
+    return int(load().pa_resize_workspace_size(num_seqs, num_blocks))
+
+
+def pa_resize_pages(k_cache, v_cache, block_tables, seq_lens, new_lens, ref_counts, free_list, free_count, workspace,
+                    stream=None) -> None:
+    """Sequences to new_lens [S] (-1: unchanged; seq_lens is updated): pages from and back to the free list, a shared
+    last page copied before it is written.  Caches as pa_tree_commit; ref_counts and free_list [NB], free_count [1],
+    all int32; workspace of at least pa_resize_workspace_size(S, NB) bytes."""
+    i32 = _torch().int32
+    kp, vp, layers, row, bs, nb, dev = _planes(k_cache, v_cache)
+    n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
+    wp, wb = _workspace(workspace, dev)
+    _check(load().pa_resize_pages(
+        kp, vp, layers, _flat(block_tables, "block_tables", i32, (n, mb), dev), mb, _flat(seq_lens, "seq_lens", i32, (n,), dev),
+        _flat(new_lens, "new_lens", i32, (n,), dev), n, _flat(ref_counts, "ref_counts", i32, (nb,), dev),
+        _flat(free_list, "free_list", i32, (nb,), dev), _flat(free_count, "free_count", i32, (1,), dev), row, bs, nb, wp, wb,
+        _raw_stream(stream, dev)), "pa_resize_pages")
 
 
 def pa_device_errors(clear: bool = True) -> int:

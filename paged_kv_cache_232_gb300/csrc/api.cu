@@ -13,6 +13,7 @@
 
 #include "kv_write.cuh"
 #include "norm_rope_write.cuh"
+#include "pages.cuh"
 #include "rope_write.cuh"
 #include "pa_launch.h"
 #include "pagedattn.h"
@@ -1050,6 +1051,300 @@ int pa_latent_prefill_chunk(void* out, const void* q, const void* latent_cache, 
     return latent_impl(out, q, latent_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens, num_chunks,
                        max_q_len, total_q, n_heads, latent_dim, rope_dim, block_size, num_blocks, scale, dtype,
                        workspace, workspace_bytes, stream, true);
+}
+
+// ---- pages: copies, accepted rows, forks, new lengths ------------------------------------------------
+
+static int block_size_ok(int block_size) {
+    return block_size == 8 || block_size == 16 || block_size == 32 || block_size == 64 || block_size == 128;
+}
+
+// The caches of all layers as planes; PA_OK or what is wrong with them.
+static int fill_planes(pa::Planes* c, void* k_cache, void* v_cache, int num_layers, int64_t row_bytes, int block_size,
+                       int64_t num_blocks) {
+    if (num_layers <= 0 || row_bytes <= 0 || block_size <= 0 || num_blocks <= 0) return PA_ERR_SHAPE;
+    if (!block_size_ok(block_size) || row_bytes % 16) return PA_ERR_UNSUPPORTED;
+    // chunks of a page and planes are 32-bit numbers in the kernels
+    if (num_blocks > INT32_MAX - 32 || row_bytes / 16 > INT32_MAX / 128 || num_layers > (1 << 16)) return PA_ERR_UNSUPPORTED;
+    c->k = static_cast<uint4*>(k_cache);
+    c->v = static_cast<uint4*>(v_cache);
+    c->layers = num_layers;
+    c->planes = v_cache ? 2 * num_layers : num_layers;
+    c->row_vecs = (int)(row_bytes / 16);
+    c->block_size = block_size;
+    c->plane_vecs = num_blocks * block_size * (row_bytes / 16);
+    c->num_blocks = (int)num_blocks;
+    return PA_OK;
+}
+
+static int check_table(int num_seqs, int max_blocks_per_seq, int block_size, int64_t num_blocks) {
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0) return PA_ERR_SHAPE;
+    if (!block_size_ok(block_size) || num_blocks > INT32_MAX - 32) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - 1024) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+int pa_copy_pages(void* k_cache, void* v_cache, int num_layers, const int32_t* pairs, int64_t num_pairs, int64_t row_bytes,
+                  int block_size, int64_t num_blocks, void* stream) {
+    pa::Planes c{};
+    if (num_pairs < 0) return PA_ERR_SHAPE;
+    int st = fill_planes(&c, k_cache, v_cache, num_layers, row_bytes, block_size, num_blocks);
+    if (st != PA_OK) return st;
+    const int page_vecs = block_size * c.row_vecs;
+    const int seg_vecs = std::min(page_vecs, pa::kCopyThreads * pa::kCopyUnroll);
+    const int64_t segs = (page_vecs + seg_vecs - 1) / seg_vecs;
+    if (num_pairs > (int64_t)INT32_MAX / c.planes / segs) return PA_ERR_UNSUPPORTED;  // items are 32-bit numbers
+    if (num_pairs == 0) return PA_OK;
+    if (!k_cache || !pairs) return PA_ERR_NULL;
+    if (!aligned16(k_cache) || (v_cache && !aligned16(v_cache))) return PA_ERR_ALIGN;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != PA_OK) return st;
+    int lanes_log2 = 3;
+    while (lanes_log2 < 8 && (pa::kCopyUnroll << lanes_log2) < seg_vecs) ++lanes_log2;
+    const int64_t items = num_pairs * c.planes * segs, per_block = pa::kCopyThreads >> lanes_log2;
+    const int grid = (int)std::min<int64_t>((items + per_block - 1) / per_block,
+                                            (int64_t)dev->sm_count * (2048 / pa::kCopyThreads));
+    pa::copy_pages_kernel<<<grid, pa::kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        c, pairs, (unsigned)items, (unsigned)segs, seg_vecs, page_vecs, lanes_log2, dev->err);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_tree_commit(void* k_cache, void* v_cache, int num_layers, const int32_t* block_tables, int max_blocks_per_seq,
+                   const int32_t* query_start_loc, const int32_t* seq_lens, const int32_t* path, int max_path,
+                   const int32_t* num_accepted, int32_t* new_lens, int num_seqs, int64_t row_bytes, int block_size,
+                   int64_t num_blocks, void* stream) {
+    if (max_path < 0) return PA_ERR_SHAPE;
+    pa::CommitParams p{};
+    int st = check_table(num_seqs, max_blocks_per_seq, block_size, num_blocks);
+    if (st == PA_OK) st = fill_planes(&p.c, k_cache, v_cache, num_layers, row_bytes, block_size, num_blocks);
+    if (st != PA_OK || num_seqs == 0) return st;
+    if (!k_cache || !block_tables || !query_start_loc || !seq_lens || (max_path > 0 && !path) || !num_accepted || !new_lens)
+        return PA_ERR_NULL;
+    if (!aligned16(k_cache) || (v_cache && !aligned16(v_cache))) return PA_ERR_ALIGN;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != PA_OK) return st;
+    p.block_tables = block_tables;
+    p.query_start_loc = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.path = path;
+    p.num_accepted = num_accepted;
+    p.new_lens = new_lens;
+    p.err = dev->err;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_path = max_path;
+    p.num_seqs = num_seqs;
+    const int64_t columns = (int64_t)p.c.planes * p.c.row_vecs;
+    const int64_t slots = (int64_t)dev->sm_count * (2048 / pa::kCommitThreads);
+    const int64_t y = std::min<int64_t>((columns + pa::kCommitThreads - 1) / pa::kCommitThreads,
+                                        std::max<int64_t>(1, slots / num_seqs));
+    pa::tree_commit_kernel<<<dim3((unsigned)num_seqs, (unsigned)std::min<int64_t>(y, 65535)), pa::kCommitThreads, 0,
+                             static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_fork_pages(int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_lens, const int32_t* parents, int num_seqs,
+                  int32_t* ref_counts, int block_size, int64_t num_blocks, void* stream) {
+    int st = check_table(num_seqs, max_blocks_per_seq, block_size, num_blocks);
+    if (st != PA_OK || num_seqs == 0) return st;
+    if (!block_tables || !seq_lens || !parents || !ref_counts) return PA_ERR_NULL;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != PA_OK) return st;
+    pa::fork_pages_kernel<<<num_seqs, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        block_tables, max_blocks_per_seq, seq_lens, parents, num_seqs, ref_counts, block_size, (int)num_blocks, dev->err);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+struct ResizeWs {
+    size_t plan_off, bits_off, total;
+};
+
+static ResizeWs resize_ws(int num_seqs, int64_t num_blocks) {
+    ResizeWs w;
+    w.plan_off = 256;
+    w.bits_off = w.plan_off + align256((size_t)num_seqs * sizeof(pa::ResizePlan));
+    w.total = w.bits_off + align256((size_t)((num_blocks + 31) / 32) * 4);
+    return w;
+}
+
+size_t pa_resize_workspace_size(int num_seqs, int64_t num_blocks) {
+    return num_seqs <= 0 || num_blocks <= 0 || num_blocks > INT32_MAX - 32 ? 0 : resize_ws(num_seqs, num_blocks).total;
+}
+
+int pa_resize_pages(void* k_cache, void* v_cache, int num_layers, int32_t* block_tables, int max_blocks_per_seq,
+                    int32_t* seq_lens, const int32_t* new_lens, int num_seqs, int32_t* ref_counts, int32_t* free_list,
+                    int32_t* free_count, int64_t row_bytes, int block_size, int64_t num_blocks, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    pa::ResizeParams p{};
+    int st = check_table(num_seqs, max_blocks_per_seq, block_size, num_blocks);
+    if (st == PA_OK) st = fill_planes(&p.c, k_cache, v_cache, num_layers, row_bytes, block_size, num_blocks);
+    if (st != PA_OK || num_seqs == 0) return st;
+    if (!k_cache || !block_tables || !seq_lens || !new_lens || !ref_counts || !free_list || !free_count) return PA_ERR_NULL;
+    if (!aligned16(k_cache) || (v_cache && !aligned16(v_cache))) return PA_ERR_ALIGN;
+    const ResizeWs w = resize_ws(num_seqs, num_blocks);
+    if (!workspace || workspace_bytes < w.total) return PA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PA_ERR_ALIGN;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != PA_OK) return st;
+    char* base = static_cast<char*>(workspace);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.ref_counts = ref_counts;
+    p.free_list = free_list;
+    p.free_count = free_count;
+    p.new_lens = new_lens;
+    p.head = reinterpret_cast<pa::ResizeHead*>(base);
+    p.plan = reinterpret_cast<pa::ResizePlan*>(base + w.plan_off);
+    p.bits = reinterpret_cast<unsigned*>(base + w.bits_off);
+    p.err = dev->err;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    pa::resize_plan_kernel<<<1, pa::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    // blocks a sequence: a block's share of a page that is copied in all planes, while all blocks still run at once
+    const int64_t vecs = (int64_t)p.c.planes * block_size * p.c.row_vecs, share = pa::kApplyThreads * pa::kCopyUnroll;
+    const int64_t slots = (int64_t)dev->sm_count * (2048 / pa::kApplyThreads);
+    const int64_t y = std::min(std::min<int64_t>((vecs + share - 1) / share, p.c.planes),
+                               std::max<int64_t>(1, slots / num_seqs));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)num_seqs, (unsigned)std::min<int64_t>(y, 65535));
+    cfg.blockDim = dim3(pa::kApplyThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pa::resize_apply_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// ---- trees of drafted tokens --------------------------------------------------------------------------
+
+int pa_tree_mask(int64_t* mask, int32_t* depth, const int32_t* parents, int num_tokens, int mask_words) {
+    if (num_tokens < 0 || mask_words < 0 || (int64_t)mask_words * 64 < num_tokens) return PA_ERR_SHAPE;
+    if (num_tokens == 0) return PA_OK;
+    if (!mask || !parents) return PA_ERR_NULL;
+    for (int j = 0; j < num_tokens; ++j)
+        if (parents[j] < -1 || parents[j] >= j) return PA_ERR_BOUNDS;
+    for (int j = 0; j < num_tokens; ++j) {
+        int64_t* row = mask + (int64_t)j * mask_words;
+        const int up = parents[j];
+        for (int w = 0; w < mask_words; ++w) row[w] = up < 0 ? 0 : mask[(int64_t)up * mask_words + w];
+        row[j / 64] |= (int64_t)(uint64_t(1) << (j % 64));
+        if (depth) depth[j] = up < 0 ? 0 : depth[up] + 1;
+    }
+    return PA_OK;
+}
+
+static int check_tree(int n_q_heads, int n_kv_heads, int head_dim, int block_size, int dtype) {
+    if (n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || n_q_heads % n_kv_heads) return PA_ERR_SHAPE;
+    if (n_q_heads / n_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256) return PA_ERR_UNSUPPORTED;
+    if (!block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+struct TreeUnits {
+    int tb, group, rows;  // tokens a unit, CTAs that walk the same keys, query rows the kernel is built for
+};
+
+// Blocks of at most 128 rows, of equal numbers of tokens; up to 8 of them side by side.
+static TreeUnits tree_units(int g_heads, int max_q_len) {
+    const int most = 128 / g_heads, blocks = (max_q_len + most - 1) / most;
+    TreeUnits u;
+    u.tb = (max_q_len + blocks - 1) / blocks;
+    const int passes = (blocks + 7) / 8;
+    u.group = (blocks + passes - 1) / passes;
+    u.rows = u.tb * g_heads <= 32 ? 32 : u.tb * g_heads <= 64 ? 64 : 128;
+    return u;
+}
+
+struct TreeWs {
+    size_t ml_off, o_off, total;
+};
+
+static TreeWs tree_ws(int unit_rows, int kdim) {
+    const size_t slots = 2 * (size_t)PA_TREE_MAX_CTAS;  // two a CTA
+    TreeWs w;
+    w.ml_off = align256(2 * PA_TREE_MAX_CTAS * sizeof(int4));
+    w.o_off = w.ml_off + align256(slots * unit_rows * 2 * sizeof(float));
+    w.total = w.o_off + slots * unit_rows * kdim * sizeof(float);
+    return w;
+}
+
+size_t pa_tree_workspace_size(int n_q_heads, int n_kv_heads, int head_dim, int max_q_len) {
+    if (max_q_len <= 0 || check_tree(n_q_heads, n_kv_heads, head_dim, 16, PA_BF16) != PA_OK) return 0;
+    return tree_ws(tree_units(n_q_heads / n_kv_heads, max_q_len).rows, kernel_dim(head_dim)).total;
+}
+
+int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                   int max_blocks_per_seq, const int32_t* query_start_loc, const int32_t* seq_lens, const int64_t* tree_mask,
+                   int mask_words, int num_seqs, int max_q_len, int64_t total_q, int n_q_heads, int n_kv_heads, int head_dim,
+                   int block_size, int64_t num_blocks, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+    if (num_seqs < 0 || max_q_len < 0 || total_q < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || mask_words < 0)
+        return PA_ERR_SHAPE;
+    int st = check_tree(n_q_heads, n_kv_heads, head_dim, block_size, dtype);
+    if (st != PA_OK) return st;
+    if ((int64_t)mask_words * 64 < max_q_len || !std::isfinite(scale)) return PA_ERR_SHAPE;
+    // token, block and output-row numbers are 32-bit in the kernel (tile ends included)
+    if (num_blocks >= INT32_MAX || (int64_t)max_blocks_per_seq * block_size > INT32_MAX - 1024 || max_q_len > (1 << 24) ||
+        mask_words > (1 << 24) || total_q > INT32_MAX - 1024 || total_q * n_q_heads > INT32_MAX - 1024)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_q_len == 0 || total_q == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !query_start_loc || !seq_lens || !tree_mask) return PA_ERR_NULL;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGN;
+    const int G = n_q_heads / n_kv_heads, kdim = kernel_dim(head_dim);
+    const TreeUnits u = tree_units(G, max_q_len);
+    const TreeWs w = tree_ws(u.rows, kdim);
+    if (!workspace || workspace_bytes < w.total) return PA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PA_ERR_ALIGN;
+    DeviceState* dev = nullptr;
+    if ((st = device_state(&dev)) != PA_OK) return st;
+    char* base = static_cast<char*>(workspace);
+    pa::TreeParams p{};
+    p.out = out;
+    p.block_tables = block_tables;
+    p.q_loc = query_start_loc;
+    p.kv_lens = seq_lens;
+    p.mask = tree_mask;
+    p.err = dev->err;
+    p.num_seqs = num_seqs;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.g_heads = G;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_blocks = (int)num_blocks;
+    p.block_size = block_size;
+    p.max_q_len = max_q_len;
+    p.total_q = (int)total_q;
+    p.mask_words = mask_words;
+    p.hd = head_dim;
+    p.tb = u.tb;
+    p.group = u.group;
+    p.tile_log2 = kdim == 256 ? 6 : 7;
+    p.block_log2 = 4 + cpb_log2_of(block_size);
+    p.unit_cost = 1;
+    p.min_tiles = 2;
+    p.qk_scale_log2 = scale * 1.4426950408889634f;
+    p.desc = reinterpret_cast<int4*>(base);
+    p.part_ml = reinterpret_cast<float*>(base + w.ml_off);
+    p.part_o = reinterpret_cast<float*>(base + w.o_off);
+    CUtensorMap tk, tv, tq;
+    if ((st = encode_cache_map(&tk, k_cache, dtype, num_blocks, block_size, n_kv_heads, head_dim)) != PA_OK) return st;
+    if ((st = encode_cache_map(&tv, v_cache, dtype, num_blocks, block_size, n_kv_heads, head_dim)) != PA_OK) return st;
+    // q [total_q, n_q_heads, head_dim]: boxes of 64 columns x the group's heads x the unit's tokens
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)n_q_heads, (cuuint64_t)total_q};
+    cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)n_q_heads * head_dim * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)u.tb};
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (g_encode(&tq, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                 const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return PA_ERR_CUDA;
+    const int ctas = std::min(dev->sm_count, PA_TREE_MAX_CTAS) / u.group * u.group;
+    cudaError_t e = pa::launch_tree(dtype == PA_BF16, kdim, u.rows, p, tk, tv, tq, ctas, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -143,4 +143,30 @@ inline int latent_unit_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32
 cudaError_t launch_latent(int bf16, int latent_dim, int unit_rows, const LatentParams& params, const CUtensorMap& tmC,
                           const CUtensorMap& tmQ, int ctas, cudaStream_t stream);
 
+// Attention of trees of drafted tokens over the paged cache (tree_kernel.cuh).
+struct TreeParams {
+    void* out;                  // [total_q, n_q_heads, hd]
+    const int32_t* block_tables;
+    const int32_t* q_loc;       // [num_seqs + 1] first query row of each sequence
+    const int32_t* kv_lens;     // [num_seqs], the drafted tokens included
+    const int64_t* mask;        // [total_q, mask_words]
+    unsigned* err;
+    int num_seqs, n_q_heads, n_kv_heads, g_heads, max_blocks_per_seq, num_blocks, block_size, max_q_len, total_q, mask_words;
+    int hd;                     // head_dim of q, out and the cache (<= D; columns hd .. D-1 are zero)
+    int tb;                     // tokens per unit of query rows
+    int group;                  // CTAs that walk the same keys, each with a block of tb tokens of the tree
+    int tile_log2, block_log2;  // log2 of the tokens per tile, per cache block
+    int unit_cost;              // what a unit's start and output cost, in tiles (evens out the ranges)
+    int min_tiles;              // least cost of a range
+    float qk_scale_log2;
+    float* part_o;              // [2 * ctas][NR][D]
+    float* part_ml;             // [2 * ctas][NR][2]: reference (base 2) and exp-sum
+    int4* desc;                 // [2][ctas]: the units cut at a range's end and at its start (partials, query rows,
+                                // first row of out, CTA they start in)
+};
+
+// unit_rows 32, 64 or 128; ctas: a multiple of params.group.
+cudaError_t launch_tree(int bf16, int head_dim, int unit_rows, const TreeParams& params, const CUtensorMap& tmK,
+                        const CUtensorMap& tmV, const CUtensorMap& tmQ, int ctas, cudaStream_t stream);
+
 }  // namespace pa

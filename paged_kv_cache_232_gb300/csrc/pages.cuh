@@ -1,0 +1,391 @@
+// pages.cuh -- what moves, shares, takes and frees the pages of a cache between two forward passes:
+// copies of pages, the accepted rows of a verified tree moved to the front of its drafted ones, forks of
+// sequences, and sequences brought to new lengths (pages from and back to a free list, a shared last page
+// copied before it is written).  The data are moved bit by bit, in all layers of a model by one call: a
+// cache is `planes` arrays (layers, K and V) of [num_blocks, block_size, row].
+//
+// All of it is memory traffic and latency.  The copies keep eight 16-byte loads in flight a thread.
+#pragma once
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+// K and V (or the latent rows alone) of all layers: plane l is layer l of k, plane layers + l layer l of v.
+struct Planes {
+    uint4 *k, *v;            // v: null where the cache is one array a layer
+    int layers, planes;
+    int row_vecs, block_size;
+    int64_t plane_vecs;      // 16-byte chunks of a layer's array
+    int num_blocks;
+};
+
+__device__ __forceinline__ uint4* plane_of(const Planes& c, int plane) {
+    return plane < c.layers ? c.k + plane * c.plane_vecs : c.v + (plane - c.layers) * c.plane_vecs;
+}
+
+// (not the read-only path: the same call writes other pages of this array)
+__device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+constexpr int kCopyThreads = 256, kCopyUnroll = 8;
+
+// Pages pairs[i][0] -> pairs[i][1] of every plane.  An item is a segment of one page of one plane, worked by
+// `lanes` threads (a power of two) with kCopyUnroll chunks each in flight.
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Planes c, const int32_t* __restrict__ pairs, unsigned items,
+                                                                 unsigned segs, int seg_vecs, int page_vecs, int lanes_log2,
+                                                                 unsigned* err) {
+    constexpr int U = kCopyUnroll;
+    const unsigned per_block = kCopyThreads >> lanes_log2;
+    const int lanes = 1 << lanes_log2, lane = threadIdx.x & (lanes - 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (unsigned it = blockIdx.x * per_block + (threadIdx.x >> lanes_log2); it < items; it += gridDim.x * per_block) {
+        const unsigned rest = it / segs, seg = it - rest * segs;
+        const unsigned pair = rest / (unsigned)c.planes, plane = rest - pair * (unsigned)c.planes;
+        const int src = __ldg(pairs + 2 * (size_t)pair), dst = __ldg(pairs + 2 * (size_t)pair + 1);
+        if (src == -1 || dst == -1) continue;
+        if (src < 0 || src >= c.num_blocks || dst < 0 || dst >= c.num_blocks) {
+            if (lane == 0) flag_error(err, PA_DEVERR_BLOCK);
+            continue;
+        }
+        uint4* const base = plane_of(c, (int)plane);
+        const int v0 = (int)seg * seg_vecs, n = min(seg_vecs, page_vecs - v0);
+        const uint4* s = base + (size_t)src * page_vecs + v0;
+        uint4* d = base + (size_t)dst * page_vecs + v0;
+        for (int e = lane; e < n; e += U * lanes) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e + u * lanes < n) x[u] = ldg_stream(s + e + u * lanes);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e + u * lanes < n) d[e + u * lanes] = x[u];
+        }
+    }
+}
+
+// ---- the accepted path of a verified tree --------------------------------------------------------
+
+struct CommitParams {
+    Planes c;
+    const int32_t *block_tables, *query_start_loc, *seq_lens, *path, *num_accepted;
+    int32_t* new_lens;
+    unsigned* err;
+    int max_blocks_per_seq, max_path, num_seqs;
+};
+
+constexpr int kCommitThreads = 256, kCommitRows = 256;  // threads; rows of a path in shared memory at a time
+
+// Row ctx + path[i] -> ctx + i for i < accepted, path rising: path[i] >= i, so a column of 16 bytes that one
+// thread moves in this order (loads of a few rows, then their stores) reads every row before it is overwritten:
+// row ctx + j is stored for i = j and read for the i with path[i] = j, which is at most j.
+__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitParams p) {
+    constexpr int U = 8;
+    __shared__ int64_t from[kCommitRows], to[kCommitRows];  // rows of a plane; -1: not moved
+    const int s = blockIdx.x, tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n = __ldg(p.query_start_loc + s + 1) - __ldg(p.query_start_loc + s), kv_len = __ldg(p.seq_lens + s);
+    const int acc = __ldg(p.num_accepted + s), ctx = kv_len - n;
+    const int cap = p.max_blocks_per_seq * p.c.block_size;
+    const bool bad_len = n < 0 || kv_len < n || kv_len > cap;
+    const int32_t* path = p.path + (size_t)s * p.max_path;
+    bool bad = !bad_len && (acc < 0 || acc > n || acc > p.max_path);
+    if (!bad && !bad_len) {
+        bool mine = false;
+        for (int i = tid; i < acc; i += kCommitThreads) {
+            const int t = __ldg(path + i), before = i > 0 ? __ldg(path + i - 1) : -1;
+            mine = mine || t <= before || t >= n;
+        }
+        bad = __syncthreads_or(mine);
+    }
+    if (bad_len || bad) {
+        if (blockIdx.y == 0 && tid == 0) {
+            flag_error(p.err, bad_len ? PA_DEVERR_LENGTH : PA_DEVERR_PATH);
+            p.new_lens[s] = bad_len ? kv_len : ctx;
+        }
+        return;
+    }
+    if (blockIdx.y == 0 && tid == 0) p.new_lens[s] = ctx + acc;
+    const int32_t* bt = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+    const int bs = p.c.block_size;
+    const int64_t columns = (int64_t)p.c.planes * p.c.row_vecs;
+    for (int i0 = 0; i0 < acc; i0 += kCommitRows) {
+        const int rows = min(kCommitRows, acc - i0);
+        __syncthreads();
+        if (tid < rows) {
+            const int a = ctx + __ldg(path + i0 + tid), b = ctx + i0 + tid;
+            int64_t f = -1, t = -1;
+            if (a != b) {
+                const int pa_ = __ldg(bt + a / bs), pb = __ldg(bt + b / bs);
+                if (pa_ < 0 || pa_ >= p.c.num_blocks || pb < 0 || pb >= p.c.num_blocks) {
+                    flag_error(p.err, PA_DEVERR_BLOCK);
+                } else {
+                    f = ((int64_t)pa_ * bs + a % bs) * p.c.row_vecs;
+                    t = ((int64_t)pb * bs + b % bs) * p.c.row_vecs;
+                }
+            }
+            from[tid] = f;
+            to[tid] = t;
+        }
+        __syncthreads();
+        for (int64_t col = (int64_t)blockIdx.y * kCommitThreads + tid; col < columns; col += (int64_t)gridDim.y * kCommitThreads) {
+            const int plane = (int)(col / p.c.row_vecs);
+            uint4* const base = plane_of(p.c, plane) + (col - (int64_t)plane * p.c.row_vecs);
+            for (int i = 0; i < rows; i += U) {
+                uint4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u < rows && from[i + u] >= 0) x[u] = ldg_stream(base + from[i + u]);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u < rows && from[i + u] >= 0) base[to[i + u]] = x[u];
+            }
+        }
+    }
+}
+
+// ---- forks ---------------------------------------------------------------------------------------
+
+// Sequence s, which is empty, becomes a fork of parents[s]: the same pages, one reference more each.  A block a
+// sequence.  No block reads what another writes: a parent is nobody's child in the call.
+__global__ void __launch_bounds__(256) fork_pages_kernel(int32_t* block_tables, int mb, int32_t* seq_lens,
+                                                         const int32_t* __restrict__ parents, int num_seqs, int32_t* ref_counts,
+                                                         int block_size, int num_blocks, unsigned* err) {
+    const int s = blockIdx.x, tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int par = __ldg(parents + s);
+    if (par == -1) return;
+    const bool known = par >= 0 && par < num_seqs;
+    const int grand = known ? __ldg(parents + par) : 0, own = seq_lens[s], len = known ? seq_lens[par] : 0;
+    __syncthreads();  // every thread has read the lengths before one of them is written
+    if (!known || grand != -1 || own != 0) {
+        if (tid == 0) flag_error(err, PA_DEVERR_FORK);
+        return;
+    }
+    if (len < 0 || len > mb * block_size) {
+        if (tid == 0) flag_error(err, PA_DEVERR_LENGTH);
+        return;
+    }
+    const int pages = (len + block_size - 1) / block_size;
+    const int32_t* from = block_tables + (size_t)par * mb;
+    int32_t* to = block_tables + (size_t)s * mb;
+    for (int c = tid; c < pages; c += 256) {
+        const int id = from[c];
+        to[c] = id;
+        if (id >= 0 && id < num_blocks) atomicAdd(ref_counts + id, 1);
+        else flag_error(err, PA_DEVERR_BLOCK);
+    }
+    if (tid == 0) seq_lens[s] = len;
+}
+
+// ---- new lengths -----------------------------------------------------------------------------------
+
+// What the plan leaves for a sequence: first of its pages among those taken from the free list (-1: nothing to
+// do), the shared last page that it copies (-1: none), its pages before and after.
+struct ResizePlan {
+    int start, cow, have, want;
+};
+struct ResizeHead {
+    int top, taken;          // entries of the free list before the call, those taken
+    unsigned ticket, freed;  // blocks done, pages whose last reference went
+};
+
+struct ResizeParams {
+    Planes c;
+    int32_t *block_tables, *seq_lens, *ref_counts, *free_list, *free_count;
+    const int32_t* new_lens;
+    ResizeHead* head;
+    ResizePlan* plan;        // [num_seqs]
+    unsigned* bits;          // [ceil(num_blocks / 32)]: pages that got free
+    unsigned* err;
+    int max_blocks_per_seq, num_seqs;
+};
+
+constexpr int kPlanThreads = 1024, kApplyThreads = 256;
+
+// One block: which sequences get their pages (in their order, as long as the free list lasts), where these
+// stand in the list, and which shared pages are copied -- all from the state before the call.
+__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(const ResizeParams p) {
+    __shared__ long long warp_sum[32];
+    __shared__ int popped;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int words = (p.c.num_blocks + 31) / 32;
+    for (int w = tid; w < words; w += kPlanThreads) p.bits[w] = 0u;
+    int top = *p.free_count;
+    if (top < 0 || top > p.c.num_blocks) {
+        if (tid == 0) flag_error(p.err, PA_DEVERR_COUNT);
+        top = -1;  // the list cannot be used: nothing is taken from it or put back
+    }
+    if (tid == 0) popped = 0;
+    const int bs = p.c.block_size, cap = p.max_blocks_per_seq * bs;
+    long long base = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        ResizePlan r{-1, -1, 0, 0};
+        int demand = 0;
+        if (s < p.num_seqs && top >= 0) {
+            const int want = __ldg(p.new_lens + s), have = p.seq_lens[s];
+            if (want < -1 || want > cap || have < 0 || have > cap) {
+                flag_error(p.err, PA_DEVERR_LENGTH);
+            } else if (want != -1 && want != have) {
+                r.start = 0;
+                r.have = (have + bs - 1) / bs;
+                r.want = (want + bs - 1) / bs;
+                if (want > have) {
+                    demand = r.want - r.have;
+                    if (have % bs) {
+                        const int last = p.block_tables[(size_t)s * p.max_blocks_per_seq + r.have - 1];
+                        if (last < 0 || last >= p.c.num_blocks) {
+                            flag_error(p.err, PA_DEVERR_BLOCK);
+                        } else if (p.ref_counts[last] > 1) {
+                            r.cow = last;
+                            ++demand;
+                        }
+                    }
+                }
+            }
+        }
+        long long end = demand;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += y;
+        }
+        __syncthreads();
+        if (lane == 31) warp_sum[warp] = end;
+        __syncthreads();
+        long long all = 0;
+        end += base;
+#pragma unroll 8
+        for (int w = 0; w < 32; ++w) {
+            const long long x = warp_sum[w];
+            if (w < warp) end += x;
+            all += x;
+        }
+        base += all;
+        if (demand > 0) {
+            if (end <= top) {
+                r.start = (int)(end - demand);
+                atomicMax(&popped, (int)end);
+            } else {
+                flag_error(p.err, PA_DEVERR_PAGES);
+                r.start = -1;
+            }
+        }
+        if (s < p.num_seqs) p.plan[s] = r;
+    }
+    __syncthreads();
+    if (tid == 0) *p.head = ResizeHead{top, popped, 0u, 0u};
+}
+
+// A reference less; the page is marked when that was the last one.
+__device__ __forceinline__ void release_page(const ResizeParams& p, int id) {
+    if (id < 0 || id >= p.c.num_blocks) {
+        flag_error(p.err, PA_DEVERR_BLOCK);
+        return;
+    }
+    const int before = atomicSub(p.ref_counts + id, 1);
+    if (before == 1) {
+        atomicOr(p.bits + (id >> 5), 1u << (id & 31));
+        atomicAdd(&p.head->freed, 1u);
+    } else if (before <= 0) {  // nobody's page: its count stays
+        atomicAdd(p.ref_counts + id, 1);
+        flag_error(p.err, PA_DEVERR_COUNT);
+    }
+}
+
+// A sequence a block column; its first block changes the table and the counts, all of them copy a shared last
+// page's rows.  The block that is done last puts the pages that got free on the list in the order of their
+// numbers, so that the same call leaves the same list whatever the order of the blocks.
+__global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const ResizeParams p) {
+    constexpr int U = kCopyUnroll, NW = kApplyThreads / 32;
+    __shared__ bool last_block;
+    __shared__ int warp_sum[NW];
+    const int s = blockIdx.x, tid = threadIdx.x, bs = p.c.block_size;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ResizePlan r = p.plan[s];
+    const int top = p.head->top;
+    if (r.start >= 0) {
+        int32_t* bt = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+        const int first = r.have - (r.cow >= 0 ? 1 : 0);
+        auto taken = [&](int i) {  // i-th page that the sequence gets, -1 where the list holds no page of the pool
+            const int id = p.free_list[top - 1 - (r.start + i)];
+            return id >= 0 && id < p.c.num_blocks ? id : -1;
+        };
+        if (r.cow >= 0) {
+            // (the lengths are written last of all, below)
+            const int dst = taken(0), n = p.seq_lens[s] % bs * p.c.row_vecs;
+            if (dst >= 0) {
+                const int64_t page = (int64_t)bs * p.c.row_vecs;
+                for (int plane = blockIdx.y; plane < p.c.planes; plane += gridDim.y) {
+                    uint4* const base = plane_of(p.c, plane);
+                    const uint4* from = base + r.cow * page;
+                    uint4* to = base + dst * page;
+                    for (int e = tid; e < n; e += U * kApplyThreads) {
+                        uint4 x[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (e + u * kApplyThreads < n) x[u] = ldg_stream(from + e + u * kApplyThreads);
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (e + u * kApplyThreads < n) to[e + u * kApplyThreads] = x[u];
+                    }
+                }
+            }
+        }
+        if (blockIdx.y == 0) {
+            for (int c = first + tid; c < r.want; c += kApplyThreads) {
+                const int id = taken(c - first);
+                bt[c] = id;
+                if (id < 0 || atomicExch(p.ref_counts + id, 1) != 0) flag_error(p.err, PA_DEVERR_COUNT);
+            }
+            for (int c = r.want + tid; c < r.have; c += kApplyThreads) {
+                release_page(p, bt[c]);
+                bt[c] = -1;
+            }
+            if (r.cow >= 0 && tid == 0) release_page(p, r.cow);
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last_block = atomicAdd(&p.head->ticket, 1u) == gridDim.x * gridDim.y - 1;
+    __syncthreads();
+    if (!last_block) return;
+    __threadfence();
+    // every other block is done: the lengths, and the pages that got free
+    for (int i = tid; i < p.num_seqs; i += kApplyThreads)
+        if (p.plan[i].start >= 0) p.seq_lens[i] = __ldg(p.new_lens + i);
+    if (top < 0) return;
+    const int left = top - p.head->taken, freed = (int)__ldcg(&p.head->freed);
+    if (tid == 0) *p.free_count = min(left + freed, p.c.num_blocks);
+    if (freed == 0) return;
+    if (left + freed > p.c.num_blocks && tid == 0) flag_error(p.err, PA_DEVERR_COUNT);
+    const int words = (p.c.num_blocks + 31) / 32, per = (words + kApplyThreads - 1) / kApplyThreads;
+    const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
+    int mine = 0;
+    for (int w = w0; w < w1; ++w) mine += __popc(__ldcg(p.bits + w));
+    int end = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, end, o);
+        if ((tid & 31) >= o) end += y;
+    }
+    if ((tid & 31) == 31) warp_sum[tid >> 5] = end;
+    __syncthreads();
+    for (int w = 0; w < (tid >> 5); ++w) end += warp_sum[w];
+    int at = left + end - mine;
+    for (int w = w0; w < w1; ++w) {
+        for (unsigned b = __ldcg(p.bits + w); b; b &= b - 1, ++at)
+            if (at < p.c.num_blocks) p.free_list[at] = 32 * w + __ffs(b) - 1;
+    }
+}
+
+}  // namespace pa

@@ -1,0 +1,932 @@
+// tree_kernel.cuh -- attention of trees of drafted tokens over the paged K/V cache, on the tcgen05
+// tensor cores.
+//
+// A sequence holds ctx cached tokens and n drafted ones behind them.  Drafted token j sees the whole
+// context and the drafted tokens k whose bit is set in its mask:
+//     out[j, h] = sum_t softmax_t(scale * q[j, h] . K_t) V_t,  t < ctx, or t = ctx + k with bit k of mask[j],
+// K_t and V_t of KV head h / G.  The tokens of a tree times the G heads of a KV head are the rows of one
+// dense contraction over the same keys: each key is read once for all of them.
+//
+// GB300 design:
+//  * A unit is up to NR query rows (32, 64 or 128) of one sequence and KV head over its keys, in tiles of
+//    BN keys (128; 64 at head_dim 256).  S = Q K^T is one M = 128 product whatever NR is: the tile holds
+//    128 / NR copies of the rows, and each copy takes its own share of the tile's keys.  So 128 threads
+//    (one a row of the tile, a TMEM lane each) share the softmax of few rows without exchanging anything:
+//    a copy is a split of the keys with a maximum and a sum of its own, and the copies are joined once, at
+//    the unit's end.  The weights go back to TMEM as the A operand of O += P V, with zeros in the columns
+//    of the other copies' keys (written once: no copy ever writes there).
+//  * K and V arrive by TMA in boxes of 16 tokens (8 in blocks of 8) x 64 columns, 128-byte swizzled, in two
+//    rings of whole tiles; K is released by its product, V by its own.  QK and PV have an issuer each.
+//  * The running maximum is lazy: weights are taken against the old one, and only where one exceeds it by
+//    2^8 are the maximum raised (to a whole power of two) and O and l rescaled.  Weights up to 2^8 are exact
+//    in fp32 and far from the 16-bit formats' limits.
+//  * A weight enters the second product rounded once to the cache's type (half a step, 2^-8 in bf16 and 2^-11
+//    in fp16, relative), and l sums the rounded weights, so that they still sum to one; everything else is
+//    fp32.  In fp16 weights are scaled by 2^7, so that small ones are not subnormal.
+//  * All units laid end to end and measured in cost (a unit's start and output, then its tiles) are cut into
+//    equal ranges, one a CTA; units that a range's end cuts leave fp32 partials which tree_merge_kernel joins in
+//    a fixed order.  No host-side lengths, no atomics, two partials a CTA.  Trees of more than 128 rows are `group`
+//    blocks of tokens (further ones in further passes), worked by CTAs next to each other, which walk the same keys
+//    at the same time and so share them in L2 (one after the other they would be read from DRAM again).
+//  * The cache rows of drafted tokens that some row does not see may hold anything (a padded token's row was never
+//    written): scores are replaced before the softmax, and a drafted V row that is not finite is zeroed in
+//    shared memory, the rows that see it becoming NaN.
+//  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set and the role goes on without waiting, so that
+//    every barrier of the block is still met; its results are not used.
+#pragma once
+
+#include "pa_launch.h"
+#include "tcgen05.cuh"
+
+#include <type_traits>
+
+namespace pa {
+namespace tree {
+
+template <bool BF16>
+constexpr float kShift = BF16 ? 0.f : 7.f;
+
+constexpr int SOFTMAX_WARPS = 4, QK_WARP = 4, PV_WARP = 5, Q_WARP = 6, K_WARP = 7, V_WARP = 9;
+constexpr int THREADS = 11 * 32;        // two warps load K, two load V: every second box each
+constexpr int MERGE_THREADS = 256;
+static_assert(PA_TREE_MAX_CTAS <= MERGE_THREADS, "the merge gives every partial of a unit a thread");
+
+template <int D, int NR>
+struct Cfg {
+    static_assert(D == 64 || D == 128 || D == 256, "head_dim of the kernel");
+    static_assert(NR == 32 || NR == 64 || NR == 128, "query rows of a unit");
+    static constexpr int BN = D == 256 ? 64 : 128;      // keys per tile
+    static constexpr int COPIES = 128 / NR;
+    static constexpr int KW = BN / COPIES;              // keys of a tile that one thread takes
+    static constexpr int SLABS = D / 64;
+    static constexpr int QSLAB = 128 * 128, KSLAB = BN * 128;
+    static constexpr int TILE = SLABS * KSLAB;          // bytes of K (or V) of a tile
+    static constexpr int NK = D == 64 ? 6 : 3, NV = D == 64 ? 6 : D == 256 ? 2 : 3;  // tiles in the rings (D 256: Q takes 64 KB)
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = SLABS * QSLAB, V_OFF = K_OFF + NK * TILE;
+    static constexpr int ML_OFF = V_OFF + NV * TILE;    // m and l of the tile's 128 rows
+    static constexpr int BAR_OFF = ML_OFF + 2 * 128 * 4;
+    static constexpr int K_FULL = 0, K_EMPTY = NK, V_FULL = 2 * NK, V_EMPTY = V_FULL + NV, Q_FULL = V_EMPTY + NV, Q_EMPTY = Q_FULL + 1,
+                         S_FULL = Q_FULL + 2, S_EMPTY = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
+                         O_FREE = Q_FULL + 10, DRAIN = Q_FULL + 11, NUM_BARS = Q_FULL + 13;
+    static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch, bad keys
+    static constexpr int SMEM_BYTES = MISC_OFF + 192 + 1024;             // + alignment slack
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert(COPIES == 1 || NR * D * 4 <= SLABS * QSLAB, "the copies are joined in the Q tile's place");
+    // TMEM: two S buffers, two P buffers (16-bit pairs), O
+    static constexpr uint32_t P_COL = D == 256 ? 128 : 384, O_COL = 256, TMEM_COLS = 512;
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t el, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t el, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                        uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %8, 0;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// barrier of the four softmax warps, plain and with an OR over them
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// The warp waits; the polling loop stays out of line.  One result for the warp.
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned* err) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
+    if (__any_sync(0xffffffffu, !mbar_try_wait(bar, parity))) return wait_slow(bar, parity, err);
+    return true;
+}
+
+template <int N>
+__device__ __forceinline__ void ldn(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 16) tc::ld16(taddr, r);
+    else if constexpr (N == 32) tc::ld32(taddr, r);
+    else tc::ld64(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void stn(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else if constexpr (N == 16) tc::st16(taddr, r);
+    else tc::st32(taddr, r);
+}
+
+// ---- the split of all units' tiles over the CTAs ---------------------------------------------
+
+// A sequence: its first query row (token), drafted tokens and keys.  Lengths out of range: it is skipped.
+struct Seq {
+    int q0, n, kv_len;
+    bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const TreeParams& p, int s) {
+    Seq k;
+    k.kv_len = __ldg(p.kv_lens + s);
+    k.q0 = __ldg(p.q_loc + s);
+    const int q1 = __ldg(p.q_loc + s + 1);
+    k.n = q1 - k.q0;
+    k.bad = k.q0 < 0 || q1 < k.q0 || q1 > p.total_q || k.n > p.max_q_len || k.kv_len < k.n ||
+            k.kv_len > p.max_blocks_per_seq * p.block_size;
+    if (k.bad) k.n = 0;
+    return k;
+}
+
+// A sequence's units: its KV heads times the passes over its blocks of tokens, `cost` each (its start and its
+// output count unit_cost tiles).  A pass is p.group blocks, one for each CTA of a group.
+__device__ __forceinline__ int tiles_of(const TreeParams& p, const Seq& k) { return (k.kv_len + (1 << p.tile_log2) - 1) >> p.tile_log2; }
+__device__ __forceinline__ int passes_of(const TreeParams& p, const Seq& k) {
+    const int per = p.tb * p.group;
+    return (k.n + per - 1) / per;
+}
+
+// A range: where it starts (sequence, unit of it, cost into that unit) and its cost.
+struct Start {
+    int s, unit, at, count, per;
+};
+static_assert(sizeof(Start) <= 32, "record area");
+
+// Range `range` of `ranges`.  Every thread of the CTA calls it; all return the same record.
+__device__ __forceinline__ Start find_start(const TreeParams& p, int range, int ranges, long long* warp_sum, Start* rec) {
+    constexpr int NW = THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) rec->count = 0;
+    Seq k{0, 0, 0, false};
+    long long mine = 0, cost = 0;  // of this thread's sequences, of the one in k
+    for (int s = tid; s < p.num_seqs; s += THREADS) {
+        k = load_seq(p, s);
+        if (k.bad && blockIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
+        cost = (long long)p.n_kv_heads * passes_of(p, k) * (tiles_of(p, k) + p.unit_cost);
+        mine += cost;
+    }
+    const bool one = p.num_seqs <= THREADS;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const long long x = warp_sum[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    const int per = (int)max((total + ranges - 1) / ranges, (long long)p.min_tiles);
+    const long long lo = (long long)range * per;
+    if (lo < total) {
+        auto found = [&](int s, const Seq& q, long long at, long long c) {
+            if (c > 0 && lo >= at && lo < at + c) {
+                const int unit = tiles_of(p, q) + p.unit_cost;
+                rec->s = s;
+                rec->unit = (int)((lo - at) / unit);
+                rec->at = (int)((lo - at) % unit);
+                rec->count = (int)min((long long)per, total - lo);
+            }
+        };
+        if (one) {
+            found(tid, k, before + incl - cost, tid < p.num_seqs ? cost : 0);
+        } else {
+            // prefix sums, THREADS sequences at a time
+            long long base = 0;
+            for (int s0 = 0; s0 < p.num_seqs && base <= lo; s0 += THREADS) {
+                __syncthreads();
+                const int s = s0 + tid;
+                Seq q{0, 0, 0, false};
+                long long m = 0;
+                if (s < p.num_seqs) {
+                    q = load_seq(p, s);
+                    m = (long long)p.n_kv_heads * passes_of(p, q) * (tiles_of(p, q) + p.unit_cost);
+                }
+                long long in = m;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, in, o);
+                    if (lane >= o) in += y;
+                }
+                if (lane == 31) warp_sum[warp] = in;
+                __syncthreads();
+                long long all = base, bef = base;
+                for (int w = 0; w < NW; ++w) {
+                    if (w < warp) bef += warp_sum[w];
+                    all += warp_sum[w];
+                }
+                found(s, q, bef + in - m, m);
+                base = all;
+            }
+        }
+    }
+    __syncthreads();
+    Start r = *rec;
+    r.per = per;
+    return r;
+}
+
+// One segment of a range: tiles [tile, tile + n) of one unit's `tiles`.
+struct Segment {
+    int s, head, tok0, toks;  // sequence, KV head, the unit's first token (of total_q) and tokens
+    int tile, n, tiles;
+    int ctx, keys, drafted;
+    int parts, back;          // ranges the unit's tiles span (0: this one alone), and how many of them are before this one
+};
+
+// Calls f for the segments of the CTA's range in which it has rows: block `blk` (of p.group) of each pass.
+template <typename F>
+__device__ __forceinline__ void for_each_segment(const TreeParams& p, const Start& st, int blk, F&& f) {
+    int s = st.s, unit = st.unit, at = st.at, left = st.count;
+    if (left <= 0) return;
+    Seq k = load_seq(p, s);
+    while (left > 0) {
+        const int passes = passes_of(p, k), tiles = tiles_of(p, k);
+        Segment g;
+        const int cost = min(tiles + p.unit_cost - at, left);  // of the unit in this range
+        left -= cost;
+        g.tiles = tiles;
+        g.tile = max(0, at - p.unit_cost);
+        g.n = max(0, at + cost - p.unit_cost) - g.tile;
+        const int rest = tiles - g.tile - g.n;
+        g.back = (g.tile + st.per - 1) / st.per;
+        g.parts = (g.tile > 0 || rest > 0) ? g.back + 1 + (rest + st.per - 1) / st.per : 0;
+        g.s = s;
+        g.head = unit / passes;
+        const int j = (unit - g.head * passes) * p.group + blk;
+        g.tok0 = k.q0 + j * p.tb;
+        g.toks = min(p.tb, k.n - j * p.tb);
+        g.ctx = k.kv_len - k.n;
+        g.keys = k.kv_len;
+        g.drafted = k.n;
+        if (g.n > 0 && g.toks > 0) f(g);
+        if (left <= 0) return;
+        at = 0;
+        if (++unit < passes * p.n_kv_heads) continue;
+        unit = 0;
+        do {
+            if (++s >= p.num_seqs) return;
+            k = load_seq(p, s);
+        } while (k.n == 0);
+    }
+}
+
+// Bits k0 .. k0 + 31 (keys) that a row sees: the context, and the drafted tokens of its mask words (32-bit ones here).
+__device__ __forceinline__ uint32_t sees32(const uint32_t* row, int words, int k0, int ctx, int drafted) {
+    const int rel = k0 - ctx;
+    if (rel <= -32) return 0xffffffffu;
+    const int b = max(rel, 0), left = drafted - b;
+    uint32_t w = 0;
+    if (left > 0) {
+        const int i = b >> 5;
+        const uint32_t lo = i < words ? __ldg(row + i) : 0u, hi = (b & 31) && i + 1 < words ? __ldg(row + i + 1) : 0u;
+        w = __funnelshift_r(lo, hi, b & 31);
+        if (left < 32) w &= (1u << left) - 1u;
+    }
+    return rel < 0 ? (w << -rel) | ((1u << -rel) - 1u) : w;
+}
+
+}  // namespace tree
+
+template <bool BF16, int D, int NR>
+__global__ void __launch_bounds__(tree::THREADS, 1)
+tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+            const __grid_constant__ CUtensorMap tmQ) {
+    using namespace tree;
+    using C = Cfg<D, NR>;
+    using F = F16x2<BF16>;
+    constexpr int BN = C::BN, KW = C::KW, H = KW < 64 ? KW : 64, COPIES = C::COPIES;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t sQ = sbase + C::Q_OFF, sK = sbase + C::K_OFF, sV = sbase + C::V_OFF, bars = sbase + C::BAR_OFF;
+    auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+    Start* rec = reinterpret_cast<Start*>(smem + C::MISC_OFF);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF + 32);
+    uint32_t* bad_keys = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF + 48);  // [BN / 32]
+    long long* warp_sum = reinterpret_cast<long long*>(smem + C::MISC_OFF + 64);
+    float* m_s = reinterpret_cast<float*>(smem + C::ML_OFF);
+    float* l_s = m_s + 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int range = (int)blockIdx.x / p.group, blk = (int)blockIdx.x % p.group;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NK; ++i) {
+            mbar_init(bar(C::K_FULL + i), 2);
+            mbar_init(bar(C::K_EMPTY + i), 1);
+        }
+        for (int i = 0; i < C::NV; ++i) {
+            mbar_init(bar(C::V_FULL + i), 2);
+            mbar_init(bar(C::V_EMPTY + i), 1);
+        }
+        mbar_init(bar(C::Q_FULL), 1);
+        mbar_init(bar(C::Q_EMPTY), COPIES > 1 ? 1 + SOFTMAX_WARPS : 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(C::S_FULL + i), 1);
+            mbar_init(bar(C::S_EMPTY + i), SOFTMAX_WARPS);
+            mbar_init(bar(C::P_FULL + i), SOFTMAX_WARPS);
+            mbar_init(bar(C::PV_DONE + i), 1);
+            mbar_init(bar(C::DRAIN + i), 1);
+        }
+        mbar_init(bar(C::O_FREE), SOFTMAX_WARPS);
+        for (int i = 0; i < 4; ++i) bad_keys[i] = 0u;
+        fence_barrier_init();
+    }
+    if (warp == QK_WARP) {
+        tc::alloc(smem_addr(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
+        tc::relinquish();
+    }
+    // a programmatic dependent of the kernel before it: nothing is read before that one is complete; the merge may be
+    // set up now (it waits for this grid before it reads)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc::fence_before();
+    const Start start = find_start(p, range, (int)gridDim.x / p.group, warp_sum, rec);  // (synchronises the CTA)
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;  // none of this warp's waits has run out
+    auto wait = [&](int b, int phase) {
+        if (ok) ok = warp_wait(bar(b), (uint32_t)(phase & 1), p.err);
+    };
+    int done = 0;    // loader warps: tiles loaded
+    int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
+
+    if (warp < SOFTMAX_WARPS) {
+        // ------------------------------------------------------------ softmax, rescale, epilogue
+        const int R = 32 * warp + lane, copy = COPIES == 1 ? 0 : (32 * warp) / NR, r = R - copy * NR;  // row of the tile; the unit's
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const uint32_t tS = tmem + lane_base + (uint32_t)(copy * KW), tO = tmem + lane_base + C::O_COL;
+        const uint32_t tP = tmem + lane_base + C::P_COL + (uint32_t)(copy * KW / 2);
+        const float sc = p.qk_scale_log2;
+        constexpr uint32_t kBitsMost = BF16 ? 0x4380u : 0x7800u;  // 2^(8 + kShift) in 16 bits
+        constexpr uint32_t kBitsInf = BF16 ? 0x7F80u : 0x7C00u;
+        if constexpr (COPIES > 1) {  // the other copies' columns of P stay zero
+            uint32_t z[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z[e] = 0u;
+#pragma unroll
+            for (int q = 0; q < BN / 32; ++q) stn<32>(tmem + lane_base + C::P_COL + 32 * q, z);
+            tc::wait_st();
+        }
+        int i = 0;  // tile number over the CTA's range
+        for_each_segment(p, start, blk, [&](const Segment& g) {
+            const int rows = g.toks * p.g_heads;
+            const bool valid = r < rows;
+            const uint32_t* mask = reinterpret_cast<const uint32_t*>(p.mask + (size_t)(g.tok0 + (valid ? r / p.g_heads : 0)) * p.mask_words);
+            float m_ref = -INFINITY, l = 0.f;
+            for (int u = 0; u < g.n; ++u, ++i) {
+                const int kbase = (g.tile + u) * BN, k0 = kbase + copy * KW, b = i & 1;
+                const bool drafts = kbase + BN > g.ctx;  // the tile holds drafted tokens or keys past them
+                constexpr int MW = (KW + 31) / 32;
+                uint32_t sees[MW];
+#pragma unroll
+                for (int w = 0; w < MW; ++w)
+                    sees[w] = drafts ? sees32(mask, 2 * p.mask_words, k0 + 32 * w, g.ctx, g.drafted) : 0xffffffffu;
+                wait(C::S_FULL + b, i >> 1);
+                tc::fence_after();
+                if (i >= 2) wait(C::PV_DONE + b, (i >> 1) - 1);  // the weights' buffer is free
+                const uint32_t tSb = tS + (uint32_t)(b * BN), tPb = tP + (uint32_t)(b * BN / 2);
+                bool redo = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
+                float add = 0.f;
+                // MASK: the tile holds keys that not every row sees
+                auto weigh = [&](auto MASK) {
+                    auto seen = [&](float v, int e) {
+                        if constexpr (decltype(MASK)::value) return (sees[e / 32] >> (e & 31)) & 1u ? v : -INFINITY;
+                        else return v;
+                    };
+#pragma unroll 1
+                    for (int attempt = 0; attempt < 2; ++attempt) {
+                        if (redo) {
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int h = 0; h < KW / H; ++h) {
+                                uint32_t x[H];
+                                ldn<H>(tSb + h * H, x);
+                                tc::wait_ld();
+                                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                                for (int e = 0; e < H; ++e) m4[e & 3] = fmaxf(m4[e & 3], seen(__uint_as_float(x[e]) * sc, h * H + e));
+                                mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                            }
+                            const float mt = ceilf(mx);
+                            float alpha = 1.f;
+                            if (valid && mt > m_ref) {
+                                alpha = m_ref == -INFINITY ? 1.f : ex2(m_ref - mt);
+                                m_ref = mt;
+                                l *= alpha;
+                            }
+                            if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                                wait(C::PV_DONE + (b ^ 1), (i - 1) >> 1);  // O holds every tile before this one
+                                tc::fence_after();
+#pragma unroll 1
+                                for (int q = 0; q < D / 16; ++q) {
+                                    uint32_t o[16];
+                                    tc::ld16(tO + 16 * q, o);
+                                    tc::wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tc::st16(tO + 16 * q, o);
+                                }
+                            }
+                        }
+                        const float mu = m_ref == -INFINITY ? 0.f : m_ref - kShift<BF16>;
+                        const float2 sc2 = make_float2(sc, sc), nmu2 = make_float2(-mu, -mu);
+                        float2 ls = make_float2(0.f, 0.f);
+                        uint32_t pmax = 0;
+#pragma unroll
+                        for (int h = 0; h < KW / H; ++h) {
+                            uint32_t x[H], w[H / 2];
+                            ldn<H>(tSb + h * H, x);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < H / 2; ++e) {
+                                const float2 v = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nmu2);
+                                w[e] = F::pack_rn(ex2(seen(v.x, h * H + 2 * e)), ex2(seen(v.y, h * H + 2 * e + 1)));
+                                ls = fadd2(ls, F::unpack(w[e]));
+                                pmax = umax16x2(pmax, w[e]);
+                            }
+                            stn<H / 2>(tPb + h * H / 2, w);
+                        }
+                        add = ls.x + ls.y;
+                        const uint32_t pm = max(pmax & 0xFFFFu, pmax >> 16);
+                        // (the second attempt writes the same columns)
+                        if (redo || !__any_sync(0xffffffffu, valid && pm > kBitsMost)) break;
+                        redo = true;  // a row outgrew its reference by more than 2^8
+                        tc::wait_st();
+                    }
+                };
+                if (drafts) weigh(std::true_type{});
+                else weigh(std::false_type{});
+                l += add;
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::S_EMPTY + b));
+                if (drafts) {
+                    // V rows of the tile: those past the keys may hold anything (their weights are 0, but 0 * NaN is
+                    // NaN) and are zeroed, up to the end of the last box that was loaded (the others are zero already);
+                    // so are drafted ones that are not finite, and the rows that see one become NaN
+                    wait(C::V_FULL + i % C::NV, i / C::NV);
+                    const int t = (int)threadIdx.x, key = kbase + t;
+                    const uint32_t vrow = sV + (uint32_t)((i % C::NV) * C::TILE + t * 128);
+                    bool bad = false;
+                    if (t < BN && key >= g.ctx && key < g.keys) {
+                        uint32_t most = 0;
+#pragma unroll
+                        for (int q = 0; q < C::SLABS * 8; ++q) {
+                            const uint4 v = lds128(vrow + (q >> 3) * C::KSLAB + (((q + t) & 7) << 4));
+                            most = umax16x2(most, v.x & 0x7FFF7FFFu);
+                            most = umax16x2(most, v.y & 0x7FFF7FFFu);
+                            most = umax16x2(most, v.z & 0x7FFF7FFFu);
+                            most = umax16x2(most, v.w & 0x7FFF7FFFu);
+                        }
+                        bad = max(most & 0xFFFFu, most >> 16) >= kBitsInf;
+                    }
+                    if (t < BN && (bad || (key >= g.keys && key < ((g.keys + 15) & ~15)))) {
+#pragma unroll
+                        for (int q = 0; q < C::SLABS * 8; ++q)
+                            sts128(vrow + (q >> 3) * C::KSLAB + (((q + t) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    if (softmax_or(bad)) {
+                        const uint32_t mine = __ballot_sync(0xffffffffu, bad);
+                        if (lane == 0 && 32 * warp < BN) bad_keys[warp] = mine;
+                        softmax_sync();
+#pragma unroll
+                        for (int w = 0; w < MW; ++w) {
+                            const int at = copy * KW + 32 * w;  // this thread's keys of the tile: KW from copy * KW on
+                            uint32_t k = bad_keys[at >> 5] >> (at & 31);
+                            if constexpr (KW < 32) k &= (1u << KW) - 1u;
+                            if (k & sees[w]) l = __uint_as_float(0x7FC00000u);
+                        }
+                        softmax_sync();
+                    }
+                    tc::fence_async_smem();
+                }
+                tc::wait_st();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::P_FULL + b));
+            }
+            // the segment's end: O / l, or the partial
+            const bool whole = g.parts == 0;
+            const int slot = 2 * (int)blockIdx.x + (g.tile == 0 ? 1 : 0);
+            const size_t row0 = (size_t)g.tok0 * p.n_q_heads + (size_t)g.head * p.g_heads;
+            wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
+            tc::fence_after();
+            if constexpr (COPIES == 1) {
+                const float f = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;
+                if (!whole && valid) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(m_ref, l);
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)(r / p.g_heads) * p.n_q_heads + r % p.g_heads) * p.hd;
+                float* part = p.part_o + ((size_t)slot * NR + r) * D;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tc::ld32(tO + 32 * q, o);
+                    tc::wait_ld();
+                    if (q == D / 32 - 1) {  // O read: the next segment's first PV may overwrite it
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::O_FREE));
+                    }
+                    if (!valid || !ok) continue;
+                    if (whole) {
+                        if (32 * q < p.hd) {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                *reinterpret_cast<uint4*>(dst + 32 * q + 8 * v) =
+                                    make_uint4(F::pack_rn(__uint_as_float(o[8 * v]) * f, __uint_as_float(o[8 * v + 1]) * f),
+                                               F::pack_rn(__uint_as_float(o[8 * v + 2]) * f, __uint_as_float(o[8 * v + 3]) * f),
+                                               F::pack_rn(__uint_as_float(o[8 * v + 4]) * f, __uint_as_float(o[8 * v + 5]) * f),
+                                               F::pack_rn(__uint_as_float(o[8 * v + 6]) * f, __uint_as_float(o[8 * v + 7]) * f));
+                        }
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<uint4*>(part + 32 * q + 4 * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                    }
+                }
+            } else {
+                // join the copies: factors 2^(m - max m), then every copy adds its O, a share of the columns at a time
+                m_s[R] = m_ref;
+                l_s[R] = l;
+                softmax_sync();
+                float mx = -INFINITY, lt = 0.f;
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) mx = fmaxf(mx, m_s[c * NR + r]);
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) {
+                    const float m = m_s[c * NR + r], lc = l_s[c * NR + r];
+                    if (m != -INFINITY) lt += lc * ex2(m - mx);
+                    else lt += lc;  // 0, or NaN
+                }
+                float f = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
+                if (whole) f = lt != 0.f ? f / lt : 0.f;
+                else if (valid && copy == 0) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(mx, lt);
+                constexpr int W = D / COPIES;           // columns of a share
+                const uint32_t srow = sQ + (uint32_t)(r * D * 4);
+#pragma unroll 1
+                for (int k = 0; k < COPIES; ++k) {
+                    const int c0 = ((copy + k) % COPIES) * W;
+#pragma unroll 1
+                    for (int q = 0; q < W / 16; ++q) {
+                        uint32_t o[16];
+                        tc::ld16(tO + (uint32_t)(c0 + 16 * q), o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const uint32_t at = srow + (uint32_t)((((c0 + 16 * q) / 4 + v) ^ (r & 7)) << 4);
+                            float4 a = make_float4(__uint_as_float(o[4 * v]) * f, __uint_as_float(o[4 * v + 1]) * f,
+                                                   __uint_as_float(o[4 * v + 2]) * f, __uint_as_float(o[4 * v + 3]) * f);
+                            if (k > 0) {
+                                const uint4 x = lds128(at);
+                                a.x += __uint_as_float(x.x);
+                                a.y += __uint_as_float(x.y);
+                                a.z += __uint_as_float(x.z);
+                                a.w += __uint_as_float(x.w);
+                            }
+                            sts128(at, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z), __float_as_uint(a.w)));
+                        }
+                    }
+                    if (k == COPIES - 1) {  // O read: the next segment's first PV may overwrite it
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::O_FREE));
+                    }
+                    softmax_sync();
+                }
+                constexpr int CH = D / 8;               // chunks of 8 columns
+                for (int e = threadIdx.x; e < rows * CH; e += 128) {
+                    const int row = e / CH, ch = e % CH;
+                    const uint32_t base = sQ + (uint32_t)(row * D * 4);
+                    const uint4 a = lds128(base + (uint32_t)(((2 * ch) ^ (row & 7)) << 4)), c = lds128(base + (uint32_t)(((2 * ch + 1) ^ (row & 7)) << 4));
+                    if (!ok) continue;
+                    if (whole) {
+                        if (8 * ch < p.hd)
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                      (row0 + (size_t)(row / p.g_heads) * p.n_q_heads + row % p.g_heads) * p.hd + 8 * ch) =
+                                make_uint4(F::pack_rn(__uint_as_float(a.x), __uint_as_float(a.y)), F::pack_rn(__uint_as_float(a.z), __uint_as_float(a.w)),
+                                           F::pack_rn(__uint_as_float(c.x), __uint_as_float(c.y)), F::pack_rn(__uint_as_float(c.z), __uint_as_float(c.w)));
+                    } else {
+                        uint4* part = reinterpret_cast<uint4*>(p.part_o + ((size_t)slot * NR + row) * D + 8 * ch);
+                        part[0] = a;
+                        part[1] = c;
+                    }
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::Q_EMPTY));
+            }
+            // what the merge needs to know of a cut unit, from each range that it spans: ranges, rows, first row of out,
+            // the CTA it starts in
+            if (!whole)
+                (g.tile == 0 ? begins : goes_on) = make_int4(g.parts, rows, (int)row0, (int)blockIdx.x - g.back * p.group);
+        });
+    } else if (warp >= K_WARP) {
+        // ------------------------------------------------------------ cache rows into the rings, every second box of K or V
+        const bool is_v = warp >= V_WARP;
+        const int odd = (warp - K_WARP) & 1;
+        const CUtensorMap* map = is_v ? &tmV : &tmK;
+        if (lane == 0) tma_prefetch_desc(map);
+        const uint64_t pol = p.group == 1 ? l2_policy_evict_first() : l2_policy_normal();  // read once, or by the group's CTAs
+        const int br = min(p.block_size, 16), nbox = BN / br;
+        const int full0 = is_v ? C::V_FULL : C::K_FULL, empty0 = is_v ? C::V_EMPTY : C::K_EMPTY;
+        const int slots = is_v ? C::NV : C::NK;
+        const uint32_t ring = is_v ? sV : sK, el = elect_one();
+        for_each_segment(p, start, blk, [&](const Segment& g) {
+            const int32_t* bt = p.block_tables + (size_t)g.s * p.max_blocks_per_seq;
+            auto entry = [&](int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
+                const int t = tile * BN + lane * br;
+                if (lane >= nbox || t >= g.keys) return p.num_blocks;
+                const int e = __ldg(bt + (t >> p.block_log2));
+                if (e < 0 || e >= p.num_blocks) {
+                    flag_error(p.err, PA_DEVERR_BLOCK);
+                    return p.num_blocks;
+                }
+                return e;
+            };
+            int id = entry(g.tile);
+            for (int u = 0; u < g.n; ++u, ++done) {
+                const int tile = g.tile + u;
+                const int nxt = u + 1 < g.n ? entry(tile + 1) : 0;
+                const int st = (int)uniform((uint32_t)(done % slots)), use = done / slots;
+                if (use > 0) wait(empty0 + st, use - 1);
+                const uint32_t full = bar(full0 + st), dst = ring + (uint32_t)(st * C::TILE);
+                if (el) mbar_arrive_expect_tx(full, C::TILE / 2);
+                __syncwarp();
+#pragma unroll 1
+                for (int x = odd; x < nbox; x += 2) {
+                    const int e = __shfl_sync(0xffffffffu, id, x);
+                    const int row = (int)uniform((uint32_t)((tile * BN + x * br) & (p.block_size - 1)));
+#pragma unroll
+                    for (int sl = 0; sl < C::SLABS; ++sl)
+                        tma_box(el, dst + (uint32_t)(sl * C::KSLAB + x * br * 128), map, sl * 64, g.head, row, e, full, pol);
+                }
+                id = nxt;
+            }
+        });
+    } else if (warp == Q_WARP && lane == 0) {
+        // ------------------------------------------------------------ the units' query rows, once for each copy
+        tma_prefetch_desc(&tmQ);
+        int seg = 0;
+        const uint32_t box = (uint32_t)(p.tb * p.g_heads * 128);
+        for_each_segment(p, start, blk, [&](const Segment& g) {
+            if (seg > 0 && ok) ok = mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err);
+            mbar_arrive_expect_tx(bar(C::Q_FULL), box * C::SLABS * COPIES);
+#pragma unroll 1
+            for (int c = 0; c < COPIES; ++c)
+#pragma unroll 1
+                for (int sl = 0; sl < C::SLABS; ++sl)
+                    tma_q(sQ + (uint32_t)(sl * C::QSLAB + c * NR * 128), &tmQ, sl * 64, g.head * p.g_heads, g.tok0, bar(C::Q_FULL));
+            ++seg;
+        });
+        if (seg > 0) (void)mbar_wait(bar(C::Q_FULL), (uint32_t)((seg - 1) & 1), p.err);
+    } else if (warp == QK_WARP) {
+        // ------------------------------------------------------------ QK issue: the whole warp walks the loop and one elected
+        // lane issues, from descriptors that a shuffle makes warp-uniform
+        constexpr uint32_t ID_QK = tc::idesc_f16(BF16, false, 128, BN);
+        const uint64_t dq = tc::sdesc_sw128(sQ, 16, 1024), dk0 = tc::sdesc_sw128(sK, 16, 1024);
+        const uint32_t el = elect_one(), tS = uniform(tmem);
+        int i = 0, seg = 0;
+        for_each_segment(p, start, blk, [&](const Segment& g) {
+            wait(C::Q_FULL, seg);
+            for (int u = 0; u < g.n; ++u, ++i) {
+                const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NK));
+                if (i >= 2) wait(C::S_EMPTY + b, (i >> 1) - 1);
+                wait(C::K_FULL + st, i / C::NK);
+                tc::fence_after();
+                const uint64_t dk = dk0 + (uint32_t)((st * C::TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(el, tS + (uint32_t)(b * BN), dq + (uint32_t)(((kk >> 2) * C::QSLAB + (kk & 3) * 32) >> 4),
+                           dk + (uint32_t)(((kk >> 2) * C::KSLAB + (kk & 3) * 32) >> 4), ID_QK, kk > 0);
+                commit(el, bar(C::S_FULL + b));
+                commit(el, bar(C::K_EMPTY + st));
+                if (u == g.n - 1) commit(el, bar(C::Q_EMPTY));
+            }
+            ++seg;
+        });
+        if (i > 0) {  // every MMA must be complete before TMEM is released
+            commit(el, bar(C::DRAIN));
+            (void)warp_wait(bar(C::DRAIN), 0, p.err);
+        }
+    } else if (warp == PV_WARP) {
+        // ------------------------------------------------------------ PV issue: O += P V, P in tensor memory
+        constexpr uint32_t ID_PV = tc::idesc_f16(BF16, true, 128, D);
+        const uint64_t dv0 = tc::sdesc_sw128(sV, C::KSLAB, 1024);
+        const uint32_t el = elect_one(), dO = uniform(tmem + C::O_COL), tP = uniform(tmem + C::P_COL);
+        int i = 0, seg = 0;
+        for_each_segment(p, start, blk, [&](const Segment& g) {
+            if (seg > 0) wait(C::O_FREE, seg - 1);  // O of the segment before has been read
+            for (int u = 0; u < g.n; ++u, ++i) {
+                const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NV));
+                const uint32_t acc = uniform(u > 0);
+                wait(C::V_FULL + st, i / C::NV);
+                wait(C::P_FULL + b, i >> 1);
+                tc::fence_after();
+                const uint64_t dv = dv0 + (uint32_t)((st * C::TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    mma_ts(el, dO, tP + (uint32_t)(b * (BN / 2) + 8 * kk), dv + (uint32_t)((kk * 2048) >> 4), ID_PV, kk > 0 ? 1u : acc);
+                commit(el, bar(C::V_EMPTY + st));
+                commit(el, bar(C::PV_DONE + b));
+            }
+            ++seg;
+        });
+        if (i > 0) {
+            commit(el, bar(C::DRAIN + 1));
+            (void)warp_wait(bar(C::DRAIN + 1), 0, p.err);
+        }
+    }
+    tc::fence_before();
+    // Every load is behind a wait of the issuers.  If all went well nothing is in flight now; if some role's wait ran
+    // out, no copy may be left behind: the last ones of each ring
+    const bool failed = __syncthreads_or(!ok);
+    if (failed && warp >= K_WARP) {
+        const int full0 = warp >= V_WARP ? C::V_FULL : C::K_FULL, slots = warp >= V_WARP ? C::NV : C::NK;
+        for (int t = max(0, done - slots); t < done; ++t) (void)warp_wait(bar(full0 + t % slots), (uint32_t)((t / slots) & 1), p.err);
+    }
+    if (threadIdx.x == 0) {
+        if (failed) begins = goes_on = make_int4(0, 0, 0, 0);
+        p.desc[blockIdx.x] = begins;
+        p.desc[gridDim.x + blockIdx.x] = goes_on;
+    }
+    if (warp == QK_WARP) {
+        tc::fence_after();
+        tc::dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Joins the partials of the units that the ranges' ends cut: out = sum_k 2^(m_k - max m) o_k / sum_k 2^(m_k - max m) l_k,
+// in a fixed order.  A unit of few partials by the blocks of the CTA it starts in, a warp a row; one of many (few long
+// contexts) by the blocks of all the CTAs it spans, a block a row, whose warps take every 8th partial each.
+template <bool BF16, int D, int NR>
+__global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const TreeParams p) {
+    using F = F16x2<BF16>;
+    constexpr int NW = tree::MERGE_THREADS / 32, V = D / 64;  // pairs of columns a lane: 2 lane + 64 v
+    constexpr int kFew = 8;
+    __shared__ float2 acc[NW][D / 2];
+    __shared__ float wt[tree::MERGE_THREADS], red[2][NW];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = (int)blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the next kernel of the step may start its launch; it waits for this grid before reading anything
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int4 cut[2] = {__ldcg(p.desc + cta), __ldcg(p.desc + gridDim.x + cta)};
+    auto out_row = [&](int row0, int row) {
+        return static_cast<uint16_t*>(p.out) + ((size_t)row0 + (size_t)(row / p.g_heads) * p.n_q_heads + row % p.g_heads) * p.hd;
+    };
+    auto store = [&](int row0, int row, int v, float2 a, float inv) {
+        const int col = 2 * lane + 64 * v;
+        if (col < p.hd) *reinterpret_cast<uint32_t*>(out_row(row0, row) + col) = F::pack_rn(a.x * inv, a.y * inv);
+    };
+    const int4 few = cut[0].x <= kFew ? cut[0] : make_int4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int row = (int)blockIdx.y * 16 + warp; row < min(few.y, ((int)blockIdx.y + 1) * 16); row += NW) {
+        auto slot_at = [&](int k) { return (size_t)(2 * (cta + k * p.group) + (k == 0)); };
+        float2 x[kFew][V];
+#pragma unroll
+        for (int k = 0; k < kFew; ++k)
+            if (k < few.x) {
+                const float2* o = reinterpret_cast<const float2*>(p.part_o + (slot_at(k) * NR + row) * D) + lane;
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[k][v] = __ldcg(o + 32 * v);
+            }
+        float m = -INFINITY, l = 0.f;
+        if (lane < few.x) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_at(lane) * NR + row);
+            m = ml.x;
+            l = ml.y;
+        }
+        float mx = m;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = __shfl_sync(0xffffffffu, mx, 0);
+        const float w = m == -INFINITY ? 0.f : ex2(m - mx);
+        float lw = m == -INFINITY ? l : l * w;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+        lw = __shfl_sync(0xffffffffu, lw, 0);
+        float2 a[V] = {};
+#pragma unroll
+        for (int k = 0; k < kFew; ++k)
+            if (k < few.x) {
+                const float f = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+                for (int v = 0; v < V; ++v) a[v] = ffma2(x[k][v], make_float2(f, f), a[v]);
+            }
+        const float inv = lw != 0.f ? 1.f / lw : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) store(few.z, row, v, a[v], inv);
+    }
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int4 u = which == 0 ? cut[0] : cut[1];
+        const int parts = u.x, b = u.w;
+        if (parts <= kFew) continue;
+        auto slot_at = [&](int k) { return (size_t)(2 * (b + k * p.group) + (k == 0)); };
+        const int mine = (cta - b) / p.group;
+        for (int row = mine * (int)gridDim.y + (int)blockIdx.y; row < u.y; row += parts * (int)gridDim.y) {
+            float m = -INFINITY, l = 0.f;
+            if (tid < parts) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_at(tid) * NR + row);
+                m = ml.x;
+                l = ml.y;
+            }
+            float mx = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane == 0) red[0][warp] = mx;
+            __syncthreads();
+            mx = red[0][0];
+            for (int w = 1; w < NW; ++w) mx = fmaxf(mx, red[0][w]);
+            const float w = m == -INFINITY ? 0.f : ex2(m - mx);
+            wt[tid] = w;
+            float lw = m == -INFINITY ? l : l * w;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+            if (lane == 0) red[1][warp] = lw;
+            __syncthreads();
+            float2 a[V] = {};
+#pragma unroll 4
+            for (int k = warp; k < parts; k += NW) {
+                const float2* o = reinterpret_cast<const float2*>(p.part_o + (slot_at(k) * NR + row) * D) + lane;
+                const float f = wt[k];
+#pragma unroll
+                for (int v = 0; v < V; ++v) a[v] = ffma2(__ldcg(o + 32 * v), make_float2(f, f), a[v]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[warp][lane + 32 * v] = a[v];
+            __syncthreads();
+            if (warp == 0) {
+                float lt = 0.f;
+                for (int k = 0; k < NW; ++k) lt += red[1][k];
+                const float inv = lt != 0.f ? 1.f / lt : 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float2 t = acc[0][lane + 32 * v];
+                    for (int k = 1; k < NW; ++k) t = fadd2(t, acc[k][lane + 32 * v]);
+                    store(u.z, row, v, t, inv);
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+}  // namespace pa
