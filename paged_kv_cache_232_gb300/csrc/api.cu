@@ -68,7 +68,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // column slab of one head's 16-token chunk; with block_size 32..128 the kernels address the
 // chunk's rows inside its block by the row coordinate).  Out-of-range block ids read zeros.
 int encode_cache_map(CUtensorMap* m, const void* base, int dtype, int64_t num_blocks, int block_size,
-                     int n_kv_heads, int head_dim) {
+                     int n_kv_heads, int head_dim,
+                     CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)n_kv_heads, (cuuint64_t)block_size,
                           (cuuint64_t)num_blocks};
     cuuint64_t strides[3] = {(cuuint64_t)head_dim * 2, (cuuint64_t)n_kv_heads * head_dim * 2,
@@ -78,8 +79,7 @@ int encode_cache_map(CUtensorMap* m, const void* base, int dtype, int64_t num_bl
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = g_encode(m, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                           const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -1149,7 +1149,7 @@ int pa_fork_pages(int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_le
     if (!block_tables || !seq_lens || !parents || !ref_counts) return PA_ERR_NULL;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != PA_OK) return st;
-    pa::fork_pages_kernel<<<num_seqs, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+    pa::fork_pages_kernel<<<(num_seqs + pa::kForkSeqs - 1) / pa::kForkSeqs, pa::kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(
         block_tables, max_blocks_per_seq, seq_lens, parents, num_seqs, ref_counts, block_size, (int)num_blocks, dev->err);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -1331,8 +1331,10 @@ int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_
     p.part_ml = reinterpret_cast<float*>(base + w.ml_off);
     p.part_o = reinterpret_cast<float*>(base + w.o_off);
     CUtensorMap tk, tv, tq;
-    if ((st = encode_cache_map(&tk, k_cache, dtype, num_blocks, block_size, n_kv_heads, head_dim)) != PA_OK) return st;
-    if ((st = encode_cache_map(&tv, v_cache, dtype, num_blocks, block_size, n_kv_heads, head_dim)) != PA_OK) return st;
+    // a token's row of one head is 2 head_dim bytes, its neighbours other heads': no more is fetched into L2 than that
+    const CUtensorMapL2promotion fetch = head_dim < 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    if ((st = encode_cache_map(&tk, k_cache, dtype, num_blocks, block_size, n_kv_heads, head_dim, fetch)) != PA_OK) return st;
+    if ((st = encode_cache_map(&tv, v_cache, dtype, num_blocks, block_size, n_kv_heads, head_dim, fetch)) != PA_OK) return st;
     // q [total_q, n_q_heads, head_dim]: boxes of 64 columns x the group's heads x the unit's tokens
     cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)n_q_heads, (cuuint64_t)total_q};
     cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)n_q_heads * head_dim * 2};

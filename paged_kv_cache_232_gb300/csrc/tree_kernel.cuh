@@ -46,8 +46,6 @@ namespace tree {
 template <bool BF16>
 constexpr float kShift = BF16 ? 0.f : 7.f;
 
-constexpr int SOFTMAX_WARPS = 4, QK_WARP = 4, PV_WARP = 5, Q_WARP = 6, K_WARP = 7, V_WARP = 9;
-constexpr int THREADS = 11 * 32;        // two warps load K, two load V: every second box each
 constexpr int MERGE_THREADS = 256;
 static_assert(PA_TREE_MAX_CTAS <= MERGE_THREADS, "the merge gives every partial of a unit a thread");
 
@@ -57,14 +55,22 @@ struct Cfg {
     static_assert(NR == 32 || NR == 64 || NR == 128, "query rows of a unit");
     static constexpr int BN = D == 256 ? 64 : 128;      // keys per tile
     static constexpr int COPIES = 128 / NR;
-    static constexpr int KW = BN / COPIES;              // keys of a tile that one thread takes
+    static constexpr int SPLIT = NR == 128 ? 2 : 1;      // threads a row of the tile
+    static constexpr int KW = BN / COPIES / SPLIT;      // keys of a tile that one thread takes
+    static constexpr int SOFTMAX = 4 * SPLIT;           // softmax warps; then the issuers, the Q loader, two K and two V loaders
+    static constexpr int QK_WARP = SOFTMAX, PV_WARP = SOFTMAX + 1, Q_WARP = SOFTMAX + 2, K_WARP = SOFTMAX + 3,
+                         V_WARP = SOFTMAX + 5, THREADS = (SOFTMAX + 7) * 32;
     static constexpr int SLABS = D / 64;
     static constexpr int QSLAB = 128 * 128, KSLAB = BN * 128;
     static constexpr int TILE = SLABS * KSLAB;          // bytes of K (or V) of a tile
-    static constexpr int NK = D == 64 ? 6 : 3, NV = D == 64 ? 6 : D == 256 ? 2 : 3;  // tiles in the rings (D 256: Q takes 64 KB)
+    // The copies are joined in a place of their own where there is one (then the next unit's Q can load meanwhile), at
+    // D 256 in the Q tile's.  Tiles in the rings: what fits beside that
+    static constexpr bool OWN_STAGE = COPIES > 1 && D < 256;
+    static constexpr int NK = D == 64 ? 6 : 3, NV = D == 64 ? 6 : D == 256 || OWN_STAGE ? 2 : 3;
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = SLABS * QSLAB, V_OFF = K_OFF + NK * TILE;
-    static constexpr int ML_OFF = V_OFF + NV * TILE;    // m and l of the tile's 128 rows
+    static constexpr int STAGE_OFF = OWN_STAGE ? V_OFF + NV * TILE : Q_OFF;
+    static constexpr int ML_OFF = V_OFF + NV * TILE + (OWN_STAGE ? NR * D * 4 : 0);  // what a row's threads tell each other
     static constexpr int BAR_OFF = ML_OFF + 2 * 128 * 4;
     static constexpr int K_FULL = 0, K_EMPTY = NK, V_FULL = 2 * NK, V_EMPTY = V_FULL + NV, Q_FULL = V_EMPTY + NV, Q_EMPTY = Q_FULL + 1,
                          S_FULL = Q_FULL + 2, S_EMPTY = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
@@ -72,7 +78,7 @@ struct Cfg {
     static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch, bad keys
     static constexpr int SMEM_BYTES = MISC_OFF + 192 + 1024;             // + alignment slack
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-    static_assert(COPIES == 1 || NR * D * 4 <= SLABS * QSLAB, "the copies are joined in the Q tile's place");
+    static_assert(COPIES == 1 || OWN_STAGE || NR * D * 4 <= SLABS * QSLAB, "the copies are joined in the Q tile's place");
     // TMEM: two S buffers, two P buffers (16-bit pairs), O
     static constexpr uint32_t P_COL = D == 256 ? 128 : 384, O_COL = 256, TMEM_COLS = 512;
 };
@@ -132,17 +138,21 @@ __device__ __forceinline__ uint64_t l2_policy_normal() {
     return p;
 }
 
-// barrier of the four softmax warps, plain and with an OR over them
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_or(bool v) {
+// barrier of N threads, plain and with an OR over them: 1: all softmax warps; 2 + q: the two warps of lanes 32 q .. 32 q + 31
+template <int N>
+__device__ __forceinline__ void bar_sync(int id) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ bool bar_or(int id, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "r"(id), "n"(N)
         : "memory");
     return r != 0;
 }
@@ -206,6 +216,7 @@ struct Start {
 static_assert(sizeof(Start) <= 32, "record area");
 
 // Range `range` of `ranges`.  Every thread of the CTA calls it; all return the same record.
+template <int THREADS>
 __device__ __forceinline__ Start find_start(const TreeParams& p, int range, int ranges, long long* warp_sum, Start* rec) {
     constexpr int NW = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -347,17 +358,18 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t* row, int words, int k
 }  // namespace tree
 
 template <bool BF16, int D, int NR>
-__global__ void __launch_bounds__(tree::THREADS, 1)
+__global__ void __launch_bounds__(tree::Cfg<D, NR>::THREADS, 1)
 tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const __grid_constant__ CUtensorMap tmQ) {
     using namespace tree;
     using C = Cfg<D, NR>;
     using F = F16x2<BF16>;
-    constexpr int BN = C::BN, KW = C::KW, H = KW < 64 ? KW : 64, COPIES = C::COPIES;
+    constexpr int BN = C::BN, KW = C::KW, H = C::SPLIT == 2 && KW > 32 ? 32 : KW, COPIES = C::COPIES, SPLIT = C::SPLIT, SOFTMAX = C::SOFTMAX;
+    constexpr int QK_WARP = C::QK_WARP, PV_WARP = C::PV_WARP, Q_WARP = C::Q_WARP, K_WARP = C::K_WARP, V_WARP = C::V_WARP;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_addr(smem);
-    const uint32_t sQ = sbase + C::Q_OFF, sK = sbase + C::K_OFF, sV = sbase + C::V_OFF, bars = sbase + C::BAR_OFF;
+    const uint32_t sStage = sbase + C::STAGE_OFF, sQ = sbase + C::Q_OFF, sK = sbase + C::K_OFF, sV = sbase + C::V_OFF, bars = sbase + C::BAR_OFF;
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     Start* rec = reinterpret_cast<Start*>(smem + C::MISC_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF + 32);
@@ -378,15 +390,15 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             mbar_init(bar(C::V_EMPTY + i), 1);
         }
         mbar_init(bar(C::Q_FULL), 1);
-        mbar_init(bar(C::Q_EMPTY), COPIES > 1 ? 1 + SOFTMAX_WARPS : 1);
+        mbar_init(bar(C::Q_EMPTY), COPIES > 1 && !C::OWN_STAGE ? 1 + SOFTMAX : 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::S_FULL + i), 1);
-            mbar_init(bar(C::S_EMPTY + i), SOFTMAX_WARPS);
-            mbar_init(bar(C::P_FULL + i), SOFTMAX_WARPS);
+            mbar_init(bar(C::S_EMPTY + i), SOFTMAX);
+            mbar_init(bar(C::P_FULL + i), SOFTMAX);
             mbar_init(bar(C::PV_DONE + i), 1);
             mbar_init(bar(C::DRAIN + i), 1);
         }
-        mbar_init(bar(C::O_FREE), SOFTMAX_WARPS);
+        mbar_init(bar(C::O_FREE), SOFTMAX);
         for (int i = 0; i < 4; ++i) bad_keys[i] = 0u;
         fence_barrier_init();
     }
@@ -399,7 +411,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before();
-    const Start start = find_start(p, range, (int)gridDim.x / p.group, warp_sum, rec);  // (synchronises the CTA)
+    const Start start = find_start<C::THREADS>(p, range, (int)gridDim.x / p.group, warp_sum, rec);  // (synchronises the CTA)
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     bool ok = true;  // none of this warp's waits has run out
@@ -409,12 +421,19 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     int done = 0;    // loader warps: tiles loaded
     int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
 
-    if (warp < SOFTMAX_WARPS) {
+    if (warp < SOFTMAX) {
         // ------------------------------------------------------------ softmax, rescale, epilogue
-        const int R = 32 * warp + lane, copy = COPIES == 1 ? 0 : (32 * warp) / NR, r = R - copy * NR;  // row of the tile; the unit's
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const uint32_t tS = tmem + lane_base + (uint32_t)(copy * KW), tO = tmem + lane_base + C::O_COL;
-        const uint32_t tP = tmem + lane_base + C::P_COL + (uint32_t)(copy * KW / 2);
+        // row of the tile; of the unit; which copy of it, or which of its two threads (its share of a tile's keys)
+        const int quarter = warp & 3, R = 32 * quarter + lane, share = SPLIT == 2 ? warp >> 2 : COPIES == 1 ? 0 : (32 * warp) / NR;
+        const int r = SPLIT == 2 ? R : R - share * NR;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_base + (uint32_t)(share * KW), tO = tmem + lane_base + C::O_COL;
+        const uint32_t tP = tmem + lane_base + C::P_COL + (uint32_t)(share * KW / 2);
+        // the two threads of a row share its reference: what one finds the other has to know
+        auto pair_or = [&](bool v) {
+            if constexpr (SPLIT == 2) return bar_or<64>(2 + quarter, v);
+            else return __any_sync(0xffffffffu, v) != 0;
+        };
         const float sc = p.qk_scale_log2;
         constexpr uint32_t kBitsMost = BF16 ? 0x4380u : 0x7800u;  // 2^(8 + kShift) in 16 bits
         constexpr uint32_t kBitsInf = BF16 ? 0x7F80u : 0x7C00u;
@@ -433,7 +452,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             const uint32_t* mask = reinterpret_cast<const uint32_t*>(p.mask + (size_t)(g.tok0 + (valid ? r / p.g_heads : 0)) * p.mask_words);
             float m_ref = -INFINITY, l = 0.f;
             for (int u = 0; u < g.n; ++u, ++i) {
-                const int kbase = (g.tile + u) * BN, k0 = kbase + copy * KW, b = i & 1;
+                const int kbase = (g.tile + u) * BN, k0 = kbase + share * KW, b = i & 1;
                 const bool drafts = kbase + BN > g.ctx;  // the tile holds drafted tokens or keys past them
                 constexpr int MW = (KW + 31) / 32;
                 uint32_t sees[MW];
@@ -466,6 +485,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                                 for (int e = 0; e < H; ++e) m4[e & 3] = fmaxf(m4[e & 3], seen(__uint_as_float(x[e]) * sc, h * H + e));
                                 mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                             }
+                            if constexpr (SPLIT == 2) {
+                                m_s[128 * share + R] = mx;
+                                bar_sync<64>(2 + quarter);
+                                mx = fmaxf(mx, m_s[128 * (share ^ 1) + R]);
+                            }
                             const float mt = ceilf(mx);
                             float alpha = 1.f;
                             if (valid && mt > m_ref) {
@@ -477,13 +501,14 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                                 wait(C::PV_DONE + (b ^ 1), (i - 1) >> 1);  // O holds every tile before this one
                                 tc::fence_after();
 #pragma unroll 1
-                                for (int q = 0; q < D / 16; ++q) {
+                                for (int q = 0; q < D / 16 / SPLIT; ++q) {  // (each thread of a row its part of the columns)
                                     uint32_t o[16];
-                                    tc::ld16(tO + 16 * q, o);
+                                    const uint32_t at = tO + (uint32_t)((SPLIT == 2 ? share * (D / 2) : 0) + 16 * q);
+                                    tc::ld16(at, o);
                                     tc::wait_ld();
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tc::st16(tO + 16 * q, o);
+                                    tc::st16(at, o);
                                 }
                             }
                         }
@@ -507,8 +532,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         }
                         add = ls.x + ls.y;
                         const uint32_t pm = max(pmax & 0xFFFFu, pmax >> 16);
-                        // (the second attempt writes the same columns)
-                        if (redo || !__any_sync(0xffffffffu, valid && pm > kBitsMost)) break;
+                        // (at SPLIT 2 the vote also says that the other thread has read this one's maximum)
+                        const bool over = pair_or(valid && pm > kBitsMost);
+                        if (redo || !over) break;
                         redo = true;  // a row outgrew its reference by more than 2^8
                         tc::wait_st();
                     }
@@ -544,18 +570,18 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         for (int q = 0; q < C::SLABS * 8; ++q)
                             sts128(vrow + (q >> 3) * C::KSLAB + (((q + t) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
                     }
-                    if (softmax_or(bad)) {
+                    if (bar_or<32 * SOFTMAX>(1, bad)) {
                         const uint32_t mine = __ballot_sync(0xffffffffu, bad);
                         if (lane == 0 && 32 * warp < BN) bad_keys[warp] = mine;
-                        softmax_sync();
+                        bar_sync<32 * SOFTMAX>(1);
 #pragma unroll
                         for (int w = 0; w < MW; ++w) {
-                            const int at = copy * KW + 32 * w;  // this thread's keys of the tile: KW from copy * KW on
+                            const int at = share * KW + 32 * w;  // this thread's keys of the tile: KW from share * KW on
                             uint32_t k = bad_keys[at >> 5] >> (at & 31);
                             if constexpr (KW < 32) k &= (1u << KW) - 1u;
                             if (k & sees[w]) l = __uint_as_float(0x7FC00000u);
                         }
-                        softmax_sync();
+                        bar_sync<32 * SOFTMAX>(1);
                     }
                     tc::fence_async_smem();
                 }
@@ -571,23 +597,31 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
             tc::fence_after();
             if constexpr (COPIES == 1) {
+                if constexpr (SPLIT == 2) {  // the row's sum, in a fixed order
+                    m_s[128 * share + R] = l;
+                    bar_sync<64>(2 + quarter);
+                    l = m_s[R] + m_s[128 + R];
+                    bar_sync<64>(2 + quarter);
+                }
+                constexpr int W = D / SPLIT;  // columns that this thread writes
+                const int c0 = SPLIT == 2 ? share * W : 0;
                 const float f = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;
-                if (!whole && valid) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(m_ref, l);
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)(r / p.g_heads) * p.n_q_heads + r % p.g_heads) * p.hd;
-                float* part = p.part_o + ((size_t)slot * NR + r) * D;
+                if (!whole && valid && share == 0) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(m_ref, l);
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)(r / p.g_heads) * p.n_q_heads + r % p.g_heads) * p.hd + c0;
+                float* part = p.part_o + ((size_t)slot * NR + r) * D + c0;
 #pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
+                for (int q = 0; q < W / 32; ++q) {
                     uint32_t o[32];
-                    tc::ld32(tO + 32 * q, o);
+                    tc::ld32(tO + (uint32_t)(c0 + 32 * q), o);
                     tc::wait_ld();
-                    if (q == D / 32 - 1) {  // O read: the next segment's first PV may overwrite it
+                    if (q == W / 32 - 1) {  // O read: the next segment's first PV may overwrite it
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::O_FREE));
                     }
                     if (!valid || !ok) continue;
                     if (whole) {
-                        if (32 * q < p.hd) {
+                        if (c0 + 32 * q < p.hd) {
 #pragma unroll
                             for (int v = 0; v < 4; ++v)
                                 *reinterpret_cast<uint4*>(dst + 32 * q + 8 * v) =
@@ -606,7 +640,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 // join the copies: factors 2^(m - max m), then every copy adds its O, a share of the columns at a time
                 m_s[R] = m_ref;
                 l_s[R] = l;
-                softmax_sync();
+                bar_sync<128>(1);
                 float mx = -INFINITY, lt = 0.f;
 #pragma unroll
                 for (int c = 0; c < COPIES; ++c) mx = fmaxf(mx, m_s[c * NR + r]);
@@ -618,12 +652,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 }
                 float f = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
                 if (whole) f = lt != 0.f ? f / lt : 0.f;
-                else if (valid && copy == 0) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(mx, lt);
+                else if (valid && share == 0) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(mx, lt);
                 constexpr int W = D / COPIES;           // columns of a share
-                const uint32_t srow = sQ + (uint32_t)(r * D * 4);
+                const uint32_t srow = sStage + (uint32_t)(r * D * 4);
 #pragma unroll 1
                 for (int k = 0; k < COPIES; ++k) {
-                    const int c0 = ((copy + k) % COPIES) * W;
+                    const int c0 = ((share + k) % COPIES) * W;
 #pragma unroll 1
                     for (int q = 0; q < W / 16; ++q) {
                         uint32_t o[16];
@@ -649,12 +683,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::O_FREE));
                     }
-                    softmax_sync();
+                    bar_sync<128>(1);
                 }
                 constexpr int CH = D / 8;               // chunks of 8 columns
                 for (int e = threadIdx.x; e < rows * CH; e += 128) {
                     const int row = e / CH, ch = e % CH;
-                    const uint32_t base = sQ + (uint32_t)(row * D * 4);
+                    const uint32_t base = sStage + (uint32_t)(row * D * 4);
                     const uint4 a = lds128(base + (uint32_t)(((2 * ch) ^ (row & 7)) << 4)), c = lds128(base + (uint32_t)(((2 * ch + 1) ^ (row & 7)) << 4));
                     if (!ok) continue;
                     if (whole) {
@@ -669,9 +703,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         part[1] = c;
                     }
                 }
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::Q_EMPTY));
+                if constexpr (!C::OWN_STAGE) {
+                    tc::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::Q_EMPTY));
+                }
             }
             // what the merge needs to know of a cut unit, from each range that it spans: ranges, rows, first row of out,
             // the CTA it starts in

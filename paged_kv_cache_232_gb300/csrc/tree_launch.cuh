@@ -12,7 +12,7 @@ static cudaError_t launch_tree_t(const TreeParams& p, const CUtensorMap& k, cons
     auto kern = tree_kernel<BF16, D, NR>;
     cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, s_done);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, (unsigned)ctas, tree::THREADS, C::SMEM_BYTES, st, p, k, v, q);
+    e = launch_dependent(kern, (unsigned)ctas, C::THREADS, C::SMEM_BYTES, st, p, k, v, q);
     if (e != cudaSuccess) return e;
     // the merge: a block for 16 query rows of each CTA's cut units
     cudaLaunchConfig_t cfg = {};

@@ -42,7 +42,7 @@ def test_copy_pages(layers, bs, hkv, d, latent, pairs):
     g, nb = gen(pairs + d), 2 * pairs + 5
     kc, vc = caches(g, layers, nb, bs, hkv, d, latent)
     pick = torch.randperm(nb, generator=g, device="cuda").to(torch.int32)[:2 * pairs].view(-1, 2).contiguous()
-    pick[pairs // 2:, 0] = pick[pairs // 2, 0]          # one page copied many times
+    pick[pairs // 2:, 0] = pick[pairs // 2, 0].clone()          # one page copied many times
     if pairs > 1:
         pick[0, 0], pick[1, 1] = -1, -1                  # skipped
     want = [bits(kc), bits(vc)]
