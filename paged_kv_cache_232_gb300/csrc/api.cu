@@ -1248,14 +1248,15 @@ struct TreeUnits {
     int tb, group, rows;  // tokens a unit, CTAs that walk the same keys, query rows the kernel is built for
 };
 
-// Blocks of at most 128 rows, of equal numbers of tokens; up to 8 of them side by side.
+// Blocks of at most 128 rows, of equal numbers of tokens; more than one of them side by side, an even number up to 8
+// (pairs share their loads).
 static TreeUnits tree_units(int g_heads, int max_q_len) {
     const int most = 128 / g_heads, blocks = (max_q_len + most - 1) / most;
     TreeUnits u;
-    u.tb = (max_q_len + blocks - 1) / blocks;
     const int passes = (blocks + 7) / 8;
-    u.group = (blocks + passes - 1) / passes;
-    u.rows = u.tb * g_heads <= 32 ? 32 : u.tb * g_heads <= 64 ? 64 : 128;
+    u.group = blocks == 1 ? 1 : ((blocks + passes - 1) / passes + 1) / 2 * 2;
+    u.tb = (max_q_len + u.group * passes - 1) / (u.group * passes);
+    u.rows = u.group > 1 || u.tb * g_heads > 64 ? 128 : u.tb * g_heads > 32 ? 64 : 32;
     return u;
 }
 
@@ -1320,16 +1321,19 @@ int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_
     p.total_q = (int)total_q;
     p.mask_words = mask_words;
     p.hd = head_dim;
+    p.g_magic = (65536 + G - 1) / G;
     p.tb = u.tb;
     p.group = u.group;
     p.tile_log2 = kdim == 256 ? 6 : 7;
     p.block_log2 = 4 + cpb_log2_of(block_size);
-    p.unit_cost = 1;
-    p.min_tiles = 2;
+    // in tiles of 64 KB (32 at 64 columns): 64 sequences of 100..4096 tokens at 2 / 4: 32 rows x 128 95 / 95 us (one sequence of
+    // 1000: 13.1 / 14.6), 128 rows 111 / 107, 256 rows 293 / 278, 32 rows x 64 79 / 66, 32 rows x 256 103 / 95
+    p.unit_cost = u.rows == 32 && kdim == 128 ? 2 : 4;
+    p.min_tiles = p.unit_cost + 1;
     p.qk_scale_log2 = scale * 1.4426950408889634f;
     p.desc = reinterpret_cast<int4*>(base);
-    p.part_ml = reinterpret_cast<float*>(base + w.ml_off);
-    p.part_o = reinterpret_cast<float*>(base + w.o_off);
+    p.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
+    p.part_o = reinterpret_cast<float4*>(base + w.o_off);
     CUtensorMap tk, tv, tq;
     // a token's row of one head is 2 head_dim bytes, its neighbours other heads': no more is fetched into L2 than that
     const CUtensorMapL2promotion fetch = head_dim < 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;

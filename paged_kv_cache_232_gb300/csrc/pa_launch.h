@@ -153,14 +153,15 @@ struct TreeParams {
     unsigned* err;
     int num_seqs, n_q_heads, n_kv_heads, g_heads, max_blocks_per_seq, num_blocks, block_size, max_q_len, total_q, mask_words;
     int hd;                     // head_dim of q, out and the cache (<= D; columns hd .. D-1 are zero)
+    int g_magic;                // ceil(65536 / g_heads): row / g_heads = row * g_magic >> 16
     int tb;                     // tokens per unit of query rows
     int group;                  // CTAs that walk the same keys, each with a block of tb tokens of the tree
     int tile_log2, block_log2;  // log2 of the tokens per tile, per cache block
     int unit_cost;              // what a unit's start and output cost, in tiles (evens out the ranges)
     int min_tiles;              // least cost of a range
     float qk_scale_log2;
-    float* part_o;              // [2 * ctas][NR][D]
-    float* part_ml;             // [2 * ctas][NR][2]: reference (base 2) and exp-sum
+    float4* part_o;             // [2 * ctas][D / 4][NR]: four columns of all rows next to each other
+    float2* part_ml;            // [2 * ctas][NR]: reference (base 2) and exp-sum
     int4* desc;                 // [2][ctas]: the units cut at a range's end and at its start (partials, query rows,
                                 // first row of out, CTA they start in)
 };

@@ -17,9 +17,9 @@
 //    of the other copies' keys (written once: no copy ever writes there).
 //  * K and V arrive by TMA in boxes of 16 tokens (8 in blocks of 8) x 64 columns, 128-byte swizzled, in two
 //    rings of whole tiles; K is released by its product, V by its own.  QK and PV have an issuer each.
-//  * The running maximum is lazy: weights are taken against the old one, and only where one exceeds it by
-//    2^8 are the maximum raised (to a whole power of two) and O and l rescaled.  Weights up to 2^8 are exact
-//    in fp32 and far from the 16-bit formats' limits.
+//  * The running maximum is lazy: weights are taken against the old one, and only where their sum over
+//    a thread's keys exceeds 2^8 are the maximum raised (to a whole power of two) and O and l rescaled.  Weights up to
+//    2^8 are exact in fp32 and far from the 16-bit formats' limits.
 //  * A weight enters the second product rounded once to the cache's type (half a step, 2^-8 in bf16 and 2^-11
 //    in fp16, relative), and l sums the rounded weights, so that they still sum to one; everything else is
 //    fp32.  In fp16 weights are scaled by 2^7, so that small ones are not subnormal.
@@ -38,8 +38,6 @@
 #include "pa_launch.h"
 #include "tcgen05.cuh"
 
-#include <type_traits>
-
 namespace pa {
 namespace tree {
 
@@ -55,31 +53,35 @@ struct Cfg {
     static_assert(NR == 32 || NR == 64 || NR == 128, "query rows of a unit");
     static constexpr int BN = D == 256 ? 64 : 128;      // keys per tile
     static constexpr int COPIES = 128 / NR;
-    static constexpr int SPLIT = NR == 128 ? 2 : 1;      // threads a row of the tile
+    static constexpr int SPLIT = NR < 128 ? 1 : 2;  // threads a row of the tile
     static constexpr int KW = BN / COPIES / SPLIT;      // keys of a tile that one thread takes
-    static constexpr int SOFTMAX = 4 * SPLIT;           // softmax warps; then the issuers, the Q loader, two K and two V loaders
+    static constexpr int SOFTMAX = 4 * SPLIT;           // softmax warps; then the issuers, the Q loader, two K and two V loaders, the V checker
     static constexpr int QK_WARP = SOFTMAX, PV_WARP = SOFTMAX + 1, Q_WARP = SOFTMAX + 2, K_WARP = SOFTMAX + 3,
-                         V_WARP = SOFTMAX + 5, THREADS = (SOFTMAX + 7) * 32;
+                         V_WARP = SOFTMAX + 5, CHECK_WARP = SOFTMAX + 7, THREADS = (SOFTMAX + 8) * 32;
     static constexpr int SLABS = D / 64;
     static constexpr int QSLAB = 128 * 128, KSLAB = BN * 128;
     static constexpr int TILE = SLABS * KSLAB;          // bytes of K (or V) of a tile
-    // The copies are joined in a place of their own where there is one (then the next unit's Q can load meanwhile), at
-    // D 256 in the Q tile's.  Tiles in the rings: what fits beside that
-    static constexpr bool OWN_STAGE = COPIES > 1 && D < 256;
-    static constexpr int NK = D == 64 ? 6 : 3, NV = D == 64 ? 6 : D == 256 || OWN_STAGE ? 2 : 3;
+    // The output passes through a place of its own where there is one (the copies are joined there in fp32; at 128 rows it is
+    // turned there, in 16 bits, so that rows are written whole), while the next unit's Q loads; at D 256 there is none: the
+    // copies are joined in the Q tile's, 128 rows are written as they stand.  Tiles in the rings: what fits beside that
+    static constexpr bool OWN_STAGE = D < 256;
+    static constexpr int NK = D == 64 ? 6 : 2, NV = D == 64 ? 6 : 3;
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = SLABS * QSLAB, V_OFF = K_OFF + NK * TILE;
     static constexpr int STAGE_OFF = OWN_STAGE ? V_OFF + NV * TILE : Q_OFF;
-    static constexpr int ML_OFF = V_OFF + NV * TILE + (OWN_STAGE ? NR * D * 4 : 0);  // what a row's threads tell each other
-    static constexpr int BAR_OFF = ML_OFF + 2 * 128 * 4;
-    static constexpr int K_FULL = 0, K_EMPTY = NK, V_FULL = 2 * NK, V_EMPTY = V_FULL + NV, Q_FULL = V_EMPTY + NV, Q_EMPTY = Q_FULL + 1,
+    static constexpr int ML_OFF = V_OFF + NV * TILE + (OWN_STAGE ? NR * D * (COPIES > 1 ? 4 : 2) : 0);  // what a row's threads tell each other
+    static constexpr int BAR_OFF = ML_OFF + (SPLIT > 2 ? SPLIT : 2) * 128 * 4;
+    static constexpr int K_FULL = 0, K_EMPTY = NK, V_FULL = 2 * NK, V_EMPTY = V_FULL + NV, V_OK = V_EMPTY + NV, Q_FULL = V_OK + NV, Q_EMPTY = Q_FULL + 1,
                          S_FULL = Q_FULL + 2, S_EMPTY = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
                          O_FREE = Q_FULL + 10, DRAIN = Q_FULL + 11, NUM_BARS = Q_FULL + 13;
-    static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch, bad keys
-    static constexpr int SMEM_BYTES = MISC_OFF + 192 + 1024;             // + alignment slack
+    static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch
+    static constexpr int BAD_OFF = MISC_OFF + 192;                       // V rows that are not finite: a bit a row, of 2 NV tiles (read
+                                                                         // after the tile's weights are given, so up to NV tiles late)
+    static constexpr int SMEM_BYTES = BAD_OFF + 2 * NV * 16 + 1024;          // + alignment slack
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(COPIES == 1 || OWN_STAGE || NR * D * 4 <= SLABS * QSLAB, "the copies are joined in the Q tile's place");
     // TMEM: two S buffers, two P buffers (16-bit pairs), O
+    
     static constexpr uint32_t P_COL = D == 256 ? 128 : 384, O_COL = 256, TMEM_COLS = 512;
 };
 
@@ -118,6 +120,28 @@ __device__ __forceinline__ void tma_box(uint32_t el, uint32_t dst, const CUtenso
         " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy), "r"(el)
         : "memory");
+}
+// the same box into both CTAs of a cluster, each one's barrier counting it
+__device__ __forceinline__ void tma_box_pair(uint32_t el, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                             uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
+        "setp.ne.b32 q, %8, 0;\n\tmov.b16 m, 3;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], m, %7;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t el, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\tmov.b16 m, 3;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
+        "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
@@ -158,12 +182,47 @@ __device__ __forceinline__ bool bar_or(int id, bool v) {
 }
 
 // The warp waits; the polling loop stays out of line.  One result for the warp.
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned* err) {
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned* err) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
     if (__any_sync(0xffffffffu, !mbar_try_wait(bar, parity))) return wait_slow(bar, parity, err);
     return true;
+}
+
+// ls += the pair of 16-bit values in w, in fp32 (one instruction a value: converting them first takes as many again)
+template <bool BF16>
+__device__ __forceinline__ void add16x2(float2& ls, uint32_t w) {
+    if constexpr (BF16)
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.bf16 %0, a, %0;\n\tadd.rn.f32.bf16 %1, b, %1;\n\t}"
+            : "+f"(ls.x), "+f"(ls.y)
+            : "r"(w));
+    else
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
+            : "+f"(ls.x), "+f"(ls.y)
+            : "r"(w));
+}
+
+// whether a phase is complete, without waiting
+__device__ __forceinline__ bool mbar_test(uint32_t bar, int phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"((uint32_t)(phase & 1))
+        : "memory");
+    return ok != 0;
+}
+
+// 0 * v + z for pairs of 16-bit values
+template <bool BF16>
+__device__ __forceinline__ uint32_t zero_times(uint32_t v, uint32_t z) {
+    uint32_t d;
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0u), "r"(z));
+    else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0u), "r"(z));
+    return d;
 }
 
 template <int N>
@@ -298,47 +357,57 @@ __device__ __forceinline__ Start find_start(const TreeParams& p, int range, int 
 // One segment of a range: tiles [tile, tile + n) of one unit's `tiles`.
 struct Segment {
     int s, head, tok0, toks;  // sequence, KV head, the unit's first token (of total_q) and tokens
+    int q0;                   // the sequence's first token
     int tile, n, tiles;
     int ctx, keys, drafted;
     int parts, back;          // ranges the unit's tiles span (0: this one alone), and how many of them are before this one
 };
 
-// Calls f for the segments of the CTA's range in which it has rows: block `blk` (of p.group) of each pass.
-template <typename F>
-__device__ __forceinline__ void for_each_segment(const TreeParams& p, const Start& st, int blk, F&& f) {
-    int s = st.s, unit = st.unit, at = st.at, left = st.count;
-    if (left <= 0) return;
-    Seq k = load_seq(p, s);
-    while (left > 0) {
-        const int passes = passes_of(p, k), tiles = tiles_of(p, k);
-        Segment g;
-        const int cost = min(tiles + p.unit_cost - at, left);  // of the unit in this range
-        left -= cost;
-        g.tiles = tiles;
-        g.tile = max(0, at - p.unit_cost);
-        g.n = max(0, at + cost - p.unit_cost) - g.tile;
-        const int rest = tiles - g.tile - g.n;
-        g.back = (g.tile + st.per - 1) / st.per;
-        g.parts = (g.tile > 0 || rest > 0) ? g.back + 1 + (rest + st.per - 1) / st.per : 0;
-        g.s = s;
-        g.head = unit / passes;
-        const int j = (unit - g.head * passes) * p.group + blk;
-        g.tok0 = k.q0 + j * p.tb;
-        g.toks = min(p.tb, k.n - j * p.tb);
-        g.ctx = k.kv_len - k.n;
-        g.keys = k.kv_len;
-        g.drafted = k.n;
-        if (g.n > 0 && g.toks > 0) f(g);
-        if (left <= 0) return;
-        at = 0;
-        if (++unit < passes * p.n_kv_heads) continue;
-        unit = 0;
-        do {
-            if (++s >= p.num_seqs) return;
-            k = load_seq(p, s);
-        } while (k.n == 0);
+// The segments of the CTA's range in which it has rows: block `blk` (of p.group) of each pass.  CTAs of a cluster walk
+// all segments (without rows: toks 0), since each loads a half of what both read.
+template <int CL>
+struct Walk {
+    const TreeParams& p;
+    Seq k;
+    int s, unit, at, left, per, blk;
+    __device__ __forceinline__ Walk(const TreeParams& p_, const Start& st, int blk_)
+        : p(p_), k{0, 0, 0, false}, s(st.s), unit(st.unit), at(st.at), left(st.count), per(st.per), blk(blk_) {
+        if (left > 0) k = load_seq(p, s);
     }
-}
+    // the next one, or false
+    __device__ __forceinline__ bool next(Segment& g) {
+        while (left > 0) {
+            const int passes = k.n <= p.tb * p.group ? 1 : passes_of(p, k), tiles = tiles_of(p, k);
+            const int cost = min(tiles + p.unit_cost - at, left);  // of the unit in this range
+            left -= cost;
+            g.tiles = tiles;
+            g.tile = max(0, at - p.unit_cost);
+            g.n = max(0, at + cost - p.unit_cost) - g.tile;
+            const int rest = tiles - g.tile - g.n;
+            g.back = g.tile > 0 ? (g.tile + per - 1) / per : 0;
+            g.parts = (g.tile > 0 || rest > 0) ? g.back + 1 + (rest > 0 ? (rest + per - 1) / per : 0) : 0;
+            g.s = s;
+            g.head = passes == 1 ? unit : unit / passes;
+            const int j = (unit - g.head * passes) * p.group + blk;
+            g.tok0 = k.q0 + j * p.tb;
+            g.q0 = k.q0;
+            g.toks = max(0, min(p.tb, k.n - j * p.tb));
+            g.ctx = k.kv_len - k.n;
+            g.keys = k.kv_len;
+            g.drafted = k.n;
+            at = 0;
+            if (left > 0 && ++unit == passes * p.n_kv_heads) {
+                unit = 0;
+                do {
+                    if (++s >= p.num_seqs) left = 0;
+                    else k = load_seq(p, s);
+                } while (left > 0 && k.n == 0);
+            }
+            if (g.n > 0 && (CL > 1 || g.toks > 0)) return true;
+        }
+        return false;
+    }
+};
 
 // Bits k0 .. k0 + 31 (keys) that a row sees: the context, and the drafted tokens of its mask words (32-bit ones here).
 __device__ __forceinline__ uint32_t sees32(const uint32_t* row, int words, int k0, int ctx, int drafted) {
@@ -357,14 +426,14 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t* row, int words, int k
 
 }  // namespace tree
 
-template <bool BF16, int D, int NR>
+template <bool BF16, int D, int NR, int CL>
 __global__ void __launch_bounds__(tree::Cfg<D, NR>::THREADS, 1)
 tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const __grid_constant__ CUtensorMap tmQ) {
     using namespace tree;
     using C = Cfg<D, NR>;
     using F = F16x2<BF16>;
-    constexpr int BN = C::BN, KW = C::KW, H = C::SPLIT == 2 && KW > 32 ? 32 : KW, COPIES = C::COPIES, SPLIT = C::SPLIT, SOFTMAX = C::SOFTMAX;
+    constexpr int BN = C::BN, KW = C::KW, H = KW < 32 ? KW : 32, COPIES = C::COPIES, SPLIT = C::SPLIT, SOFTMAX = C::SOFTMAX;
     constexpr int QK_WARP = C::QK_WARP, PV_WARP = C::PV_WARP, Q_WARP = C::Q_WARP, K_WARP = C::K_WARP, V_WARP = C::V_WARP;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -373,7 +442,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     Start* rec = reinterpret_cast<Start*>(smem + C::MISC_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF + 32);
-    uint32_t* bad_keys = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF + 48);  // [BN / 32]
+    volatile uint32_t* bad_keys = reinterpret_cast<volatile uint32_t*>(smem + C::BAD_OFF);  // [2 NV][4]
     long long* warp_sum = reinterpret_cast<long long*>(smem + C::MISC_OFF + 64);
     float* m_s = reinterpret_cast<float*>(smem + C::ML_OFF);
     float* l_s = m_s + 128;
@@ -383,11 +452,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NK; ++i) {
             mbar_init(bar(C::K_FULL + i), 2);
-            mbar_init(bar(C::K_EMPTY + i), 1);
+            mbar_init(bar(C::K_EMPTY + i), CL);
         }
         for (int i = 0; i < C::NV; ++i) {
             mbar_init(bar(C::V_FULL + i), 2);
-            mbar_init(bar(C::V_EMPTY + i), 1);
+            mbar_init(bar(C::V_EMPTY + i), CL);
+            mbar_init(bar(C::V_OK + i), 1);
         }
         mbar_init(bar(C::Q_FULL), 1);
         mbar_init(bar(C::Q_EMPTY), COPIES > 1 && !C::OWN_STAGE ? 1 + SOFTMAX : 1);
@@ -399,7 +469,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             mbar_init(bar(C::DRAIN + i), 1);
         }
         mbar_init(bar(C::O_FREE), SOFTMAX);
-        for (int i = 0; i < 4; ++i) bad_keys[i] = 0u;
         fence_barrier_init();
     }
     if (warp == QK_WARP) {
@@ -413,30 +482,34 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     tc::fence_before();
     const Start start = find_start<C::THREADS>(p, range, (int)gridDim.x / p.group, warp_sum, rec);  // (synchronises the CTA)
     tc::fence_after();
+    if constexpr (CL > 1) cluster_sync();  // the other CTA's barriers are ready
     const uint32_t tmem = *tmem_slot;
     bool ok = true;  // none of this warp's waits has run out
     auto wait = [&](int b, int phase) {
         if (ok) ok = warp_wait(bar(b), (uint32_t)(phase & 1), p.err);
     };
     int done = 0;    // loader warps: tiles loaded
+    // token of a unit's row, row / g_heads (exact for rows below 128 and up to 16 heads)
+    auto row_token = [&](int row) { return (int)(((uint32_t)row * (uint32_t)p.g_magic) >> 16); };
     int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
 
     if (warp < SOFTMAX) {
         // ------------------------------------------------------------ softmax, rescale, epilogue
         // row of the tile; of the unit; which copy of it, or which of its two threads (its share of a tile's keys)
-        const int quarter = warp & 3, R = 32 * quarter + lane, share = SPLIT == 2 ? warp >> 2 : COPIES == 1 ? 0 : (32 * warp) / NR;
-        const int r = SPLIT == 2 ? R : R - share * NR;
+        const int quarter = warp & 3, R = 32 * quarter + lane, share = SPLIT > 1 ? warp >> 2 : COPIES == 1 ? 0 : (32 * warp) / NR;
+        const int r = SPLIT > 1 ? R : R - share * NR;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_base + (uint32_t)(share * KW), tO = tmem + lane_base + C::O_COL;
         const uint32_t tP = tmem + lane_base + C::P_COL + (uint32_t)(share * KW / 2);
-        // the two threads of a row share its reference: what one finds the other has to know
-        auto pair_or = [&](bool v) {
-            if constexpr (SPLIT == 2) return bar_or<64>(2 + quarter, v);
+        // the threads of a row share its reference: what one finds the others have to know
+        auto row_or = [&](bool v) {
+            if constexpr (SPLIT > 1) return bar_or<32 * SPLIT>(2 + quarter, v);
             else return __any_sync(0xffffffffu, v) != 0;
         };
-        const float sc = p.qk_scale_log2;
-        constexpr uint32_t kBitsMost = BF16 ? 0x4380u : 0x7800u;  // 2^(8 + kShift) in 16 bits
-        constexpr uint32_t kBitsInf = BF16 ? 0x7F80u : 0x7C00u;
+        // (scale 0: all scores that are seen count the same, as with the smallest scale)
+        const float sc = p.qk_scale_log2 != 0.f ? p.qk_scale_log2 : 0x1p-126f;
+        const uint32_t unseen = sc > 0.f ? 0xFF800000u : 0x7F800000u;  // -inf, +inf
+        constexpr float kMost = BF16 ? 0x1p8f : 0x1p15f;  // 2^(8 + kShift)
         if constexpr (COPIES > 1) {  // the other copies' columns of P stay zero
             uint32_t z[32];
 #pragma unroll
@@ -445,150 +518,142 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             for (int q = 0; q < BN / 32; ++q) stn<32>(tmem + lane_base + C::P_COL + 32 * q, z);
             tc::wait_st();
         }
+        const int tok_r = row_token(r);
+        bool s_ready = false, pv_ready = false;  // seen during the tile before
         int i = 0;  // tile number over the CTA's range
-        for_each_segment(p, start, blk, [&](const Segment& g) {
+        constexpr int MW = (KW + 31) / 32;
+        Walk<CL> walk(p, start, blk);
+        for (Segment g; walk.next(g);) {
             const int rows = g.toks * p.g_heads;
             const bool valid = r < rows;
-            const uint32_t* mask = reinterpret_cast<const uint32_t*>(p.mask + (size_t)(g.tok0 + (valid ? r / p.g_heads : 0)) * p.mask_words);
-            float m_ref = -INFINITY, l = 0.f;
-            for (int u = 0; u < g.n; ++u, ++i) {
-                const int kbase = (g.tile + u) * BN, k0 = kbase + share * KW, b = i & 1;
-                const bool drafts = kbase + BN > g.ctx;  // the tile holds drafted tokens or keys past them
-                constexpr int MW = (KW + 31) / 32;
-                uint32_t sees[MW];
+            const uint32_t* mask = reinterpret_cast<const uint32_t*>(p.mask + (size_t)(valid ? g.tok0 + tok_r : g.q0) * p.mask_words);
+            // which keys of tile `tile` the row sees (bits of this thread's); loaded a tile ahead
+            auto row_sees = [&](int tile, uint32_t (&w)[MW]) {
 #pragma unroll
-                for (int w = 0; w < MW; ++w)
-                    sees[w] = drafts ? sees32(mask, 2 * p.mask_words, k0 + 32 * w, g.ctx, g.drafted) : 0xffffffffu;
-                wait(C::S_FULL + b, i >> 1);
+                for (int x = 0; x < MW; ++x)
+                    w[x] = sees32(mask, 2 * p.mask_words, tile * BN + share * KW + 32 * x, g.ctx, g.drafted);
+            };
+            uint32_t sees[MW], sees_next[MW];
+            float m_ref = -INFINITY, l = 0.f;
+            // a drafted V row of tile number t that is not finite makes the row NaN if it sees it
+            auto poison = [&](int t) {
+#pragma unroll
+                for (int w = 0; w < MW; ++w) {
+                    const int at = share * KW + 32 * w;  // this thread's keys of the tile: KW from share * KW on
+                    uint32_t k = bad_keys[4 * (t % (2 * C::NV)) + (at >> 5)] >> (at & 31);
+                    if constexpr (KW < 32) k &= (1u << KW) - 1u;
+                    if (k & sees[w]) l = __uint_as_float(0x7FC00000u);
+                }
+            };
+            if ((g.tile + 1) * BN > g.ctx) row_sees(g.tile, sees_next);
+            for (int u = 0; u < g.n; ++u, ++i) {
+                const int kbase = (g.tile + u) * BN, b = i & 1;
+                const bool drafts = kbase + BN > g.ctx;  // the tile holds drafted tokens or keys past them
+#pragma unroll
+                for (int w = 0; w < MW; ++w) sees[w] = sees_next[w];
+                if (kbase + 2 * BN > g.ctx) row_sees(g.tile + u + 1, sees_next);
+                if (!__all_sync(0xffffffffu, s_ready)) wait(C::S_FULL + b, i >> 1);
+                // the weights' buffer is free
+                if (i >= 2 && !__all_sync(0xffffffffu, pv_ready)) wait(C::PV_DONE + b, (i >> 1) - 1);
                 tc::fence_after();
-                if (i >= 2) wait(C::PV_DONE + b, (i >> 1) - 1);  // the weights' buffer is free
                 const uint32_t tSb = tS + (uint32_t)(b * BN), tPb = tP + (uint32_t)(b * BN / 2);
                 bool redo = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
                 float add = 0.f;
-                // MASK: the tile holds keys that not every row sees
-                auto weigh = [&](auto MASK) {
-                    auto seen = [&](float v, int e) {
-                        if constexpr (decltype(MASK)::value) return (sees[e / 32] >> (e & 31)) & 1u ? v : -INFINITY;
-                        else return v;
-                    };
-#pragma unroll 1
-                    for (int attempt = 0; attempt < 2; ++attempt) {
-                        if (redo) {
-                            float mx = -INFINITY;
+                // part h of this thread's scores; those of keys that the row does not see, where the tile holds such keys, become
+                // what the scale turns into -inf
+                auto scores = [&](int h, uint32_t (&x)[H]) {
+                    if (drafts) {
 #pragma unroll
-                            for (int h = 0; h < KW / H; ++h) {
-                                uint32_t x[H];
-                                ldn<H>(tSb + h * H, x);
-                                tc::wait_ld();
-                                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                                for (int e = 0; e < H; ++e) m4[e & 3] = fmaxf(m4[e & 3], seen(__uint_as_float(x[e]) * sc, h * H + e));
-                                mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                            }
-                            if constexpr (SPLIT == 2) {
-                                m_s[128 * share + R] = mx;
-                                bar_sync<64>(2 + quarter);
-                                mx = fmaxf(mx, m_s[128 * (share ^ 1) + R]);
-                            }
-                            const float mt = ceilf(mx);
-                            float alpha = 1.f;
-                            if (valid && mt > m_ref) {
-                                alpha = m_ref == -INFINITY ? 1.f : ex2(m_ref - mt);
-                                m_ref = mt;
-                                l *= alpha;
-                            }
-                            if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                                wait(C::PV_DONE + (b ^ 1), (i - 1) >> 1);  // O holds every tile before this one
-                                tc::fence_after();
-#pragma unroll 1
-                                for (int q = 0; q < D / 16 / SPLIT; ++q) {  // (each thread of a row its part of the columns)
-                                    uint32_t o[16];
-                                    const uint32_t at = tO + (uint32_t)((SPLIT == 2 ? share * (D / 2) : 0) + 16 * q);
-                                    tc::ld16(at, o);
-                                    tc::wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tc::st16(at, o);
-                                }
-                            }
-                        }
-                        const float mu = m_ref == -INFINITY ? 0.f : m_ref - kShift<BF16>;
-                        const float2 sc2 = make_float2(sc, sc), nmu2 = make_float2(-mu, -mu);
-                        float2 ls = make_float2(0.f, 0.f);
-                        uint32_t pmax = 0;
-#pragma unroll
-                        for (int h = 0; h < KW / H; ++h) {
-                            uint32_t x[H], w[H / 2];
-                            ldn<H>(tSb + h * H, x);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < H / 2; ++e) {
-                                const float2 v = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nmu2);
-                                w[e] = F::pack_rn(ex2(seen(v.x, h * H + 2 * e)), ex2(seen(v.y, h * H + 2 * e + 1)));
-                                ls = fadd2(ls, F::unpack(w[e]));
-                                pmax = umax16x2(pmax, w[e]);
-                            }
-                            stn<H / 2>(tPb + h * H / 2, w);
-                        }
-                        add = ls.x + ls.y;
-                        const uint32_t pm = max(pmax & 0xFFFFu, pmax >> 16);
-                        // (at SPLIT 2 the vote also says that the other thread has read this one's maximum)
-                        const bool over = pair_or(valid && pm > kBitsMost);
-                        if (redo || !over) break;
-                        redo = true;  // a row outgrew its reference by more than 2^8
-                        tc::wait_st();
+                        for (int e = 0; e < H; ++e)
+                            if (!((sees[(h * H + e) / 32] >> ((h * H + e) & 31)) & 1u)) x[e] = unseen;
                     }
                 };
-                if (drafts) weigh(std::true_type{});
-                else weigh(std::false_type{});
+#pragma unroll 1
+                for (int attempt = 0; attempt < 2; ++attempt) {
+                    if (redo) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int h = 0; h < KW / H; ++h) {
+                            uint32_t x[H];
+                            ldn<H>(tSb + h * H, x);
+                            tc::wait_ld();
+                            scores(h, x);
+                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int e = 0; e < H; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e]) * sc);
+                            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                        }
+                        if constexpr (SPLIT > 1) {
+                            m_s[128 * share + R] = mx;
+                            bar_sync<32 * SPLIT>(2 + quarter);
+#pragma unroll
+                            for (int k = 0; k < SPLIT; ++k) mx = fmaxf(mx, m_s[128 * k + R]);
+                        }
+                        const float mt = ceilf(mx);
+                        float alpha = 1.f;
+                        if (valid && mt > m_ref) {
+                            alpha = m_ref == -INFINITY ? 1.f : ex2(m_ref - mt);
+                            m_ref = mt;
+                            l *= alpha;
+                        }
+                        if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                            wait(C::PV_DONE + (b ^ 1), (i - 1) >> 1);  // O holds every tile before this one
+                            tc::fence_after();
+#pragma unroll 1
+                            for (int q = 0; q < D / 16 / SPLIT; ++q) {  // (each thread of a row its part of the columns)
+                                uint32_t o[16];
+                                const uint32_t at = tO + (uint32_t)((SPLIT > 1 ? share * (D / SPLIT) : 0) + 16 * q);
+                                tc::ld16(at, o);
+                                tc::wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tc::st16(at, o);
+                            }
+                        }
+                    }
+                    const float mu = m_ref == -INFINITY ? 0.f : m_ref - kShift<BF16>;
+                    const float2 sc2 = make_float2(sc, sc), nmu2 = make_float2(-mu, -mu);
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t x[2][H];
+                    ldn<H>(tSb, x[0]);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int h = 0; h < KW / H; ++h) {
+                        if (h + 1 < KW / H) ldn<H>(tSb + (h + 1) * H, x[(h + 1) & 1]);  // in flight during this part
+                        scores(h, x[h & 1]);
+                        uint32_t w[H / 2];
+#pragma unroll
+                        for (int e = 0; e < H / 2; ++e) {
+                            const float2 v = ffma2(make_float2(__uint_as_float(x[h & 1][2 * e]), __uint_as_float(x[h & 1][2 * e + 1])), sc2, nmu2);
+                            w[e] = F::pack_rn(ex2(v.x), ex2(v.y));
+                            add16x2<BF16>(ls[e & 1], w[e]);
+                        }
+                        stn<H / 2>(tPb + h * H / 2, w);
+                        if (h + 1 < KW / H) tc::wait_ld();
+                    }
+                    // the next tile's barriers, without waiting
+                    s_ready = mbar_test(bar(C::S_FULL + (b ^ 1)), (i + 1) >> 1);
+                    pv_ready = mbar_test(bar(C::PV_DONE + (b ^ 1)), ((i + 1) >> 1) - 1);
+                    ls[0] = fadd2(ls[0], ls[1]);
+                    add = ls[0].x + ls[0].y;
+                    // (no weight is above their sum; the vote also says that a row's other thread has read this one's maximum)
+                    const bool over = row_or(valid && add > kMost);
+                    if (redo || !over) break;
+                    redo = true;  // a row outgrew its reference by more than 2^8: once more (the same columns are written)
+                    tc::wait_st();
+                }
                 l += add;
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::S_EMPTY + b));
-                if (drafts) {
-                    // V rows of the tile: those past the keys may hold anything (their weights are 0, but 0 * NaN is
-                    // NaN) and are zeroed, up to the end of the last box that was loaded (the others are zero already);
-                    // so are drafted ones that are not finite, and the rows that see one become NaN
-                    wait(C::V_FULL + i % C::NV, i / C::NV);
-                    const int t = (int)threadIdx.x, key = kbase + t;
-                    const uint32_t vrow = sV + (uint32_t)((i % C::NV) * C::TILE + t * 128);
-                    bool bad = false;
-                    if (t < BN && key >= g.ctx && key < g.keys) {
-                        uint32_t most = 0;
-#pragma unroll
-                        for (int q = 0; q < C::SLABS * 8; ++q) {
-                            const uint4 v = lds128(vrow + (q >> 3) * C::KSLAB + (((q + t) & 7) << 4));
-                            most = umax16x2(most, v.x & 0x7FFF7FFFu);
-                            most = umax16x2(most, v.y & 0x7FFF7FFFu);
-                            most = umax16x2(most, v.z & 0x7FFF7FFFu);
-                            most = umax16x2(most, v.w & 0x7FFF7FFFu);
-                        }
-                        bad = max(most & 0xFFFFu, most >> 16) >= kBitsInf;
-                    }
-                    if (t < BN && (bad || (key >= g.keys && key < ((g.keys + 15) & ~15)))) {
-#pragma unroll
-                        for (int q = 0; q < C::SLABS * 8; ++q)
-                            sts128(vrow + (q >> 3) * C::KSLAB + (((q + t) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
-                    }
-                    if (bar_or<32 * SOFTMAX>(1, bad)) {
-                        const uint32_t mine = __ballot_sync(0xffffffffu, bad);
-                        if (lane == 0 && 32 * warp < BN) bad_keys[warp] = mine;
-                        bar_sync<32 * SOFTMAX>(1);
-#pragma unroll
-                        for (int w = 0; w < MW; ++w) {
-                            const int at = share * KW + 32 * w;  // this thread's keys of the tile: KW from share * KW on
-                            uint32_t k = bad_keys[at >> 5] >> (at & 31);
-                            if constexpr (KW < 32) k &= (1u << KW) - 1u;
-                            if (k & sees[w]) l = __uint_as_float(0x7FC00000u);
-                        }
-                        bar_sync<32 * SOFTMAX>(1);
-                    }
-                    tc::fence_async_smem();
-                }
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::P_FULL + b));
+                if (drafts && u < g.n - 1) {
+                    wait(C::V_OK + i % C::NV, i / C::NV);
+                    poison(i);
+                }
             }
             // the segment's end: O / l, or the partial
             const bool whole = g.parts == 0;
@@ -596,111 +661,135 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             const size_t row0 = (size_t)g.tok0 * p.n_q_heads + (size_t)g.head * p.g_heads;
             wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
             tc::fence_after();
+            if ((g.tile + g.n) * BN > g.ctx) poison(i - 1);  // (its product waited for the check)
             if constexpr (COPIES == 1) {
-                if constexpr (SPLIT == 2) {  // the row's sum, in a fixed order
-                    m_s[128 * share + R] = l;
-                    bar_sync<64>(2 + quarter);
-                    l = m_s[R] + m_s[128 + R];
-                    bar_sync<64>(2 + quarter);
-                }
-                constexpr int W = D / SPLIT;  // columns that this thread writes
-                const int c0 = SPLIT == 2 ? share * W : 0;
-                const float f = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;
-                if (!whole && valid && share == 0) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(m_ref, l);
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)(r / p.g_heads) * p.n_q_heads + r % p.g_heads) * p.hd + c0;
-                float* part = p.part_o + ((size_t)slot * NR + r) * D + c0;
-#pragma unroll 1
-                for (int q = 0; q < W / 32; ++q) {
-                    uint32_t o[32];
-                    tc::ld32(tO + (uint32_t)(c0 + 32 * q), o);
+                constexpr int W = D / SPLIT, CW = W < 32 ? W : 32;  // columns of this thread, at a time
+                const int c0 = share * W;
+                uint32_t o[CW];
+                auto read_o = [&](int q) {
+                    ldn<CW>(tO + (uint32_t)(c0 + CW * q), o);
                     tc::wait_ld();
-                    if (q == W / 32 - 1) {  // O read: the next segment's first PV may overwrite it
+                    if (q == W / CW - 1) {  // O read: the next segment's first PV may overwrite it
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::O_FREE));
                     }
-                    if (!valid || !ok) continue;
-                    if (whole) {
-                        if (c0 + 32 * q < p.hd) {
+                };
+                // the row's sum, in a fixed order
+                m_s[128 * share + R] = l;
+                bar_sync<32 * SPLIT>(2 + quarter);
+                l = 0.f;
 #pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                *reinterpret_cast<uint4*>(dst + 32 * q + 8 * v) =
-                                    make_uint4(F::pack_rn(__uint_as_float(o[8 * v]) * f, __uint_as_float(o[8 * v + 1]) * f),
-                                               F::pack_rn(__uint_as_float(o[8 * v + 2]) * f, __uint_as_float(o[8 * v + 3]) * f),
-                                               F::pack_rn(__uint_as_float(o[8 * v + 4]) * f, __uint_as_float(o[8 * v + 5]) * f),
-                                               F::pack_rn(__uint_as_float(o[8 * v + 6]) * f, __uint_as_float(o[8 * v + 7]) * f));
+                for (int k = 0; k < SPLIT; ++k) l += m_s[128 * k + R];
+                bar_sync<32 * SPLIT>(2 + quarter);
+                const float f = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;
+                if (!whole && valid && share == 0) p.part_ml[(size_t)slot * NR + r] = make_float2(m_ref, l);
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)tok_r * p.n_q_heads + (r - tok_r * p.g_heads)) * p.hd + c0;
+                float4* part = p.part_o + ((size_t)slot * (D / 4) + c0 / 4) * NR + r;
+#pragma unroll
+                for (int q = 0; q < W / CW; ++q) {
+                    read_o(q);
+                    if (!whole) {
+                        if (valid && ok) {
+#pragma unroll
+                            for (int v = 0; v < CW / 4; ++v)
+                                part[(CW / 4 * q + v) * NR] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                                          __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
                         }
-                    } else {
+                        continue;
+                    }
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            *reinterpret_cast<uint4*>(part + 32 * q + 4 * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                    for (int v = 0; v < CW / 8; ++v) {
+                        const uint4 w = make_uint4(F::pack_rn(__uint_as_float(o[8 * v]) * f, __uint_as_float(o[8 * v + 1]) * f),
+                                                   F::pack_rn(__uint_as_float(o[8 * v + 2]) * f, __uint_as_float(o[8 * v + 3]) * f),
+                                                   F::pack_rn(__uint_as_float(o[8 * v + 4]) * f, __uint_as_float(o[8 * v + 5]) * f),
+                                                   F::pack_rn(__uint_as_float(o[8 * v + 6]) * f, __uint_as_float(o[8 * v + 7]) * f));
+                        const int ch = (c0 + CW * q) / 8 + v;
+                        if constexpr (C::OWN_STAGE) sts128(sStage + (uint32_t)(R * D * 2 + ((ch ^ (R & 7)) << 4)), w);
+                        else if (valid && ok && 8 * ch < p.hd) *reinterpret_cast<uint4*>(dst + CW * q + 8 * v) = w;
+                    }
+                }
+                if constexpr (C::OWN_STAGE) {
+                    if (whole) {  // rows of this quarter, whole rows by neighbouring lanes
+                        bar_sync<32 * SPLIT>(2 + quarter);
+                        constexpr int CH = D / 8, RP = 32 * SPLIT / CH;  // chunks a row, rows at a time
+                        const int ch = lane % CH;
+#pragma unroll
+                        for (int q = 0; q < 32 / RP; ++q) {
+                            const int row = 32 * quarter + RP * q + (32 * share + lane) / CH, tok = row_token(row);
+                            const uint4 w = lds128(sStage + (uint32_t)(row * D * 2 + ((ch ^ (row & 7)) << 4)));
+                            if (row < rows && ok && 8 * ch < p.hd)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                          (row0 + (size_t)tok * p.n_q_heads + (row - tok * p.g_heads)) * p.hd + 8 * ch) = w;
+                        }
                     }
                 }
             } else {
-                // join the copies: factors 2^(m - max m), then every copy adds its O, a share of the columns at a time
+                // join the copies: factors 2^(m - max m), then every copy adds its O, a share of the columns at a time; who adds
+                // last has the sum
                 m_s[R] = m_ref;
                 l_s[R] = l;
                 bar_sync<128>(1);
-                float mx = -INFINITY, lt = 0.f;
-#pragma unroll
-                for (int c = 0; c < COPIES; ++c) mx = fmaxf(mx, m_s[c * NR + r]);
-#pragma unroll
-                for (int c = 0; c < COPIES; ++c) {
-                    const float m = m_s[c * NR + r], lc = l_s[c * NR + r];
-                    if (m != -INFINITY) lt += lc * ex2(m - mx);
-                    else lt += lc;  // 0, or NaN
+                float mx = m_ref, lt = 0.f;
+#pragma unroll 1
+                for (int c = r; c < 128; c += NR) mx = fmaxf(mx, m_s[c]);
+#pragma unroll 1
+                for (int c = r; c < 128; c += NR) {
+                    const float m = m_s[c];
+                    lt = fmaf(l_s[c], m == -INFINITY ? 1.f : ex2(m - mx), lt);  // (l is 0 there, or NaN)
                 }
                 float f = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
                 if (whole) f = lt != 0.f ? f / lt : 0.f;
-                else if (valid && share == 0) *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * NR + r) * 2) = make_float2(mx, lt);
-                constexpr int W = D / COPIES;           // columns of a share
+                else if (valid && share == 0) p.part_ml[(size_t)slot * NR + r] = make_float2(mx, lt);
+                constexpr int W = D / COPIES, CW = W < 32 ? W : 32;  // columns of a share, at a time
                 const uint32_t srow = sStage + (uint32_t)(r * D * 4);
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)tok_r * p.n_q_heads + (r - tok_r * p.g_heads)) * p.hd;
+                float4* part = p.part_o + (size_t)slot * (D / 4) * NR + r;
 #pragma unroll 1
                 for (int k = 0; k < COPIES; ++k) {
                     const int c0 = ((share + k) % COPIES) * W;
+                    const bool last = k == COPIES - 1;
 #pragma unroll 1
-                    for (int q = 0; q < W / 16; ++q) {
-                        uint32_t o[16];
-                        tc::ld16(tO + (uint32_t)(c0 + 16 * q), o);
+                    for (int c = c0; c < c0 + W; c += CW) {
+                        uint32_t o[CW];
+                        uint4 x[CW / 4];
+                        ldn<CW>(tO + (uint32_t)c, o);
+#pragma unroll
+                        for (int v = 0; v < CW / 4; ++v)
+                            x[v] = k > 0 ? lds128(srow + (uint32_t)(((c / 4 + v) ^ (r & 7)) << 4)) : make_uint4(0u, 0u, 0u, 0u);
                         tc::wait_ld();
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const uint32_t at = srow + (uint32_t)((((c0 + 16 * q) / 4 + v) ^ (r & 7)) << 4);
-                            float4 a = make_float4(__uint_as_float(o[4 * v]) * f, __uint_as_float(o[4 * v + 1]) * f,
-                                                   __uint_as_float(o[4 * v + 2]) * f, __uint_as_float(o[4 * v + 3]) * f);
-                            if (k > 0) {
-                                const uint4 x = lds128(at);
-                                a.x += __uint_as_float(x.x);
-                                a.y += __uint_as_float(x.y);
-                                a.z += __uint_as_float(x.z);
-                                a.w += __uint_as_float(x.w);
-                            }
-                            sts128(at, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z), __float_as_uint(a.w)));
+                        for (int e = 0; e < CW; ++e) {
+                            const uint32_t before = e % 4 == 0 ? x[e / 4].x : e % 4 == 1 ? x[e / 4].y : e % 4 == 2 ? x[e / 4].z : x[e / 4].w;
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f, __uint_as_float(before)));
+                        }
+                        if (!last) {
+#pragma unroll
+                            for (int v = 0; v < CW / 4; ++v)
+                                sts128(srow + (uint32_t)(((c / 4 + v) ^ (r & 7)) << 4), make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
+                        } else if (!valid || !ok) {
+                        } else if (whole) {
+#pragma unroll
+                            for (int v = 0; v < CW / 8; ++v)
+                                if (c + 8 * v < p.hd)
+                                    *reinterpret_cast<uint4*>(dst + c + 8 * v) =
+                                        make_uint4(F::pack_rn(__uint_as_float(o[8 * v]), __uint_as_float(o[8 * v + 1])),
+                                                   F::pack_rn(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3])),
+                                                   F::pack_rn(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5])),
+                                                   F::pack_rn(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7])));
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < CW / 4; ++v)
+                                part[(c / 4 + v) * NR] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                                     __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
                         }
                     }
-                    if (k == COPIES - 1) {  // O read: the next segment's first PV may overwrite it
+                    if (last) {  // O read: the next segment's first PV may overwrite it
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::O_FREE));
-                    }
-                    bar_sync<128>(1);
-                }
-                constexpr int CH = D / 8;               // chunks of 8 columns
-                for (int e = threadIdx.x; e < rows * CH; e += 128) {
-                    const int row = e / CH, ch = e % CH;
-                    const uint32_t base = sStage + (uint32_t)(row * D * 4);
-                    const uint4 a = lds128(base + (uint32_t)(((2 * ch) ^ (row & 7)) << 4)), c = lds128(base + (uint32_t)(((2 * ch + 1) ^ (row & 7)) << 4));
-                    if (!ok) continue;
-                    if (whole) {
-                        if (8 * ch < p.hd)
-                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                                      (row0 + (size_t)(row / p.g_heads) * p.n_q_heads + row % p.g_heads) * p.hd + 8 * ch) =
-                                make_uint4(F::pack_rn(__uint_as_float(a.x), __uint_as_float(a.y)), F::pack_rn(__uint_as_float(a.z), __uint_as_float(a.w)),
-                                           F::pack_rn(__uint_as_float(c.x), __uint_as_float(c.y)), F::pack_rn(__uint_as_float(c.z), __uint_as_float(c.w)));
                     } else {
-                        uint4* part = reinterpret_cast<uint4*>(p.part_o + ((size_t)slot * NR + row) * D + 8 * ch);
-                        part[0] = a;
-                        part[1] = c;
+                        bar_sync<128>(1);
                     }
                 }
                 if constexpr (!C::OWN_STAGE) {
@@ -713,56 +802,117 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             // the CTA it starts in
             if (!whole)
                 (g.tile == 0 ? begins : goes_on) = make_int4(g.parts, rows, (int)row0, (int)blockIdx.x - g.back * p.group);
-        });
+        }
+    } else if (warp == C::CHECK_WARP) {
+        // ------------------------------------------------------------ V rows of tiles with drafted tokens, before their product:
+        // rows past the keys may hold anything (their weights are 0, but 0 * NaN is NaN) and are zeroed, up to the end of the
+        // last box that was loaded (the others are zero already); so are drafted rows that are not finite, which are noted
+        int i = 0;
+        Walk<CL> walk(p, start, blk);
+        for (Segment g; walk.next(g);) {
+            for (int u = 0; u < g.n; ++u, ++i) {
+                const int kbase = (g.tile + u) * BN, st = i % C::NV;
+                wait(C::V_FULL + st, i / C::NV);
+                if (kbase + BN > g.ctx) {
+                    volatile uint32_t* bits = bad_keys + 4 * (i % (2 * C::NV));
+                    const uint32_t tile = sV + (uint32_t)(st * C::TILE);
+                    if (lane < 4) bits[lane] = 0u;
+                    // 16 rows at a time, two lanes each: half of its chunks, starting at different banks
+                    const int half = lane & 1, d1 = min(BN, g.keys - kbase);
+#pragma unroll 1
+                    for (int t0 = max(0, g.ctx - kbase); t0 < d1; t0 += 16) {
+                        const int t = t0 + (lane >> 1);
+                        const uint32_t vrow = tile + (uint32_t)(t * 128);
+                        uint32_t z[4] = {0u, 0u, 0u, 0u};  // 0 * v: NaN where v is not finite
+                        if (t < d1) {
+#pragma unroll
+                            for (int c = 0; c < C::SLABS * 4; ++c) {
+                                const uint4 v = lds128(vrow + (uint32_t)((c >> 2) * C::KSLAB + (((c & 3) + 4 * half + t) & 7) * 16));
+                                z[0] = zero_times<BF16>(v.x, z[0]);
+                                z[1] = zero_times<BF16>(v.y, z[1]);
+                                z[2] = zero_times<BF16>(v.z, z[2]);
+                                z[3] = zero_times<BF16>(v.w, z[3]);
+                            }
+                        }
+                        bool bad = ((z[0] | z[1] | z[2] | z[3]) & 0x7FFF7FFFu) != 0u;
+                        const uint32_t all = __ballot_sync(0xffffffffu, bad);
+                        if (all) {
+                            bad = (all >> (lane & ~1) & 3u) != 0u;  // either half
+                            if (bad) {
+                                if (half == 0) atomicOr(const_cast<uint32_t*>(bits) + (t >> 5), 1u << (t & 31));
+                                for (int c = half; c < C::SLABS * 8; c += 2) sts128(vrow + (uint32_t)((c >> 3) * C::KSLAB + (c & 7) * 16), make_uint4(0u, 0u, 0u, 0u));
+                            }
+                        }
+                    }
+                    // the rows past the keys, up to the end of the last box
+                    const int z1 = min(BN, ((g.keys + 15) & ~15) - kbase);
+                    for (int e = lane; e < (z1 - d1) * C::SLABS * 8; e += 32) {
+                        const int c = e % (C::SLABS * 8);
+                        sts128(tile + (uint32_t)((d1 + e / (C::SLABS * 8)) * 128 + (c >> 3) * C::KSLAB + (c & 7) * 16), make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    tc::fence_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::V_OK + st));
+            }
+        }
     } else if (warp >= K_WARP) {
         // ------------------------------------------------------------ cache rows into the rings, every second box of K or V
         const bool is_v = warp >= V_WARP;
-        const int odd = (warp - K_WARP) & 1;
+        // in a cluster every box goes to both CTAs and each issues half of them
+        const int first = ((warp - K_WARP) & 1) + (CL > 1 ? 2 * (blk & 1) : 0);
         const CUtensorMap* map = is_v ? &tmV : &tmK;
         if (lane == 0) tma_prefetch_desc(map);
-        const uint64_t pol = p.group == 1 ? l2_policy_evict_first() : l2_policy_normal();  // read once, or by the group's CTAs
+        const uint64_t pol = p.group == CL ? l2_policy_evict_first() : l2_policy_normal();  // read once, or by the group's CTAs
         const int br = min(p.block_size, 16), nbox = BN / br;
         const int full0 = is_v ? C::V_FULL : C::K_FULL, empty0 = is_v ? C::V_EMPTY : C::K_EMPTY;
         const int slots = is_v ? C::NV : C::NK;
         const uint32_t ring = is_v ? sV : sK, el = elect_one();
-        for_each_segment(p, start, blk, [&](const Segment& g) {
-            const int32_t* bt = p.block_tables + (size_t)g.s * p.max_blocks_per_seq;
-            auto entry = [&](int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
-                const int t = tile * BN + lane * br;
-                if (lane >= nbox || t >= g.keys) return p.num_blocks;
-                const int e = __ldg(bt + (t >> p.block_log2));
-                if (e < 0 || e >= p.num_blocks) {
-                    flag_error(p.err, PA_DEVERR_BLOCK);
-                    return p.num_blocks;
-                }
-                return e;
-            };
-            int id = entry(g.tile);
+        auto entry = [&](const Segment& g, int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
+            const int t = tile * BN + lane * br;
+            if (lane >= nbox || t >= g.keys) return p.num_blocks;
+            const int e = __ldg(p.block_tables + (size_t)g.s * p.max_blocks_per_seq + (t >> p.block_log2));
+            if (e < 0 || e >= p.num_blocks) {
+                flag_error(p.err, PA_DEVERR_BLOCK);
+                return p.num_blocks;
+            }
+            return e;
+        };
+        Walk<CL> walk(p, start, blk);
+        Segment g, ahead;
+        bool more = walk.next(g);
+        int id = more ? entry(g, g.tile) : 0;
+        for (; more; g = ahead) {
+            more = walk.next(ahead);
             for (int u = 0; u < g.n; ++u, ++done) {
                 const int tile = g.tile + u;
-                const int nxt = u + 1 < g.n ? entry(tile + 1) : 0;
+                const int nxt = u + 1 < g.n ? entry(g, tile + 1) : more ? entry(ahead, ahead.tile) : 0;
                 const int st = (int)uniform((uint32_t)(done % slots)), use = done / slots;
                 if (use > 0) wait(empty0 + st, use - 1);
                 const uint32_t full = bar(full0 + st), dst = ring + (uint32_t)(st * C::TILE);
                 if (el) mbar_arrive_expect_tx(full, C::TILE / 2);
                 __syncwarp();
 #pragma unroll 1
-                for (int x = odd; x < nbox; x += 2) {
+                for (int x = first; x < nbox; x += 2 * CL) {
                     const int e = __shfl_sync(0xffffffffu, id, x);
                     const int row = (int)uniform((uint32_t)((tile * BN + x * br) & (p.block_size - 1)));
 #pragma unroll
-                    for (int sl = 0; sl < C::SLABS; ++sl)
-                        tma_box(el, dst + (uint32_t)(sl * C::KSLAB + x * br * 128), map, sl * 64, g.head, row, e, full, pol);
+                    for (int sl = 0; sl < C::SLABS; ++sl) {
+                        const uint32_t to = dst + (uint32_t)(sl * C::KSLAB + x * br * 128);
+                        if constexpr (CL > 1) tma_box_pair(el, to, map, sl * 64, g.head, row, e, full, pol);
+                        else tma_box(el, to, map, sl * 64, g.head, row, e, full, pol);
+                    }
                 }
                 id = nxt;
             }
-        });
+        }
     } else if (warp == Q_WARP && lane == 0) {
         // ------------------------------------------------------------ the units' query rows, once for each copy
         tma_prefetch_desc(&tmQ);
         int seg = 0;
         const uint32_t box = (uint32_t)(p.tb * p.g_heads * 128);
-        for_each_segment(p, start, blk, [&](const Segment& g) {
+        Walk<CL> walk(p, start, blk);
+        for (Segment g; walk.next(g);) {
             if (seg > 0 && ok) ok = mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err);
             mbar_arrive_expect_tx(bar(C::Q_FULL), box * C::SLABS * COPIES);
 #pragma unroll 1
@@ -771,7 +921,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 for (int sl = 0; sl < C::SLABS; ++sl)
                     tma_q(sQ + (uint32_t)(sl * C::QSLAB + c * NR * 128), &tmQ, sl * 64, g.head * p.g_heads, g.tok0, bar(C::Q_FULL));
             ++seg;
-        });
+        }
         if (seg > 0) (void)mbar_wait(bar(C::Q_FULL), (uint32_t)((seg - 1) & 1), p.err);
     } else if (warp == QK_WARP) {
         // ------------------------------------------------------------ QK issue: the whole warp walks the loop and one elected
@@ -780,12 +930,13 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         const uint64_t dq = tc::sdesc_sw128(sQ, 16, 1024), dk0 = tc::sdesc_sw128(sK, 16, 1024);
         const uint32_t el = elect_one(), tS = uniform(tmem);
         int i = 0, seg = 0;
-        for_each_segment(p, start, blk, [&](const Segment& g) {
+        Walk<CL> walk(p, start, blk);
+        for (Segment g; walk.next(g);) {
             wait(C::Q_FULL, seg);
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NK));
-                if (i >= 2) wait(C::S_EMPTY + b, (i >> 1) - 1);
                 wait(C::K_FULL + st, i / C::NK);
+                if (i >= 2) wait(C::S_EMPTY + b, (i >> 1) - 1);
                 tc::fence_after();
                 const uint64_t dk = dk0 + (uint32_t)((st * C::TILE) >> 4);
 #pragma unroll
@@ -793,11 +944,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                     mma_ss(el, tS + (uint32_t)(b * BN), dq + (uint32_t)(((kk >> 2) * C::QSLAB + (kk & 3) * 32) >> 4),
                            dk + (uint32_t)(((kk >> 2) * C::KSLAB + (kk & 3) * 32) >> 4), ID_QK, kk > 0);
                 commit(el, bar(C::S_FULL + b));
-                commit(el, bar(C::K_EMPTY + st));
+                if constexpr (CL > 1) commit_pair(el, bar(C::K_EMPTY + st));
+                else commit(el, bar(C::K_EMPTY + st));
                 if (u == g.n - 1) commit(el, bar(C::Q_EMPTY));
             }
             ++seg;
-        });
+        }
         if (i > 0) {  // every MMA must be complete before TMEM is released
             commit(el, bar(C::DRAIN));
             (void)warp_wait(bar(C::DRAIN), 0, p.err);
@@ -808,23 +960,26 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         const uint64_t dv0 = tc::sdesc_sw128(sV, C::KSLAB, 1024);
         const uint32_t el = elect_one(), dO = uniform(tmem + C::O_COL), tP = uniform(tmem + C::P_COL);
         int i = 0, seg = 0;
-        for_each_segment(p, start, blk, [&](const Segment& g) {
+        Walk<CL> walk(p, start, blk);
+        for (Segment g; walk.next(g);) {
             if (seg > 0) wait(C::O_FREE, seg - 1);  // O of the segment before has been read
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NV));
                 const uint32_t acc = uniform(u > 0);
-                wait(C::V_FULL + st, i / C::NV);
+                wait((g.tile + u + 1) * BN > g.ctx ? C::V_OK + st : C::V_FULL + st, i / C::NV);
                 wait(C::P_FULL + b, i >> 1);
                 tc::fence_after();
                 const uint64_t dv = dv0 + (uint32_t)((st * C::TILE) >> 4);
+                const int steps = (int)uniform((uint32_t)((g.keys - (g.tile + u) * BN + 15) / 16));  // those that hold keys
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
-                    mma_ts(el, dO, tP + (uint32_t)(b * (BN / 2) + 8 * kk), dv + (uint32_t)((kk * 2048) >> 4), ID_PV, kk > 0 ? 1u : acc);
-                commit(el, bar(C::V_EMPTY + st));
+                    mma_ts(kk < steps ? el : 0u, dO, tP + (uint32_t)(b * (BN / 2) + 8 * kk), dv + (uint32_t)((kk * 2048) >> 4), ID_PV, kk > 0 ? 1u : acc);
+                if constexpr (CL > 1) commit_pair(el, bar(C::V_EMPTY + st));
+                else commit(el, bar(C::V_EMPTY + st));
                 commit(el, bar(C::PV_DONE + b));
             }
             ++seg;
-        });
+        }
         if (i > 0) {
             commit(el, bar(C::DRAIN + 1));
             (void)warp_wait(bar(C::DRAIN + 1), 0, p.err);
@@ -847,68 +1002,79 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         tc::fence_after();
         tc::dealloc(tmem, C::TMEM_COLS);
     }
+    if constexpr (CL > 1) {
+        __syncwarp();
+        cluster_sync();  // nothing more arrives in either CTA's shared memory
+    }
 }
 
 // Joins the partials of the units that the ranges' ends cut: out = sum_k 2^(m_k - max m) o_k / sum_k 2^(m_k - max m) l_k,
-// in a fixed order.  A unit of few partials by the blocks of the CTA it starts in, a warp a row; one of many (few long
-// contexts) by the blocks of all the CTAs it spans, a block a row, whose warps take every 8th partial each.
+// in a fixed order.  A partial holds columns 4 c .. 4 c + 3 of all its rows next to each other.  A unit of few partials by
+// the blocks of the CTA it starts in (a block for 16 rows, their columns over its threads); one of many (few long contexts) by
+// the blocks of all the CTAs it spans, a block a row, whose warps take every 8th partial each.
 template <bool BF16, int D, int NR>
 __global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const TreeParams p) {
     using F = F16x2<BF16>;
-    constexpr int NW = tree::MERGE_THREADS / 32, V = D / 64;  // pairs of columns a lane: 2 lane + 64 v
+    constexpr int NW = tree::MERGE_THREADS / 32, V = D / 64, V4 = (D / 4 + 31) / 32;  // 16-byte columns a thread; a lane
     constexpr int kFew = 8;
-    __shared__ float2 acc[NW][D / 2];
+    __shared__ float4 acc[NW][D / 4];
     __shared__ float wt[tree::MERGE_THREADS], red[2][NW];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = (int)blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // the next kernel of the step may start its launch; it waits for this grid before reading anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int4 cut[2] = {__ldcg(p.desc + cta), __ldcg(p.desc + gridDim.x + cta)};
-    auto out_row = [&](int row0, int row) {
-        return static_cast<uint16_t*>(p.out) + ((size_t)row0 + (size_t)(row / p.g_heads) * p.n_q_heads + row % p.g_heads) * p.hd;
+    auto store = [&](int row0, int row, int c4, float4 a, float inv) {
+        const int tok = (int)(((uint32_t)row * (uint32_t)p.g_magic) >> 16);
+        if (4 * c4 < p.hd)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                                      ((size_t)row0 + (size_t)tok * p.n_q_heads + (row - tok * p.g_heads)) * p.hd + 4 * c4) =
+                make_uint2(F::pack_rn(a.x * inv, a.y * inv), F::pack_rn(a.z * inv, a.w * inv));
     };
-    auto store = [&](int row0, int row, int v, float2 a, float inv) {
-        const int col = 2 * lane + 64 * v;
-        if (col < p.hd) *reinterpret_cast<uint32_t*>(out_row(row0, row) + col) = F::pack_rn(a.x * inv, a.y * inv);
+    auto add = [](float4& a, const float4& x, float f) {
+        a.x = fmaf(x.x, f, a.x);
+        a.y = fmaf(x.y, f, a.y);
+        a.z = fmaf(x.z, f, a.z);
+        a.w = fmaf(x.w, f, a.w);
     };
-    const int4 few = cut[0].x <= kFew ? cut[0] : make_int4(0, 0, 0, 0);
-#pragma unroll 1
-    for (int row = (int)blockIdx.y * 16 + warp; row < min(few.y, ((int)blockIdx.y + 1) * 16); row += NW) {
+    const int row16 = (int)blockIdx.y * 16 + (tid & 15);
+    if (cut[0].x > 0 && cut[0].x <= kFew && row16 < cut[0].y) {
+        const int4 u = cut[0];
+        const int c = (tid >> 4) * V;  // this thread's columns
         auto slot_at = [&](int k) { return (size_t)(2 * (cta + k * p.group) + (k == 0)); };
-        float2 x[kFew][V];
+        float2 ml[kFew];
 #pragma unroll
-        for (int k = 0; k < kFew; ++k)
-            if (k < few.x) {
-                const float2* o = reinterpret_cast<const float2*>(p.part_o + (slot_at(k) * NR + row) * D) + lane;
+        for (int k = 0; k < kFew; ++k) ml[k] = k < u.x ? __ldcg(p.part_ml + slot_at(k) * NR + row16) : make_float2(-INFINITY, 0.f);
+        float4 a[V] = {}, x[4][V];
+        auto fetch = [&](int k0) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) x[k][v] = __ldcg(o + 32 * v);
-            }
-        float m = -INFINITY, l = 0.f;
-        if (lane < few.x) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_at(lane) * NR + row);
-            m = ml.x;
-            l = ml.y;
+            for (int k = 0; k < 4; ++k)
+                if (k0 + k < u.x)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[k][v] = __ldcg(p.part_o + (slot_at(k0 + k) * (D / 4) + c + v) * NR + row16);
+        };
+        fetch(0);
+        float mx = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) mx = fmaxf(mx, ml[k].x);
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - mx);
+            l += ml[k].x == -INFINITY ? ml[k].y : ml[k].y * f;
+            ml[k].x = f;
         }
-        float mx = m;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        mx = __shfl_sync(0xffffffffu, mx, 0);
-        const float w = m == -INFINITY ? 0.f : ex2(m - mx);
-        float lw = m == -INFINITY ? l : l * w;
+        for (int k0 = 0; k0 < kFew; k0 += 4) {
+            if (k0 > 0 && k0 < u.x) fetch(k0);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-        lw = __shfl_sync(0xffffffffu, lw, 0);
-        float2 a[V] = {};
+            for (int k = 0; k < 4; ++k)
+                if (k0 + k < u.x)
 #pragma unroll
-        for (int k = 0; k < kFew; ++k)
-            if (k < few.x) {
-                const float f = __shfl_sync(0xffffffffu, w, k);
+                    for (int v = 0; v < V; ++v) add(a[v], x[k][v], ml[k0 + k].x);
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) a[v] = ffma2(x[k][v], make_float2(f, f), a[v]);
-            }
-        const float inv = lw != 0.f ? 1.f / lw : 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) store(few.z, row, v, a[v], inv);
+        for (int v = 0; v < V; ++v) store(u.z, row16, c + v, a[v], inv);
     }
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -918,12 +1084,8 @@ __global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const T
         auto slot_at = [&](int k) { return (size_t)(2 * (b + k * p.group) + (k == 0)); };
         const int mine = (cta - b) / p.group;
         for (int row = mine * (int)gridDim.y + (int)blockIdx.y; row < u.y; row += parts * (int)gridDim.y) {
-            float m = -INFINITY, l = 0.f;
-            if (tid < parts) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_at(tid) * NR + row);
-                m = ml.x;
-                l = ml.y;
-            }
+            const float2 ml = tid < parts ? __ldcg(p.part_ml + slot_at(tid) * NR + row) : make_float2(-INFINITY, 0.f);
+            const float m = ml.x;
             float mx = m;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -933,32 +1095,29 @@ __global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const T
             for (int w = 1; w < NW; ++w) mx = fmaxf(mx, red[0][w]);
             const float w = m == -INFINITY ? 0.f : ex2(m - mx);
             wt[tid] = w;
-            float lw = m == -INFINITY ? l : l * w;
+            float lw = m == -INFINITY ? ml.y : ml.y * w;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
             if (lane == 0) red[1][warp] = lw;
             __syncthreads();
-            float2 a[V] = {};
+            float4 a[V4] = {};
 #pragma unroll 4
             for (int k = warp; k < parts; k += NW) {
-                const float2* o = reinterpret_cast<const float2*>(p.part_o + (slot_at(k) * NR + row) * D) + lane;
                 const float f = wt[k];
 #pragma unroll
-                for (int v = 0; v < V; ++v) a[v] = ffma2(__ldcg(o + 32 * v), make_float2(f, f), a[v]);
+                for (int v = 0; v < V4; ++v)
+                    if (lane + 32 * v < D / 4) add(a[v], __ldcg(p.part_o + (slot_at(k) * (D / 4) + lane + 32 * v) * NR + row), f);
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[warp][lane + 32 * v] = a[v];
+            for (int v = 0; v < V4; ++v)
+                if (lane + 32 * v < D / 4) acc[warp][lane + 32 * v] = a[v];
             __syncthreads();
-            if (warp == 0) {
+            if (tid < D / 4) {
                 float lt = 0.f;
                 for (int k = 0; k < NW; ++k) lt += red[1][k];
-                const float inv = lt != 0.f ? 1.f / lt : 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float2 t = acc[0][lane + 32 * v];
-                    for (int k = 1; k < NW; ++k) t = fadd2(t, acc[k][lane + 32 * v]);
-                    store(u.z, row, v, t, inv);
-                }
+                float4 s = acc[0][tid];
+                for (int k = 1; k < NW; ++k) add(s, acc[k][tid], 1.f);
+                store(u.z, row, tid, s, lt != 0.f ? 1.f / lt : 0.f);
             }
             __syncthreads();
         }
