@@ -1198,6 +1198,8 @@ int pa_resize_pages(void* k_cache, void* v_cache, int num_layers, int32_t* block
     p.err = dev->err;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.num_seqs = num_seqs;
+    const int words = (int)((num_blocks + 31) / 32);
+    p.push_blocks = words <= pa::kScanWords ? 0 : (words + pa::kScanWords - 1) / pa::kScanWords;
     pa::resize_plan_kernel<<<1, pa::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     // blocks a sequence: a block's share of a page that is copied in all planes, while all blocks still run at once
@@ -1214,7 +1216,10 @@ int pa_resize_pages(void* k_cache, void* v_cache, int num_layers, int32_t* block
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, pa::resize_apply_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, pa::resize_apply_kernel, p);
+    if (e != cudaSuccess || p.push_blocks == 0) return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    cfg.gridDim = dim3((unsigned)p.push_blocks);
+    return cudaLaunchKernelEx(&cfg, pa::resize_push_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // ---- trees of drafted tokens --------------------------------------------------------------------------

@@ -233,9 +233,10 @@ struct ResizeParams {
     unsigned* bits;          // [ceil(num_blocks / 32)]: pages that got free
     unsigned* err;
     int max_blocks_per_seq, num_seqs;
+    int push_blocks;         // blocks of resize_push_kernel, 0: none
 };
 
-constexpr int kPlanThreads = 1024, kApplyThreads = 512;
+constexpr int kPlanThreads = 1024, kApplyThreads = 512, kScanWords = 512;
 
 // One block: which sequences get their pages (in their order, as long as the free list lasts), where these
 // stand in the list, and which shared pages are copied -- all from the state before the call.
@@ -332,15 +333,69 @@ __device__ __forceinline__ int release_page(const ResizeParams& p, int id) {
     return 0;
 }
 
-// A sequence a block column; its first block changes the table and the counts, all of them copy a shared last
-// page's rows.  The block that is done last puts the pages that got free on the list in the order of their
-// numbers, so that the same call leaves the same list whatever the order of the blocks.
-__global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const ResizeParams p) {
-    constexpr int U = kCopyUnroll, NW = kApplyThreads / 32;
-    __shared__ bool last_block;
+// Sequences to their lengths, by the threads of `blocks` blocks.
+__device__ __forceinline__ void write_lengths(const ResizeParams& p, int block, int blocks) {
+    for (int i = block * kApplyThreads + (int)threadIdx.x; i < p.num_seqs; i += blocks * kApplyThreads)
+        if (p.plan[i].start >= 0) p.seq_lens[i] = __ldg(p.new_lens + i);
+}
+
+__device__ __forceinline__ void write_count(const ResizeParams& p, int count) {
+    if (count > p.c.num_blocks) flag_error(p.err, PA_DEVERR_COUNT);  // (a page was on the list and in a table)
+    *p.free_count = min(count, p.c.num_blocks);
+}
+
+// The marked pages of words [w0, w0 + kScanWords) into the list from entry `at` on, in the order of their numbers; a block.
+// Loaded together; a warp's run of them is counted, then its pages put behind those of the warps before, a word by 32
+// lanes.
+__device__ __forceinline__ void push_pages(const ResizeParams& p, int w0, int at) {
+    constexpr int NW = kApplyThreads / 32, RUN = kScanWords / NW;
+    __shared__ unsigned words_s[kScanWords];
     __shared__ int warp_sum[NW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, words = (p.c.num_blocks + 31) / 32;
+#pragma unroll
+    for (int k = tid; k < kScanWords; k += kApplyThreads) words_s[k] = w0 + k < words ? __ldcg(p.bits + w0 + k) : 0u;
+    __syncthreads();
+    const unsigned* run = words_s + warp * RUN;
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < RUN / 32; ++k) mine += __popc(run[32 * k + lane]);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) warp_sum[warp] = mine;
+    __syncthreads();
+    if (mine == 0) return;
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+#pragma unroll 1
+    for (int k = 0; k < RUN; k += 32) {
+        const unsigned my = run[k + lane];
+        int end = __popc(my);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += y;
+        }
+        const int before = at + end - __popc(my);
+        at += __shfl_sync(0xffffffffu, end, 31);
+#pragma unroll 4
+        for (unsigned any = __ballot_sync(0xffffffffu, my != 0u); any; any &= any - 1) {
+            const int j = __ffs(any) - 1;
+            const unsigned b = run[k + j];
+            const int to = __shfl_sync(0xffffffffu, before, j) + __popc(b & ((1u << lane) - 1u));
+            if ((b >> lane & 1u) && to < p.c.num_blocks) p.free_list[to] = 32 * (w0 + warp * RUN + k + j) + lane;
+        }
+    }
+}
+
+// A sequence a block column; its first block changes the table and the counts, all of them copy a shared last
+// page's rows.  The pages that got free go on the list in the order of their numbers, so that the same call leaves the
+// same list whatever the order of the blocks: in pools of up to 32 kScanWords pages by the block that is done last, in
+// larger ones by a kernel behind this one (one block takes 10 us for 262144 pages of which 500 got free and 60 for
+// 131000; the launch 2).
+__global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const ResizeParams p) {
+    constexpr int U = kCopyUnroll;
+    __shared__ bool last_block;
     const int s = blockIdx.x, tid = threadIdx.x, bs = p.c.block_size;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const ResizePlan r = p.plan[s];
     const int top = p.head->top;
     if (r.start >= 0) {
@@ -377,7 +432,7 @@ __global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const Resiz
                 bt[c] = id;
                 if (id < 0 || atomicExch(p.ref_counts + id, 1) != 0) flag_error(p.err, PA_DEVERR_COUNT);
             }
-            int freed = 0;  // (one addition a warp: 134K on one address took 60 us)
+            int freed = 0;  // (one addition a warp: 134000 on one address took 60 us)
             for (int c = r.want + tid; c < r.have; c += kApplyThreads) {
                 freed += release_page(p, bt[c]);
                 bt[c] = -1;
@@ -387,47 +442,44 @@ __global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const Resiz
             if (freed > 0 && (tid & 31) == 0) atomicAdd(&p.head->freed, (unsigned)freed);
         }
     }
+    if (p.push_blocks > 0) return;
     __threadfence();
     __syncthreads();
     if (tid == 0) last_block = atomicAdd(&p.head->ticket, 1u) == gridDim.x * gridDim.y - 1;
     __syncthreads();
     if (!last_block) return;
     __threadfence();
-    // every other block is done: the lengths, and the pages that got free
-    for (int i = tid; i < p.num_seqs; i += kApplyThreads)
-        if (p.plan[i].start >= 0) p.seq_lens[i] = __ldg(p.new_lens + i);
+    write_lengths(p, 0, 1);
     if (top < 0) return;
     const int left = top - p.head->taken, freed = (int)__ldcg(&p.head->freed);
-    if (tid == 0) *p.free_count = min(left + freed, p.c.num_blocks);
+    if (tid == 0) write_count(p, left + freed);
+    if (freed > 0) push_pages(p, 0, left);
+}
+
+__global__ void __launch_bounds__(kApplyThreads) resize_push_kernel(const ResizeParams p) {
+    __shared__ int sum;
+    const int tid = threadIdx.x, b = (int)blockIdx.x;
+    if (tid == 0) sum = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    write_lengths(p, b, (int)gridDim.x);
+    const int top = p.head->top;
+    if (top < 0) return;
+    const int left = top - p.head->taken, freed = (int)p.head->freed;
+    if (b == 0 && tid == 0) write_count(p, left + freed);
     if (freed == 0) return;
-    if (left + freed > p.c.num_blocks && tid == 0) flag_error(p.err, PA_DEVERR_COUNT);
-    // a warp takes a run of words: their pages counted, then put behind those of the warps before, a word at a time
-    const int words = (p.c.num_blocks + 31) / 32, per = ((words + NW - 1) / NW + 31) / 32 * 32;
-    const int lane = tid & 31, w0 = min((tid >> 5) * per, words), w1 = min(w0 + per, words);
-    int mine = 0;
-    for (int w = w0 + lane; w < w1; w += 32) mine += __popc(__ldcg(p.bits + w));
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0) warp_sum[tid >> 5] = mine;
-    __syncthreads();
-    int at = left;
-    for (int w = 0; w < (tid >> 5); ++w) at += warp_sum[w];
-    for (int w = w0; w < w1; w += 32) {
-        const unsigned my = w + lane < w1 ? __ldcg(p.bits + w + lane) : 0u;
-        int end = __popc(my);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, end, o);
-            if (lane >= o) end += y;
-        }
-        const int first = at + end - __popc(my);
-        for (unsigned any = __ballot_sync(0xffffffffu, my != 0u); any; any &= any - 1) {
-            const int k = __ffs(any) - 1;
-            const unsigned b = __shfl_sync(0xffffffffu, my, k);
-            const int to = __shfl_sync(0xffffffffu, first, k) + __popc(b & ((1u << lane) - 1u));
-            if ((b >> lane & 1u) && to < p.c.num_blocks) p.free_list[to] = 32 * (w + k) + lane;
-        }
-        at += __shfl_sync(0xffffffffu, end, 31);
+    // pages of the words before this block's
+    int before = 0;
+    const uint4* bits = reinterpret_cast<const uint4*>(p.bits);
+#pragma unroll 4
+    for (int w = tid; w < b * (kScanWords / 4); w += kApplyThreads) {
+        const uint4 v = __ldcg(bits + w);
+        before += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
     }
+    __syncthreads();
+    before = __reduce_add_sync(0xffffffffu, before);
+    if ((tid & 31) == 0 && before > 0) atomicAdd(&sum, before);
+    __syncthreads();
+    push_pages(p, b * kScanWords, left + sum);
 }
 
 }  // namespace pa

@@ -226,7 +226,8 @@ class Ledger:
                 drops += self.bt[s][want:have]
                 self.bt[s][want:have] = [-1] * (have - want)
             self.lens[s] = n
-            self.count = count - end
+            if demand:                        # (a refused sequence takes none, nor do those behind it)
+                self.count = count - end
         freed = []
         for i in drops:
             self.ref[i] -= 1
@@ -304,6 +305,20 @@ def test_forks_and_lengths_follow_the_model(seqs, mb, bs, nb, layers, hkv, d, la
         used = [i for r, n in zip(m.bt, m.lens) for i in r[:m.pages(n)]]
         assert all(m.ref[i] == used.count(i) for i in set(used)) and m.count + len(set(used)) == nb
     assert cow > 0 or seqs == 1
+    step(m, dev, [0] * seqs, "all freed")
+    assert m.count == nb
+
+
+@pytest.mark.parametrize("seqs,mb,bs,nb", [(12, 2500, 8, 16384), (12, 2500, 8, 16385), (30, 2500, 8, 50021), (700, 150, 16, 70000)])
+def test_large_pools(seqs, mb, bs, nb):
+    """Pools whose freed pages are put back by many blocks, and the largest that one block takes."""
+    rng = random.Random(nb)
+    m = Ledger(rng, seqs, mb, bs, nb)
+    dev = Device(m)
+    for turn in range(6):
+        most = mb * bs
+        step(m, dev, [-1 if rng.random() < 0.2 else rng.choice([0, rng.randint(0, most), rng.randint(0, most)]) for _ in range(seqs)],
+             f"turn {turn}")
     step(m, dev, [0] * seqs, "all freed")
     assert m.count == nb
 
