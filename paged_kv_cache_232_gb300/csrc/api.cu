@@ -390,6 +390,21 @@ int plan(int64_t units, int max_context_len, int sm_count, int resident, int blo
     return 2;
 }
 
+// Launches a kernel that waits for the one before it itself (griddepcontrol.wait), so that its launch overlaps that one's end.
+template <typename Kern, typename... Args>
+int launch_waiting(Kern kern, dim3 grid, int threads, void* stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1104,9 +1119,8 @@ int pa_copy_pages(void* k_cache, void* v_cache, int num_layers, const int32_t* p
     const int64_t items = num_pairs * c.planes * segs, per_block = pa::kCopyThreads >> lanes_log2;
     const int grid = (int)std::min<int64_t>((items + per_block - 1) / per_block,
                                             (int64_t)dev->sm_count * (2048 / pa::kCopyThreads));
-    pa::copy_pages_kernel<<<grid, pa::kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        c, pairs, (unsigned)items, (unsigned)segs, seg_vecs, page_vecs, lanes_log2, dev->err);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_waiting(pa::copy_pages_kernel, dim3((unsigned)grid), pa::kCopyThreads, stream, c, pairs, (unsigned)items,
+                          (unsigned)segs, seg_vecs, page_vecs, lanes_log2, dev->err);
 }
 
 int pa_tree_commit(void* k_cache, void* v_cache, int num_layers, const int32_t* block_tables, int max_blocks_per_seq,
@@ -1137,9 +1151,8 @@ int pa_tree_commit(void* k_cache, void* v_cache, int num_layers, const int32_t* 
     const int64_t slots = (int64_t)dev->sm_count * (2048 / pa::kCommitThreads);
     const int64_t y = std::min<int64_t>((columns + pa::kCommitThreads - 1) / pa::kCommitThreads,
                                         std::max<int64_t>(1, slots / num_seqs));
-    pa::tree_commit_kernel<<<dim3((unsigned)num_seqs, (unsigned)std::min<int64_t>(y, 65535)), pa::kCommitThreads, 0,
-                             static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_waiting(pa::tree_commit_kernel, dim3((unsigned)num_seqs, (unsigned)std::min<int64_t>(y, 65535)),
+                          pa::kCommitThreads, stream, p);
 }
 
 int pa_fork_pages(int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_lens, const int32_t* parents, int num_seqs,
@@ -1149,9 +1162,9 @@ int pa_fork_pages(int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_le
     if (!block_tables || !seq_lens || !parents || !ref_counts) return PA_ERR_NULL;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != PA_OK) return st;
-    pa::fork_pages_kernel<<<(num_seqs + pa::kForkSeqs - 1) / pa::kForkSeqs, pa::kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        block_tables, max_blocks_per_seq, seq_lens, parents, num_seqs, ref_counts, block_size, (int)num_blocks, dev->err);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_waiting(pa::fork_pages_kernel, dim3((unsigned)((num_seqs + pa::kForkSeqs - 1) / pa::kForkSeqs)),
+                          pa::kForkThreads, stream, block_tables, max_blocks_per_seq, seq_lens, parents, num_seqs, ref_counts,
+                          block_size, (int)num_blocks, dev->err);
 }
 
 struct ResizeWs {
@@ -1200,26 +1213,16 @@ int pa_resize_pages(void* k_cache, void* v_cache, int num_layers, int32_t* block
     p.num_seqs = num_seqs;
     const int words = (int)((num_blocks + 31) / 32);
     p.push_blocks = words <= pa::kScanWords ? 0 : (words + pa::kScanWords - 1) / pa::kScanWords;
-    pa::resize_plan_kernel<<<1, pa::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    if ((st = launch_waiting(pa::resize_plan_kernel, dim3(1), pa::kPlanThreads, stream, p)) != PA_OK) return st;
     // blocks a sequence: a block's share of a page that is copied in all planes, while all blocks still run at once
     const int64_t vecs = (int64_t)p.c.planes * block_size * p.c.row_vecs, share = pa::kApplyThreads * pa::kCopyUnroll;
     const int64_t slots = (int64_t)dev->sm_count * (2048 / pa::kApplyThreads);
     const int64_t y = std::min(std::min<int64_t>((vecs + share - 1) / share, p.c.planes),
                                std::max<int64_t>(1, slots / num_seqs));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)num_seqs, (unsigned)std::min<int64_t>(y, 65535));
-    cfg.blockDim = dim3(pa::kApplyThreads);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, pa::resize_apply_kernel, p);
-    if (e != cudaSuccess || p.push_blocks == 0) return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-    cfg.gridDim = dim3((unsigned)p.push_blocks);
-    return cudaLaunchKernelEx(&cfg, pa::resize_push_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    st = launch_waiting(pa::resize_apply_kernel, dim3((unsigned)num_seqs, (unsigned)std::min<int64_t>(y, 65535)),
+                        pa::kApplyThreads, stream, p);
+    if (st != PA_OK || p.push_blocks == 0) return st;
+    return launch_waiting(pa::resize_push_kernel, dim3((unsigned)p.push_blocks), pa::kApplyThreads, stream, p);
 }
 
 // ---- trees of drafted tokens --------------------------------------------------------------------------

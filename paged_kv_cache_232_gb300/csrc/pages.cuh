@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Planes c
     const unsigned per_block = kCopyThreads >> lanes_log2;
     const int lanes = 1 << lanes_log2, lane = threadIdx.x & (lanes - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (unsigned it = blockIdx.x * per_block + (threadIdx.x >> lanes_log2); it < items; it += gridDim.x * per_block) {
         const unsigned rest = it / segs, seg = it - rest * segs;
         const unsigned pair = rest / (unsigned)c.planes, plane = rest - pair * (unsigned)c.planes;
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     __shared__ int64_t from[kCommitRows], to[kCommitRows];  // rows of a plane; -1: not moved
     const int s = blockIdx.x, tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int n = __ldg(p.query_start_loc + s + 1) - __ldg(p.query_start_loc + s), kv_len = __ldg(p.seq_lens + s);
     const int acc = __ldg(p.num_accepted + s), ctx = kv_len - n;
     const int cap = p.max_blocks_per_seq * p.c.block_size;
@@ -165,6 +167,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(int32_t* block
     __shared__ int parent_s[kForkSeqs], len_s[kForkSeqs];
     const int tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < kForkSeqs) {
         const int s = blockIdx.x * kForkSeqs + tid;
         int par = s < num_seqs ? __ldg(parents + s) : -1, len = 0;
@@ -461,6 +464,7 @@ __global__ void __launch_bounds__(kApplyThreads) resize_push_kernel(const Resize
     const int tid = threadIdx.x, b = (int)blockIdx.x;
     if (tid == 0) sum = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     write_lengths(p, b, (int)gridDim.x);
     const int top = p.head->top;
     if (top < 0) return;
