@@ -544,7 +544,7 @@ int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_
  *  Row ctx + path[s][i] of every layer goes to ctx + i (i < num_accepted[s]), as if all were read before any is
  *  written, and new_lens[s] (int32, written; must not overlap the inputs) = ctx + num_accepted[s].
  *  A path that does not rise within [0, n_s), or with more entries than max_path or n_s: no row is moved, new_lens[s] =
- *  ctx, PA_DEVERR_PATH.  Lengths out of range: nothing is moved, new_lens[s] = seq_lens[s], PA_DEVERR_LENGTH.  A row
+ *  ctx, PA_DEVERR_PATH.  (new_lens that is seq_lens or num_accepted: PA_ERR_SHAPE.)  Lengths out of range: nothing is moved, new_lens[s] = seq_lens[s], PA_DEVERR_LENGTH.  A row
  *  whose page is not in the pool stays, PA_DEVERR_BLOCK.  Rows that are moved must lie in pages of their sequence
  *  alone (pa_resize_pages sees to that for the tokens that it adds).
  */
@@ -582,7 +582,8 @@ int pa_fork_pages(int32_t* block_tables, int max_blocks_per_seq, int32_t* seq_le
  * pa_resize_pages -- sequences to new lengths: pages taken for those that grow, dropped by those that shrink
  * (to 0: the sequence is freed), and the last page of a growing sequence made its own.
  *
- *  new_lens [num_seqs] int32 (must not overlap the ledger or the tables); -1: s stays as it is
+ *  new_lens [num_seqs] int32 (must not overlap the ledger, the tables or seq_lens; seq_lens itself: PA_ERR_SHAPE);
+ *         -1: s stays as it is
  *  seq_lens [num_seqs], updated to new_lens
  *  A sequence that grows gets ceil(new / block_size) - ceil(old / block_size) pages into its table; one more where
  *  its last page is partly filled and had a count above 1 when the call began: the page's rows in use are

@@ -1134,6 +1134,7 @@ int pa_tree_commit(void* k_cache, void* v_cache, int num_layers, const int32_t* 
     if (st != PA_OK || num_seqs == 0) return st;
     if (!k_cache || !block_tables || !query_start_loc || !seq_lens || (max_path > 0 && !path) || !num_accepted || !new_lens)
         return PA_ERR_NULL;
+    if (new_lens == seq_lens || new_lens == num_accepted) return PA_ERR_SHAPE;  // read by blocks that are not done
     if (!aligned16(k_cache) || (v_cache && !aligned16(v_cache))) return PA_ERR_ALIGN;
     DeviceState* dev = nullptr;
     if ((st = device_state(&dev)) != PA_OK) return st;
@@ -1193,6 +1194,7 @@ int pa_resize_pages(void* k_cache, void* v_cache, int num_layers, int32_t* block
     if (st != PA_OK || num_seqs == 0) return st;
     if (!k_cache || !block_tables || !seq_lens || !new_lens || !ref_counts || !free_list || !free_count) return PA_ERR_NULL;
     if (!aligned16(k_cache) || (v_cache && !aligned16(v_cache))) return PA_ERR_ALIGN;
+    if (new_lens == seq_lens) return PA_ERR_SHAPE;
     const ResizeWs w = resize_ws(num_seqs, num_blocks);
     if (!workspace || workspace_bytes < w.total) return PA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PA_ERR_ALIGN;

@@ -8,31 +8,52 @@
 // dense contraction over the same keys: each key is read once for all of them.
 //
 // GB300 design:
-//  * A unit is up to NR query rows (32, 64 or 128) of one sequence and KV head over its keys, in tiles of
-//    BN keys (128; 64 at head_dim 256).  S = Q K^T is one M = 128 product whatever NR is: the tile holds
-//    128 / NR copies of the rows, and each copy takes its own share of the tile's keys.  So 128 threads
-//    (one a row of the tile, a TMEM lane each) share the softmax of few rows without exchanging anything:
-//    a copy is a split of the keys with a maximum and a sum of its own, and the copies are joined once, at
-//    the unit's end.  The weights go back to TMEM as the A operand of O += P V, with zeros in the columns
-//    of the other copies' keys (written once: no copy ever writes there).
-//  * K and V arrive by TMA in boxes of 16 tokens (8 in blocks of 8) x 64 columns, 128-byte swizzled, in two
-//    rings of whole tiles; K is released by its product, V by its own.  QK and PV have an issuer each.
-//  * The running maximum is lazy: weights are taken against the old one, and only where their sum over
-//    a thread's keys exceeds 2^8 are the maximum raised (to a whole power of two) and O and l rescaled.  Weights up to
-//    2^8 are exact in fp32 and far from the 16-bit formats' limits.
-//  * A weight enters the second product rounded once to the cache's type (half a step, 2^-8 in bf16 and 2^-11
-//    in fp16, relative), and l sums the rounded weights, so that they still sum to one; everything else is
-//    fp32.  In fp16 weights are scaled by 2^7, so that small ones are not subnormal.
-//  * All units laid end to end and measured in cost (a unit's start and output, then its tiles) are cut into
-//    equal ranges, one a CTA; units that a range's end cuts leave fp32 partials which tree_merge_kernel joins in
-//    a fixed order.  No host-side lengths, no atomics, two partials a CTA.  Trees of more than 128 rows are `group`
-//    blocks of tokens (further ones in further passes), worked by CTAs next to each other, which walk the same keys
-//    at the same time and so share them in L2 (one after the other they would be read from DRAM again).
+//  * A unit is up to NR query rows (32, 64 or 128) of one sequence and KV head over its keys, in tiles of BN keys (128;
+//    64 at head_dim 256).  S = Q K^T is one M = 128 product whatever NR is: the tile holds 128 / NR copies of the rows, and
+//    each copy takes its own share of the tile's keys.  So 128 threads (one a row of the tile, a TMEM lane each) share the
+//    softmax of few rows without exchanging anything: a copy is a split of the keys with a maximum and a sum of its own,
+//    and the copies are joined once, at the unit's end.  The weights go back to TMEM as the A operand of O += P V, with zeros
+//    in the columns of the other copies' keys (written once: no copy ever writes there).  The least NR that holds the rows:
+//    16 rows in the 32 / 64 / 128-row kernels, 256 sequences of 50..650 tokens 125 / 151 / 165 us, 64 of 100..4096 98 / 100 / 102.
+//  * At 128 rows two threads share a row, half a tile's keys each (the tensor core's pace allows ~1100 cycles a tile; one
+//    thread a row takes ~2200, four in 80 registers each are slower than two: 64 sequences of 8K tokens x 256 rows 553 / 521 / 456 us).
+//    They keep one reference, by a vote of the row's two warps a tile.
+//  * K and V arrive by TMA in boxes of 16 tokens (8 in blocks of 8) x 64 columns, 128-byte swizzled, in two rings of whole
+//    tiles; K is released by its product, V by its own.  QK and PV have an issuer each.  (Boxes of 64 tokens: no faster.
+//    A third V tile beside three of K takes the L1 that block tables and masks need; 2 K and 3 V tiles 1..2 % faster than 3
+//    and 2.  Tiles prefetched into L2: 328 -> 360 us.)
+//  * The running maximum is lazy: weights are taken against the old one, and only where their sum over a thread's keys
+//    exceeds 2^8 are the maximum raised (to a whole power of two) and O and l rescaled.  Weights up to 2^8 are exact in
+//    fp32 and far from the 16-bit formats' limits.
+//  * A weight enters the second product rounded once to the cache's type (half a step, 2^-8 in bf16 and 2^-11 in fp16,
+//    relative), and l sums the rounded weights, so that they still sum to one; everything else is fp32.  In fp16 weights are
+//    scaled by 2^7, so that small ones are not subnormal.  Both sides measured: root-mean-square error against 64 bits,
+//    relative to the output, 0.0023 in bf16 (32-bit weights: 0.0017) and 0.00025..0.00029 in fp16 (0.00021), the most where
+//    values are independent.  The remainders as further products: the second product issued twice, 64 sequences of
+//    100..4096 tokens at 32 / 64 / 128 rows 98 -> 106, 99 -> 104, 109 -> 118 us, 256 rows x 8K 467 -> 543; with the remainders'
+//    own arithmetic (twice the keys a thread at 32 rows) 256 sequences of 50..650 tokens 125 -> 151; at 128 rows they have no
+//    room in TMEM.  One product stays, by one rule for all units.
+//  * All units laid end to end and measured in cost (a unit's start and output, then its tiles) are cut into equal ranges,
+//    one a CTA; units that a range's end cuts leave fp32 partials which tree_merge_kernel joins in a fixed order.  No
+//    host-side lengths, no atomics, two partials a CTA.
+//  * Trees of more than 128 rows are `group` blocks of tokens (further ones in further passes), worked by CTAs next to each
+//    other that walk the same keys at the same time; pairs of them are a cluster, each loading half of every tile into
+//    both (64 sequences of 8K tokens x 256 rows: read by each CTA on its own through L2 521 us, the loads alone 475;
+//    multicast 467 and 385).
 //  * The cache rows of drafted tokens that some row does not see may hold anything (a padded token's row was never
-//    written): scores are replaced before the softmax, and a drafted V row that is not finite is zeroed in
-//    shared memory, the rows that see it becoming NaN.
-//  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set and the role goes on without waiting, so that
-//    every barrier of the block is still met; its results are not used.
+//    written): scores are replaced before the softmax, and a warp of its own looks at the drafted V rows before their
+//    product: one that is not finite is zeroed in shared memory, the rows that see it becoming NaN.
+//  * A successful wait on a barrier costs ~200 cycles of a warp that does nothing else, so the softmax looks at the next
+//    tile's barriers while this one's weights are under way (493 -> 463 us at 256 rows).
+//  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set and the role goes on without waiting, so that every barrier
+//    of the block is still met; its results are not used.
+//
+// What bounds it: memory up to 128 rows, 6.4..6.8 TB/s between the starts and ends of units (a tile of 64 KB in ~2800
+// cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the softmax (~1800 cycles a tile) beside loads (~1500 for
+// a pair's) and products (1024; the tensor pipe is 46 % active).  Fixed: ~4 us to the first weights, ~3 us a unit that the rings do
+// not cover (the last product, the join, the first tile's maximum; cold instructions: the first pass through a
+// unit's end costs 3 x the next), ~5 us of merge.  Whole calls (GB300): 64 sequences of 100..4096 tokens, 16 drafted, 16 q / 8 KV
+// heads 96 us (82 us of bytes at the copy rate), 4 x 32K 89 (76), 64 x 1K..8K, 64 drafted, 32 q heads 296 (190).
 #pragma once
 
 #include "pa_launch.h"
@@ -659,9 +680,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             const bool whole = g.parts == 0;
             const int slot = 2 * (int)blockIdx.x + (g.tile == 0 ? 1 : 0);
             const size_t row0 = (size_t)g.tok0 * p.n_q_heads + (size_t)g.head * p.g_heads;
+            const bool checked = (g.tile + g.n) * BN > g.ctx;  // the last tile holds drafted tokens
+            if (checked) wait(C::V_OK + (i - 1) % C::NV, (i - 1) / C::NV);
             wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
             tc::fence_after();
-            if ((g.tile + g.n) * BN > g.ctx) poison(i - 1);  // (its product waited for the check)
+            if (checked) poison(i - 1);
             if constexpr (COPIES == 1) {
                 constexpr int W = D / SPLIT, CW = W < 32 ? W : 32;  // columns of this thread, at a time
                 const int c0 = share * W;
@@ -817,6 +840,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                     volatile uint32_t* bits = bad_keys + 4 * (i % (2 * C::NV));
                     const uint32_t tile = sV + (uint32_t)(st * C::TILE);
                     if (lane < 4) bits[lane] = 0u;
+                    __syncwarp();
                     // 16 rows at a time, two lanes each: half of its chunks, starting at different banks
                     const int half = lane & 1, d1 = min(BN, g.keys - kbase);
 #pragma unroll 1

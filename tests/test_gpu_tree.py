@@ -123,7 +123,8 @@ def test_any_mask(ty, hq, hkv, d, n):
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("hq,hkv,d,n,pad", [(2, 1, 128, 16, 5), (8, 1, 128, 16, 16), (2, 2, 64, 40, 7), (2, 1, 256, 30, 3)])
+@pytest.mark.parametrize("hq,hkv,d,n,pad", [(2, 1, 128, 16, 5), (8, 1, 128, 16, 16), (2, 2, 64, 40, 7), (2, 1, 256, 30, 3),
+                                              (2, 1, 128, 200, 150), (8, 1, 64, 70, 30)])
 def test_padded_tokens_rows_may_hold_anything(hq, hkv, d, n, pad):
     """Rows of drafted tokens that nobody sees were never written: NaN and infinities there change nothing."""
     rng = random.Random(7)
@@ -144,15 +145,23 @@ def test_padded_tokens_rows_may_hold_anything(hq, hkv, d, n, pad):
 
 
 def test_value_that_is_not_finite_reaches_the_rows_that_see_it_alone():
-    n = 12
-    sees = [[[k <= j for k in range(n)] for j in range(n)]]
-    for hq, hkv, d in ((2, 1, 128), (8, 1, 128), (16, 1, 128), (1, 1, 64), (2, 1, 256)):
+    """One such row in the last tile, in an earlier one (trees over several tiles), in blocks of tokens that other CTAs
+    work, in each half of a row's columns, and several at once."""
+    for n, hq, hkv, d in ((12, 2, 1, 128), (12, 8, 1, 128), (12, 16, 1, 128), (12, 1, 1, 64), (12, 2, 1, 256), (300, 1, 1, 128),
+                          (300, 2, 1, 64), (150, 2, 1, 256), (40, 8, 2, 128)):
+        sees = [[[k <= j for k in range(n)] for j in range(n)]]
         b = Batch("fp16", hq, hkv, d, 16, [n], [250], seed=9, sees=sees)
         want = b.run()
-        t = 250 + 5
-        b.vc[b.bt[0, t // 16].long(), t % 16, 0, d - 3] = float("inf")
-        out = b.run()
-        assert torch.equal(out[:5], want[:5]) and out[5:].isnan().all()
+        for rows, col, value in (([5], d - 3, "inf"), ([n - 1], 2, "nan"), ([n // 2, n // 2 + 3], d // 2 - 1, "-inf")):
+            kept = b.vc.clone()
+            for j in rows:
+                t = 250 + j
+                b.vc[b.bt[0, t // 16].long(), t % 16, 0, col] = float(value)
+            out = b.run()
+            g = hq // hkv
+            assert torch.equal(out[:rows[0], :g], want[:rows[0], :g]) and out[rows[0]:, :g].isnan().all(), (n, hq, d, rows)
+            assert torch.equal(out[:, g:], want[:, g:])          # the other KV heads' rows
+            b.vc = kept
 
 
 @pytest.mark.parametrize("d,n", [(128, 40), (64, 9), (256, 16)])
@@ -298,7 +307,8 @@ def test_two_streams_with_a_workspace_each():
 def test_graphs_share_a_workspace_and_take_new_inputs():
     """Two captured calls replayed in turn over one workspace; lengths, masks and queries change between replays."""
     bs = [Batch("fp16", 8, 4, 128, 16, [12] * 4, [500, 30, 1000, 64], seed=20),
-          Batch("fp16", 8, 4, 64, 16, [9, 2, 7], [2000, 10, 300], seed=21)]
+          Batch("fp16", 8, 4, 64, 16, [9, 2, 7], [2000, 10, 300], seed=21),
+          Batch("bf16", 8, 1, 128, 16, [40, 12], [700, 90], seed=23)]
     ws = torch.full((max(b.ws().numel() for b in bs),), 0xFF, device="cuda", dtype=torch.uint8)
     graphs, outs = [], []
     for b in bs:

@@ -15,7 +15,7 @@ def lib():
     return pa.load()
 
 
-VP, ODD = ctypes.c_void_p(16), ctypes.c_void_p(8)     # never dereferenced
+VP, ODD, NEW = ctypes.c_void_p(16), ctypes.c_void_p(8), ctypes.c_void_p(48)     # never dereferenced
 
 
 def test_tree_mask_is_the_ancestors():
@@ -88,7 +88,7 @@ def test_pages_refusals(lib):
     def copy(kc=VP, vc=VP, L=2, pairs=VP, n=3, row=256, bs=16, nb=10):
         return lib.pa_copy_pages(kc, vc, L, pairs, n, row, bs, nb, None)
 
-    def commit(kc=VP, vc=VP, L=2, bt=VP, mb=8, loc=VP, sl=VP, path=VP, mp=4, acc=VP, new=VP, S=2, row=256, bs=16, nb=10):
+    def commit(kc=VP, vc=VP, L=2, bt=VP, mb=8, loc=VP, sl=VP, path=VP, mp=4, acc=VP, new=NEW, S=2, row=256, bs=16, nb=10):
         return lib.pa_tree_commit(kc, vc, L, bt, mb, loc, sl, path, mp, acc, new, S, row, bs, nb, None)
 
     def fork(bt=VP, mb=8, sl=VP, par=VP, S=2, ref=VP, bs=16, nb=10):
@@ -96,7 +96,7 @@ def test_pages_refusals(lib):
 
     size = lib.pa_resize_workspace_size(2, 10)
 
-    def resize(kc=VP, vc=VP, L=2, bt=VP, mb=8, sl=VP, new=VP, S=2, ref=VP, fl=VP, fc=VP, row=256, bs=16, nb=10, ws=VP, wb=size):
+    def resize(kc=VP, vc=VP, L=2, bt=VP, mb=8, sl=VP, new=NEW, S=2, ref=VP, fl=VP, fc=VP, row=256, bs=16, nb=10, ws=VP, wb=size):
         return lib.pa_resize_pages(kc, vc, L, bt, mb, sl, new, S, ref, fl, fc, row, bs, nb, ws, wb, None)
 
     for fn, names in ((copy, ("kc", "pairs")), (commit, ("kc", "bt", "loc", "sl", "path", "acc", "new")),
@@ -113,6 +113,7 @@ def test_pages_refusals(lib):
         assert fn(S=-1) == -2 and fn(mb=0) == -2 and fn(mb=2 ** 28) == -3 and fn(bs=12) == -3 and fn(nb=0) == -2
     assert copy(n=-1) == -2 and copy(n=2 ** 40) == -3 and copy(n=0, pairs=None) == 0
     assert commit(mp=-1) == -2 and commit(S=0, bt=None) == 0
+    assert commit(sl=NEW) == -2 and commit(acc=NEW) == -2 and resize(sl=NEW) == -2     # read and written by one call
     assert fork(S=0, bt=None) == 0 and fork(nb=2 ** 31) == -3
     assert resize(ws=None) == -7 and resize(wb=size - 1) == -7 and resize(ws=ODD) == -6 and resize(S=0, bt=None) == 0
 
