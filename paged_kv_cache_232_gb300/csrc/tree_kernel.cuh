@@ -45,8 +45,13 @@
 //    product: one that is not finite is zeroed in shared memory, the rows that see it becoming NaN.
 //  * A successful wait on a barrier costs ~200 cycles of a warp that does nothing else, so the softmax looks at the next
 //    tile's barriers while this one's weights are under way (493 -> 463 us at 256 rows).
-//  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set and the role goes on without waiting, so that every barrier
-//    of the block is still met; its results are not used.
+//  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set, the warps that load or issue products stop there, and the
+//    others go on without waiting, so that every barrier of the block is still met.  Loads and products under way are
+//    waited for (again with the limit); the results are not used.
+//  * No wait can be overtaken: a barrier two phases on looks like one that is not complete.  So what a warp waits for goes
+//    on only after that warp has arrived at something that it needs: every V tile passes the checker on its way to the
+//    product, and the softmax looks at the checker's barrier before it hands over the tile's weights.  (Tiles without
+//    drafted tokens straight to the product, released by the checker as well: 256 rows x 8K 551 us instead of 450.)
 //
 // What bounds it: memory up to 128 rows, 6.4..6.8 TB/s between the starts and ends of units (a tile of 64 KB in ~2800
 // cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the softmax (~1800 cycles a tile) beside loads (~1500 for
@@ -96,9 +101,8 @@ struct Cfg {
                          S_FULL = Q_FULL + 2, S_EMPTY = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
                          O_FREE = Q_FULL + 10, DRAIN = Q_FULL + 11, NUM_BARS = Q_FULL + 13;
     static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch
-    static constexpr int BAD_OFF = MISC_OFF + 192;                       // V rows that are not finite: a bit a row, of 2 NV tiles (read
-                                                                         // after the tile's weights are given, so up to NV tiles late)
-    static constexpr int SMEM_BYTES = BAD_OFF + 2 * NV * 16 + 1024;          // + alignment slack
+    static constexpr int BAD_OFF = MISC_OFF + 192;                       // the V ring's rows that are not finite: a bit a row
+    static constexpr int SMEM_BYTES = BAD_OFF + NV * 16 + 1024;          // + alignment slack
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(COPIES == 1 || OWN_STAGE || NR * D * 4 <= SLABS * QSLAB, "the copies are joined in the Q tile's place");
     // TMEM: two S buffers, two P buffers (16-bit pairs), O
@@ -454,7 +458,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     using namespace tree;
     using C = Cfg<D, NR>;
     using F = F16x2<BF16>;
-    constexpr int BN = C::BN, KW = C::KW, H = KW < 32 ? KW : 32, COPIES = C::COPIES, SPLIT = C::SPLIT, SOFTMAX = C::SOFTMAX;
+    constexpr int BN = C::BN, KW = C::KW, H = KW, COPIES = C::COPIES, SPLIT = C::SPLIT, SOFTMAX = C::SOFTMAX;
     constexpr int QK_WARP = C::QK_WARP, PV_WARP = C::PV_WARP, Q_WARP = C::Q_WARP, K_WARP = C::K_WARP, V_WARP = C::V_WARP;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -463,7 +467,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     Start* rec = reinterpret_cast<Start*>(smem + C::MISC_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::MISC_OFF + 32);
-    volatile uint32_t* bad_keys = reinterpret_cast<volatile uint32_t*>(smem + C::BAD_OFF);  // [2 NV][4]
+    volatile uint32_t* bad_keys = reinterpret_cast<volatile uint32_t*>(smem + C::BAD_OFF);  // [NV][4]
     long long* warp_sum = reinterpret_cast<long long*>(smem + C::MISC_OFF + 64);
     float* m_s = reinterpret_cast<float*>(smem + C::ML_OFF);
     float* l_s = m_s + 128;
@@ -540,7 +544,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             tc::wait_st();
         }
         const int tok_r = row_token(r);
-        bool s_ready = false, pv_ready = false;  // seen during the tile before
+        bool s_ready = false, pv_ready = false, v_ready = false;  // barriers seen complete ahead of time
         int i = 0;  // tile number over the CTA's range
         constexpr int MW = (KW + 31) / 32;
         Walk<CL> walk(p, start, blk);
@@ -556,16 +560,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             };
             uint32_t sees[MW], sees_next[MW];
             float m_ref = -INFINITY, l = 0.f;
-            // a drafted V row of tile number t that is not finite makes the row NaN if it sees it
-            auto poison = [&](int t) {
-#pragma unroll
-                for (int w = 0; w < MW; ++w) {
-                    const int at = share * KW + 32 * w;  // this thread's keys of the tile: KW from share * KW on
-                    uint32_t k = bad_keys[4 * (t % (2 * C::NV)) + (at >> 5)] >> (at & 31);
-                    if constexpr (KW < 32) k &= (1u << KW) - 1u;
-                    if (k & sees[w]) l = __uint_as_float(0x7FC00000u);
-                }
-            };
             if ((g.tile + 1) * BN > g.ctx) row_sees(g.tile, sees_next);
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int kbase = (g.tile + u) * BN, b = i & 1;
@@ -655,6 +649,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                     // the next tile's barriers, without waiting
                     s_ready = mbar_test(bar(C::S_FULL + (b ^ 1)), (i + 1) >> 1);
                     pv_ready = mbar_test(bar(C::PV_DONE + (b ^ 1)), ((i + 1) >> 1) - 1);
+                    if (drafts) v_ready = mbar_test(bar(C::V_OK + i % C::NV), i / C::NV);
                     ls[0] = fadd2(ls[0], ls[1]);
                     add = ls[0].x + ls[0].y;
                     // (no weight is above their sum; the vote also says that a row's other thread has read this one's maximum)
@@ -667,24 +662,29 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::S_EMPTY + b));
+                if (drafts) {
+                    // a drafted V row that is not finite makes the row NaN if it sees it.  (Before the weights are given: the
+                    // tile's product releases its slot, and a slot's barrier is not looked at two phases late)
+                    if (!__all_sync(0xffffffffu, v_ready)) wait(C::V_OK + i % C::NV, i / C::NV);
+#pragma unroll
+                    for (int w = 0; w < MW; ++w) {
+                        const int at = share * KW + 32 * w;  // this thread's keys of the tile: KW from share * KW on
+                        uint32_t k = bad_keys[4 * (i % C::NV) + (at >> 5)] >> (at & 31);
+                        if constexpr (KW < 32) k &= (1u << KW) - 1u;
+                        if (k & sees[w]) l = __uint_as_float(0x7FC00000u);
+                    }
+                }
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::P_FULL + b));
-                if (drafts && u < g.n - 1) {
-                    wait(C::V_OK + i % C::NV, i / C::NV);
-                    poison(i);
-                }
             }
             // the segment's end: O / l, or the partial
             const bool whole = g.parts == 0;
             const int slot = 2 * (int)blockIdx.x + (g.tile == 0 ? 1 : 0);
             const size_t row0 = (size_t)g.tok0 * p.n_q_heads + (size_t)g.head * p.g_heads;
-            const bool checked = (g.tile + g.n) * BN > g.ctx;  // the last tile holds drafted tokens
-            if (checked) wait(C::V_OK + (i - 1) % C::NV, (i - 1) / C::NV);
             wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
             tc::fence_after();
-            if (checked) poison(i - 1);
             if constexpr (COPIES == 1) {
                 constexpr int W = D / SPLIT, CW = W < 32 ? W : 32;  // columns of this thread, at a time
                 const int c0 = share * W;
@@ -837,7 +837,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 const int kbase = (g.tile + u) * BN, st = i % C::NV;
                 wait(C::V_FULL + st, i / C::NV);
                 if (kbase + BN > g.ctx) {
-                    volatile uint32_t* bits = bad_keys + 4 * (i % (2 * C::NV));
+                    volatile uint32_t* bits = bad_keys + 4 * st;
                     const uint32_t tile = sV + (uint32_t)(st * C::TILE);
                     if (lane < 4) bits[lane] = 0u;
                     __syncwarp();
@@ -906,13 +906,14 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         Segment g, ahead;
         bool more = walk.next(g);
         int id = more ? entry(g, g.tile) : 0;
-        for (; more; g = ahead) {
+        for (; more && ok; g = ahead) {
             more = walk.next(ahead);
             for (int u = 0; u < g.n; ++u, ++done) {
                 const int tile = g.tile + u;
                 const int nxt = u + 1 < g.n ? entry(g, tile + 1) : more ? entry(ahead, ahead.tile) : 0;
                 const int st = (int)uniform((uint32_t)(done % slots)), use = done / slots;
                 if (use > 0) wait(empty0 + st, use - 1);
+                if (!ok) break;
                 const uint32_t full = bar(full0 + st), dst = ring + (uint32_t)(st * C::TILE);
                 if (el) mbar_arrive_expect_tx(full, C::TILE / 2);
                 __syncwarp();
@@ -930,6 +931,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 id = nxt;
             }
         }
+        // the last releases too: none is on its way, least of all from the other CTA of a cluster, when this one leaves
+        for (int t = max(0, done - slots); t < done; ++t) wait(empty0 + t % slots, t / slots);
     } else if (warp == Q_WARP && lane == 0) {
         // ------------------------------------------------------------ the units' query rows, once for each copy
         tma_prefetch_desc(&tmQ);
@@ -937,7 +940,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         const uint32_t box = (uint32_t)(p.tb * p.g_heads * 128);
         Walk<CL> walk(p, start, blk);
         for (Segment g; walk.next(g);) {
-            if (seg > 0 && ok) ok = mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err);
+            if (seg > 0) ok = mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err);
+            if (!ok) break;
             mbar_arrive_expect_tx(bar(C::Q_FULL), box * C::SLABS * COPIES);
 #pragma unroll 1
             for (int c = 0; c < COPIES; ++c)
@@ -961,6 +965,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NK));
                 wait(C::K_FULL + st, i / C::NK);
                 if (i >= 2) wait(C::S_EMPTY + b, (i >> 1) - 1);
+                if (!ok) break;
                 tc::fence_after();
                 const uint64_t dk = dk0 + (uint32_t)((st * C::TILE) >> 4);
 #pragma unroll
@@ -972,6 +977,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 else commit(el, bar(C::K_EMPTY + st));
                 if (u == g.n - 1) commit(el, bar(C::Q_EMPTY));
             }
+            if (!ok) break;
             ++seg;
         }
         if (i > 0) {  // every MMA must be complete before TMEM is released
@@ -990,8 +996,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NV));
                 const uint32_t acc = uniform(u > 0);
-                wait((g.tile + u + 1) * BN > g.ctx ? C::V_OK + st : C::V_FULL + st, i / C::NV);
+                wait(C::V_OK + st, i / C::NV);
                 wait(C::P_FULL + b, i >> 1);
+                if (!ok) break;
                 tc::fence_after();
                 const uint64_t dv = dv0 + (uint32_t)((st * C::TILE) >> 4);
                 const int steps = (int)uniform((uint32_t)((g.keys - (g.tile + u) * BN + 15) / 16));  // those that hold keys
@@ -1002,6 +1009,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 else commit(el, bar(C::V_EMPTY + st));
                 commit(el, bar(C::PV_DONE + b));
             }
+            if (!ok) break;
             ++seg;
         }
         if (i > 0) {
@@ -1011,7 +1019,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     }
     tc::fence_before();
     // Every load is behind a wait of the issuers.  If all went well nothing is in flight now; if some role's wait ran
-    // out, no copy may be left behind: the last ones of each ring
+    // out, no copy may be left behind: the last ones of each ring (the loaders stopped there; a phase that waits for another
+    // loader's arrival as well runs out, long after the copies themselves are done)
     const bool failed = __syncthreads_or(!ok);
     if (failed && warp >= K_WARP) {
         const int full0 = warp >= V_WARP ? C::V_FULL : C::K_FULL, slots = warp >= V_WARP ? C::NV : C::NK;
