@@ -35,7 +35,9 @@
 //    room in TMEM.  One product stays, by one rule for all units.
 //  * All units laid end to end and measured in cost (a unit's start and output, then its tiles) are cut into equal ranges,
 //    one a CTA; units that a range's end cuts leave fp32 partials which tree_merge_kernel joins in a fixed order.  No
-//    host-side lengths, no atomics, two partials a CTA.
+//    host-side lengths, no atomics, two partials a CTA.  One thread of a CTA walks its range and tells the other warps the
+//    segments through a ring (each warp walking on its own, 4 KB of code in each that runs once a unit: 256 sequences of
+//    50..650 tokens 127 us instead of 99, 64 of 100..4096 104 instead of 95, x 256 rows 277 instead of 265).
 //  * Trees of more than 128 rows are `group` blocks of tokens (further ones in further passes), worked by CTAs next to each
 //    other that walk the same keys at the same time; pairs of them are a cluster, each loading half of every tile into
 //    both (64 sequences of 8K tokens x 256 rows: read by each CTA on its own through L2 521 us, the loads alone 475;
@@ -92,6 +94,7 @@ struct Cfg {
     // copies are joined in the Q tile's, 128 rows are written as they stand.  Tiles in the rings: what fits beside that
     static constexpr bool OWN_STAGE = D < 256;
     static constexpr int NK = D == 64 ? 6 : 2, NV = D == 64 ? 6 : 3;
+    static constexpr int SEGS = D == 64 ? 6 : 8, READERS = SOFTMAX + 7;  // segments told ahead; warps that are told
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = SLABS * QSLAB, V_OFF = K_OFF + NK * TILE;
     static constexpr int STAGE_OFF = OWN_STAGE ? V_OFF + NV * TILE : Q_OFF;
@@ -99,10 +102,11 @@ struct Cfg {
     static constexpr int BAR_OFF = ML_OFF + (SPLIT > 2 ? SPLIT : 2) * 128 * 4;
     static constexpr int K_FULL = 0, K_EMPTY = NK, V_FULL = 2 * NK, V_EMPTY = V_FULL + NV, V_OK = V_EMPTY + NV, Q_FULL = V_OK + NV, Q_EMPTY = Q_FULL + 1,
                          S_FULL = Q_FULL + 2, S_EMPTY = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
-                         O_FREE = Q_FULL + 10, DRAIN = Q_FULL + 11, NUM_BARS = Q_FULL + 13;
+                         O_FREE = Q_FULL + 10, DRAIN = Q_FULL + 11, SEG_FULL = Q_FULL + 13, SEG_EMPTY = SEG_FULL + SEGS, NUM_BARS = SEG_EMPTY + SEGS;
     static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch
     static constexpr int BAD_OFF = MISC_OFF + 192;                       // the V ring's rows that are not finite: a bit a row
-    static constexpr int SMEM_BYTES = BAD_OFF + NV * 16 + 1024;          // + alignment slack
+    static constexpr int SEG_OFF = BAD_OFF + NV * 16;                    // the ring of segments
+    static constexpr int SMEM_BYTES = SEG_OFF + SEGS * 48 + 1024;        // + alignment slack
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(COPIES == 1 || OWN_STAGE || NR * D * 4 <= SLABS * QSLAB, "the copies are joined in the Q tile's place");
     // TMEM: two S buffers, two P buffers (16-bit pairs), O
@@ -288,105 +292,135 @@ __device__ __forceinline__ Seq load_seq(const TreeParams& p, int s) {
 // A sequence's units: its KV heads times the passes over its blocks of tokens, `cost` each (its start and its
 // output count unit_cost tiles).  A pass is p.group blocks, one for each CTA of a group.
 __device__ __forceinline__ int tiles_of(const TreeParams& p, const Seq& k) { return (k.kv_len + (1 << p.tile_log2) - 1) >> p.tile_log2; }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// ceil(n / d), n below 2^26 and d > 0, from an estimate that is off by a few (an integer division is much more code, and
+// code that runs once is paid for by its size)
+__device__ __forceinline__ int ceil_div(int n, int d) {
+    int q = (int)((float)n * rcp((float)d));
+    while ((long long)q * d < n) ++q;
+    while (q > 0 && (long long)(q - 1) * d >= n) --q;
+    return q;
+}
+// n / d and n mod d, n >= 0 and d > 0: an estimate is right to 2^-20, of 24 bits at once, of more in four steps
+__device__ __forceinline__ long long quotient(long long n, int d, int& rest) {
+    const float r = rcp((float)d);
+    if (n < 1 << 24) {
+        const int m = (int)n, q = (int)((float)m * r);
+        rest = m - q * d;
+        const int off = rest < 0 ? -1 : rest >= d ? 1 : 0;
+        rest -= off * d;
+        return q + off;
+    }
+    long long q = 0;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        const long long e = (long long)((float)n * r);
+        q += e;
+        n -= e * d;
+    }
+    while (n < 0) n += d, --q;
+    while (n >= d) n -= d, ++q;
+    rest = (int)n;
+    return q;
+}
 __device__ __forceinline__ int passes_of(const TreeParams& p, const Seq& k) {
     const int per = p.tb * p.group;
-    return (k.n + per - 1) / per;
+    return k.n > per ? ceil_div(k.n, per) : k.n > 0;
 }
 
-// A range: where it starts (sequence, unit of it, cost into that unit) and its cost.
+// A range: where it starts (sequence, cost into its units) and its cost.
 struct Start {
-    int s, unit, at, count, per;
+    long long at;
+    int s, q0, n, kv_len, per;  // per 0: nothing
 };
 static_assert(sizeof(Start) <= 32, "record area");
 
-// Range `range` of `ranges`.  Every thread of the CTA calls it; all return the same record.
+// Range `range` of `ranges` equal ones, found by all THREADS threads of the block.  (Then the CTA is synchronised.)
 template <int THREADS>
-__device__ __forceinline__ Start find_start(const TreeParams& p, int range, int ranges, long long* warp_sum, Start* rec) {
+__device__ __forceinline__ void find_start(const TreeParams& p, int range, int ranges, volatile long long* warp_sum, Start* rec) {
     constexpr int NW = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) rec->count = 0;
+    if (tid == 0) rec->per = 0;
     Seq k{0, 0, 0, false};
-    long long mine = 0, cost = 0;  // of this thread's sequences, of the one in k
-    for (int s = tid; s < p.num_seqs; s += THREADS) {
+    auto cost_of = [&](int s) {
         k = load_seq(p, s);
+        return (long long)p.n_kv_heads * passes_of(p, k) * (tiles_of(p, k) + p.unit_cost);
+    };
+    auto prefix = [&](long long v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        if (lane == 31) warp_sum[warp] = v;
+        return v;
+    };
+    long long mine = 0, cost = 0;  // of this thread's sequences, of its last one
+#pragma unroll 1
+    for (int s = tid; s < p.num_seqs; s += THREADS) {
+        cost = cost_of(s);
         if (k.bad && blockIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
-        cost = (long long)p.n_kv_heads * passes_of(p, k) * (tiles_of(p, k) + p.unit_cost);
         mine += cost;
     }
-    const bool one = p.num_seqs <= THREADS;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
+    long long incl = prefix(mine);
     __syncthreads();
     long long total = 0, before = 0;
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < NW; ++w) {
         const long long x = warp_sum[w];
         if (w < warp) before += x;
         total += x;
     }
-    const int per = (int)max((total + ranges - 1) / ranges, (long long)p.min_tiles);
+    int rest;
+    const int per = (int)max(quotient(total + ranges - 1, ranges, rest), (long long)p.min_tiles);
     const long long lo = (long long)range * per;
     if (lo < total) {
-        auto found = [&](int s, const Seq& q, long long at, long long c) {
-            if (c > 0 && lo >= at && lo < at + c) {
-                const int unit = tiles_of(p, q) + p.unit_cost;
-                rec->s = s;
-                rec->unit = (int)((lo - at) / unit);
-                rec->at = (int)((lo - at) % unit);
-                rec->count = (int)min((long long)per, total - lo);
-            }
-        };
-        if (one) {
-            found(tid, k, before + incl - cost, tid < p.num_seqs ? cost : 0);
-        } else {
-            // prefix sums, THREADS sequences at a time
-            long long base = 0;
-            for (int s0 = 0; s0 < p.num_seqs && base <= lo; s0 += THREADS) {
+        // the sequence that holds it: by prefix sums, THREADS sequences at a time (those of the first pass are still here)
+        long long base = 0;
+#pragma unroll 1
+        for (int s0 = 0; s0 < p.num_seqs && base <= lo; s0 += THREADS) {
+            const int s = s0 + tid;
+            if (p.num_seqs > THREADS) {
                 __syncthreads();
-                const int s = s0 + tid;
-                Seq q{0, 0, 0, false};
-                long long m = 0;
-                if (s < p.num_seqs) {
-                    q = load_seq(p, s);
-                    m = (long long)p.n_kv_heads * passes_of(p, q) * (tiles_of(p, q) + p.unit_cost);
-                }
-                long long in = m;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, in, o);
-                    if (lane >= o) in += y;
-                }
-                if (lane == 31) warp_sum[warp] = in;
+                cost = s < p.num_seqs ? cost_of(s) : 0;
+                incl = prefix(cost);
                 __syncthreads();
-                long long all = base, bef = base;
+                before = total = 0;
+#pragma unroll 1
                 for (int w = 0; w < NW; ++w) {
-                    if (w < warp) bef += warp_sum[w];
-                    all += warp_sum[w];
+                    const long long x = warp_sum[w];
+                    if (w < warp) before += x;
+                    total += x;
                 }
-                found(s, q, bef + in - m, m);
-                base = all;
             }
+            const long long from = base + before + incl - cost;
+            if (cost > 0 && lo >= from && lo < from + cost) {
+                rec->s = s;
+                rec->at = lo - from;
+                rec->q0 = k.q0;
+                rec->n = k.n;
+                rec->kv_len = k.kv_len;
+                rec->per = per;
+            }
+            base += total;
         }
     }
     __syncthreads();
-    Start r = *rec;
-    r.per = per;
-    return r;
 }
 
-// One segment of a range: tiles [tile, tile + n) of one unit's `tiles`.
+// One segment of a range: tiles [tile, tile + n) of one unit's.  n == 0: there are no more.
 struct Segment {
     int s, head, tok0, toks;  // sequence, KV head, the unit's first token (of total_q) and tokens
     int q0;                   // the sequence's first token
-    int tile, n, tiles;
+    int tile, n;
     int ctx, keys, drafted;
     int parts, back;          // ranges the unit's tiles span (0: this one alone), and how many of them are before this one
 };
+static_assert(sizeof(Segment) == 48, "three 16-byte words");
 
 // The segments of the CTA's range in which it has rows: block `blk` (of p.group) of each pass.  CTAs of a cluster walk
 // all segments (without rows: toks 0), since each loads a half of what both read.
@@ -394,26 +428,30 @@ template <int CL>
 struct Walk {
     const TreeParams& p;
     Seq k;
-    int s, unit, at, left, per, blk;
+    int s, head, pass, passes, at, left, per, blk;  // `at`: cost into the unit
     __device__ __forceinline__ Walk(const TreeParams& p_, const Start& st, int blk_)
-        : p(p_), k{0, 0, 0, false}, s(st.s), unit(st.unit), at(st.at), left(st.count), per(st.per), blk(blk_) {
-        if (left > 0) k = load_seq(p, s);
+        : p(p_), k{st.q0, st.n, st.kv_len, false}, s(st.s), head(0), pass(0), passes(1), at(0), left(st.per), per(st.per), blk(blk_) {
+        if (left <= 0) return;
+        passes = passes_of(p, k);
+        const int unit = (int)quotient(st.at, tiles_of(p, k) + p.unit_cost, at);
+        head = unit;
+        if (passes > 1) head = (int)quotient(unit, passes, pass);
     }
-    // the next one, or false
-    __device__ __forceinline__ bool next(Segment& g) {
+    // the next one
+    __device__ __forceinline__ void next(Segment& g) {
+        g.n = 0;
         while (left > 0) {
-            const int passes = k.n <= p.tb * p.group ? 1 : passes_of(p, k), tiles = tiles_of(p, k);
+            const int tiles = tiles_of(p, k);
             const int cost = min(tiles + p.unit_cost - at, left);  // of the unit in this range
             left -= cost;
-            g.tiles = tiles;
             g.tile = max(0, at - p.unit_cost);
             g.n = max(0, at + cost - p.unit_cost) - g.tile;
             const int rest = tiles - g.tile - g.n;
-            g.back = g.tile > 0 ? (g.tile + per - 1) / per : 0;
-            g.parts = (g.tile > 0 || rest > 0) ? g.back + 1 + (rest > 0 ? (rest + per - 1) / per : 0) : 0;
+            g.back = g.tile > 0 ? ceil_div(g.tile, per) : 0;
+            g.parts = (g.tile > 0 || rest > 0) ? g.back + 1 + (rest > 0 ? ceil_div(rest, per) : 0) : 0;
             g.s = s;
-            g.head = passes == 1 ? unit : unit / passes;
-            const int j = (unit - g.head * passes) * p.group + blk;
+            g.head = head;
+            const int j = pass * p.group + blk;
             g.tok0 = k.q0 + j * p.tb;
             g.q0 = k.q0;
             g.toks = max(0, min(p.tb, k.n - j * p.tb));
@@ -421,16 +459,20 @@ struct Walk {
             g.keys = k.kv_len;
             g.drafted = k.n;
             at = 0;
-            if (left > 0 && ++unit == passes * p.n_kv_heads) {
-                unit = 0;
-                do {
-                    if (++s >= p.num_seqs) left = 0;
-                    else k = load_seq(p, s);
-                } while (left > 0 && k.n == 0);
+            if (left > 0 && ++pass == passes) {
+                pass = 0;
+                if (++head == p.n_kv_heads) {
+                    head = 0;
+                    do {
+                        if (++s >= p.num_seqs) left = 0;
+                        else k = load_seq(p, s);
+                    } while (left > 0 && k.n == 0);
+                    passes = passes_of(p, k);
+                }
             }
-            if (g.n > 0 && (CL > 1 || g.toks > 0)) return true;
+            if (g.n > 0 && (CL > 1 || g.toks > 0)) return;
+            g.n = 0;
         }
-        return false;
     }
 };
 
@@ -494,6 +536,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             mbar_init(bar(C::DRAIN + i), 1);
         }
         mbar_init(bar(C::O_FREE), SOFTMAX);
+        for (int i = 0; i < C::SEGS; ++i) {
+            mbar_init(bar(C::SEG_FULL + i), 1);
+            mbar_init(bar(C::SEG_EMPTY + i), C::READERS);
+        }
         fence_barrier_init();
     }
     if (warp == QK_WARP) {
@@ -505,13 +551,26 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before();
-    const Start start = find_start<C::THREADS>(p, range, (int)gridDim.x / p.group, warp_sum, rec);  // (synchronises the CTA)
+    find_start<C::THREADS>(p, range, (int)gridDim.x / p.group, warp_sum, rec);
     tc::fence_after();
     if constexpr (CL > 1) cluster_sync();  // the other CTA's barriers are ready
     const uint32_t tmem = *tmem_slot;
     bool ok = true;  // none of this warp's waits has run out
     auto wait = [&](int b, int phase) {
         if (ok) ok = warp_wait(bar(b), (uint32_t)(phase & 1), p.err);
+    };
+    // segment number j, as the walking thread told it; false: there is none, or a wait has run out
+    auto segment = [&](int j, Segment& g) {
+        wait(C::SEG_FULL + j % C::SEGS, j / C::SEGS);
+        if (!ok) return false;
+        const uint32_t at = sbase + C::SEG_OFF + (uint32_t)(j % C::SEGS) * 48u;
+        const uint4 a = lds128(at), b = lds128(at + 16), c = lds128(at + 32);
+        g.s = (int)a.x, g.head = (int)a.y, g.tok0 = (int)a.z, g.toks = (int)a.w;
+        g.q0 = (int)b.x, g.tile = (int)b.y, g.n = (int)b.z, g.ctx = (int)b.w;
+        g.keys = (int)c.x, g.drafted = (int)c.y, g.parts = (int)c.z, g.back = (int)c.w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::SEG_EMPTY + j % C::SEGS));
+        return g.n > 0;
     };
     int done = 0;    // loader warps: tiles loaded
     // token of a unit's row, row / g_heads (exact for rows below 128 and up to 16 heads)
@@ -547,8 +606,9 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         bool s_ready = false, pv_ready = false, v_ready = false;  // barriers seen complete ahead of time
         int i = 0;  // tile number over the CTA's range
         constexpr int MW = (KW + 31) / 32;
-        Walk<CL> walk(p, start, blk);
-        for (Segment g; walk.next(g);) {
+        Segment g;
+        // (a wait that ran out ends all of these warps' loops at the same segment: they meet at barriers inside)
+        for (int seg = 0; !bar_or<32 * SOFTMAX>(6, !segment(seg, g)); ++seg) {
             const int rows = g.toks * p.g_heads;
             const bool valid = r < rows;
             const uint32_t* mask = reinterpret_cast<const uint32_t*>(p.mask + (size_t)(valid ? g.tok0 + tok_r : g.q0) * p.mask_words);
@@ -831,11 +891,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         // rows past the keys may hold anything (their weights are 0, but 0 * NaN is NaN) and are zeroed, up to the end of the
         // last box that was loaded (the others are zero already); so are drafted rows that are not finite, which are noted
         int i = 0;
-        Walk<CL> walk(p, start, blk);
-        for (Segment g; walk.next(g);) {
+        Segment g;
+        for (int seg = 0; segment(seg, g); ++seg) {
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int kbase = (g.tile + u) * BN, st = i % C::NV;
                 wait(C::V_FULL + st, i / C::NV);
+                if (!ok) break;
                 if (kbase + BN > g.ctx) {
                     volatile uint32_t* bits = bad_keys + 4 * st;
                     const uint32_t tile = sV + (uint32_t)(st * C::TILE);
@@ -902,15 +963,15 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             }
             return e;
         };
-        Walk<CL> walk(p, start, blk);
         Segment g, ahead;
-        bool more = walk.next(g);
+        bool more = segment(0, g);
         int id = more ? entry(g, g.tile) : 0;
-        for (; more && ok; g = ahead) {
-            more = walk.next(ahead);
+        for (int seg = 1; more && ok; ++seg, g = ahead) {
             for (int u = 0; u < g.n; ++u, ++done) {
                 const int tile = g.tile + u;
-                const int nxt = u + 1 < g.n ? entry(g, tile + 1) : more ? entry(ahead, ahead.tile) : 0;
+                int nxt = 0;
+                if (u + 1 == g.n) more = segment(seg, ahead);
+                if (u + 1 < g.n || more) nxt = u + 1 < g.n ? entry(g, tile + 1) : entry(ahead, ahead.tile);
                 const int st = (int)uniform((uint32_t)(done % slots)), use = done / slots;
                 if (use > 0) wait(empty0 + st, use - 1);
                 if (!ok) break;
@@ -934,12 +995,37 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         // the last releases too: none is on its way, least of all from the other CTA of a cluster, when this one leaves
         for (int t = max(0, done - slots); t < done; ++t) wait(empty0 + t % slots, t / slots);
     } else if (warp == Q_WARP && lane == 0) {
-        // ------------------------------------------------------------ the units' query rows, once for each copy
+        // ------------------------------------------------------------ tells the others the segments, and loads the units'
+        // query rows, once for each copy.  Two segments are told ahead whatever it takes (the loaders look one ahead of the
+        // products), more where the others have read what was there
         tma_prefetch_desc(&tmQ);
-        int seg = 0;
         const uint32_t box = (uint32_t)(p.tb * p.g_heads * 128);
-        Walk<CL> walk(p, start, blk);
-        for (Segment g; walk.next(g);) {
+        uint4* ring = reinterpret_cast<uint4*>(smem + C::SEG_OFF);
+        Walk<CL> walk(p, *rec, blk);
+        int told = 0, seg = 0;  // segments told; query rows loaded
+        bool more = true;
+        for (;;) {
+            bool tell = more && told < seg + C::SEGS && (told != 1 || seg > 0);
+            if (tell && told >= C::SEGS) {
+                const int sl = told % C::SEGS, phase = told / C::SEGS - 1;
+                if (told < seg + 2) ok = mbar_wait(bar(C::SEG_EMPTY + sl), (uint32_t)(phase & 1), p.err);
+                else tell = mbar_test(bar(C::SEG_EMPTY + sl), phase);
+                if (!ok) break;
+            }
+            if (tell) {
+                Segment g;
+                walk.next(g);
+                more = g.n > 0;
+                uint4* to = ring + 3 * (told % C::SEGS);
+                to[0] = make_uint4((uint32_t)g.s, (uint32_t)g.head, (uint32_t)g.tok0, (uint32_t)g.toks);
+                to[1] = make_uint4((uint32_t)g.q0, (uint32_t)g.tile, (uint32_t)g.n, (uint32_t)g.ctx);
+                to[2] = make_uint4((uint32_t)g.keys, (uint32_t)g.drafted, (uint32_t)g.parts, (uint32_t)g.back);
+                mbar_arrive(bar(C::SEG_FULL + told % C::SEGS));
+                ++told;
+                continue;
+            }
+            const uint4 a = ring[3 * (seg % C::SEGS)];
+            if (ring[3 * (seg % C::SEGS) + 1].z == 0u) break;
             if (seg > 0) ok = mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err);
             if (!ok) break;
             mbar_arrive_expect_tx(bar(C::Q_FULL), box * C::SLABS * COPIES);
@@ -947,7 +1033,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             for (int c = 0; c < COPIES; ++c)
 #pragma unroll 1
                 for (int sl = 0; sl < C::SLABS; ++sl)
-                    tma_q(sQ + (uint32_t)(sl * C::QSLAB + c * NR * 128), &tmQ, sl * 64, g.head * p.g_heads, g.tok0, bar(C::Q_FULL));
+                    tma_q(sQ + (uint32_t)(sl * C::QSLAB + c * NR * 128), &tmQ, sl * 64, (int)a.y * p.g_heads, (int)a.z, bar(C::Q_FULL));
             ++seg;
         }
         if (seg > 0) (void)mbar_wait(bar(C::Q_FULL), (uint32_t)((seg - 1) & 1), p.err);
@@ -958,8 +1044,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         const uint64_t dq = tc::sdesc_sw128(sQ, 16, 1024), dk0 = tc::sdesc_sw128(sK, 16, 1024);
         const uint32_t el = elect_one(), tS = uniform(tmem);
         int i = 0, seg = 0;
-        Walk<CL> walk(p, start, blk);
-        for (Segment g; walk.next(g);) {
+        for (Segment g; segment(seg, g);) {
             wait(C::Q_FULL, seg);
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NK));
@@ -990,8 +1075,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         const uint64_t dv0 = tc::sdesc_sw128(sV, C::KSLAB, 1024);
         const uint32_t el = elect_one(), dO = uniform(tmem + C::O_COL), tP = uniform(tmem + C::P_COL);
         int i = 0, seg = 0;
-        Walk<CL> walk(p, start, blk);
-        for (Segment g; walk.next(g);) {
+        for (Segment g; segment(seg, g);) {
             if (seg > 0) wait(C::O_FREE, seg - 1);  // O of the segment before has been read
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NV));
