@@ -46,7 +46,8 @@
 //    written): scores are replaced before the softmax, and a warp of its own looks at the drafted V rows before their
 //    product: one that is not finite is zeroed in shared memory, the rows that see it becoming NaN.
 //  * A successful wait on a barrier costs ~200 cycles of a warp that does nothing else, so the softmax looks at the next
-//    tile's barriers while this one's weights are under way (493 -> 463 us at 256 rows).
+//    tile's barriers while this one's weights are under way (493 -> 463 us at 256 rows).  A thread reads all its scores of a
+//    tile at once (64 in two parts: 494 instead of 450); tiles of context alone have a loop of their own without a test.
 //  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set, the warps that load or issue products stop there, and the
 //    others go on without waiting, so that every barrier of the block is still met.  Loads and products under way are
 //    waited for (again with the limit); the results are not used.
@@ -56,12 +57,16 @@
 //    drafted tokens straight to the product, released by the checker as well: 256 rows x 8K 551 us instead of 450.)
 //
 // What bounds it: memory up to 128 rows, 6.4..6.8 TB/s between the starts and ends of units (a tile of 64 KB in ~2800
-// cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the softmax (~1800 cycles a tile) beside loads (~1500 for
-// a pair's) and products (1024; the tensor pipe is 46 % active).  Fixed: ~4 us to the first weights, ~3 us a unit that the rings do
-// not cover (the last product, the join, the first tile's maximum; cold instructions: the first pass through a
-// unit's end costs 3 x the next), ~5 us of merge.  Whole calls (GB300): 64 sequences of 100..4096 tokens, 16 drafted, 16 q / 8 KV
-// heads 96 us (82 us of bytes at the copy rate), 4 x 32K 89 (76), 64 x 1K..8K, 64 drafted, 32 q heads 296 (190).
+// cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the softmax (a chain of ~1750 cycles a tile: ~850 of arithmetic
+// of two warps that vote on the reference every tile, the rest a dozen short dependent steps) beside loads (a pair's alone
+// 388 of 437 us at 64 x 8K) and products (1024 cycles; everything but the loads 409 us).  A further K or V tile in the rings
+// makes pairs slower (268 -> 278).  Fixed: ~4 us to the first weights, 1.5..2.3 us a unit that the rings do not cover (the last
+// product, the join, the first tile's maximum), ~5 us of merge.  Whole calls (GB300): 64 sequences of 100..4096 tokens, 16
+// drafted, 16 q / 8 KV heads 94 us (82 us of bytes at the copy rate), 4 x 32K 87 (76), 64 x 1K..8K, 64 drafted, 32 q heads
+// 265 (190), 256 x 50..650 98 (56).
 #pragma once
+
+#include <type_traits>
 
 #include "pa_launch.h"
 #include "tcgen05.cuh"
@@ -101,8 +106,8 @@ struct Cfg {
     static constexpr int ML_OFF = V_OFF + NV * TILE + (OWN_STAGE ? NR * D * (COPIES > 1 ? 4 : 2) : 0);  // what a row's threads tell each other
     static constexpr int BAR_OFF = ML_OFF + (SPLIT > 2 ? SPLIT : 2) * 128 * 4;
     static constexpr int K_FULL = 0, K_EMPTY = NK, V_FULL = 2 * NK, V_EMPTY = V_FULL + NV, V_OK = V_EMPTY + NV, Q_FULL = V_OK + NV, Q_EMPTY = Q_FULL + 1,
-                         S_FULL = Q_FULL + 2, S_EMPTY = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
-                         O_FREE = Q_FULL + 10, DRAIN = Q_FULL + 11, SEG_FULL = Q_FULL + 13, SEG_EMPTY = SEG_FULL + SEGS, NUM_BARS = SEG_EMPTY + SEGS;
+                         S_FULL = Q_FULL + 2, P_FULL = Q_FULL + 4, PV_DONE = Q_FULL + 6,
+                         O_FREE = Q_FULL + 8, DRAIN = Q_FULL + 9, SEG_FULL = Q_FULL + 11, SEG_EMPTY = SEG_FULL + SEGS, NUM_BARS = SEG_EMPTY + SEGS;
     static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch
     static constexpr int BAD_OFF = MISC_OFF + 192;                       // the V ring's rows that are not finite: a bit a row
     static constexpr int SEG_OFF = BAD_OFF + NV * 16;                    // the ring of segments
@@ -210,12 +215,15 @@ __device__ __forceinline__ bool bar_or(int id, bool v) {
     return r != 0;
 }
 
+// Branches that few tiles take: their code is laid out of the others' way.
+__device__ __forceinline__ bool rare(bool v) { return __builtin_expect(v, 0); }
+
 // The warp waits; the polling loop stays out of line.  One result for the warp.
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned* err) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
-    if (__any_sync(0xffffffffu, !mbar_try_wait(bar, parity))) return wait_slow(bar, parity, err);
+    if (rare(__any_sync(0xffffffffu, !mbar_try_wait(bar, parity)))) return wait_slow(bar, parity, err);
     return true;
 }
 
@@ -530,7 +538,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         mbar_init(bar(C::Q_EMPTY), COPIES > 1 && !C::OWN_STAGE ? 1 + SOFTMAX : 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::S_FULL + i), 1);
-            mbar_init(bar(C::S_EMPTY + i), SOFTMAX);
             mbar_init(bar(C::P_FULL + i), SOFTMAX);
             mbar_init(bar(C::PV_DONE + i), 1);
             mbar_init(bar(C::DRAIN + i), 1);
@@ -603,7 +610,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             tc::wait_st();
         }
         const int tok_r = row_token(r);
-        bool s_ready = false, pv_ready = false, v_ready = false;  // barriers seen complete ahead of time
+        bool ready = false;  // the next tile's barriers were seen complete
         int i = 0;  // tile number over the CTA's range
         constexpr int MW = (KW + 31) / 32;
         Segment g;
@@ -620,32 +627,34 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             };
             uint32_t sees[MW], sees_next[MW];
             float m_ref = -INFINITY, l = 0.f;
-            if ((g.tile + 1) * BN > g.ctx) row_sees(g.tile, sees_next);
-            for (int u = 0; u < g.n; ++u, ++i) {
-                const int kbase = (g.tile + u) * BN, b = i & 1;
-                const bool drafts = kbase + BN > g.ctx;  // the tile holds drafted tokens or keys past them
-#pragma unroll
-                for (int w = 0; w < MW; ++w) sees[w] = sees_next[w];
-                if (kbase + 2 * BN > g.ctx) row_sees(g.tile + u + 1, sees_next);
-                if (!__all_sync(0xffffffffu, s_ready)) wait(C::S_FULL + b, i >> 1);
-                // the weights' buffer is free
-                if (i >= 2 && !__all_sync(0xffffffffu, pv_ready)) wait(C::PV_DONE + b, (i >> 1) - 1);
+            bool fresh = true;  // a row may be without a reference
+            // tiles of context alone, then those that hold drafted tokens or keys past them
+            const int plain = max(0, min(g.n, g.ctx / BN - g.tile));
+            if (plain < g.n) row_sees(g.tile + plain, sees_next);
+            int u = 0;
+            auto step = [&](auto with_drafts) {
+                constexpr bool DRAFTS = decltype(with_drafts)::value;
+                const int b = i & 1;
+                if (rare(!__all_sync(0xffffffffu, ready))) {
+                    wait(C::S_FULL + b, i >> 1);
+                    if (i >= 2) wait(C::PV_DONE + b, (i >> 1) - 1);  // the weights' buffer is free
+                }
                 tc::fence_after();
                 const uint32_t tSb = tS + (uint32_t)(b * BN), tPb = tP + (uint32_t)(b * BN / 2);
-                bool redo = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
                 float add = 0.f;
                 // part h of this thread's scores; those of keys that the row does not see, where the tile holds such keys, become
                 // what the scale turns into -inf
                 auto scores = [&](int h, uint32_t (&x)[H]) {
-                    if (drafts) {
+                    if constexpr (DRAFTS) {
 #pragma unroll
                         for (int e = 0; e < H; ++e)
                             if (!((sees[(h * H + e) / 32] >> ((h * H + e) & 31)) & 1u)) x[e] = unseen;
                     }
                 };
+                bool raise = fresh, raised = false;
 #pragma unroll 1
-                for (int attempt = 0; attempt < 2; ++attempt) {
-                    if (redo) {
+                for (;;) {
+                    if (rare(raise)) {
                         float mx = -INFINITY;
 #pragma unroll
                         for (int h = 0; h < KW / H; ++h) {
@@ -671,6 +680,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                             m_ref = mt;
                             l *= alpha;
                         }
+                        fresh = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
                         if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                             wait(C::PV_DONE + (b ^ 1), (i - 1) >> 1);  // O holds every tile before this one
                             tc::fence_after();
@@ -685,6 +695,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                                 tc::st16(at, o);
                             }
                         }
+                        raised = true;
                     }
                     const float mu = m_ref == -INFINITY ? 0.f : m_ref - kShift<BF16>;
                     const float2 sc2 = make_float2(sc, sc), nmu2 = make_float2(-mu, -mu);
@@ -707,25 +718,21 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         if (h + 1 < KW / H) tc::wait_ld();
                     }
                     // the next tile's barriers, without waiting
-                    s_ready = mbar_test(bar(C::S_FULL + (b ^ 1)), (i + 1) >> 1);
-                    pv_ready = mbar_test(bar(C::PV_DONE + (b ^ 1)), ((i + 1) >> 1) - 1);
-                    if (drafts) v_ready = mbar_test(bar(C::V_OK + i % C::NV), i / C::NV);
+                    ready = mbar_test(bar(C::S_FULL + (b ^ 1)), (i + 1) >> 1);
+                    ready = mbar_test(bar(C::PV_DONE + (b ^ 1)), ((i + 1) >> 1) - 1) && ready;
                     ls[0] = fadd2(ls[0], ls[1]);
                     add = ls[0].x + ls[0].y;
                     // (no weight is above their sum; the vote also says that a row's other thread has read this one's maximum)
-                    const bool over = row_or(valid && add > kMost);
-                    if (redo || !over) break;
-                    redo = true;  // a row outgrew its reference by more than 2^8: once more (the same columns are written)
+                    raise = row_or(valid && add > kMost);
+                    if (!rare(raise) || raised) break;
+                    // a row outgrew its reference by more than 2^8: once more (the same columns are written)
                     tc::wait_st();
                 }
                 l += add;
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::S_EMPTY + b));
-                if (drafts) {
+                if constexpr (DRAFTS) {
                     // a drafted V row that is not finite makes the row NaN if it sees it.  (Before the weights are given: the
                     // tile's product releases its slot, and a slot's barrier is not looked at two phases late)
-                    if (!__all_sync(0xffffffffu, v_ready)) wait(C::V_OK + i % C::NV, i / C::NV);
+                    wait(C::V_OK + i % C::NV, i / C::NV);
 #pragma unroll
                     for (int w = 0; w < MW; ++w) {
                         const int at = share * KW + 32 * w;  // this thread's keys of the tile: KW from share * KW on
@@ -737,7 +744,17 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::P_FULL + b));
+                if (lane == 0) mbar_arrive(bar(C::P_FULL + b));  // the scores have been read, too
+                ++i;
+            };
+#pragma unroll 1
+            for (; u < plain; ++u) step(std::false_type{});
+#pragma unroll 1
+            for (; u < g.n; ++u) {
+#pragma unroll
+                for (int w = 0; w < MW; ++w) sees[w] = sees_next[w];
+                if (u + 1 < g.n) row_sees(g.tile + u + 1, sees_next);  // a tile ahead
+                step(std::true_type{});
             }
             // the segment's end: O / l, or the partial
             const bool whole = g.parts == 0;
@@ -1049,7 +1066,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             for (int u = 0; u < g.n; ++u, ++i) {
                 const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NK));
                 wait(C::K_FULL + st, i / C::NK);
-                if (i >= 2) wait(C::S_EMPTY + b, (i >> 1) - 1);
+                if (i >= 2) wait(C::P_FULL + b, (i >> 1) - 1);  // S has been read
                 if (!ok) break;
                 tc::fence_after();
                 const uint64_t dk = dk0 + (uint32_t)((st * C::TILE) >> 4);
