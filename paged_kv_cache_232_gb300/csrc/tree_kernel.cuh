@@ -313,10 +313,10 @@ __device__ __forceinline__ int ceil_div(int n, int d) {
     while (q > 0 && (long long)(q - 1) * d >= n) --q;
     return q;
 }
-// n / d and n mod d, n >= 0 and d > 0: an estimate is right to 2^-20, of 24 bits at once, of more in four steps
+// n / d and n mod d, n >= 0 and d > 0: an estimate is right to 2^-21, of 22 bits at once, of more in four steps
 __device__ __forceinline__ long long quotient(long long n, int d, int& rest) {
     const float r = rcp((float)d);
-    if (n < 1 << 24) {
+    if (n < 1 << 22) {
         const int m = (int)n, q = (int)((float)m * r);
         rest = m - q * d;
         const int off = rest < 0 ? -1 : rest >= d ? 1 : 0;

@@ -105,6 +105,13 @@ def test_many_sequences(hq, hkv, d):
     _check("fp16", hq, hkv, d, 16, [i % 6 for i in range(701)], [(37 * i) % 150 for i in range(701)], seed=3)
 
 
+@pytest.mark.parametrize("hq,hkv,d,n", [(16, 8, 128, 5), (32, 8, 128, 16), (64, 8, 128, 16), (32, 4, 128, 40), (64, 4, 128, 130),
+                                        (8, 8, 64, 6), (16, 4, 64, 64), (8, 8, 256, 4), (32, 8, 256, 40)])
+def test_many_units_a_cta(hq, hkv, d, n):
+    """A CTA has more units than are told ahead of their work, most of a single tile."""
+    _check("bf16", hq, hkv, d, 16, [1 + (7 * i) % n for i in range(300)], [(53 * i) % 290 for i in range(300)], seed=n)
+
+
 @pytest.mark.parametrize("ty", ["bf16", "fp16"])
 @pytest.mark.parametrize("hq,hkv,d,n", [(1, 1, 128, 21), (4, 1, 128, 16), (8, 1, 128, 16), (2, 2, 64, 20), (2, 1, 256, 16)])
 def test_any_mask(ty, hq, hkv, d, n):
