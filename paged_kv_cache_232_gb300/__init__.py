@@ -137,18 +137,24 @@ def status_string(status: int) -> str:
 # ------------------------------------------------------------------ marshalling helpers
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
+    torch, ty = _torch(), t.dtype
+    if ty == torch.bfloat16:
         return PA_BF16
-    if t.dtype == torch.float16:
+    if ty == torch.float16:
         return PA_F16
-    raise TypeError(f"expected float16 or bfloat16, got {t.dtype}")
+    raise TypeError(f"expected float16 or bfloat16, got {ty}")
 
 
 def _dev(t, name: str, dtype=None):
@@ -361,10 +367,11 @@ def pa_prefill_chunk(out, q, k_cache, v_cache, block_tables, query_start_loc, se
 
 def _device(t) -> int:
     """Index of the device a call runs on: t's, which has to be the current one (the library launches there)."""
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError("every tensor must be a CUDA tensor")
-    dev = _torch().cuda.current_device()
-    if t.get_device() != dev:
+    dev = _torch()._C._cuda_getDevice()
+    if at != dev:
         raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     return dev
 
@@ -381,9 +388,10 @@ def _refuse(t, name: str, dtype, shape, dev, what: str):
 
 def _dims(t, name: str, shape: str, n: int):
     """t's sizes, n of them (shape: what the message calls them)."""
-    if t.dim() != n:
-        raise ValueError(f"{name} must be {shape}, got {list(t.shape)}")
-    return t.shape
+    dims = t.shape
+    if len(dims) != n:
+        raise ValueError(f"{name} must be {shape}, got {list(dims)}")
+    return dims
 
 
 def _rows(t, name: str, dtype, shape, dev):
@@ -401,6 +409,13 @@ def _flat(t, name: str, dtype, shape, dev):
     """Pointer of a contiguous tensor of this type and shape."""
     if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, name, dtype, shape, dev, "contiguous")
+    return t.data_ptr()
+
+
+def _ptr(t, name: str, dtype, dev):
+    """Pointer of a contiguous tensor of this type, whose own sizes the call takes."""
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, t.shape, dev, "contiguous")
     return t.data_ptr()
 
 
@@ -554,8 +569,9 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, query_start_loc, seq_
     query_start_loc[s] .. query_start_loc[s + 1], seq_lens [S] with the drafted tokens, tree_mask [T, words] int64 (bit k
     of a row: it sees the k-th drafted token); workspace of at least pa_tree_workspace_size(Hq, Hkv, D, max_q_len) bytes."""
     torch = _torch()
-    ty, dt = q.dtype, _dtype_code(q)
-    nb, bs, hkv, d = _dims(k_cache, "k_cache", "[num_blocks, block_size, Hkv, D]", 4)
+    ty, dt, i32 = q.dtype, _dtype_code(q), torch.int32
+    cache = _dims(k_cache, "k_cache", "[num_blocks, block_size, Hkv, D]", 4)
+    nb, bs, hkv, d = cache
     rows, hq, _ = _dims(q, "q", "[T, Hq, D]", 3)
     n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
     _, words = _dims(tree_mask, "tree_mask", "[T, words]", 2)
@@ -563,9 +579,9 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, query_start_loc, seq_
     wp, wb = _workspace(workspace, dev)
     _check(load().pa_tree_decode(
         _flat(out, "out", ty, (rows, hq, d), dev), _flat(q, "q", ty, (rows, hq, d), dev),
-        _flat(k_cache, "k_cache", ty, (nb, bs, hkv, d), dev), _flat(v_cache, "v_cache", ty, (nb, bs, hkv, d), dev),
-        _flat(block_tables, "block_tables", torch.int32, (n, mb), dev), mb,
-        _flat(query_start_loc, "query_start_loc", torch.int32, (n + 1,), dev), _flat(seq_lens, "seq_lens", torch.int32, (n,), dev),
+        _ptr(k_cache, "k_cache", ty, dev), _flat(v_cache, "v_cache", ty, cache, dev),
+        _ptr(block_tables, "block_tables", i32, dev), mb,
+        _flat(query_start_loc, "query_start_loc", i32, (n + 1,), dev), _flat(seq_lens, "seq_lens", i32, (n,), dev),
         _flat(tree_mask, "tree_mask", torch.int64, (rows, words), dev), words, n, int(max_q_len), rows, hq, hkv, d, bs, nb,
         float(scale), dt, wp, wb, _raw_stream(stream, dev)), "pa_tree_decode")
 
@@ -573,24 +589,28 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, query_start_loc, seq_
 def _workspace(workspace, dev):
     if workspace is None:
         return 0, 0
-    return _flat(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.nbytes
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(workspace, "workspace", workspace.dtype, workspace.shape, dev, "contiguous")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _planes(k_cache, v_cache):
     """(k pointer, v pointer, layers, row bytes, block_size, num_blocks, device) of caches [NB, bs, Hkv, D] or, of all
     layers, [L, NB, bs, Hkv, D]; v_cache None: of one array a layer, [NB, bs, row] or [L, NB, bs, row]."""
     inner = 2 if v_cache is not None else 1
-    if k_cache.dim() not in (2 + inner, 3 + inner):
+    shape = k_cache.shape
+    if len(shape) not in (2 + inner, 3 + inner):
         raise ValueError("k_cache must be " + ("[num_blocks, block_size, Hkv, D]" if inner == 2 else "[num_blocks, block_size, row]")
-                         + f" (layers before it where there are several), got {list(k_cache.shape)}")
+                         + f" (layers before it where there are several), got {list(shape)}")
     _dtype_code(k_cache)
-    dev, shape = _device(k_cache), k_cache.shape
+    dev = _device(k_cache)
     layers = shape[0] if len(shape) == 3 + inner else 1
     nb, bs = shape[-2 - inner], shape[-1 - inner]
     row = shape[-1] * (shape[-2] if inner == 2 else 1) * 2
-    kp = _flat(k_cache, "k_cache", k_cache.dtype, shape, dev)
+    if not k_cache.is_contiguous():
+        _refuse(k_cache, "k_cache", k_cache.dtype, shape, dev, "contiguous")
     vp = None if v_cache is None else _flat(v_cache, "v_cache", k_cache.dtype, shape, dev)
-    return kp, vp, layers, row, bs, nb, dev
+    return k_cache.data_ptr(), vp, layers, row, bs, nb, dev
 
 
 def pa_tree_commit(k_cache, v_cache, block_tables, query_start_loc, seq_lens, path, num_accepted, new_lens, stream=None) -> None:
@@ -602,7 +622,7 @@ def pa_tree_commit(k_cache, v_cache, block_tables, query_start_loc, seq_lens, pa
     n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
     _, most = _dims(path, "path", "[sequences, max_path]", 2)
     _check(load().pa_tree_commit(
-        kp, vp, layers, _flat(block_tables, "block_tables", i32, (n, mb), dev), mb,
+        kp, vp, layers, _ptr(block_tables, "block_tables", i32, dev), mb,
         _flat(query_start_loc, "query_start_loc", i32, (n + 1,), dev), _flat(seq_lens, "seq_lens", i32, (n,), dev),
         _flat(path, "path", i32, (n, most), dev), most, _flat(num_accepted, "num_accepted", i32, (n,), dev),
         _flat(new_lens, "new_lens", i32, (n,), dev), n, row, bs, nb, _raw_stream(stream, dev)), "pa_tree_commit")
@@ -624,8 +644,8 @@ def pa_fork_pages(block_tables, seq_lens, parents, ref_counts, block_size: int, 
     nb, = _dims(ref_counts, "ref_counts", "[num_blocks]", 1)
     dev = _device(block_tables)
     _check(load().pa_fork_pages(
-        _flat(block_tables, "block_tables", i32, (n, mb), dev), mb, _flat(seq_lens, "seq_lens", i32, (n,), dev),
-        _flat(parents, "parents", i32, (n,), dev), n, _flat(ref_counts, "ref_counts", i32, (nb,), dev), int(block_size), nb,
+        _ptr(block_tables, "block_tables", i32, dev), mb, _flat(seq_lens, "seq_lens", i32, (n,), dev),
+        _flat(parents, "parents", i32, (n,), dev), n, _ptr(ref_counts, "ref_counts", i32, dev), int(block_size), nb,
         _raw_stream(stream, dev)), "pa_fork_pages")
 
 
@@ -643,7 +663,7 @@ def pa_resize_pages(k_cache, v_cache, block_tables, seq_lens, new_lens, ref_coun
     n, mb = _dims(block_tables, "block_tables", "[sequences, max_blocks]", 2)
     wp, wb = _workspace(workspace, dev)
     _check(load().pa_resize_pages(
-        kp, vp, layers, _flat(block_tables, "block_tables", i32, (n, mb), dev), mb, _flat(seq_lens, "seq_lens", i32, (n,), dev),
+        kp, vp, layers, _ptr(block_tables, "block_tables", i32, dev), mb, _flat(seq_lens, "seq_lens", i32, (n,), dev),
         _flat(new_lens, "new_lens", i32, (n,), dev), n, _flat(ref_counts, "ref_counts", i32, (nb,), dev),
         _flat(free_list, "free_list", i32, (nb,), dev), _flat(free_count, "free_count", i32, (1,), dev), row, bs, nb, wp, wb,
         _raw_stream(stream, dev)), "pa_resize_pages")
