@@ -61,9 +61,9 @@
 // of two warps that vote on the reference every tile, the rest a dozen short dependent steps) beside loads (a pair's alone
 // 388 of 437 us at 64 x 8K) and products (1024 cycles; everything but the loads 409 us).  A further K or V tile in the rings
 // makes pairs slower (268 -> 278).  Fixed: ~4 us to the first weights, 1.5..2.3 us a unit that the rings do not cover (the last
-// product, the join, the first tile's maximum), ~5 us of merge.  Whole calls (GB300): 64 sequences of 100..4096 tokens, 16
-// drafted, 16 q / 8 KV heads 94 us (82 us of bytes at the copy rate), 4 x 32K 87 (76), 64 x 1K..8K, 64 drafted, 32 q heads
-// 265 (190), 256 x 50..650 98 (56).
+// product, the join, the first tile's maximum), ~3 us of merge.  Whole calls (GB300, in a graph): 64 sequences of 100..4096
+// tokens, 16 drafted, 16 q / 8 KV heads 93 us (82 us of bytes at the copy rate), 4 x 32K 86 (76), 64 x 1K..8K, 64 drafted, 32 q
+// heads 265 (190), 256 x 50..650 99 (56), one of 100 9.5.
 #pragma once
 
 #include <type_traits>
