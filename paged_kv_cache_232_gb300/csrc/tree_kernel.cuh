@@ -788,8 +788,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             const bool whole = g.parts == 0;
             const int slot = 2 * (int)blockIdx.x + (g.tile == 0 ? 1 : 0);
             const size_t row0 = (size_t)g.tok0 * p.n_q_heads + (size_t)g.head * p.g_heads;
-            wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
-            tc::fence_after();
+            auto product = [&]() {  // the last one; what the row's threads have to tell each other is told before
+                wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
+                tc::fence_after();
+            };
             if constexpr (COPIES == 1) {
                 constexpr int W = D / SPLIT, CW = W < 32 ? W : 32;  // columns of this thread, at a time
                 const int c0 = share * W;
@@ -814,6 +816,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 if (!whole && valid && share == 0) p.part_ml[(size_t)slot * NR + r] = make_float2(m_ref, l);
                 uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)tok_r * p.n_q_heads + (r - tok_r * p.g_heads)) * p.hd + c0;
                 float4* part = p.part_o + ((size_t)slot * (D / 4) + c0 / 4) * NR + r;
+                product();
 #pragma unroll
                 for (int q = 0; q < W / CW; ++q) {
                     read_o(q);
@@ -870,6 +873,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 const uint32_t srow = sStage + (uint32_t)(r * D * 4);
                 uint16_t* dst = static_cast<uint16_t*>(p.out) + (row0 + (size_t)tok_r * p.n_q_heads + (r - tok_r * p.g_heads)) * p.hd;
                 float4* part = p.part_o + (size_t)slot * (D / 4) * NR + r;
+                product();
 #pragma unroll 1
                 for (int k = 0; k < COPIES; ++k) {
                     const int c0 = ((share + k) % COPIES) * W;
