@@ -52,9 +52,9 @@
 //    others go on without waiting, so that every barrier of the block is still met.  Loads and products under way are
 //    waited for (again with the limit); the results are not used.
 //  * No wait can be overtaken: a barrier two phases on looks like one that is not complete.  So what a warp waits for goes
-//    on only after that warp has arrived at something that it needs: every V tile passes the checker on its way to the
-//    product, and the softmax looks at the checker's barrier before it hands over the tile's weights.  (Tiles without
-//    drafted tokens straight to the product, released by the checker as well: 256 rows x 8K 551 us instead of 450.)
+//    on only after that warp has arrived at something that it needs: every V tile passes the scanner on its way to the
+//    product, and the softmax looks at the scanner's barrier before it hands over the tile's weights.  (Tiles without
+//    drafted tokens straight to the product, released by the scanner as well: 256 rows x 8K 551 us instead of 450.)
 //
 // What bounds it: memory up to 128 rows, 6.4..6.8 TB/s between the starts and ends of units (a tile of 64 KB in ~2800
 // cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the softmax (a chain of ~1750 cycles a tile: ~850 of arithmetic
@@ -88,7 +88,7 @@ struct Cfg {
     static constexpr int COPIES = 128 / NR;
     static constexpr int SPLIT = NR < 128 ? 1 : 2;  // threads a row of the tile
     static constexpr int KW = BN / COPIES / SPLIT;      // keys of a tile that one thread takes
-    static constexpr int SOFTMAX = 4 * SPLIT;           // softmax warps; then the issuers, the Q loader, two K and two V loaders, the V checker
+    static constexpr int SOFTMAX = 4 * SPLIT;           // softmax warps; then the issuers, the Q loader, two K and two V loaders, the V scanner
     static constexpr int QK_WARP = SOFTMAX, PV_WARP = SOFTMAX + 1, Q_WARP = SOFTMAX + 2, K_WARP = SOFTMAX + 3,
                          V_WARP = SOFTMAX + 5, CHECK_WARP = SOFTMAX + 7, THREADS = (SOFTMAX + 8) * 32;
     static constexpr int SLABS = D / 64;
