@@ -1258,13 +1258,12 @@ struct TreeUnits {
     int tb, group, rows;  // tokens a unit, CTAs that walk the same keys, query rows the kernel is built for
 };
 
-// Blocks of at most 128 rows, of equal numbers of tokens; more than one of them side by side, an even number up to 8
-// (pairs share their loads).
+// Blocks of at most 128 rows, of equal numbers of tokens; up to 8 of them side by side.
 static TreeUnits tree_units(int g_heads, int max_q_len) {
     const int most = 128 / g_heads, blocks = (max_q_len + most - 1) / most;
     TreeUnits u;
     const int passes = (blocks + 7) / 8;
-    u.group = blocks == 1 ? 1 : ((blocks + passes - 1) / passes + 1) / 2 * 2;
+    u.group = (blocks + passes - 1) / passes;
     u.tb = (max_q_len + u.group * passes - 1) / (u.group * passes);
     u.rows = u.group > 1 || u.tb * g_heads > 64 ? 128 : u.tb * g_heads > 32 ? 64 : 32;
     return u;

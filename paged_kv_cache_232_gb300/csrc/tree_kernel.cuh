@@ -39,9 +39,10 @@
 //    segments through a ring (each warp walking on its own, 4 KB of code in each that runs once a unit: 256 sequences of
 //    50..650 tokens 127 us instead of 99, 64 of 100..4096 104 instead of 95, x 256 rows 277 instead of 265).
 //  * Trees of more than 128 rows are `group` blocks of tokens (further ones in further passes), worked by CTAs next to each
-//    other that walk the same keys at the same time; pairs of them are a cluster, each loading half of every tile into
-//    both (64 sequences of 8K tokens x 256 rows: read by each CTA on its own through L2 521 us, the loads alone 475;
-//    multicast 467 and 385).
+//    other that walk the same keys at the same time, each loading them for itself: all but the first find them in L2.  A
+//    CTA passes over the sequences in which its block has no rows.  (One load for two blocks, sent to both CTAs of a
+//    cluster, took 437 us where this takes 492, 64 sequences of 8K tokens x 256 rows.  It is not used: a cache may lie in
+//    memory of another GPU, where such loads are not safe.)
 //  * The cache rows of drafted tokens that some row does not see may hold anything (a padded token's row was never
 //    written): scores are replaced before the softmax, and a warp of its own looks at the drafted V rows before their
 //    product: one that is not finite is zeroed in shared memory, the rows that see it becoming NaN.
@@ -58,12 +59,11 @@
 //
 // What bounds it: memory up to 128 rows, 6.4..6.8 TB/s between the starts and ends of units (a tile of 64 KB in ~2800
 // cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the softmax (a chain of ~1750 cycles a tile: ~850 of arithmetic
-// of two warps that vote on the reference every tile, the rest a dozen short dependent steps) beside loads (a pair's alone
-// 388 of 437 us at 64 x 8K) and products (1024 cycles; everything but the loads 409 us).  A further K or V tile in the rings
-// makes pairs slower (268 -> 278).  Fixed: ~4 us to the first weights, 1.5..2.3 us a unit that the rings do not cover (the last
+// of two warps that vote on the reference every tile, the rest a dozen short dependent steps) beside loads (475 of 492 us
+// alone at 64 x 8K) and products (1024 cycles; everything but the loads 409 us).  Fixed: ~4 us to the first weights, 1.5..2.3 us a unit that the rings do not cover (the last
 // product, the join, the first tile's maximum), ~3 us of merge.  Whole calls (GB300, in a graph): 64 sequences of 100..4096
 // tokens, 16 drafted, 16 q / 8 KV heads 93 us (82 us of bytes at the copy rate), 4 x 32K 86 (76), 64 x 1K..8K, 64 drafted, 32 q
-// heads 265 (190), 256 x 50..650 99 (56), one of 100 9.5.
+// heads 298 (190), 256 x 50..650 99 (56), one of 100 9.5.
 #pragma once
 
 #include <type_traits>
@@ -154,28 +154,6 @@ __device__ __forceinline__ void tma_box(uint32_t el, uint32_t dst, const CUtenso
         " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy), "r"(el)
         : "memory");
-}
-// the same box into both CTAs of a cluster, each one's barrier counting it
-__device__ __forceinline__ void tma_box_pair(uint32_t el, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                             uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
-        "setp.ne.b32 q, %8, 0;\n\tmov.b16 m, 3;\n\t"
-        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], m, %7;\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy), "r"(el)
-        : "memory");
-}
-__device__ __forceinline__ void commit_pair(uint32_t el, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\tmov.b16 m, 3;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
-        "r"(el)
-        : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
@@ -456,9 +434,7 @@ struct Segment {
 };
 static_assert(sizeof(Segment) == 48, "three 16-byte words");
 
-// The segments of the CTA's range in which it has rows: block `blk` (of p.group) of each pass.  CTAs of a cluster walk
-// all segments (without rows: toks 0), since each loads a half of what both read.
-template <int CL>
+// The segments of the CTA's range in which it has rows: block `blk` (of p.group) of each pass.
 struct Walk {
     const TreeParams& p;
     Seq k;
@@ -504,7 +480,7 @@ struct Walk {
                     passes = passes_of(p, k);
                 }
             }
-            if (g.n > 0 && (CL > 1 || g.toks > 0)) return;
+            if (g.n > 0 && g.toks > 0) return;
             g.n = 0;
         }
     }
@@ -527,7 +503,7 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t* row, int words, int k
 
 }  // namespace tree
 
-template <bool BF16, int D, int NR, int CL>
+template <bool BF16, int D, int NR>
 __global__ void __launch_bounds__(tree::Cfg<D, NR>::THREADS, 1)
 tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const __grid_constant__ CUtensorMap tmQ) {
@@ -553,11 +529,11 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NK; ++i) {
             mbar_init(bar(C::K_FULL + i), 2);
-            mbar_init(bar(C::K_EMPTY + i), CL);
+            mbar_init(bar(C::K_EMPTY + i), 1);
         }
         for (int i = 0; i < C::NV; ++i) {
             mbar_init(bar(C::V_FULL + i), 2);
-            mbar_init(bar(C::V_EMPTY + i), CL);
+            mbar_init(bar(C::V_EMPTY + i), 1);
             mbar_init(bar(C::V_OK + i), 1);
         }
         mbar_init(bar(C::Q_FULL), 1);
@@ -588,7 +564,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     if (by_warp) __syncthreads();
     else find_start<C::THREADS>(p, range, (int)gridDim.x / p.group, warp_sum, rec);
     tc::fence_after();
-    if constexpr (CL > 1) cluster_sync();  // the other CTA's barriers are ready
     const uint32_t tmem = *tmem_slot;
     bool ok = true;  // none of this warp's waits has run out
     auto wait = [&](int b, int phase) {
@@ -990,11 +965,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     } else if (warp >= K_WARP) {
         // ------------------------------------------------------------ cache rows into the rings, every second box of K or V
         const bool is_v = warp >= V_WARP;
-        // in a cluster every box goes to both CTAs and each issues half of them
-        const int first = ((warp - K_WARP) & 1) + (CL > 1 ? 2 * (blk & 1) : 0);
+        const int first = (warp - K_WARP) & 1;
         const CUtensorMap* map = is_v ? &tmV : &tmK;
         if (lane == 0) tma_prefetch_desc(map);
-        const uint64_t pol = p.group == CL ? l2_policy_evict_first() : l2_policy_normal();  // read once, or by the group's CTAs
+        const uint64_t pol = p.group == 1 ? l2_policy_evict_first() : l2_policy_normal();  // read once, or by the group's CTAs
         const int br = min(p.block_size, 16), nbox = BN / br;
         const int full0 = is_v ? C::V_FULL : C::K_FULL, empty0 = is_v ? C::V_EMPTY : C::K_EMPTY;
         const int slots = is_v ? C::NV : C::NK;
@@ -1025,20 +999,17 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 if (el) mbar_arrive_expect_tx(full, C::TILE / 2);
                 __syncwarp();
 #pragma unroll 1
-                for (int x = first; x < nbox; x += 2 * CL) {
+                for (int x = first; x < nbox; x += 2) {
                     const int e = __shfl_sync(0xffffffffu, id, x);
                     const int row = (int)uniform((uint32_t)((tile * BN + x * br) & (p.block_size - 1)));
 #pragma unroll
-                    for (int sl = 0; sl < C::SLABS; ++sl) {
-                        const uint32_t to = dst + (uint32_t)(sl * C::KSLAB + x * br * 128);
-                        if constexpr (CL > 1) tma_box_pair(el, to, map, sl * 64, g.head, row, e, full, pol);
-                        else tma_box(el, to, map, sl * 64, g.head, row, e, full, pol);
-                    }
+                    for (int sl = 0; sl < C::SLABS; ++sl)
+                        tma_box(el, dst + (uint32_t)(sl * C::KSLAB + x * br * 128), map, sl * 64, g.head, row, e, full, pol);
                 }
                 id = nxt;
             }
         }
-        // the last releases too: none is on its way, least of all from the other CTA of a cluster, when this one leaves
+        // the last releases too: none is on its way when the block leaves
         for (int t = max(0, done - slots); t < done; ++t) wait(empty0 + t % slots, t / slots);
     } else if (warp == Q_WARP) {
         // ------------------------------------------------------------ tells the others the segments, and loads the units'
@@ -1049,7 +1020,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             tma_prefetch_desc(&tmQ);
             const uint32_t box = (uint32_t)(p.tb * p.g_heads * 128);
             uint4* ring = reinterpret_cast<uint4*>(smem + C::SEG_OFF);
-            Walk<CL> walk(p, start, blk);
+            Walk walk(p, start, blk);
             int told = 0, seg = 0;  // segments told; query rows loaded
             bool more = true;
             for (;;) {
@@ -1107,8 +1078,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                     mma_ss(el, tS + (uint32_t)(b * BN), dq + (uint32_t)(((kk >> 2) * C::QSLAB + (kk & 3) * 32) >> 4),
                            dk + (uint32_t)(((kk >> 2) * C::KSLAB + (kk & 3) * 32) >> 4), ID_QK, kk > 0);
                 commit(el, bar(C::S_FULL + b));
-                if constexpr (CL > 1) commit_pair(el, bar(C::K_EMPTY + st));
-                else commit(el, bar(C::K_EMPTY + st));
+                commit(el, bar(C::K_EMPTY + st));
                 if (u == g.n - 1) commit(el, bar(C::Q_EMPTY));
             }
             if (!ok) break;
@@ -1138,8 +1108,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
                     mma_ts(kk < steps ? el : 0u, dO, tP + (uint32_t)(b * (BN / 2) + 8 * kk), dv + (uint32_t)((kk * 2048) >> 4), ID_PV, kk > 0 ? 1u : acc);
-                if constexpr (CL > 1) commit_pair(el, bar(C::V_EMPTY + st));
-                else commit(el, bar(C::V_EMPTY + st));
+                commit(el, bar(C::V_EMPTY + st));
                 commit(el, bar(C::PV_DONE + b));
             }
             if (!ok) break;
@@ -1167,10 +1136,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     if (warp == QK_WARP) {
         tc::fence_after();
         tc::dealloc(tmem, C::TMEM_COLS);
-    }
-    if constexpr (CL > 1) {
-        __syncwarp();
-        cluster_sync();  // nothing more arrives in either CTA's shared memory
     }
 }
 

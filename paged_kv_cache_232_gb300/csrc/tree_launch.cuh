@@ -4,12 +4,12 @@
 
 namespace pa {
 
-template <bool BF16, int D, int NR, int CL>
+template <bool BF16, int D, int NR>
 static cudaError_t launch_tree_t(const TreeParams& p, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int ctas,
                                  cudaStream_t st) {
     static std::atomic<unsigned long long> s_done{0};
     using C = tree::Cfg<D, NR>;
-    auto kern = tree_kernel<BF16, D, NR, CL>;
+    auto kern = tree_kernel<BF16, D, NR>;
     cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, s_done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -17,21 +17,17 @@ static cudaError_t launch_tree_t(const TreeParams& p, const CUtensorMap& k, cons
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CL;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CL > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p, k, v, q);
     if (e != cudaSuccess) return e;
     // the merge: a block for 16 query rows of each CTA's cut units
     cfg.gridDim = dim3((unsigned)ctas, NR / 16);
     cfg.blockDim = dim3(tree::MERGE_THREADS);
     cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, tree_merge_kernel<BF16, D, NR>, p);
 }
 
@@ -39,11 +35,9 @@ template <bool BF16, int D>
 static cudaError_t tree_by_rows(int unit_rows, const TreeParams& p, const CUtensorMap& k, const CUtensorMap& v,
                                 const CUtensorMap& q, int ctas, cudaStream_t st) {
     switch (unit_rows) {
-        case 32: return launch_tree_t<BF16, D, 32, 1>(p, k, v, q, ctas, st);
-        case 64: return launch_tree_t<BF16, D, 64, 1>(p, k, v, q, ctas, st);
-        default:
-            return p.group > 1 ? launch_tree_t<BF16, D, 128, 2>(p, k, v, q, ctas, st)
-                               : launch_tree_t<BF16, D, 128, 1>(p, k, v, q, ctas, st);
+        case 32: return launch_tree_t<BF16, D, 32>(p, k, v, q, ctas, st);
+        case 64: return launch_tree_t<BF16, D, 64>(p, k, v, q, ctas, st);
+        default: return launch_tree_t<BF16, D, 128>(p, k, v, q, ctas, st);
     }
 }
 
