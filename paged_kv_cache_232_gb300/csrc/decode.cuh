@@ -183,7 +183,7 @@ __device__ __forceinline__ int seq_at_rank(const DecodeParams& p, int r, int* sc
     int* hist = scratch + S;
     for (int i = tid; i < nb; i += blockDim.x) hist[i] = 0;
     for (int i = tid; i < S; i += blockDim.x) {
-        int L = __ldg(p.context_lens + i);
+        int L = ld_global(p.context_lens + i);
         L = L < 0 ? 0 : min(L, cap);
         len[i] = (streamed_tokens(p, L) + 15) >> 4;
     }
@@ -244,7 +244,7 @@ __device__ __forceinline__ int lpt_units(const DecodeParams& p, int* scratch, in
     int* order = start + nb;   // sequence at each rank
     for (int i = tid; i < nb; i += blockDim.x) hist[i] = 0;
     for (int i = tid; i < S; i += blockDim.x) {
-        int L = __ldg(p.context_lens + i);
+        int L = ld_global(p.context_lens + i);
         L = L < 0 ? 0 : min(L, cap);
         len[i] = (streamed_tokens(p, L) + 15) >> 4;
     }
@@ -581,9 +581,9 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, con
     const bool spec = p.part_tokens == 0 && p.prefix_tokens == 0 && p.cpb_log2 >= 0;
     int spec_blk = 0;
     if (spec && warp == C::NCW && (lane >> p.cpb_log2) < p.max_blocks_per_seq)
-        spec_blk = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + (lane >> p.cpb_log2));
+        spec_blk = ld_global(p.block_tables + (size_t)s * p.max_blocks_per_seq + (lane >> p.cpb_log2));
     // context length, clamped to what the table (and the split-K grid) can address
-    int L = __ldg(p.context_lens + s);
+    int L = ld_global(p.context_lens + s);
     int cap = table_row_tokens(p.max_blocks_per_seq, p.cpb_log2);  // tokens the table row addresses
     if (p.part_tokens > 0 && p.prefix_tokens + p.cover_parts * p.part_tokens < cap)
         cap = p.prefix_tokens + p.cover_parts * p.part_tokens;
@@ -630,7 +630,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, con
             int my = p.num_blocks;  // outside the tensor map: TMA fills zeros
             const int e = half8 ? 2 * (blk0 + b0) + lane : (blk0 + b0 + lane) >> p.cpb_log2;
             if (half8 ? (lane < 2 * nb && 8 * e < L) : (lane < nb)) {
-                my = (spec && b0 == 0) ? spec_blk : __ldg(bt + e);
+                my = (spec && b0 == 0) ? spec_blk : ld_global(bt + e);
                 if (my < 0 || my >= p.num_blocks) {
                     flag_error(p.err, PA_DEVERR_BLOCK);
                     my = p.num_blocks;
@@ -702,7 +702,7 @@ decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, con
         for (int h = 0; h < G; ++h)
 #pragma unroll
             for (int j = 0; j < C::CPL; ++j) {
-                uint4 raw = chunk_col[j] < p.hd ? ldg_nc_128(qrow + h * p.hd + chunk_col[j]) : make_uint4(0u, 0u, 0u, 0u);
+                uint4 raw = chunk_col[j] < p.hd ? ld_stream(qrow + h * p.hd + chunk_col[j]) : make_uint4(0u, 0u, 0u, 0u);
                 unpack8<BF16>(raw, qf[h][j]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) qf[h][j][e] *= p.qk_scale_log2;
@@ -877,7 +877,7 @@ decode_kernel_persistent(const DecodeParams p, const __grid_constant__ CUtensorM
         Unit u;
         u.s = list[3 * k];
         u.g = list[3 * k + 1];
-        int L = __ldg(p.context_lens + u.s);
+        int L = ld_global(p.context_lens + u.s);
         if (L < 0 || L > cap) {
             if (report && u.g == 0 && threadIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
             L = L < 0 ? 0 : cap;
@@ -912,7 +912,7 @@ decode_kernel_persistent(const DecodeParams p, const __grid_constant__ CUtensorM
                 int my = p.num_blocks;  // outside the tensor map: TMA fills zeros
                 const int e = half8 ? 2 * (c0 + b0) + lane : (c0 + b0 + lane) >> p.cpb_log2;
                 if (half8 ? (lane < 2 * nb && 8 * e < u.L) : (lane < nb)) {
-                    my = __ldg(bt + e);
+                    my = ld_global(bt + e);
                     if (my < 0 || my >= p.num_blocks) {
                         flag_error(p.err, PA_DEVERR_BLOCK);
                         my = p.num_blocks;
@@ -1013,18 +1013,18 @@ decode_kernel_persistent(const DecodeParams p, const __grid_constant__ CUtensorM
             }
             if (r == 0) {
                 // the slot must be that of the context's last token, the one the last chunk holds
-                int L = __ldg(p.context_lens + s);
+                int L = ld_global(p.context_lens + s);
                 L = L < 0 ? 0 : min(L, cap);
                 const int e = L > 0 ? (L - 1) / bs : 0;
                 const long long want = L > 0 && e < p.max_blocks_per_seq
-                                           ? (long long)__ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + e) * bs + (L - 1) % bs
+                                           ? (long long)ld_global(p.block_tables + (size_t)s * p.max_blocks_per_seq + e) * bs + (L - 1) % bs
                                            : -1;
                 if (slot != want) flag_error(p.err, PA_DEVERR_SLOT);
             }
             const size_t from = (size_t)s * p.row_vecs + (size_t)g * hv + c;
             const size_t to = (size_t)slot * p.row_vecs + (size_t)g * hv + c;
-            if (kv == 0) p.k_cache_w[to] = __ldg(p.new_k + from);
-            else p.v_cache_w[to] = __ldg(p.new_v + from);
+            if (kv == 0) p.k_cache_w[to] = ld_global(p.new_k + from);
+            else p.v_cache_w[to] = ld_global(p.new_v + from);
         }
         asm volatile("fence.proxy.async.global;" ::: "memory");
         __syncwarp();
@@ -1050,7 +1050,7 @@ decode_kernel_persistent(const DecodeParams p, const __grid_constant__ CUtensorM
             for (int h = 0; h < G; ++h)
 #pragma unroll
                 for (int j = 0; j < C::CPL; ++j) {
-                    uint4 raw = chunk_col[j] < p.hd ? ldg_nc_128(qrow + h * p.hd + chunk_col[j])
+                    uint4 raw = chunk_col[j] < p.hd ? ld_stream(qrow + h * p.hd + chunk_col[j])
                                                     : make_uint4(0u, 0u, 0u, 0u);
                     unpack8<BF16>(raw, qf[h][j]);
 #pragma unroll
@@ -1167,7 +1167,7 @@ __device__ __forceinline__ void dyn_unit_order(const DecodeParams& p, int cap, i
     int* start = hist + nb;
     for (int i = tid; i < nb; i += blockDim.x) hist[i] = 0;
     for (int i = tid; i < S; i += blockDim.x) {
-        int L = __ldg(p.context_lens + i);
+        int L = ld_global(p.context_lens + i);
         if (L < 0 || L > cap) {
             if (blockIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
             L = L < 0 ? 0 : cap;
@@ -1211,7 +1211,7 @@ __device__ __forceinline__ void dyn_unit_order(const DecodeParams& p, int cap, i
 __device__ __forceinline__ void dyn_piece_counts(const DecodeParams& p, int cap, int* len, int* cumA, int* cumB) {
     const int S = p.num_seqs, tid = threadIdx.x, lane = tid & 31;
     for (int i = tid; i < S; i += blockDim.x) {
-        int L = __ldg(p.context_lens + i);
+        int L = ld_global(p.context_lens + i);
         if (L < 0 || L > cap) {
             if (blockIdx.x == 0) flag_error(p.err, PA_DEVERR_LENGTH);
             L = L < 0 ? 0 : cap;
@@ -1314,7 +1314,7 @@ decode_kernel_dyn(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
     bool fixed = false;  // the counter is not known to start at zero: CTA b takes items b, b + grid, ...
     if (warp == C::NCW && lane == 0) {
         first = atomicAdd(p.dyn_counter, 1);
-        if (p.dyn_tag) fixed = __ldcg(p.dyn_tag) != kDynTag;
+        if (p.dyn_tag) fixed = ld_l2(p.dyn_tag) != kDynTag;
     }
     {
         long long lines = ((long long)p.num_seqs * p.max_blocks_per_seq * 4 + 127) / 128;
@@ -1386,7 +1386,7 @@ decode_kernel_dyn(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                 s = sg / p.n_kv_heads;
                 g = sg - s * p.n_kv_heads;
                 if (p.dyn_units) s = o_order[s];  // units longest first
-                int L = __ldg(p.context_lens + s);
+                int L = ld_global(p.context_lens + s);
                 if (L < 0 || L > cap) {
                     if (piece == 0 && g == 0 && lane == 0) flag_error(p.err, PA_DEVERR_LENGTH);
                     L = L < 0 ? 0 : cap;
@@ -1428,7 +1428,7 @@ decode_kernel_dyn(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
             long long nslot = -1;
             uint4 nrow[2];
             if (row_item) {
-                nslot = __ldg(p.new_slots + s);
+                nslot = ld_global(p.new_slots + s);
                 if (nslot >= p.n_slots) {
                     if (lane == 0) flag_error(p.err, PA_DEVERR_SLOT);
                     nslot = -1;
@@ -1437,7 +1437,7 @@ decode_kernel_dyn(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
                     for (int i2 = 0; i2 < 2; ++i2) {
                         const int c = lane + 32 * i2, kv = c / hv, cc = c - kv * hv;
-                        if (c < 2 * hv) nrow[i2] = __ldg((kv ? p.new_v : p.new_k) + (size_t)s * p.row_vecs + (size_t)g * hv + cc);
+                        if (c < 2 * hv) nrow[i2] = ld_global((kv ? p.new_v : p.new_k) + (size_t)s * p.row_vecs + (size_t)g * hv + cc);
                     }
                 }
             }
@@ -1466,7 +1466,7 @@ decode_kernel_dyn(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                 int my = p.num_blocks;  // outside the tensor map: TMA fills zeros
                 const int e = half8 ? 2 * (blk0 + b0) + lane : (blk0 + b0 + lane) >> p.cpb_log2;
                 if (half8 ? (lane < 2 * nb && 8 * e < t_end) : (lane < nb)) {
-                    my = __ldg(bt + e);
+                    my = ld_global(bt + e);
                     if (my < 0 || my >= p.num_blocks) {
                         flag_error(p.err, PA_DEVERR_BLOCK);
                         my = p.num_blocks;
@@ -1569,7 +1569,7 @@ decode_kernel_dyn(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
             for (int h = 0; h < G; ++h)
 #pragma unroll
                 for (int j = 0; j < C::CPL; ++j) {
-                    uint4 raw = chunk_col[j] < p.hd ? ldg_nc_128(qrow + h * p.hd + chunk_col[j]) : make_uint4(0u, 0u, 0u, 0u);
+                    uint4 raw = chunk_col[j] < p.hd ? ld_stream(qrow + h * p.hd + chunk_col[j]) : make_uint4(0u, 0u, 0u, 0u);
                     unpack8<BF16>(raw, qf[h][j]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) qf[h][j][e] *= p.qk_scale_log2;
@@ -1722,7 +1722,7 @@ __global__ void __launch_bounds__(256, 2) splitk_merge_kernel(const DecodeParams
     const int row = blockIdx.x * (blockDim.x >> 5) + warp;  // s * Hq + h
     if (row >= p.num_seqs * p.n_q_heads) return;
     const int s = row / p.n_q_heads;
-    int L = __ldg(p.context_lens + s);
+    int L = ld_global(p.context_lens + s);
     const int cap = min(table_row_tokens(p.max_blocks_per_seq, p.cpb_log2), p.prefix_tokens + p.cover_parts * p.part_tokens);
     L = L < 0 ? 0 : (L > cap ? cap : L);
     const int n_parts = pieces_of(p, L);

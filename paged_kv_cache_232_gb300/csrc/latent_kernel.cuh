@@ -203,15 +203,15 @@ struct Chunk {
 __device__ __forceinline__ Chunk load_chunk(const LatentParams& p, int c) {
     Chunk k;
     const int cap = p.max_blocks_per_seq * p.block_size;
-    k.kv_len = __ldg(p.kv_lens + c);
+    k.kv_len = ld_global(p.kv_lens + c);
     if (p.q_loc == nullptr) {
         k.q0 = c;
         k.q_len = 1;
         k.bad = k.kv_len < 0 || k.kv_len > cap;
         if (k.bad) k.kv_len = 0;
     } else {
-        k.q0 = __ldg(p.q_loc + c);
-        const int q1 = __ldg(p.q_loc + c + 1);
+        k.q0 = ld_global(p.q_loc + c);
+        const int q1 = ld_global(p.q_loc + c + 1);
         k.q_len = q1 - k.q0;
         k.bad = k.q0 < 0 || q1 < k.q0 || q1 > p.total_q || k.q_len > p.max_q_len || k.kv_len < k.q_len ||
                 k.kv_len > cap;
@@ -699,7 +699,7 @@ latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC, con
             auto entry = [&](int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
                 const int t = tile * TK + lane * br;
                 if (lane >= nbox || t >= g.keys) return p.num_blocks;
-                const int e = __ldg(bt + (t >> p.block_log2));
+                const int e = ld_global(bt + (t >> p.block_log2));
                 if (e < 0 || e >= p.num_blocks) {
                     flag_error(p.err, PA_DEVERR_BLOCK);
                     return p.num_blocks;
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(lat::merge_threads(NR)) latent_merge_kernel(co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // the next kernel of the step may start its launch; it waits for this grid before reading anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int4 cut[2] = {__ldcg(p.desc + range), __ldcg(p.desc + gridDim.x + range)};
+    const int4 cut[2] = {ld_l2(p.desc + range), ld_l2(p.desc + gridDim.x + range)};
     const int4 few = cut[0].x <= kFew ? cut[0] : make_int4(0, 0, 0, 0);
 #pragma unroll 1
     for (int row = (int)blockIdx.y * 16 + warp; row < min(few.y, ((int)blockIdx.y + 1) * 16); row += NW) {
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(lat::merge_threads(NR)) latent_merge_kernel(co
         float m = -INFINITY, l = 0.f;
         if (lane < u.x) {
             const int slot = 2 * (range + lane) + (lane == 0);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot * NR + row);
+            const float2 ml = ld_l2(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot * NR + row);
             m = ml.x;
             l = ml.y;
         }
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(lat::merge_threads(NR)) latent_merge_kernel(co
                 const int slot = 2 * (range + k0 + k) + (k0 + k == 0);
 #pragma unroll
                 for (int c = 0; c < CV; ++c)
-                    v[k][c] = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * NR + row) * DL) + lane + 32 * c);
+                    v[k][c] = ld_l2(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot * NR + row) * DL) + lane + 32 * c);
             }
         };
         fetch4(0);  // in flight before their weights are known
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(lat::merge_threads(NR)) latent_merge_kernel(co
         for (int row = (range - b) * (int)gridDim.y + (int)blockIdx.y; row < u.y; row += parts * (int)gridDim.y) {
             float m = -INFINITY, l = 0.f;
             if (tid < parts) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot_at(tid) * NR + row);
+                const float2 ml = ld_l2(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot_at(tid) * NR + row);
                 m = ml.x;
                 l = ml.y;
             }
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(lat::merge_threads(NR)) latent_merge_kernel(co
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
             for (int k = gidx; k < parts; k += KG) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_at(k) * NR + row) * DL) + t);
+                const float4 v = ld_l2(reinterpret_cast<const float4*>(p.part_o + ((size_t)slot_at(k) * NR + row) * DL) + t);
                 const float f = wt[k];
                 if (f != 0.f) {
                     a.x = fmaf(v.x, f, a.x);

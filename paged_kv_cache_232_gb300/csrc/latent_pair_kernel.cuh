@@ -505,7 +505,7 @@ latent_pair_kernel(const LatentParams p, const __grid_constant__ CUtensorMap tmC
             auto entry = [&](int tile) {
                 const int t = tile * TK + half * 64 + lane * br;
                 if (lane >= nbox || t >= g.keys) return p.num_blocks;
-                const int e = __ldg(bt + (t >> p.block_log2));
+                const int e = ld_global(bt + (t >> p.block_log2));
                 if (e < 0 || e >= p.num_blocks) {
                     flag_error(p.err, PA_DEVERR_BLOCK);
                     return p.num_blocks;

@@ -164,6 +164,68 @@ __device__ __forceinline__ uint4 ldg_nc_128(const void* p) {
     return v;
 }
 
+// Loads of a kernel that waits for the one before it (griddepcontrol.wait).  It is resident while that one still writes, so
+// what it reads changes while it runs: the non-coherent path (__ldg, ld.global.nc) is not defined for such data.  Volatile, with
+// a clobber: none of them is moved ahead of the wait.  (Decode, chunks, latent decode and trees
+// take what they took, within 0.5 %: 256 x 1K tokens of decode 169..171 us both.)
+__device__ __forceinline__ uint32_t ld_global(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int32_t ld_global(const int32_t* p) {
+    return (int32_t)ld_global(reinterpret_cast<const uint32_t*>(p));
+}
+__device__ __forceinline__ int64_t ld_global(const int64_t* p) {
+    int64_t v;
+    asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_global(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+// data read once: not kept in L1
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+// from L2: what other blocks of the same grid write, and partials that are read once
+__device__ __forceinline__ uint32_t ld_l2(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long ld_l2(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.global.cg.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int32_t ld_l2(const int32_t* p) { return (int32_t)ld_l2(reinterpret_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ uint4 ld_l2(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int4 ld_l2(const int4* p) {
+    const uint4 v = ld_l2(reinterpret_cast<const uint4*>(p));
+    return make_int4((int)v.x, (int)v.y, (int)v.z, (int)v.w);
+}
+__device__ __forceinline__ float4 ld_l2(const float4* p) {
+    const uint4 v = ld_l2(reinterpret_cast<const uint4*>(p));
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ float2 ld_l2(const float2* p) {
+    float2 v;
+    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
+}
+
 // ---- 16-bit float formats ------------------------------------------------------------
 
 template <bool BF16>

@@ -27,21 +27,11 @@ __device__ __forceinline__ uint4* plane_of(const Planes& c, int plane) {
     return plane < c.layers ? c.k + plane * c.plane_vecs : c.v + (plane - c.layers) * c.plane_vecs;
 }
 
-// (not the read-only path: the same call writes other pages of this array)
-__device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-
 constexpr int kCopyThreads = 256, kCopyUnroll = 8;
 
 // Pages pairs[i][0] -> pairs[i][1] of every plane.  An item is a segment of one page of one plane, worked by
 // `lanes` threads (a power of two) with kCopyUnroll chunks each in flight.
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Planes c, const int32_t* __restrict__ pairs, unsigned items,
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Planes c, const int32_t* pairs, unsigned items,
                                                                  unsigned segs, int seg_vecs, int page_vecs, int lanes_log2,
                                                                  unsigned* err) {
     constexpr int U = kCopyUnroll;
@@ -52,7 +42,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Planes c
     for (unsigned it = blockIdx.x * per_block + (threadIdx.x >> lanes_log2); it < items; it += gridDim.x * per_block) {
         const unsigned rest = it / segs, seg = it - rest * segs;
         const unsigned pair = rest / (unsigned)c.planes, plane = rest - pair * (unsigned)c.planes;
-        const int src = __ldg(pairs + 2 * (size_t)pair), dst = __ldg(pairs + 2 * (size_t)pair + 1);
+        const int src = ld_global(pairs + 2 * (size_t)pair), dst = ld_global(pairs + 2 * (size_t)pair + 1);
         if (src == -1 || dst == -1) continue;
         if (src < 0 || src >= c.num_blocks || dst < 0 || dst >= c.num_blocks) {
             if (lane == 0) flag_error(err, PA_DEVERR_BLOCK);
@@ -66,7 +56,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const Planes c
             uint4 x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (e + u * lanes < n) x[u] = ldg_stream(s + e + u * lanes);
+                if (e + u * lanes < n) x[u] = ld_stream(s + e + u * lanes);
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (e + u * lanes < n) d[e + u * lanes] = x[u];
@@ -95,8 +85,8 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     const int s = blockIdx.x, tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int n = __ldg(p.query_start_loc + s + 1) - __ldg(p.query_start_loc + s), kv_len = __ldg(p.seq_lens + s);
-    const int acc = __ldg(p.num_accepted + s), ctx = kv_len - n;
+    const int n = ld_global(p.query_start_loc + s + 1) - ld_global(p.query_start_loc + s), kv_len = ld_global(p.seq_lens + s);
+    const int acc = ld_global(p.num_accepted + s), ctx = kv_len - n;
     const int cap = p.max_blocks_per_seq * p.c.block_size;
     const bool bad_len = n < 0 || kv_len < n || kv_len > cap;
     const int32_t* path = p.path + (size_t)s * p.max_path;
@@ -104,7 +94,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     if (!bad && !bad_len) {
         bool mine = false;
         for (int i = tid; i < acc; i += kCommitThreads) {
-            const int t = __ldg(path + i), before = i > 0 ? __ldg(path + i - 1) : -1;
+            const int t = ld_global(path + i), before = i > 0 ? ld_global(path + i - 1) : -1;
             mine = mine || t <= before || t >= n;
         }
         bad = __syncthreads_or(mine);
@@ -124,10 +114,10 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
         const int rows = min(kCommitRows, acc - i0);
         __syncthreads();
         if (tid < rows) {
-            const int a = ctx + __ldg(path + i0 + tid), b = ctx + i0 + tid;
+            const int a = ctx + ld_global(path + i0 + tid), b = ctx + i0 + tid;
             int64_t f = -1, t = -1;
             if (a != b) {
-                const int pa_ = __ldg(bt + a / bs), pb = __ldg(bt + b / bs);
+                const int pa_ = ld_global(bt + a / bs), pb = ld_global(bt + b / bs);
                 if (pa_ < 0 || pa_ >= p.c.num_blocks || pb < 0 || pb >= p.c.num_blocks) {
                     flag_error(p.err, PA_DEVERR_BLOCK);
                 } else {
@@ -146,7 +136,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
                 uint4 x[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (i + u < rows && from[i + u] >= 0) x[u] = ldg_stream(base + from[i + u]);
+                    if (i + u < rows && from[i + u] >= 0) x[u] = ld_stream(base + from[i + u]);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (i + u < rows && from[i + u] >= 0) base[to[i + u]] = x[u];
@@ -164,7 +154,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
 constexpr int kForkThreads = 512, kForkSeqs = 8;
 
 __global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(int32_t* block_tables, int mb, int32_t* seq_lens,
-                                                                 const int32_t* __restrict__ parents, int num_seqs,
+                                                                 const int32_t* parents, int num_seqs,
                                                                  int32_t* ref_counts, int block_size, int num_blocks, unsigned* err) {
     constexpr int U = 4;
     __shared__ int parent_s[kForkSeqs], len_s[kForkSeqs];
@@ -173,10 +163,10 @@ __global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(int32_t* block
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < kForkSeqs) {
         const int s = blockIdx.x * kForkSeqs + tid;
-        int par = s < num_seqs ? __ldg(parents + s) : -1, len = 0;
+        int par = s < num_seqs ? ld_global(parents + s) : -1, len = 0;
         if (par != -1) {
             const bool known = par >= 0 && par < num_seqs;
-            if (!known || __ldg(parents + par) != -1 || seq_lens[s] != 0) {
+            if (!known || ld_global(parents + par) != -1 || seq_lens[s] != 0) {
                 flag_error(err, PA_DEVERR_FORK);
                 par = -1;
             } else {
@@ -267,7 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(const ResizeP
         ResizePlan r{-1, -1, 0, 0};
         int demand = 0;
         if (s < p.num_seqs && top >= 0) {
-            const int want = __ldg(p.new_lens + s), have = p.seq_lens[s];
+            const int want = ld_global(p.new_lens + s), have = p.seq_lens[s];
             if (want < -1 || want > cap || have < 0 || have > cap) {
                 flag_error(p.err, PA_DEVERR_LENGTH);
             } else if (want != -1 && want != have) {
@@ -342,7 +332,7 @@ __device__ __forceinline__ int release_page(const ResizeParams& p, int id) {
 // Sequences to their lengths, by the threads of `blocks` blocks.
 __device__ __forceinline__ void write_lengths(const ResizeParams& p, int block, int blocks) {
     for (int i = block * kApplyThreads + (int)threadIdx.x; i < p.num_seqs; i += blocks * kApplyThreads)
-        if (p.plan[i].start >= 0) p.seq_lens[i] = __ldg(p.new_lens + i);
+        if (p.plan[i].start >= 0) p.seq_lens[i] = ld_global(p.new_lens + i);
 }
 
 __device__ __forceinline__ void write_count(const ResizeParams& p, int count) {
@@ -359,7 +349,7 @@ __device__ __forceinline__ void push_pages(const ResizeParams& p, int w0, int at
     __shared__ int warp_sum[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, words = (p.c.num_blocks + 31) / 32;
 #pragma unroll
-    for (int k = tid; k < kScanWords; k += kApplyThreads) words_s[k] = w0 + k < words ? __ldcg(p.bits + w0 + k) : 0u;
+    for (int k = tid; k < kScanWords; k += kApplyThreads) words_s[k] = w0 + k < words ? ld_l2(p.bits + w0 + k) : 0u;
     __syncthreads();
     const unsigned* run = words_s + warp * RUN;
     int mine = 0;
@@ -424,7 +414,7 @@ __global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const Resiz
                         uint4 x[U];
 #pragma unroll
                         for (int u = 0; u < U; ++u)
-                            if (e + u * kApplyThreads < n) x[u] = ldg_stream(from + e + u * kApplyThreads);
+                            if (e + u * kApplyThreads < n) x[u] = ld_stream(from + e + u * kApplyThreads);
 #pragma unroll
                         for (int u = 0; u < U; ++u)
                             if (e + u * kApplyThreads < n) to[e + u * kApplyThreads] = x[u];
@@ -457,7 +447,7 @@ __global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const Resiz
     __threadfence();
     write_lengths(p, 0, 1);
     if (top < 0) return;
-    const int left = top - p.head->taken, freed = (int)__ldcg(&p.head->freed);
+    const int left = top - p.head->taken, freed = (int)ld_l2(&p.head->freed);
     if (tid == 0) write_count(p, left + freed);
     if (freed > 0) push_pages(p, 0, left);
 }
@@ -479,7 +469,7 @@ __global__ void __launch_bounds__(kApplyThreads) resize_push_kernel(const Resize
     const uint4* bits = reinterpret_cast<const uint4*>(p.bits);
 #pragma unroll 4
     for (int w = tid; w < b * (kScanWords / 4); w += kApplyThreads) {
-        const uint4 v = __ldcg(bits + w);
+        const uint4 v = ld_l2(bits + w);
         before += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
     }
     __syncthreads();

@@ -119,8 +119,8 @@ __device__ __forceinline__ int lpt_unit(const PrefillParams& p, unsigned char* s
     int* hist = kvl + C;
     int* sel = hist + ncost;  // [0] bucket, [1] rank within the bucket, [2] chosen unit, [3..] warp counts
     const int tid = threadIdx.x, nt = blockDim.x;
-    for (int i = tid; i <= C; i += nt) qsl[i] = __ldg(p.query_start_loc + i);
-    for (int i = tid; i < C; i += nt) kvl[i] = __ldg(p.seq_lens + i);
+    for (int i = tid; i <= C; i += nt) qsl[i] = ld_global(p.query_start_loc + i);
+    for (int i = tid; i < C; i += nt) kvl[i] = ld_global(p.seq_lens + i);
     for (int i = tid; i < ncost; i += nt) hist[i] = 0;
     __syncthreads();
     for (int u = tid; u < U; u += nt) {
@@ -329,7 +329,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmK, c
         __syncthreads();
         const int s0 = unit * NQ * TQ, s1 = min(s0 + NQ * TQ, q_len);
         int mine = 0;
-        for (int s = s0 + (int)threadIdx.x; s < s1; s += (int)blockDim.x) mine = max(mine, __ldg(p.context_lens + s));
+        for (int s = s0 + (int)threadIdx.x; s < s1; s += (int)blockDim.x) mine = max(mine, ld_global(p.context_lens + s));
         mine = __reduce_max_sync(0xffffffffu, mine);
         if (lane == 0 && mine > 0) atomicMax(lmax, mine);
         __syncthreads();
@@ -347,9 +347,9 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmK, c
 
         // the CTA-order step left query_start_loc and seq_lens in shared memory
         const int* sched = reinterpret_cast<const int*>(smem + L::SCHED_OFF);
-        q0 = p.lpt ? sched[c] : __ldg(p.query_start_loc + c);
-        q_len = (p.lpt ? sched[c + 1] : __ldg(p.query_start_loc + c + 1)) - q0;
-        kv_len = p.lpt ? sched[p.num_chunks + 1 + c] : __ldg(p.seq_lens + c);
+        q0 = p.lpt ? sched[c] : ld_global(p.query_start_loc + c);
+        q_len = (p.lpt ? sched[c + 1] : ld_global(p.query_start_loc + c + 1)) - q0;
+        kv_len = p.lpt ? sched[p.num_chunks + 1 + c] : ld_global(p.seq_lens + c);
         // a chunk longer than max_q_len (which sized the grid) would leave rows past the grid unwritten:
         // it is flagged and skipped like the other bad lengths
         if (q_len < 0 || q_len > p.max_q_len || kv_len < q_len ||
@@ -422,7 +422,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmK, c
         const bool row_valid = r >= 0 && jr < q_len;
         int lim, lim_min;  // keys <= lim are visible to this row; lim_min: smallest limit of the warp's rows
         if constexpr (PREFIX) {
-            const int Ls = row_valid ? max(__ldg(p.context_lens + jr), 0) : 0;
+            const int Ls = row_valid ? max(ld_global(p.context_lens + jr), 0) : 0;
             lim = min(Ls, kv_len) - 1;
             lim_min = __reduce_min_sync(0xffffffffu, lim);
         } else {
@@ -447,7 +447,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmK, c
                     const int tok = jt0 + R / G;
                     const uint16_t* src = static_cast<const uint16_t*>(p.q) +
                                           ((size_t)(q0 + tok) * p.n_q_heads + g * G + R % G) * p.hd + ch * 8;
-                    v[i] = (tok < q_len && ch * 8 < p.hd) ? ldg_nc_128(src) : make_uint4(0u, 0u, 0u, 0u);
+                    v[i] = (tok < q_len && ch * 8 < p.hd) ? ld_stream(src) : make_uint4(0u, 0u, 0u, 0u);
                 }
 #pragma unroll
                 for (int i = 0; i < PASS; ++i) {
@@ -575,7 +575,7 @@ prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmK, c
             const int ci = kc0 + i * CHUNKS;  // the stage's first chunk
             const int e = half8 ? 2 * ci + lane : (ci + lane % CHUNKS) >> p.cpb_log2;
             if (half8 ? (lane < 2 * CHUNKS && 8 * e < kv_len) : (lane < CHUNKS && ci + lane < nblk_seq)) {
-                my = __ldg(bt + e);
+                my = ld_global(bt + e);
                 if (my < 0 || my >= p.num_blocks) {
                     if (kv == 0) flag_error(p.err, PA_DEVERR_BLOCK);
                     my = p.num_blocks;

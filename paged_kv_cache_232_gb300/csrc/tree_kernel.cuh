@@ -265,9 +265,9 @@ struct Seq {
 };
 __device__ __forceinline__ Seq load_seq(const TreeParams& p, int s) {
     Seq k;
-    k.kv_len = __ldg(p.kv_lens + s);
-    k.q0 = __ldg(p.q_loc + s);
-    const int q1 = __ldg(p.q_loc + s + 1);
+    k.kv_len = ld_global(p.kv_lens + s);
+    k.q0 = ld_global(p.q_loc + s);
+    const int q1 = ld_global(p.q_loc + s + 1);
     k.n = q1 - k.q0;
     k.bad = k.q0 < 0 || q1 < k.q0 || q1 > p.total_q || k.n > p.max_q_len || k.kv_len < k.n ||
             k.kv_len > p.max_blocks_per_seq * p.block_size;
@@ -494,7 +494,7 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t* row, int words, int k
     uint32_t w = 0;
     if (left > 0) {
         const int i = b >> 5;
-        const uint32_t lo = i < words ? __ldg(row + i) : 0u, hi = (b & 31) && i + 1 < words ? __ldg(row + i + 1) : 0u;
+        const uint32_t lo = i < words ? ld_global(row + i) : 0u, hi = (b & 31) && i + 1 < words ? ld_global(row + i + 1) : 0u;
         w = __funnelshift_r(lo, hi, b & 31);
         if (left < 32) w &= (1u << left) - 1u;
     }
@@ -976,7 +976,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         auto entry = [&](const Segment& g, int tile) {  // block id of box `lane` of the tile; past the keys or invalid: zero fill
             const int t = tile * BN + lane * br;
             if (lane >= nbox || t >= g.keys) return p.num_blocks;
-            const int e = __ldg(p.block_tables + (size_t)g.s * p.max_blocks_per_seq + (t >> p.block_log2));
+            const int e = ld_global(p.block_tables + (size_t)g.s * p.max_blocks_per_seq + (t >> p.block_log2));
             if (e < 0 || e >= p.num_blocks) {
                 flag_error(p.err, PA_DEVERR_BLOCK);
                 return p.num_blocks;
@@ -1154,7 +1154,7 @@ __global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const T
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // the next kernel of the step may start its launch; it waits for this grid before reading anything
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int4 cut[2] = {__ldcg(p.desc + cta), __ldcg(p.desc + gridDim.x + cta)};
+    const int4 cut[2] = {ld_l2(p.desc + cta), ld_l2(p.desc + gridDim.x + cta)};
     auto store = [&](int row0, int row, int c4, float4 a, float inv) {
         const int tok = (int)(((uint32_t)row * (uint32_t)p.g_magic) >> 16);
         if (4 * c4 < p.hd)
@@ -1175,14 +1175,14 @@ __global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const T
         auto slot_at = [&](int k) { return (size_t)(2 * (cta + k * p.group) + (k == 0)); };
         float2 ml[kFew];
 #pragma unroll
-        for (int k = 0; k < kFew; ++k) ml[k] = k < u.x ? __ldcg(p.part_ml + slot_at(k) * NR + row16) : make_float2(-INFINITY, 0.f);
+        for (int k = 0; k < kFew; ++k) ml[k] = k < u.x ? ld_l2(p.part_ml + slot_at(k) * NR + row16) : make_float2(-INFINITY, 0.f);
         float4 a[V] = {}, x[4][V];
         auto fetch = [&](int k0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (k0 + k < u.x)
 #pragma unroll
-                    for (int v = 0; v < V; ++v) x[k][v] = __ldcg(p.part_o + (slot_at(k0 + k) * (D / 4) + c + v) * NR + row16);
+                    for (int v = 0; v < V; ++v) x[k][v] = ld_l2(p.part_o + (slot_at(k0 + k) * (D / 4) + c + v) * NR + row16);
         };
         fetch(0);
         float mx = -INFINITY, l = 0.f;
@@ -1215,7 +1215,7 @@ __global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const T
         auto slot_at = [&](int k) { return (size_t)(2 * (b + k * p.group) + (k == 0)); };
         const int mine = (cta - b) / p.group;
         for (int row = mine * (int)gridDim.y + (int)blockIdx.y; row < u.y; row += parts * (int)gridDim.y) {
-            const float2 ml = tid < parts ? __ldcg(p.part_ml + slot_at(tid) * NR + row) : make_float2(-INFINITY, 0.f);
+            const float2 ml = tid < parts ? ld_l2(p.part_ml + slot_at(tid) * NR + row) : make_float2(-INFINITY, 0.f);
             const float m = ml.x;
             float mx = m;
 #pragma unroll
@@ -1237,7 +1237,7 @@ __global__ void __launch_bounds__(tree::MERGE_THREADS) tree_merge_kernel(const T
                 const float f = wt[k];
 #pragma unroll
                 for (int v = 0; v < V4; ++v)
-                    if (lane + 32 * v < D / 4) add(a[v], __ldcg(p.part_o + (slot_at(k) * (D / 4) + lane + 32 * v) * NR + row), f);
+                    if (lane + 32 * v < D / 4) add(a[v], ld_l2(p.part_o + (slot_at(k) * (D / 4) + lane + 32 * v) * NR + row), f);
             }
 #pragma unroll
             for (int v = 0; v < V4; ++v)

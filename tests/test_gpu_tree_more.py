@@ -1,8 +1,13 @@
-"""pa_tree_decode where the largest tree is far above the batch's."""
+"""pa_tree_decode where the largest tree is far above the batch's, and the calls of a verification step back to back on
+the device, each reading what the one before has just written."""
+import random
+
 import pytest
+import torch
 
 import paged_kv_cache_232_gb300 as pa
 from test_gpu_tree import Batch
+from tree_testutil import gen, randn, tree_sees, words_of
 
 pytestmark = pytest.mark.gpu
 
@@ -18,3 +23,72 @@ def test_largest_tree_far_above_the_batch(hq, hkv, d, ns, most):
     out = b.run()
     assert pa.pa_device_errors(clear=True) == 0
     b.check(out)
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(4, 2, 128, 16), (8, 8, 64, 32), (16, 4, 128, 8)])
+def test_each_call_reads_what_the_one_before_wrote(hq, hkv, d, bs):
+    """Room for the drafted tokens, attention, the accepted path, the rest given back, a fork, decode and a causal chunk, without
+    another kernel between them: the same as with a wait after each call."""
+    dt, S, mb = torch.bfloat16, 40, 64 * 16 // bs
+    nb = S * mb + 5
+    g, rng = gen(bs + d), random.Random(bs)
+    i32 = lambda v: torch.tensor(v, device="cuda", dtype=torch.int32)
+    kc, vc = (randn(g, (nb, bs, hkv, d), dt) for _ in range(2))
+    free0 = torch.randperm(nb, generator=g, device="cuda").to(torch.int32)
+    ws = torch.empty(pa.pa_resize_workspace_size(S, nb), device="cuda", dtype=torch.uint8)
+    most, parents = 12, [-1] * S
+    for s in range(1, S, 4):          # every fourth sequence is ended and becomes a fork of the one before
+        parents[s] = s - 1
+
+    def make(turn):
+        """A step's inputs: lengths, trees, paths."""
+        ns = [rng.randint(1, most) for _ in range(S)]
+        ctx = [rng.randint(1, 900) for _ in range(S)]
+        sees = [tree_sees(rng, n) for n in ns]
+        paths = [sorted(rng.sample(range(n), rng.randint(1, n))) for n in ns]
+        loc = i32([sum(ns[:s]) for s in range(S + 1)])
+        return dict(ctx=i32(ctx), grown=i32([c + n for c, n in zip(ctx, ns)]), loc=loc,
+                    mask=torch.tensor([w for x in sees for w in words_of(x, 1)], device="cuda"),
+                    path=i32([p + [-1] * (most - len(p)) for p in paths]), acc=i32([len(p) for p in paths]),
+                    ended=i32([0 if p >= 0 else -1 for p in parents]), parents=i32(parents),
+                    q=randn(g, (sum(ns), hq, d), dt), dq=randn(g, (S, hq, d), dt),
+                    none=torch.zeros(S, device="cuda", dtype=torch.int32))
+
+    tws = torch.empty(pa.pa_tree_workspace_size(hq, hkv, d, most), device="cuda", dtype=torch.uint8)
+    dws = torch.empty(max(16, pa.pa_decode_workspace_size(S, hq, d, mb * bs, 0)), device="cuda", dtype=torch.uint8)
+
+    def step(x, wait):
+        st = dict(k=kc.clone(), v=vc.clone(), bt=torch.full((S, mb), -1, device="cuda", dtype=torch.int32),
+                  lens=torch.zeros(S, device="cuda", dtype=torch.int32), ref=torch.zeros(nb, device="cuda", dtype=torch.int32),
+                  free=free0.clone(), count=i32([nb]), new=torch.zeros(S, device="cuda", dtype=torch.int32),
+                  out=torch.zeros_like(x["q"]), dec=torch.zeros_like(x["dq"]), chunk=torch.zeros_like(x["dq"]))
+        one = torch.arange(S + 1, device="cuda", dtype=torch.int32)
+
+        def resize(new):
+            pa.pa_resize_pages(st["k"], st["v"], st["bt"], st["lens"], new, st["ref"], st["free"], st["count"], ws)
+
+        calls = [lambda: resize(x["ctx"]), lambda: resize(x["grown"]),
+                 lambda: pa.pa_tree_decode(st["out"], x["q"], st["k"], st["v"], st["bt"], x["loc"], st["lens"], x["mask"], most,
+                                           0.1, tws),
+                 lambda: pa.pa_tree_commit(st["k"], st["v"], st["bt"], x["loc"], st["lens"], x["path"], x["acc"], st["new"]),
+                 lambda: resize(st["new"]), lambda: resize(x["ended"]),
+                 lambda: pa.pa_fork_pages(st["bt"], st["lens"], x["parents"], st["ref"], bs),
+                 lambda: pa.pa_decode(st["dec"], x["dq"], st["k"], st["v"], st["bt"], st["lens"], mb * bs, 0.1, workspace=dws),
+                 lambda: pa.pa_prefill_chunk(st["chunk"], x["dq"], st["k"], st["v"], st["bt"], one, st["lens"], 1, 0.1),
+                 lambda: resize(x["none"])]
+        torch.cuda.synchronize()
+        for call in calls:
+            call()
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return st
+
+    pa.pa_device_errors(clear=True)
+    for turn in range(6):
+        x = make(turn)
+        want, got = step(x, True), step(x, False)
+        for name in want:
+            assert torch.equal(want[name], got[name]), (turn, name)
+        assert got["count"].item() == nb and not got["ref"].any()
+    assert pa.pa_device_errors(clear=True) == 0

@@ -32,3 +32,15 @@ def test_no_load_is_sent_to_several_blocks():
                     seen += 1
                     assert "multi" + "cast" not in line, f"{name}: {line}"
     assert seen >= 4      # the loads were found at all
+
+
+def test_no_read_of_changing_data_through_the_non_coherent_path():
+    """A kernel that waits for the one before it (griddepcontrol.wait) is resident while that one still writes, so what it
+    reads may change while it runs: the read-only path is not defined for that, nor may a load be moved ahead of the wait."""
+    waiting = []
+    for name, text in sources():
+        if "griddepcontrol.wait" in text:
+            waiting.append(name)
+            for form in ("__ldg(", "__ldcg(", "ldg_nc_128(", "ldg_f4(", "ld.global.nc", "__restrict__"):
+                assert form not in text, f"{name}: {form}"
+    assert {"decode.cuh", "latent_kernel.cuh", "pages.cuh", "prefill_kernel.cuh", "tree_kernel.cuh"} <= set(waiting)
