@@ -1713,11 +1713,14 @@ __global__ void __launch_bounds__(256, 2) splitk_merge_kernel(const DecodeParams
     constexpr int PRE = 64 / CW;  // pieces whose columns are loaded up front: 32, 16 or 8
     constexpr float kLn2 = 0.69314718055994531f;  // the prefix partials' m is base 2
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // once the dynamic grid has ended: its counter back to zero, and marked so, for the next call
-    if (p.dyn_tag && blockIdx.x == 0 && threadIdx.x == 0) {
+    // one thread waits whatever the rows are: a kernel behind this one that waits for it alone (a copy of the pages that the
+    // piece kernel has written) has then waited for the piece kernel, too, where no row has anything to merge
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        *p.dyn_counter = 0;
-        *p.dyn_tag = kDynTag;
+        if (p.dyn_tag) {  // the dynamic grid has ended: its counter back to zero, and marked so, for the next call
+            *p.dyn_counter = 0;
+            *p.dyn_tag = kDynTag;
+        }
     }
     const int row = blockIdx.x * (blockDim.x >> 5) + warp;  // s * Hq + h
     if (row >= p.num_seqs * p.n_q_heads) return;

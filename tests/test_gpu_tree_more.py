@@ -92,3 +92,31 @@ def test_each_call_reads_what_the_one_before_wrote(hq, hkv, d, bs):
             assert torch.equal(want[name], got[name]), (turn, name)
         assert got["count"].item() == nb and not got["ref"].any()
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("hq,S,longest", [(8, 6, 5000), (4, 200, 900), (4, 3, 100)])
+def test_copy_of_pages_that_a_decode_step_has_just_written(hq, S, longest):
+    """The step's rows (one call writes and decodes; with a bound on the lengths that asks for a merge, though no row has
+    anything to merge) are in the copies that follow at once."""
+    dt, bs, hkv, d = torch.bfloat16, 16, 4, 128
+    g, nb, mb = gen(S), 4 * S + 1, -(-longest // 16)
+    kc, vc = (randn(g, (nb, bs, hkv, d), dt) for _ in range(2))
+    lens = [1 + (7 * i) % 30 for i in range(S)]
+    bt = torch.full((S, mb), -1, device="cuda", dtype=torch.int32)
+    bt[:, :2] = torch.randperm(nb, generator=g, device="cuda")[:2 * S].view(S, 2).to(torch.int32)
+    cl = torch.tensor(lens, device="cuda", dtype=torch.int32)
+    last = torch.gather(bt.long(), 1, ((cl.long() - 1) // bs)[:, None])[:, 0]
+    used = torch.zeros(nb, device="cuda", dtype=torch.bool)
+    used[bt[:, :2].long()] = True
+    to = torch.nonzero(~used)[:S, 0]
+    pairs = torch.stack([last, to], 1).to(torch.int32).contiguous()
+    ws = torch.empty(max(16, pa.pa_decode_workspace_size(S, hq, d, longest, 0)), device="cuda", dtype=torch.uint8)
+    q, out = randn(g, (S, hq, d), dt), torch.empty((S, hq, d), device="cuda", dtype=dt)
+    at = (cl.long() - 1) % bs
+    for _ in range(10):
+        k, v = randn(g, (S, hkv, d), dt), randn(g, (S, hkv, d), dt)
+        torch.cuda.synchronize()
+        pa.pa_decode_write(out, q, kc, vc, bt, cl, longest, 0.1, k, v, last * bs + at, workspace=ws)
+        pa.pa_copy_pages(kc, vc, pairs)
+        assert torch.equal(kc[to, at], k) and torch.equal(vc[to, at], v)
+        assert torch.equal(kc[to], kc[last]) and torch.equal(vc[to], vc[last])
