@@ -13,7 +13,7 @@
 //    each copy takes its own share of the tile's keys.  So 128 threads (one a row of the tile, a TMEM lane each) share the
 //    softmax of few rows without exchanging anything: a copy is a split of the keys with a maximum and a sum of its own,
 //    and the copies are joined once, at the unit's end.  The weights go back to TMEM as the A operand of O += P V, with zeros
-//    in the columns of the other copies' keys (written once: no copy ever writes there).  The least NR that holds the rows:
+//    in the columns of the other copies' keys.  The least NR that holds the rows:
 //    16 rows in the 32 / 64 / 128-row kernels, 256 sequences of 50..650 tokens 125 / 151 / 165 us, 64 of 100..4096 98 / 100 / 102.
 //  * At 128 rows two threads share a row, half a tile's keys each (the tensor core's pace allows ~1100 cycles a tile; one
 //    thread a row takes ~2200, four in 80 registers each are slower than two: 64 sequences of 8K tokens x 256 rows 553 / 521 / 456 us).
@@ -24,15 +24,16 @@
 //    and 2.  Tiles prefetched into L2: 328 -> 360 us.)
 //  * The running maximum is lazy: weights are taken against the old one, and only where their sum over a thread's keys
 //    exceeds 2^8 are the maximum raised (to a whole power of two) and O and l rescaled.  Weights up to 2^8 are exact in
-//    fp32 and far from the 16-bit formats' limits.
-//  * A weight enters the second product rounded once to the cache's type (half a step, 2^-8 in bf16 and 2^-11 in fp16,
-//    relative), and l sums the rounded weights, so that they still sum to one; everything else is fp32.  In fp16 weights are
-//    scaled by 2^7, so that small ones are not subnormal.  Both sides measured: root-mean-square error against 64 bits,
-//    relative to the output, 0.0023 in bf16 (32-bit weights: 0.0017) and 0.00025..0.00029 in fp16 (0.00021), the most where
-//    values are independent.  The remainders as further products: the second product issued twice, 64 sequences of
-//    100..4096 tokens at 32 / 64 / 128 rows 98 -> 106, 99 -> 104, 109 -> 118 us, 256 rows x 8K 467 -> 543; with the remainders'
-//    own arithmetic (twice the keys a thread at 32 rows) 256 sequences of 50..650 tokens 125 -> 151; at 128 rows they have no
-//    room in TMEM.  One product stays, by one rule for all units.
+//    fp32; in fp16, where they are scaled by 2^7, their sum of up to 2^15 is half of what the format holds.
+//  * A weight enters the second product as its value rounded to the cache's type and the remainder rounded likewise (16 bits
+//    in bf16, 22 in fp16), two instructions on the same V rows, as in the chunks' kernel; l sums the unrounded weights and
+//    everything else is fp32.  In fp16 weights are scaled by 2^7, so that small ones are not subnormal.  Both sides
+//    measured: root-mean-square error against 64 bits, relative to the output, 0.0016..0.0017 in bf16 and 0.00021 in fp16,
+//    which are the output's own rounding (weights rounded once: 0.0023 and 0.00025..0.00029).  Time with remainders / without: 64
+//    sequences of 100..4096 tokens at 32 / 64 / 128 rows 96.6 / 95.7, 101 / 99.4, 111 / 102 us, 256 of 50..650 109 / 102, 64 of
+//    1K..8K at 256 rows 370 / 299.
+//  * Weights lie over the scores that they come from: the remainders double what is handed over, and scores and weights with
+//    places of their own leave room for one buffer of weights (32 / 128 rows: 97.3 / 119, 256 short ones 116).
 //  * All units laid end to end and measured in cost (a unit's start and output, then its tiles) are cut into equal ranges,
 //    one a CTA; units that a range's end cuts leave fp32 partials which tree_merge_kernel joins in a fixed order.  No
 //    host-side lengths, no atomics, two partials a CTA.  One thread of a CTA walks its range and tells the other warps the
@@ -91,6 +92,10 @@ struct Cfg {
     static constexpr int SOFTMAX = 4 * SPLIT;           // softmax warps; then the issuers, the Q loader, two K and two V loaders, the V scanner
     static constexpr int QK_WARP = SOFTMAX, PV_WARP = SOFTMAX + 1, Q_WARP = SOFTMAX + 2, K_WARP = SOFTMAX + 3,
                          V_WARP = SOFTMAX + 5, CHECK_WARP = SOFTMAX + 7, THREADS = (SOFTMAX + 8) * 32;
+    // registers a thread: launched with as many as fit (a multiple of 8), then split
+    static constexpr int REGS = 65536 / THREADS / 8 * 8, REGS_OTHERS = 96, REGS_SOFTMAX = SPLIT > 1 ? 160 : 232;
+    static_assert(32 * SOFTMAX * REGS_SOFTMAX + (THREADS - 32 * SOFTMAX) * REGS_OTHERS <= THREADS * REGS, "the split exceeds the launch");
+    static constexpr int NS = 3;                        // score buffers
     static constexpr int SLABS = D / 64;
     static constexpr int QSLAB = 128 * 128, KSLAB = BN * 128;
     static constexpr int TILE = SLABS * KSLAB;          // bytes of K (or V) of a tile
@@ -106,17 +111,19 @@ struct Cfg {
     static constexpr int ML_OFF = V_OFF + NV * TILE + (OWN_STAGE ? NR * D * (COPIES > 1 ? 4 : 2) : 0);  // what a row's threads tell each other
     static constexpr int BAR_OFF = ML_OFF + (SPLIT > 2 ? SPLIT : 2) * 128 * 4;
     static constexpr int K_FULL = 0, K_EMPTY = NK, V_FULL = 2 * NK, V_EMPTY = V_FULL + NV, V_OK = V_EMPTY + NV, Q_FULL = V_OK + NV, Q_EMPTY = Q_FULL + 1,
-                         S_FULL = Q_FULL + 2, P_FULL = Q_FULL + 4, PV_DONE = Q_FULL + 6,
-                         O_FREE = Q_FULL + 8, DRAIN = Q_FULL + 9, SEG_FULL = Q_FULL + 11, SEG_EMPTY = SEG_FULL + SEGS, NUM_BARS = SEG_EMPTY + SEGS;
+                         S_FULL = Q_FULL + 2, P_FULL = S_FULL + NS, PV_DONE = P_FULL + NS,
+                         O_FREE = PV_DONE + NS, DRAIN = O_FREE + 1, SEG_FULL = DRAIN + 2, SEG_EMPTY = SEG_FULL + SEGS, NUM_BARS = SEG_EMPTY + SEGS;
     static constexpr int MISC_OFF = (BAR_OFF + NUM_BARS * 8 + 15) & ~15;  // start record, TMEM address, scan scratch
     static constexpr int BAD_OFF = MISC_OFF + 192;                       // the V ring's rows that are not finite: a bit a row
     static constexpr int SEG_OFF = BAD_OFF + NV * 16;                    // the ring of segments
     static constexpr int SMEM_BYTES = SEG_OFF + SEGS * 48 + 1024;        // + alignment slack
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(COPIES == 1 || OWN_STAGE || NR * D * 4 <= SLABS * QSLAB, "the copies are joined in the Q tile's place");
-    // TMEM: two S buffers, two P buffers (16-bit pairs), O
-    
-    static constexpr uint32_t P_COL = D == 256 ? 128 : 384, O_COL = 256, TMEM_COLS = 512;
+    // TMEM: three S buffers and O.  A weight takes as many columns as a score, 16 bits and its remainder's 16: a thread writes
+    // them over the scores that it has read
+    static constexpr uint32_t S2_COL = D == 256 ? 128 : 384, O_COL = 256, TMEM_COLS = 512;
+    static_assert(2 * BN <= (int)O_COL && (D == 256 ? S2_COL + BN <= O_COL : O_COL + D <= S2_COL && S2_COL + BN <= TMEM_COLS), "columns");
+    static __device__ __forceinline__ uint32_t s_col(int b) { return b < 2 ? (uint32_t)(b * BN) : S2_COL; }
 };
 
 __device__ __forceinline__ void mma_ss(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -203,19 +210,6 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigne
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
     if (rare(__any_sync(0xffffffffu, !mbar_try_wait(bar, parity)))) return wait_slow(bar, parity, err);
     return true;
-}
-
-// ls += the pair of 16-bit values in w, in fp32 (one instruction a value: converting them first takes as many again)
-template <bool BF16>
-__device__ __forceinline__ void add16x2(float2& ls, uint32_t w) {
-    if constexpr (BF16)
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.bf16 %0, a, %0;\n\tadd.rn.f32.bf16 %1, b, %1;\n\t}"
-            : "+f"(ls.x), "+f"(ls.y)
-            : "r"(w));
-    else
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
-            : "+f"(ls.x), "+f"(ls.y)
-            : "r"(w));
 }
 
 // whether a phase is complete, without waiting
@@ -510,7 +504,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     using namespace tree;
     using C = Cfg<D, NR>;
     using F = F16x2<BF16>;
-    constexpr int BN = C::BN, KW = C::KW, H = KW, COPIES = C::COPIES, SPLIT = C::SPLIT, SOFTMAX = C::SOFTMAX;
+    constexpr int BN = C::BN, KW = C::KW, NS = C::NS, COPIES = C::COPIES, SPLIT = C::SPLIT, SOFTMAX = C::SOFTMAX;
     constexpr int QK_WARP = C::QK_WARP, PV_WARP = C::PV_WARP, Q_WARP = C::Q_WARP, K_WARP = C::K_WARP, V_WARP = C::V_WARP;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -538,12 +532,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         }
         mbar_init(bar(C::Q_FULL), 1);
         mbar_init(bar(C::Q_EMPTY), COPIES > 1 && !C::OWN_STAGE ? 1 + SOFTMAX : 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NS; ++i) {
             mbar_init(bar(C::S_FULL + i), 1);
             mbar_init(bar(C::P_FULL + i), SOFTMAX);
             mbar_init(bar(C::PV_DONE + i), 1);
-            mbar_init(bar(C::DRAIN + i), 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(bar(C::DRAIN + i), 1);
         mbar_init(bar(C::O_FREE), SOFTMAX);
         for (int i = 0; i < C::SEGS; ++i) {
             mbar_init(bar(C::SEG_FULL + i), 1);
@@ -587,6 +581,10 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     auto row_token = [&](int row) { return (int)(((uint32_t)row * (uint32_t)p.g_magic) >> 16); };
     int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
 
+    // registers from the warps that move data to those that compute (a thread of 64 keys holds as many scores and as many
+    // weights: without, 128 rows of 100..4096 tokens 119 us instead of 111)
+    if (warp < SOFTMAX) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHERS));
     if (warp < SOFTMAX) {
         // ------------------------------------------------------------ softmax, rescale, epilogue
         // row of the tile; of the unit; which copy of it, or which of its two threads (its share of a tile's keys)
@@ -594,7 +592,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         const int r = SPLIT > 1 ? R : R - share * NR;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_base + (uint32_t)(share * KW), tO = tmem + lane_base + C::O_COL;
-        const uint32_t tP = tmem + lane_base + C::P_COL + (uint32_t)(share * KW / 2);
         // the threads of a row share its reference: what one finds the others have to know
         auto row_or = [&](bool v) {
             if constexpr (SPLIT > 1) return bar_or<32 * SPLIT>(2 + quarter, v);
@@ -604,14 +601,6 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         const float sc = p.qk_scale_log2 != 0.f ? p.qk_scale_log2 : 0x1p-126f;
         const uint32_t unseen = sc > 0.f ? 0xFF800000u : 0x7F800000u;  // -inf, +inf
         constexpr float kMost = BF16 ? 0x1p8f : 0x1p15f;  // 2^(8 + kShift)
-        if constexpr (COPIES > 1) {  // the other copies' columns of P stay zero
-            uint32_t z[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) z[e] = 0u;
-#pragma unroll
-            for (int q = 0; q < BN / 32; ++q) stn<32>(tmem + lane_base + C::P_COL + 32 * q, z);
-            tc::wait_st();
-        }
         const int tok_r = row_token(r);
         bool ready = false;  // the next tile's barriers were seen complete
         int i = 0;  // tile number over the CTA's range
@@ -637,39 +626,42 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             int u = 0;
             auto step = [&](auto with_drafts) {
                 constexpr bool DRAFTS = decltype(with_drafts)::value;
-                const int b = i & 1;
-                if (rare(!__all_sync(0xffffffffu, ready))) {
-                    wait(C::S_FULL + b, i >> 1);
-                    if (i >= 2) wait(C::PV_DONE + b, (i >> 1) - 1);  // the weights' buffer is free
-                }
+                const int b = i % NS, before = (i + NS - 1) % NS, next = (i + 1) % NS;
+                if (rare(!__all_sync(0xffffffffu, ready))) wait(C::S_FULL + b, i / NS);
                 tc::fence_after();
-                const uint32_t tSb = tS + (uint32_t)(b * BN), tPb = tP + (uint32_t)(b * BN / 2);
+                const uint32_t tSb = tS + C::s_col(b);
+                if constexpr (COPIES > 1) {  // no weights of the other copies' keys
+                    constexpr int Z = KW < 32 ? KW : 32;
+                    uint32_t z[Z];
+#pragma unroll
+                    for (int e = 0; e < Z; ++e) z[e] = 0u;
+#pragma unroll
+                    for (int c = Z; c < BN; c += Z)
+                        if (KW <= Z || c >= KW) stn<Z>(tmem + lane_base + C::s_col(b) + (uint32_t)((share * KW + c) & (BN - 1)), z);
+                }
                 float add = 0.f;
-                // part h of this thread's scores; those of keys that the row does not see, where the tile holds such keys, become
-                // what the scale turns into -inf
-                auto scores = [&](int h, uint32_t (&x)[H]) {
+                uint32_t w[KW / 2], rem[KW / 2];
+                // this thread's scores; those of keys that the row does not see, where the tile holds such keys, become what the
+                // scale turns into -inf
+                auto scores = [&](uint32_t (&x)[KW]) {
+                    ldn<KW>(tSb, x);
+                    tc::wait_ld();
                     if constexpr (DRAFTS) {
 #pragma unroll
-                        for (int e = 0; e < H; ++e)
-                            if (!((sees[(h * H + e) / 32] >> ((h * H + e) & 31)) & 1u)) x[e] = unseen;
+                        for (int e = 0; e < KW; ++e)
+                            if (!((sees[e / 32] >> (e & 31)) & 1u)) x[e] = unseen;
                     }
                 };
                 bool raise = fresh, raised = false;
 #pragma unroll 1
                 for (;;) {
                     if (rare(raise)) {
-                        float mx = -INFINITY;
+                        uint32_t x[KW];
+                        scores(x);
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int h = 0; h < KW / H; ++h) {
-                            uint32_t x[H];
-                            ldn<H>(tSb + h * H, x);
-                            tc::wait_ld();
-                            scores(h, x);
-                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int e = 0; e < H; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e]) * sc);
-                            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                        }
+                        for (int e = 0; e < KW; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e]) * sc);
+                        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                         if constexpr (SPLIT > 1) {
                             m_s[128 * share + R] = mx;
                             bar_sync<32 * SPLIT>(2 + quarter);
@@ -685,7 +677,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         }
                         fresh = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
                         if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                            wait(C::PV_DONE + (b ^ 1), (i - 1) >> 1);  // O holds every tile before this one
+                            wait(C::PV_DONE + before, (i - 1) / NS);  // O holds every tile before this one
                             tc::fence_after();
 #pragma unroll 1
                             for (int q = 0; q < D / 16 / SPLIT; ++q) {  // (each thread of a row its part of the columns)
@@ -703,35 +695,29 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                     const float mu = m_ref == -INFINITY ? 0.f : m_ref - kShift<BF16>;
                     const float2 sc2 = make_float2(sc, sc), nmu2 = make_float2(-mu, -mu);
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t x[2][H];
-                    ldn<H>(tSb, x[0]);
-                    tc::wait_ld();
+                    uint32_t x[KW];
+                    scores(x);
 #pragma unroll
-                    for (int h = 0; h < KW / H; ++h) {
-                        if (h + 1 < KW / H) ldn<H>(tSb + (h + 1) * H, x[(h + 1) & 1]);  // in flight during this part
-                        scores(h, x[h & 1]);
-                        uint32_t w[H / 2];
-#pragma unroll
-                        for (int e = 0; e < H / 2; ++e) {
-                            const float2 v = ffma2(make_float2(__uint_as_float(x[h & 1][2 * e]), __uint_as_float(x[h & 1][2 * e + 1])), sc2, nmu2);
-                            w[e] = F::pack_rn(ex2(v.x), ex2(v.y));
-                            add16x2<BF16>(ls[e & 1], w[e]);
-                        }
-                        stn<H / 2>(tPb + h * H / 2, w);
-                        if (h + 1 < KW / H) tc::wait_ld();
+                    for (int e = 0; e < KW / 2; ++e) {
+                        float2 v = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nmu2);
+                        v = make_float2(ex2(v.x), ex2(v.y));
+                        ls[e & 1] = fadd2(ls[e & 1], v);
+                        w[e] = F::pack_rn(v.x, v.y);
+                        v = fsub2(v, F::unpack(w[e]));
+                        rem[e] = F::pack_rn(v.x, v.y);
                     }
-                    // the next tile's barriers, without waiting
-                    ready = mbar_test(bar(C::S_FULL + (b ^ 1)), (i + 1) >> 1);
-                    ready = mbar_test(bar(C::PV_DONE + (b ^ 1)), ((i + 1) >> 1) - 1) && ready;
+                    // the next tile's scores, without waiting
+                    ready = mbar_test(bar(C::S_FULL + next), (i + 1) / NS);
                     ls[0] = fadd2(ls[0], ls[1]);
                     add = ls[0].x + ls[0].y;
                     // (no weight is above their sum; the vote also says that a row's other thread has read this one's maximum)
                     raise = row_or(valid && add > kMost);
                     if (!rare(raise) || raised) break;
-                    // a row outgrew its reference by more than 2^8: once more (the same columns are written)
-                    tc::wait_st();
+                    // a row outgrew its reference by more than 2^8: once more
                 }
                 l += add;
+                stn<KW / 2>(tSb, w);
+                stn<KW / 2>(tSb + KW / 2, rem);
                 if constexpr (DRAFTS) {
                     // a drafted V row that is not finite makes the row NaN if it sees it.  (Before the weights are given: the
                     // tile's product releases its slot, and a slot's barrier is not looked at two phases late)
@@ -747,7 +733,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::P_FULL + b));  // the scores have been read, too
+                if (lane == 0) mbar_arrive(bar(C::P_FULL + b));  // (the scores have been read, too)
                 ++i;
             };
 #pragma unroll 1
@@ -764,7 +750,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
             const int slot = 2 * (int)blockIdx.x + (g.tile == 0 ? 1 : 0);
             const size_t row0 = (size_t)g.tok0 * p.n_q_heads + (size_t)g.head * p.g_heads;
             auto product = [&]() {  // the last one; what the row's threads have to tell each other is told before
-                wait(C::PV_DONE + ((i - 1) & 1), (i - 1) >> 1);
+                wait(C::PV_DONE + (i - 1) % NS, (i - 1) / NS);
                 tc::fence_after();
             };
             if constexpr (COPIES == 1) {
@@ -1067,15 +1053,15 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         for (Segment g; segment(seg, g);) {
             wait(C::Q_FULL, seg);
             for (int u = 0; u < g.n; ++u, ++i) {
-                const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NK));
+                const int b = (int)uniform((uint32_t)(i % NS)), st = (int)uniform((uint32_t)(i % C::NK));
                 wait(C::K_FULL + st, i / C::NK);
-                if (i >= 2) wait(C::P_FULL + b, (i >> 1) - 1);  // S has been read
+                if (i >= NS) wait(C::PV_DONE + b, i / NS - 1);  // the weights in the buffer have been used
                 if (!ok) break;
                 tc::fence_after();
                 const uint64_t dk = dk0 + (uint32_t)((st * C::TILE) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(el, tS + (uint32_t)(b * BN), dq + (uint32_t)(((kk >> 2) * C::QSLAB + (kk & 3) * 32) >> 4),
+                    mma_ss(el, tS + C::s_col(b), dq + (uint32_t)(((kk >> 2) * C::QSLAB + (kk & 3) * 32) >> 4),
                            dk + (uint32_t)(((kk >> 2) * C::KSLAB + (kk & 3) * 32) >> 4), ID_QK, kk > 0);
                 commit(el, bar(C::S_FULL + b));
                 commit(el, bar(C::K_EMPTY + st));
@@ -1092,22 +1078,26 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         // ------------------------------------------------------------ PV issue: O += P V, P in tensor memory
         constexpr uint32_t ID_PV = tc::idesc_f16(BF16, true, 128, D);
         const uint64_t dv0 = tc::sdesc_sw128(sV, C::KSLAB, 1024);
-        const uint32_t el = elect_one(), dO = uniform(tmem + C::O_COL), tP = uniform(tmem + C::P_COL);
+        const uint32_t el = elect_one(), dO = uniform(tmem + C::O_COL), tP = uniform(tmem);
         int i = 0, seg = 0;
         for (Segment g; segment(seg, g);) {
             if (seg > 0) wait(C::O_FREE, seg - 1);  // O of the segment before has been read
             for (int u = 0; u < g.n; ++u, ++i) {
-                const int b = (int)uniform((uint32_t)(i & 1)), st = (int)uniform((uint32_t)(i % C::NV));
+                const int b = (int)uniform((uint32_t)(i % NS)), st = (int)uniform((uint32_t)(i % C::NV));
                 const uint32_t acc = uniform(u > 0);
                 wait(C::V_OK + st, i / C::NV);
-                wait(C::P_FULL + b, i >> 1);
+                wait(C::P_FULL + b, i / NS);
                 if (!ok) break;
                 tc::fence_after();
                 const uint64_t dv = dv0 + (uint32_t)((st * C::TILE) >> 4);
                 const int steps = (int)uniform((uint32_t)((g.keys - (g.tile + u) * BN + 15) / 16));  // those that hold keys
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    mma_ts(kk < steps ? el : 0u, dO, tP + (uint32_t)(b * (BN / 2) + 8 * kk), dv + (uint32_t)((kk * 2048) >> 4), ID_PV, kk > 0 ? 1u : acc);
+                for (int kk = 0; kk < BN / 16; ++kk) {
+                    // the columns of 16 keys' weights and of their remainders
+                    const uint32_t at = tP + C::s_col(b) + (uint32_t)(kk / (KW / 16) * KW + 8 * (kk % (KW / 16)));
+                    mma_ts(kk < steps ? el : 0u, dO, at, dv + (uint32_t)((kk * 2048) >> 4), ID_PV, kk > 0 ? 1u : acc);
+                    mma_ts(kk < steps ? el : 0u, dO, at + (uint32_t)(KW / 2), dv + (uint32_t)((kk * 2048) >> 4), ID_PV, 1u);
+                }
                 commit(el, bar(C::V_EMPTY + st));
                 commit(el, bar(C::PV_DONE + b));
             }

@@ -7,7 +7,7 @@ import torch
 
 import paged_kv_cache_232_gb300 as pa
 from test_gpu_tree import Batch
-from tree_testutil import gen, randn, tree_sees, words_of
+from tree_testutil import attend64, gen, half_step, randn, tiny, tree_sees, words_of
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,37 @@ def test_copy_of_pages_that_a_decode_step_has_just_written(hq, S, longest):
         pa.pa_copy_pages(kc, vc, pairs)
         assert torch.equal(kc[to, at], k) and torch.equal(vc[to, at], v)
         assert torch.equal(kc[to], kc[last]) and torch.equal(vc[to], vc[last])
+
+
+def _check_weights(out, q, k, v, sees, scale, what):
+    """The bound of tree_testutil with weights of twice the type's bits: a weight enters the product as its rounded value and
+    the rounded remainder, so it is off by u^2 of itself (u: half a step of the type) instead of u, and in fp16, where a
+    remainder below 2^-20 of the largest weight is subnormal, by at most 2^-31 of the sum; twice as many additions."""
+    dt, T = out.dtype, k.shape[0]
+    want, spread, mag, ds = attend64(q, k, v, sees, scale)
+    e = ds + 2.0 ** -20 + half_step(dt) ** 2
+    d = e / (1 - e) * spread + (2 * T / 16 + 40) * 2.0 ** -23 * mag
+    if dt == torch.float16:
+        d = d + T * 2.0 ** -31 * v.double().abs().amax() * sees.any(-1)[:, None, None, None]
+    err = (out.double().reshape(want.shape) - want).abs()
+    bad = ~(err <= half_step(dt) * (want.abs() + d) + d + tiny(dt))
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} values off; largest error {float(err.max()):.3e}"
+
+
+@pytest.mark.parametrize("ty", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv,d,n", [(2, 1, 128, 9), (4, 1, 128, 12), (8, 2, 128, 30), (4, 1, 128, 70), (2, 2, 64, 16), (3, 1, 64, 20),
+                                          (8, 1, 64, 16), (6, 2, 96, 40), (2, 1, 256, 16), (4, 1, 256, 16), (4, 2, 256, 33)])
+def test_weights_keep_their_remainders(ty, hq, hkv, d, n):
+    """A value is off by its own rounding and hardly more: as pa_prefill_chunk's, whose causal chunk a chain of drafted tokens
+    is.  Contexts within a tile, over several and split over CTAs; references raised on the way; every kernel."""
+    for ctxs, growth in (([0, 40, 300], 0), ([9000, 5, 700], 0), ([1500, 700, 30], 30)):
+        b = Batch(ty, hq, hkv, d, 16, [n] * 3, ctxs, seed=d + n + growth)
+        if growth:                        # keys that grow along the context
+            for s in range(3):
+                t = torch.arange(b.lens[s], device="cuda")
+                b.k[s] = (b.k[s].float() * (t.float()[:, None, None] / b.lens[s] * growth)).to(b.dt)
+                b.kc[b.bt[s, t // 16].long(), t % 16] = b.k[s]
+        out = b.run()
+        for s in range(3):
+            at = slice(b.loc[s], b.loc[s + 1])
+            _check_weights(out[at], b.q[at], b.k[s], b.v[s], b.all_seen(s), b.scale, f"{ctxs[s]} tokens, growth {growth}")
