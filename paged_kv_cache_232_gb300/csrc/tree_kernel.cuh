@@ -50,6 +50,10 @@
 //  * A successful wait on a barrier costs ~200 cycles of a warp that does nothing else, so the softmax looks at the next
 //    tile's barriers while this one's weights are under way (493 -> 463 us at 256 rows).  A thread reads all its scores of a
 //    tile at once (64 in two parts: 494 instead of 450); tiles of context alone have a loop of their own without a test.
+//  * The kernels are 90..110 KB of code and sensitive to its size and place: 100 instructions that never run, in front of the
+//    loaders' loop, cost 11 % at 128 rows and more (110 -> 123 us; 256 rows 365 -> 412).  So what stands at every wait and
+//    every division is kept short, and loops that run once a unit are not unrolled (125 -> 111 KB: 128 rows 111 -> 104,
+//    256 rows 366 -> 327, 256 sequences of 50..650 tokens 111 -> 100).
 //  * Waits have a time limit; on expiry PA_DEVERR_TIMEOUT is set, the warps that load or issue products stop there, and the
 //    others go on without waiting, so that every barrier of the block is still met.  Loads and products under way are
 //    waited for (again with the limit); the results are not used.
@@ -203,9 +207,21 @@ __device__ __forceinline__ bool bar_or(int id, bool v) {
 // Branches that few tiles take: their code is laid out of the others' way.
 __device__ __forceinline__ bool rare(bool v) { return __builtin_expect(v, 0); }
 
+// Waits, with the limit of all waits (few instructions: it stands at every wait).
+__device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, unsigned* err) {
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+    bool done;
+    do {
+        done = mbar_try_wait(bar, parity);
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    } while (!done && t - t0 < (uint32_t)kWaitLimitNs);
+    if (!done) flag_error(err, PA_DEVERR_TIMEOUT);
+    return done;
+}
 // The warp waits; the polling loop stays out of line.  One result for the warp.
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, unsigned* err) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+    return __all_sync(0xffffffffu, wait_limited(bar, parity, err));
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err) {
     if (rare(__any_sync(0xffffffffu, !mbar_try_wait(bar, parity)))) return wait_slow(bar, parity, err);
@@ -277,15 +293,12 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// ceil(n / d), n below 2^26 and d > 0, from an estimate that is off by a few (an integer division is much more code, and
-// code that runs once is paid for by its size)
+// ceil(n / d), n >= 0, d > 0 and a result of at most 21 bits: the estimate, right to 2^-22, is off by one at most
 __device__ __forceinline__ int ceil_div(int n, int d) {
-    int q = (int)((float)n * rcp((float)d));
-    while ((long long)q * d < n) ++q;
-    while (q > 0 && (long long)(q - 1) * d >= n) --q;
-    return q;
+    const int q = (int)((float)n * rcp((float)d)), rest = n - q * d;
+    return q + (rest > 0 ? 1 : 0) + (rest > d ? 1 : 0) - (rest <= -d ? 1 : 0);
 }
-// n / d and n mod d, n >= 0 and d > 0: an estimate is right to 2^-21, of 22 bits at once, of more in four steps
+// n / d and n mod d, n >= 0 and d > 0: of 22 bits from an estimate
 __device__ __forceinline__ long long quotient(long long n, int d, int& rest) {
     const float r = rcp((float)d);
     if (n < 1 << 22) {
@@ -295,16 +308,8 @@ __device__ __forceinline__ long long quotient(long long n, int d, int& rest) {
         rest -= off * d;
         return q + off;
     }
-    long long q = 0;
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-        const long long e = (long long)((float)n * r);
-        q += e;
-        n -= e * d;
-    }
-    while (n < 0) n += d, --q;
-    while (n >= d) n -= d, ++q;
-    rest = (int)n;
+    const long long q = n / d;
+    rest = (int)(n - q * d);
     return q;
 }
 __device__ __forceinline__ int passes_of(const TreeParams& p, const Seq& k) {
@@ -378,7 +383,7 @@ __device__ __forceinline__ void find_start(const TreeParams& p, int range, int r
     if (lane == 31) warp_sum[warp] = mine;
     __syncthreads();
     long long total = 0;
-#pragma unroll 4
+#pragma unroll 1
     for (int w = 0; w < NW; ++w) total += warp_sum[w];
     const int per = cost_of_range(p, total, ranges);
     const long long lo = (long long)range * per;
@@ -398,7 +403,7 @@ __device__ __forceinline__ void find_start(const TreeParams& p, int range, int r
             if (lane == 31) warp_sum[warp] = incl;
             __syncthreads();
             long long before = base;
-#pragma unroll 4
+#pragma unroll 1
             for (int w = 0; w < NW; ++w) {
                 const long long x = warp_sum[w];
                 if (w < warp) before += x;
@@ -576,7 +581,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         if (lane == 0) mbar_arrive(bar(C::SEG_EMPTY + j % C::SEGS));
         return g.n > 0;
     };
-    int done = 0;    // loader warps: tiles loaded
+    int slot = 0, use = 0;  // loader warps: the next tile's slot of the ring, and how often it has been filled
     // token of a unit's row, row / g_heads (exact for rows below 128 and up to 16 heads)
     auto row_token = [&](int row) { return (int)(((uint32_t)row * (uint32_t)p.g_magic) >> 16); };
     int4 begins = make_int4(0, 0, 0, 0), goes_on = begins;  // the units cut at the range's end and at its start
@@ -917,7 +922,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         const uint32_t vrow = tile + (uint32_t)(t * 128);
                         uint32_t z[4] = {0u, 0u, 0u, 0u};  // 0 * v: NaN where v is not finite
                         if (t < d1) {
-#pragma unroll
+#pragma unroll 2
                             for (int c = 0; c < C::SLABS * 4; ++c) {
                                 const uint4 v = lds128(vrow + (uint32_t)((c >> 2) * C::KSLAB + (((c & 3) + 4 * half + t) & 7) * 16));
                                 z[0] = zero_times<BF16>(v.x, z[0]);
@@ -973,12 +978,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
         bool more = segment(0, g);
         int id = more ? entry(g, g.tile) : 0;
         for (int seg = 1; more && ok; ++seg, g = ahead) {
-            for (int u = 0; u < g.n; ++u, ++done) {
+            for (int u = 0; u < g.n; ++u) {
                 const int tile = g.tile + u;
                 int nxt = 0;
                 if (u + 1 == g.n) more = segment(seg, ahead);
                 if (u + 1 < g.n || more) nxt = u + 1 < g.n ? entry(g, tile + 1) : entry(ahead, ahead.tile);
-                const int st = (int)uniform((uint32_t)(done % slots)), use = done / slots;
+                const int st = (int)uniform((uint32_t)slot);
                 if (use > 0) wait(empty0 + st, use - 1);
                 if (!ok) break;
                 const uint32_t full = bar(full0 + st), dst = ring + (uint32_t)(st * C::TILE);
@@ -993,10 +998,12 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         tma_box(el, dst + (uint32_t)(sl * C::KSLAB + x * br * 128), map, sl * 64, g.head, row, e, full, pol);
                 }
                 id = nxt;
+                if (++slot == slots) slot = 0, ++use;
             }
         }
         // the last releases too: none is on its way when the block leaves
-        for (int t = max(0, done - slots); t < done; ++t) wait(empty0 + t % slots, t / slots);
+        for (int s = 0; s < slots; ++s)
+            if (use > 0 || s < slot) wait(empty0 + s, s < slot ? use : use - 1);
     } else if (warp == Q_WARP) {
         // ------------------------------------------------------------ tells the others the segments, and loads the units'
         // query rows, once for each copy.  Two segments are told ahead whatever it takes (the loaders look one ahead of the
@@ -1013,7 +1020,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 bool tell = more && told < seg + C::SEGS && (told != 1 || seg > 0);
                 if (tell && told >= C::SEGS) {
                     const int sl = told % C::SEGS, phase = told / C::SEGS - 1;
-                    if (told < seg + 2) ok = mbar_wait(bar(C::SEG_EMPTY + sl), (uint32_t)(phase & 1), p.err);
+                    if (told < seg + 2) ok = wait_limited(bar(C::SEG_EMPTY + sl), (uint32_t)(phase & 1), p.err);
                     else tell = mbar_test(bar(C::SEG_EMPTY + sl), phase);
                     if (!ok) break;
                 }
@@ -1031,7 +1038,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                 }
                 const uint4 a = ring[3 * (seg % C::SEGS)];
                 if (ring[3 * (seg % C::SEGS) + 1].z == 0u) break;
-                if (seg > 0) ok = mbar_wait(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err);
+                if (seg > 0) ok = wait_limited(bar(C::Q_EMPTY), (uint32_t)((seg - 1) & 1), p.err);
                 if (!ok) break;
                 mbar_arrive_expect_tx(bar(C::Q_FULL), box * C::SLABS * COPIES);
 #pragma unroll 1
@@ -1041,7 +1048,7 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
                         tma_q(sQ + (uint32_t)(sl * C::QSLAB + c * NR * 128), &tmQ, sl * 64, (int)a.y * p.g_heads, (int)a.z, bar(C::Q_FULL));
                 ++seg;
             }
-            if (seg > 0) (void)mbar_wait(bar(C::Q_FULL), (uint32_t)((seg - 1) & 1), p.err);
+            if (seg > 0) (void)wait_limited(bar(C::Q_FULL), (uint32_t)((seg - 1) & 1), p.err);
         }
     } else if (warp == QK_WARP) {
         // ------------------------------------------------------------ QK issue: the whole warp walks the loop and one elected
@@ -1116,7 +1123,8 @@ tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const _
     const bool failed = __syncthreads_or(!ok);
     if (failed && warp >= K_WARP) {
         const int full0 = warp >= V_WARP ? C::V_FULL : C::K_FULL, slots = warp >= V_WARP ? C::NV : C::NK;
-        for (int t = max(0, done - slots); t < done; ++t) (void)warp_wait(bar(full0 + t % slots), (uint32_t)((t / slots) & 1), p.err);
+        for (int s = 0; s < slots; ++s)
+            if (use > 0 || s < slot) (void)warp_wait(bar(full0 + s), (uint32_t)((s < slot ? use : use - 1) & 1), p.err);
     }
     if (threadIdx.x == 0) {
         if (failed) begins = goes_on = make_int4(0, 0, 0, 0);
