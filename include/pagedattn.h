@@ -510,14 +510,16 @@ size_t pa_tree_workspace_size(int n_q_heads, int n_kv_heads, int head_dim, int m
  *  seq_lens [num_seqs] int32: tokens in the cache, the drafted ones included (ctx = seq_lens[s] - n_s)
  *  tree_mask [total_q, mask_words] int64, 64 mask_words >= max_q_len: drafted token j of a sequence sees every
  *         token t < ctx, and drafted token k (at ctx + k) where bit k of its row is set (its own bit too: nothing is
- *         implied); bits from n_s on are ignored.  A row that sees nothing is zero.
+ *         implied); bits from n_s on are ignored.  A row that sees nothing is zero, and so is one whose scores are all
+ *         -infinity.
  *  out[j, h] = sum_t softmax_t(scale * q[j, h] . K_t) V_t over the tokens that j sees, head h of KV head h / G.
  *  Any group size G = n_q_heads / n_kv_heads up to 16; head_dim 64, 96, 128 or 256; block_size 8 .. 128; trees of
  *  any size (a sequence longer than max_q_len or its table, shorter than its tree, or with rows outside
  *  [0, total_q) is skipped and sets PA_DEVERR_LENGTH).
  *  Cache rows of drafted tokens may hold anything for rows that do not see them (a padded token's slot is
- *  never written); a row that sees a V row which is not finite becomes NaN throughout.  Softmax weights enter
- *  the second product rounded to dtype; sums are fp32.
+ *  never written); a row that sees a drafted token whose V row is not finite becomes NaN throughout.  A value of the
+ *  context that is not finite, which every row sees, makes its column of those rows infinite or NaN, and no other.
+ *  Softmax weights enter the second product as two values of dtype, rounded and remainder; sums are fp32.
  */
 int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                    int max_blocks_per_seq, const int32_t* query_start_loc, const int32_t* seq_lens, const int64_t* tree_mask,
@@ -534,7 +536,7 @@ int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_
  *         head_dim * 2; a multiple of 16), num_layers 1 for one layer's cache; v_cache NULL for caches of one
  *         array a layer (the latent cache).  Data are copied bit by bit, whatever their type.
  *  block_tables [num_seqs, max_blocks_per_seq], seq_lens [num_seqs] as for attention: sequence s holds
- *         ceil(seq_lens[s] / block_size) pages.
+ *         ceil(seq_lens[s] / block_size) pages, block_size 8, 16, 32, 64 or 128.
  *
  * pa_tree_commit -- the rows of the accepted drafted tokens moved to the front of the drafted ones.
  *

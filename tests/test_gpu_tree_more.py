@@ -154,3 +154,33 @@ def test_weights_keep_their_remainders(ty, hq, hkv, d, n):
         for s in range(3):
             at = slice(b.loc[s], b.loc[s + 1])
             _check_weights(out[at], b.q[at], b.k[s], b.v[s], b.all_seen(s), b.scale, f"{ctxs[s]} tokens, growth {growth}")
+
+
+@pytest.mark.parametrize("ty,value", [("fp16", "inf"), ("bf16", "-inf"), ("bf16", "nan"), ("fp16", "nan")])
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 2, 128, 9), (8, 2, 128, 16), (16, 2, 128, 16), (8, 2, 128, 70), (4, 2, 64, 16), (16, 2, 64, 16),
+                                          (4, 2, 256, 16), (16, 2, 256, 16)])
+def test_cached_value_that_is_not_finite_spoils_its_column_alone(ty, value, hq, hkv, d, n):
+    """A V row of the context, which every drafted token sees: that column of its KV head's rows is not finite, whatever the
+    number of rows (32, 64, 128 and more of them), and nothing else changes.  In a tile of context alone and in the
+    last one, beside the drafted tokens."""
+    b = Batch(ty, hq, hkv, d, 16, [n, n], [270, 100], seed=n + d)
+    want, kept, g = b.run(), b.vc.clone(), hq // hkv
+    assert want.isfinite().all()
+    for t, col in ((30, 5), (269, d - 1)):
+        b.vc[b.bt[0, t // 16].long(), t % 16, 1, col] = float(value)
+        out = b.run()
+        assert not out[:n, g:, col].isfinite().any()
+        out[:n, g:, col] = want[:n, g:, col]
+        assert torch.equal(out, want)
+        b.vc.copy_(kept)
+
+
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 2, 128, 9), (8, 2, 128, 16), (16, 2, 128, 16), (8, 2, 64, 70), (16, 2, 256, 16)])
+def test_scores_that_are_all_minus_infinity(hq, hkv, d, n):
+    """Such rows are zero, as those that see nothing; the other KV head's rows are not touched by it."""
+    b = Batch("bf16", hq, hkv, d, 16, [n, n], [270, 3], seed=n)
+    want, g = b.run(), hq // hkv
+    b.q[:, g:, 0] = 1.0
+    b.kc[:, :, 1, 0] = float("-inf")
+    out = b.run()
+    assert not out[:, g:].any() and torch.equal(out[:, :g], want[:, :g])
