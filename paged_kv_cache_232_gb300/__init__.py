@@ -370,7 +370,7 @@ def _device(t) -> int:
     at = t.get_device()
     if at < 0:
         raise ValueError("every tensor must be a CUDA tensor")
-    dev = _torch()._C._cuda_getDevice()
+    dev = _torch().cuda.current_device()
     if at != dev:
         raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     return dev
