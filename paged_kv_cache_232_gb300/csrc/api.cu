@@ -1335,9 +1335,9 @@ int pa_tree_decode(void* out, const void* q, const void* k_cache, const void* v_
     p.group = u.group;
     p.tile_log2 = kdim == 256 ? 6 : 7;
     p.block_log2 = 4 + cpb_log2_of(block_size);
-    // in tiles of 64 KB (32 at 64 columns): 64 sequences of 100..4096 tokens at 2 / 4: 32 rows x 128 91 / 93 us (one sequence of
-    // 1000: 13.2 / 14.8), 128 rows 101 / 101, 256 rows 277 / 266, 32 rows x 64 71 / 60, 32 rows x 256 105 / 93
-    p.unit_cost = u.rows == 32 && kdim == 128 ? 2 : 4;
+    // in tiles of 64 KB (32 at 64 columns): 64 sequences of 100..4096 tokens at 2 / 4: 32 rows x 128 95.7 / 97.0 us (one sequence
+    // of 1000: 11.9 / 13.6), 32 rows x 64 63.9 / 66.4, 64 and 128 rows the same, 512 rows 211 / 185, 32 rows x 256 102 / 97
+    p.unit_cost = u.rows == 32 && kdim <= 128 ? 2 : 4;
     p.min_tiles = p.unit_cost + 1;
     p.qk_scale_log2 = scale * 1.4426950408889634f;
     p.desc = reinterpret_cast<int4*>(base);
