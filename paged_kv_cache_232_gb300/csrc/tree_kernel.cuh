@@ -7,21 +7,24 @@
 // K_t and V_t of KV head h / G.  The tokens of a tree times the G heads of a KV head are the rows of one
 // dense contraction over the same keys: each key is read once for all of them.
 //
-// GB300 design:
+// GB300 design (times of 64 sequences of 8K tokens x 256 rows are of a build with weights rounded once, those between 437 and
+// 470 us with loads shared by two CTAs as well; both sides of a choice are always of one build):
 //  * A unit is up to NR query rows (32, 64 or 128) of one sequence and KV head over its keys, in tiles of BN keys (128;
 //    64 at head_dim 256).  S = Q K^T is one M = 128 product whatever NR is: the tile holds 128 / NR copies of the rows, and
 //    each copy takes its own share of the tile's keys.  So 128 threads (one a row of the tile, a TMEM lane each) share the
 //    softmax of few rows without exchanging anything: a copy is a split of the keys with a maximum and a sum of its own,
 //    and the copies are joined once, at the unit's end.  The weights go back to TMEM as the A operand of O += P V, with zeros
 //    in the columns of the other copies' keys.  The least NR that holds the rows:
-//    16 rows in the 32 / 64 / 128-row kernels, 256 sequences of 50..650 tokens 125 / 151 / 165 us, 64 of 100..4096 98 / 100 / 102.
-//  * At 128 rows two threads share a row, half a tile's keys each (the tensor core's pace allows ~1100 cycles a tile; one
-//    thread a row takes ~2200, four in 80 registers each are slower than two: 64 sequences of 8K tokens x 256 rows 553 / 521 / 456 us).
-//    They keep one reference, by a vote of the row's two warps a tile.
+//    16 rows in the 32 / 64 / 128-row kernels, 256 sequences of 50..650 tokens 100 / 129 / 127 us, 64 of 100..4096 96 / 98 / 97, one of
+//    1000 12.0 / 14.0 / 14.4, 64 at 64 columns 66 / 72 / 79.
+//  * At 128 rows two threads share a row, half a tile's keys each (one thread a row, or four in 80 registers each, with weights
+//    rounded once: 64 sequences of 8K tokens x 256 rows 553 / 521, two 456 us).  They keep one reference, by a vote of the
+//    row's two warps a tile (a reference and an accumulator for each, in two buffers: 128 rows 104 -> 113 us; a vote that is cast
+//    before the remainders' arithmetic and read behind it: 109).
 //  * K and V arrive by TMA in boxes of 16 tokens (8 in blocks of 8) x 64 columns, 128-byte swizzled, in two rings of whole
 //    tiles; K is released by its product, V by its own.  QK and PV have an issuer each.  (Boxes of 64 tokens: no faster.
 //    A third V tile beside three of K takes the L1 that block tables and masks need; 2 K and 3 V tiles 1..2 % faster than 3
-//    and 2.  Tiles prefetched into L2: 328 -> 360 us.)
+//    and 2, 256 rows 335..341 us to 341..346.  Tiles prefetched into L2: 328 -> 360 us.)
 //  * The running maximum is lazy: weights are taken against the old one, and only where their sum over a thread's keys
 //    exceeds 2^8 are the maximum raised (to a whole power of two) and O and l rescaled.  Weights up to 2^8 are exact in
 //    fp32; in fp16, where they are scaled by 2^7, their sum of up to 2^15 is half of what the format holds.
@@ -30,8 +33,8 @@
 //    everything else is fp32.  In fp16 weights are scaled by 2^7, so that small ones are not subnormal.  Both sides
 //    measured: root-mean-square error against 64 bits, relative to the output, 0.0016..0.0017 in bf16 and 0.00021 in fp16,
 //    which are the output's own rounding (weights rounded once: 0.0023 and 0.00025..0.00029).  Time with remainders / without: 64
-//    sequences of 100..4096 tokens at 32 / 64 / 128 rows 96.6 / 95.7, 101 / 99.4, 111 / 102 us, 256 of 50..650 109 / 102, 64 of
-//    1K..8K at 256 rows 370 / 299.
+//    sequences of 100..4096 tokens at 32 / 64 / 128 rows 96 / 95.7, 100 / 99.4, 104 / 102 us, 256 of 50..650 100 / 102, 64 of
+//    1K..8K at 256 rows 325 / 299 (without: before the code was shortened, below).
 //  * Weights lie over the scores that they come from: the remainders double what is handed over, and scores and weights with
 //    places of their own leave room for one buffer of weights (32 / 128 rows: 97.3 / 119, 256 short ones 116).
 //  * All units laid end to end and measured in cost (a unit's start and output, then its tiles) are cut into equal ranges,
@@ -49,7 +52,8 @@
 //    product: one that is not finite is zeroed in shared memory, the rows that see it becoming NaN.
 //  * A successful wait on a barrier costs ~200 cycles of a warp that does nothing else, so the softmax looks at the next
 //    tile's barriers while this one's weights are under way (493 -> 463 us at 256 rows).  A thread reads all its scores of a
-//    tile at once (64 in two parts: 494 instead of 450); tiles of context alone have a loop of their own without a test.
+//    tile at once (64 in two parts: 494 instead of 450); tiles of context alone have a loop of their own without a test
+//    (64 columns 66 us, 256 rows 324; with one loop 72 and 335).
 //  * The kernels are 90..110 KB of code and sensitive to its size and place: 100 instructions that never run, in front of the
 //    loaders' loop, cost 11 % at 128 rows and more (110 -> 123 us; 256 rows 365 -> 412).  So what stands at every wait and
 //    every division is kept short, and loops that run once a unit are not unrolled (125 -> 111 KB: 128 rows 111 -> 104,
@@ -59,16 +63,18 @@
 //    waited for (again with the limit); the results are not used.
 //  * No wait can be overtaken: a barrier two phases on looks like one that is not complete.  So what a warp waits for goes
 //    on only after that warp has arrived at something that it needs: every V tile passes the scanner on its way to the
-//    product, and the softmax looks at the scanner's barrier before it hands over the tile's weights.  (Tiles without
+//    product, the softmax looks at the scanner's barrier before it hands over the tile's weights, and a score buffer is written
+//    again only when the product of its weights is complete.  (Tiles without
 //    drafted tokens straight to the product, released by the scanner as well: 256 rows x 8K 551 us instead of 450.)
 //
 // What bounds it: memory up to 128 rows, 6.4..6.8 TB/s between the starts and ends of units (a tile of 64 KB in ~2800
-// cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the softmax (a chain of ~1750 cycles a tile: ~850 of arithmetic
-// of two warps that vote on the reference every tile, the rest a dozen short dependent steps) beside loads (475 of 492 us
-// alone at 64 x 8K) and products (1024 cycles; everything but the loads 409 us).  Fixed: ~4 us to the first weights, 1.5..2.3 us a unit that the rings do not cover (the last
-// product, the join, the first tile's maximum), ~3 us of merge.  Whole calls (GB300, in a graph): 64 sequences of 100..4096
-// tokens, 16 drafted, 16 q / 8 KV heads 93 us (82 us of bytes at the copy rate), 4 x 32K 86 (76), 64 x 1K..8K, 64 drafted, 32 q
-// heads 298 (190), 256 x 50..650 99 (56), one of 100 9.5.
+// cycles; DRAM traffic 1.00 x the keys' bytes).  At 256 rows the products (three of 512 cycles at best a tile, the tensor pipe 64 %
+// busy) and the softmax beside them: of 363 us for 64 x 1K..8K the remainders' product takes 49, their arithmetic 50, the
+// vote of a row's warps 28 (each left out alone); in a row of calls the chip's power limit lowers the clock, 330 -> 360.  Fixed: ~4
+// us to the first weights, 1.5..2.3 us a unit that the rings do not cover (the last product, the join, the first tile's
+// maximum), ~3 us of merge.  Whole calls (GB300, in a graph): 64 sequences of 100..4096 tokens, 16 drafted, 16 q / 8 KV heads
+// 94..96 us (83 us of bytes at the copy rate), 4 x 30K..32K 90..92 (76), 64 x 1K..8K, 64 drafted, 32 q heads 325..365 (190), 256 x
+// 50..650 100 (61), one of 100 9.1.
 #pragma once
 
 #include <type_traits>
